@@ -44,7 +44,7 @@
 extern "C" {
 #endif
 
-#define MUON_STEP_ABI_VERSION 4
+#define MUON_STEP_ABI_VERSION 5
 
 /* Bytes of the fixed per-GPU device scratch muon_step_noalloc works in. */
 #define MUON_NOALLOC_SCRATCH_BYTES 134217728
@@ -127,6 +127,11 @@ typedef struct muon_matrix {
  *   nesterov      1: NS input mu*M_t + G_t;  0: NS input M_t.
  *   ns_precision  muon_ns_precision.
  *   scale_mode    muon_scale_mode (other values: INVALID_ARGUMENT).
+ *   grad_factor   optional device float (muon_grad_norm's factor): G_t is then
+ *                 fl32(factor * G_t), one rounding, wherever the step reads it.
+ *                 It is read when the step runs.  NULL: no factor.  It must not
+ *                 lie in memory that the step writes.  Read by muon_step and
+ *                 muon_step_noalloc only.
  * lr, momentum, weight_decay and gamma must be finite. */
 typedef struct muon_hparams {
     double lr;
@@ -138,6 +143,7 @@ typedef struct muon_hparams {
     int32_t nesterov;
     int32_t ns_precision;
     int32_t scale_mode; /* muon_scale_mode */
+    const float *grad_factor;
 } muon_hparams;
 
 /* One tensor handed to muon_adamw_step: numel contiguous fp32 elements each
@@ -171,6 +177,63 @@ typedef struct muon_adamw_hparams {
     int64_t step;
 } muon_adamw_hparams;
 
+/* One tensor handed to muon_adamw_mixed_step: numel contiguous elements of
+ * each.
+ *   param       device, param_dtype, in and out
+ *   master      optional device fp32 (with bf16 param only): the weights the
+ *               step is applied to, in and out; param is then written only, and
+ *               receives their values rounded to bf16 (nearest even).  NULL: the
+ *               step is applied to param itself, and rounded to its type.
+ *   grad        device, grad_dtype, read only
+ *   exp_avg, exp_avg_sq  device fp32, in and out
+ * Every address must be a multiple of its element's size; 16-byte aligned ones
+ * run in wider accesses, with the same results.  Pointers of a tensor with
+ * numel 0 are not looked at.  No written range may overlap any other range of
+ * the call; gradients may share memory. */
+typedef struct muon_adamw_mixed_tensor {
+    void *param;
+    float *master;
+    const void *grad;
+    float *exp_avg;
+    float *exp_avg_sq;
+    int64_t numel;
+    int32_t param_dtype; /* muon_dtype */
+    int32_t grad_dtype;  /* muon_dtype */
+} muon_adamw_mixed_tensor;
+
+/* Elements of a tensor that share one scale in 8-bit moments. */
+#define MUON_ADAMW8_BLOCK 32
+
+/* One tensor handed to muon_adamw8_step; param, master, grad and the rules for
+ * all pointers as in muon_adamw_mixed_tensor.  Each moment is held in
+ *   codes   numel bytes: e4m3 (sign, 4 exponent bits of bias 7, 3 mantissa
+ *           bits; largest 448, 0x7f and 0xff NaN), and
+ *   scale   ceil(numel / 32) bytes: e8m0, byte e of elements 32 k .. 32 k + 31
+ *           standing for 2^(e - 127), 255 for NaN;
+ * an element's value is its code's times its block's scale.  All bytes zero
+ * are moments of zero, the state before the first step.  The step writes
+ * exactly these bytes: codes past numel in the last block have no memory. */
+typedef struct muon_adamw8_tensor {
+    void *param;
+    float *master;
+    const void *grad;
+    uint8_t *exp_avg;
+    uint8_t *exp_avg_sq;
+    uint8_t *exp_avg_scale;
+    uint8_t *exp_avg_sq_scale;
+    int64_t numel;
+    int32_t param_dtype; /* muon_dtype */
+    int32_t grad_dtype;  /* muon_dtype */
+} muon_adamw8_tensor;
+
+/* One gradient of muon_grad_norm: numel contiguous elements, read only. */
+typedef struct muon_grad {
+    const void *grad; /* device */
+    int64_t numel;
+    int32_t dtype; /* muon_dtype */
+    int32_t reserved;
+} muon_grad;
+
 typedef struct muon_context muon_context; /* opaque */
 
 /* ABI version of the loaded library (MUON_STEP_ABI_VERSION it was built with). */
@@ -199,6 +262,16 @@ muon_status muon_check_step_args(const muon_matrix *mats, int64_t count, const m
 /* Host-only validation of a muon_adamw_step argument list. */
 muon_status muon_check_adamw_args(const muon_adamw_tensor *ts, int64_t count,
                                   const muon_adamw_hparams *hp, char *msg, size_t msg_cap);
+
+/* Host-only validation of the argument lists of muon_adamw_mixed_step,
+ * muon_adamw8_step and muon_grad_norm. */
+muon_status muon_check_adamw_mixed_args(const muon_adamw_mixed_tensor *ts, int64_t count,
+                                        const muon_adamw_hparams *hp, const float *grad_factor, char *msg,
+                                        size_t msg_cap);
+muon_status muon_check_adamw8_args(const muon_adamw8_tensor *ts, int64_t count, const muon_adamw_hparams *hp,
+                                   const float *grad_factor, char *msg, size_t msg_cap);
+muon_status muon_check_grad_norm_args(const muon_grad *gs, int64_t count, double max_norm, const double *norm,
+                                      const float *factor, char *msg, size_t msg_cap);
 
 /* Workspace the library would allocate for this argument list when nothing
  * caps it: the largest per-group chunk of Newton-Schulz buffers (with
@@ -273,6 +346,70 @@ muon_status muon_step_noalloc(muon_context *ctx, const muon_matrix *mats, int64_
 muon_status muon_adamw_step(muon_context *ctx, const muon_adamw_tensor *ts, int64_t count,
                             const muon_adamw_hparams *hp, void *hip_stream);
 
+/* The three entry points below upload nothing and allocate nothing: their
+ * descriptors travel as kernel arguments.  They may be captured into a graph,
+ * on their first call too; a replay uses the addresses and the host scalars of
+ * the capture (lr, step and the rounding's key with it) and reads grad_factor
+ * anew.  As everywhere, tensors, norm and factor must stay allocated until the
+ * work has run. */
+
+/* AdamW over `count` tensors (host array ts) of mixed types, with moments in
+ * 32 bits: per element the operations of muon_adamw_step in the same order and
+ * rounding, on fp32 values of param (or master) and grad; fp32 tensors get the
+ * same bits as there.  With grad_factor (device float, or NULL) the gradient
+ * is fl32(factor * grad); the factor is read when the step runs, so it may be
+ * what muon_grad_norm writes on the same stream.  hp as in muon_adamw_step,
+ * with beta1 and beta2 in [0, 1) and eps >= 0.  Non-finite values propagate
+ * element by element (IEEE).  A tensor's result does not depend on the other
+ * tensors of the call. */
+muon_status muon_adamw_mixed_step(muon_context *ctx, const muon_adamw_mixed_tensor *ts, int64_t count,
+                                  const muon_adamw_hparams *hp, const float *grad_factor, void *hip_stream);
+
+/* The same step with moments in 8 bits.  In fp32, one rounding per operation
+ * (g the gradient as above, m and v the values of the stored moments):
+ *   m1 = b1 m + (1-b1) g,   v1 = b2 v + ((1-b2) g) g,
+ * and from them, before they are coded,
+ *   p <- (1 - lr wd) p - (lr / (1 - b1^step)) m1 / (sqrt(v1 / (1 - b2^step)) + eps)
+ * in fp32 within 2^-20 of the update's and 2^-22 of p's magnitude (1 / (1 -
+ * b2^step) as a factor, square root and reciprocal within 1 ulp; v1 / (1 -
+ * b2^step) of 2^104 or more counts as infinite; eps must be 0 or at least
+ * 2^-126).  The moments are then coded block by block:
+ *   e     the smallest exponent byte, 17 at least, with |x| 2^(127-e) <= 448
+ *         for every value x of the block; y = x 2^(127-e)
+ *   v1    a value below 2^-9 counts as y = 2^-9 (the smallest code above zero)
+ *         if any of its block is above zero, so a second moment is never
+ *         rounded to nothing; it is then held too large, and the element's
+ *         steps are smaller than without the rounding
+ *   code  |y| rounded to e4m3 stochastically: up if the part of it below the
+ *         code's last place, in units of that place, plus u is 1 or more.
+ *         u = (r >> 12) / 2^20 with r from element i of its tensor, the seed
+ *         and the step: q = i / 4, j = i % 4, r = mix((q mod 2^32) ^ key ^
+ *         ((q / 2^32) 0x9E3779B9 mod 2^32)) turned left by 8 j bits (16 more
+ *         for v1, modulo 32), key = mix(seed_lo ^ mix(seed_hi ^ mix(step_lo ^
+ *         mix(step_hi)))), mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15;
+ *         x *= 0xBB67AE85; x ^= x >> 16 (32 bits).
+ * The codes are thus fixed bit for bit.  A block that holds an infinity or a
+ * NaN in m1 (v1) becomes NaN in that moment, all 32 elements of it.  Use one
+ * seed per run; the step count varies the rounding.  A tensor's result does
+ * not depend on the other tensors of the call. */
+muon_status muon_adamw8_step(muon_context *ctx, const muon_adamw8_tensor *ts, int64_t count,
+                             const muon_adamw_hparams *hp, uint64_t seed, const float *grad_factor,
+                             void *hip_stream);
+
+/* The 2-norm of `count` gradients (host array gs) taken together, and the
+ * factor that clips it to max_norm (> 0; infinity: never):
+ *   *norm = sqrt(sum g^2), squares and sums in fp64 in an order that depends on
+ *           the list's sizes alone
+ *   *factor = fl32(max_norm / norm) if norm > max_norm, 1 if not, NaN if the
+ *           norm is infinite or NaN (a step that reads it then writes NaN
+ *           everywhere).
+ * norm and factor are device memory outside every gradient; no gradient is
+ * written.  The sums pass through memory of the context: as for every entry
+ * point, calls on one context (and replays of graphs that captured it) must be
+ * ordered. */
+muon_status muon_grad_norm(muon_context *ctx, const muon_grad *gs, int64_t count, double max_norm, double *norm,
+                           float *factor, void *hip_stream);
+
 /* Normalisation + Newton-Schulz only: x_out (device fp32 rows x cols)
  * receives NS(n_in / ||n_in||_F) for the device fp32 rows x cols input n_in,
  * with hp's schedule and precision (lr, momentum, weight_decay, gamma,
@@ -343,9 +480,9 @@ muon_status muon_stream_probe(muon_context *ctx, const void *src, void *dst, int
  * A A, and the bytes it must move to and from HBM) is recorded with it.
  * Stage names: "momentum_nesterov", "norm_finalize", "normalize", "gram",
  * "poly", "apply", "apply_update" (the last product with the fused decay and
- * update), "update", "adamw", "import", "export", "unit_rms" (the per-matrix
- * ||X||^2 reduction and scale of the unit-RMS mode), "stream_probe"
- * (muon_stream_probe), "prenormalize" (the bf16
+ * update), "update", "adamw", "adamw_mixed", "adamw8", "grad_norm", "import",
+ * "export", "unit_rms" (the per-matrix ||X||^2 reduction and scale of the
+ * unit-RMS mode), "stream_probe" (muon_stream_probe), "prenormalize" (the bf16
  * path's normalisation of the matrices whose ||N_t|| lies outside the range
  * in which the first step folds 1/||N_t|| into its products). */
 typedef struct muon_stage_stats {

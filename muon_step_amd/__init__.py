@@ -35,11 +35,15 @@ EXPORTS = (
     "muon_last_error", "muon_step", "muon_adamw_step", "muon_ns_only", "muon_apply_update",
     "muon_last_norms", "muon_profile_enable", "muon_profile_read", "muon_step_noalloc",
     "muon_stream_probe", "muon_ns_stage", "muon_set_concurrent_groups",
+    "muon_adamw_mixed_step", "muon_adamw8_step", "muon_grad_norm", "muon_check_adamw_mixed_args",
+    "muon_check_adamw8_args", "muon_check_grad_norm_args",
 )
 
 MUON_STAGE_GRAM = 0
 MUON_STAGE_POLY = 1
 MUON_STAGE_APPLY = 2
+
+MUON_ADAMW8_BLOCK = 32
 
 
 class MuonError(RuntimeError):
@@ -63,7 +67,7 @@ class muon_hparams(ctypes.Structure):
                 ("weight_decay", ctypes.c_double), ("gamma", ctypes.c_double),
                 ("schedule", ctypes.POINTER(muon_ns_coeff)), ("num_ns_steps", ctypes.c_int32),
                 ("nesterov", ctypes.c_int32), ("ns_precision", ctypes.c_int32),
-                ("scale_mode", ctypes.c_int32)]
+                ("scale_mode", ctypes.c_int32), ("grad_factor", ctypes.c_void_p)]
 
 
 class muon_adamw_tensor(ctypes.Structure):
@@ -75,6 +79,24 @@ class muon_adamw_tensor(ctypes.Structure):
 class muon_adamw_hparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64)]
+
+
+class muon_adamw_mixed_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class muon_adamw8_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scale", ctypes.c_void_p), ("exp_avg_sq_scale", ctypes.c_void_p),
+                ("numel", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class muon_grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class muon_stage_stats(ctypes.Structure):
@@ -113,6 +135,16 @@ def load(path=LIB_PATH):
         "muon_step_noalloc": (i32, [vp, c.POINTER(muon_matrix), i64, c.POINTER(muon_hparams), vp]),
         "muon_adamw_step": (i32, [vp, c.POINTER(muon_adamw_tensor), i64,
                                   c.POINTER(muon_adamw_hparams), vp]),
+        "muon_adamw_mixed_step": (i32, [vp, c.POINTER(muon_adamw_mixed_tensor), i64,
+                                        c.POINTER(muon_adamw_hparams), vp, vp]),
+        "muon_adamw8_step": (i32, [vp, c.POINTER(muon_adamw8_tensor), i64, c.POINTER(muon_adamw_hparams),
+                                   c.c_uint64, vp, vp]),
+        "muon_grad_norm": (i32, [vp, c.POINTER(muon_grad), i64, c.c_double, vp, vp, vp]),
+        "muon_check_adamw_mixed_args": (i32, [c.POINTER(muon_adamw_mixed_tensor), i64,
+                                              c.POINTER(muon_adamw_hparams), vp, c.c_char_p, sz]),
+        "muon_check_adamw8_args": (i32, [c.POINTER(muon_adamw8_tensor), i64, c.POINTER(muon_adamw_hparams), vp,
+                                         c.c_char_p, sz]),
+        "muon_check_grad_norm_args": (i32, [c.POINTER(muon_grad), i64, c.c_double, vp, vp, c.c_char_p, sz]),
         "muon_ns_only": (i32, [vp, vp, vp, i64, i64, c.POINTER(muon_hparams), vp]),
         "muon_apply_update": (i32, [vp, vp, i32, vp, i64, i64, c.POINTER(muon_hparams), vp]),
         "muon_last_norms": (i32, [vp, c.POINTER(c.c_double), i64, c.POINTER(i64)]),
@@ -144,16 +176,18 @@ def schedule(name="deepseekv4"):
 
 
 def make_hparams(lr=0.02, momentum=0.95, weight_decay=0.1, gamma=0.2, nesterov=True,
-                 coeffs=None, ns_precision=MUON_NS_BF16, scale_mode=MUON_SCALE_SQRT_MAX):
-    """Builds a muon_hparams; `coeffs` defaults to the DeepSeek-V4 hybrid schedule.
-    The returned object keeps its schedule array alive."""
+                 coeffs=None, ns_precision=MUON_NS_BF16, scale_mode=MUON_SCALE_SQRT_MAX, grad_factor=None):
+    """Builds a muon_hparams; `coeffs` defaults to the DeepSeek-V4 hybrid schedule, `grad_factor` is an
+    optional one-element float32 GPU tensor that every gradient is multiplied by.
+    The returned object keeps its schedule array and the factor alive."""
     if coeffs is None:
         coeffs = schedule("deepseekv4")
     arr = (muon_ns_coeff * max(1, len(coeffs)))(*[muon_ns_coeff(*c) for c in coeffs])
     hp = muon_hparams(lr, momentum, weight_decay, gamma,
                       ctypes.cast(arr, ctypes.POINTER(muon_ns_coeff)) if coeffs else None,
-                      len(coeffs), 1 if nesterov else 0, ns_precision, scale_mode)
+                      len(coeffs), 1 if nesterov else 0, ns_precision, scale_mode, _factor_ptr(grad_factor))
     hp._keep = arr
+    hp._factor = grad_factor
     return hp
 
 
@@ -166,10 +200,11 @@ def _dtype_code(t):
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-def _stream_handle(stream):
+def _stream_handle(stream, device=None):
+    """The HIP stream of `stream`; None: the current one (of `device`, when given)."""
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -197,6 +232,48 @@ def _require_f32(named):
     for name, t in named:
         if t.dtype != torch.float32:
             raise TypeError(f"{name} must be float32, got {t.dtype}")
+
+
+def _one_element(name, t, dtype, what):
+    if t.dtype != dtype or t.numel() != 1:
+        raise TypeError(f"{name} must be one {what} element, got {t.numel()} of {t.dtype}")
+
+
+def _factor_ptr(t):
+    """Address of a clip factor (a one-element float32 GPU tensor), or None."""
+    if t is None:
+        return None
+    import torch
+    _one_element("grad_factor", t, torch.float32, "float32")
+    _on_one_gpu([("grad_factor", t)])
+    return t.data_ptr()
+
+
+def _array(items, kind):
+    """A ctypes array of `kind` descriptors: `items` itself if it is a table() of them."""
+    if isinstance(items, ctypes.Array):
+        if items._type_ is not kind:
+            raise TypeError(f"expected a table of {kind.__name__}, got one of {items._type_.__name__}")
+        return items
+    for k, it in enumerate(items):
+        if not isinstance(it, kind):
+            raise TypeError(f"item {k}: expected a {kind.__name__}, got {type(it).__name__}")
+    return (kind * len(items))(*items)
+
+
+def table(items):
+    """The descriptors of `items` (all of one kind) as an array that may be passed in the place of the list, and
+    that keeps them; a caller whose tensors stay where they are makes it once."""
+    items = list(items)
+    if not items:
+        raise ValueError("a table needs at least one descriptor")
+    arr = _array(items, type(items[0]))
+    devices = {d for d in (getattr(it, "_device", None) for it in items) if d is not None}
+    if len(devices) > 1:
+        raise ValueError(f"the descriptors live on several GPUs: {sorted(devices)}")
+    arr._device = devices.pop() if devices else None
+    arr._items = items
+    return arr
 
 
 def matrix(param, grad, momentum, ns_out=None):
@@ -248,6 +325,8 @@ class Context:
             pass
 
     def _check_device(self, items, what):
+        if isinstance(items, ctypes.Array):  # a table(): checked when it was made
+            items = [items]
         for k, it in enumerate(items):
             dev = getattr(it, "_device", None)
             if dev is not None and dev != self.device:
@@ -276,6 +355,45 @@ class Context:
         st = self.lib.muon_adamw_step(self.handle, arr, len(tensors), ctypes.byref(hp),
                                       _stream_handle(stream))
         _check(self.lib, self.handle, st, "muon_adamw_step")
+
+    def _check_factor(self, grad_factor):
+        ptr = _factor_ptr(grad_factor)
+        if ptr is not None:
+            self._check_tensors([("grad_factor", grad_factor)])
+        return ptr
+
+    def muon_adamw_mixed_step(self, tensors, hp, grad_factor=None, stream=None):
+        """tensors: a list of adamw_mixed_tensor() or a table() of them; hp: adamw_hparams(); grad_factor: a
+        one-element float32 GPU tensor (muon_grad_norm's factor), read when the step runs."""
+        self._check_device(tensors, "tensor")
+        arr, factor = _array(tensors, muon_adamw_mixed_tensor), self._check_factor(grad_factor)
+        st = self.lib.muon_adamw_mixed_step(self.handle, arr, len(arr), ctypes.byref(hp), factor,
+                                            _stream_handle(stream, self.device))
+        _check(self.lib, self.handle, st, "muon_adamw_mixed_step")
+
+    def muon_adamw8_step(self, tensors, hp, seed=0, grad_factor=None, stream=None):
+        """tensors: a list of adamw8_tensor() or a table() of them; seed: of the moments' stochastic rounding,
+        one for a run (0 <= seed < 2^64)."""
+        if not 0 <= seed < 1 << 64:
+            raise ValueError(f"seed must lie in [0, 2^64), got {seed}")
+        self._check_device(tensors, "tensor")
+        arr, factor = _array(tensors, muon_adamw8_tensor), self._check_factor(grad_factor)
+        st = self.lib.muon_adamw8_step(self.handle, arr, len(arr), ctypes.byref(hp), seed, factor,
+                                       _stream_handle(stream, self.device))
+        _check(self.lib, self.handle, st, "muon_adamw8_step")
+
+    def muon_grad_norm(self, grads, max_norm, norm, factor, stream=None):
+        """grads: a list of grad() or a table() of them; norm (one float64 element) and factor (one float32
+        element) are GPU tensors that receive the norm of all of them and the factor that clips it to max_norm."""
+        import torch
+        _one_element("norm", norm, torch.float64, "float64")
+        _one_element("factor", factor, torch.float32, "float32")
+        self._check_device(grads, "tensor")
+        self._check_tensors([("norm", norm), ("factor", factor)])
+        arr = _array(grads, muon_grad)
+        st = self.lib.muon_grad_norm(self.handle, arr, len(arr), max_norm, norm.data_ptr(), factor.data_ptr(),
+                                     _stream_handle(stream, self.device))
+        _check(self.lib, self.handle, st, "muon_grad_norm")
 
     def muon_ns_only(self, n_in, x_out, hp, stream=None):
         named = [("n_in", n_in), ("x_out", x_out)]
@@ -374,3 +492,104 @@ def adamw_tensor(param, grad, exp_avg, exp_avg_sq):
 
 def adamw_hparams(lr=0.02, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=1):
     return muon_adamw_hparams(lr, beta1, beta2, eps, weight_decay, step)
+
+
+def _owning(desc, device, named):
+    """Notes a descriptor's device, and keeps its tensors alive with it."""
+    desc._device = device
+    desc._tensors = [t for _, t in named]
+    return desc
+
+
+def _weights(param, grad, master):
+    """The checks that the mixed-type AdamW descriptors share; returns their (name, tensor) pairs."""
+    named = [("param", param), ("grad", grad)]
+    if master is not None:
+        import torch
+        if param.dtype != torch.bfloat16:
+            raise TypeError("a master copy goes with a bfloat16 param")
+        named.append(("master", master))
+        _require_f32(named[2:])
+    for name, t in named:
+        if not t.is_contiguous() or t.numel() != param.numel():
+            raise ValueError(f"{name} must be contiguous, with param's number of elements")
+    return named
+
+
+def adamw_mixed_tensor(param, grad, exp_avg, exp_avg_sq, master=None):
+    """muon_adamw_mixed_tensor for torch tensors (contiguous, equal numel, one GPU; param and grad float32 or
+    bfloat16, the others float32; master only with a bfloat16 param)."""
+    named = _weights(param, grad, master)
+    moments = [("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)]
+    for name, t in moments:
+        if not t.is_contiguous() or t.numel() != param.numel():
+            raise ValueError(f"{name} must be contiguous, with param's number of elements")
+    _require_f32(moments)
+    pd, gd = _dtype_code(param), _dtype_code(grad)
+    dev = _on_one_gpu(named + moments)
+    t = muon_adamw_mixed_tensor(param.data_ptr(), master.data_ptr() if master is not None else None,
+                                grad.data_ptr(), exp_avg.data_ptr(), exp_avg_sq.data_ptr(), param.numel(), pd, gd)
+    return _owning(t, dev, named + moments)
+
+
+def adamw8_state(param):
+    """Moments of zero for muon_adamw8_step on param's device: (exp_avg, exp_avg_scale, exp_avg_sq,
+    exp_avg_sq_scale), codes as float8_e4m3fn tensors of param's shape, scales as uint8 (the exponent bytes)."""
+    import torch
+    n = param.numel()
+    blocks = (n + MUON_ADAMW8_BLOCK - 1) // MUON_ADAMW8_BLOCK
+
+    def zeros(count):
+        return torch.zeros(count, dtype=torch.uint8, device=param.device)
+
+    out = []
+    for _ in range(2):
+        out += [zeros(n).view(torch.float8_e4m3fn).view(param.shape), zeros(blocks)]
+    return tuple(out)
+
+
+def adamw8_moments(state):
+    """(exp_avg, exp_avg_sq) of an 8-bit state as float32 tensors (for inspection and checkpoints)."""
+    import torch
+    out = []
+    for codes, scale in (state[:2], state[2:]):
+        e = scale.view(torch.uint8).int()
+        s = torch.where(e == 255, float("nan"), (e << 23).clamp(min=1 << 22).view(torch.float32))  # 2^(e - 127)
+        s = s.repeat_interleave(MUON_ADAMW8_BLOCK)[:codes.numel()]
+        out.append(codes.float() * s.view(codes.shape))
+    return tuple(out)
+
+
+def adamw8_tensor(param, grad, state, master=None):
+    """muon_adamw8_tensor for torch tensors; state as adamw8_state() makes it (codes of one byte an element,
+    float8_e4m3fn or uint8, and uint8 or float8_e8m0fnu scales of one byte for 32 elements)."""
+    import torch
+    named = _weights(param, grad, master)
+    n = param.numel()
+    blocks = (n + MUON_ADAMW8_BLOCK - 1) // MUON_ADAMW8_BLOCK
+    names = ("exp_avg", "exp_avg_scale", "exp_avg_sq", "exp_avg_sq_scale")
+    if len(state) != 4:
+        raise ValueError("state must hold exp_avg, exp_avg_scale, exp_avg_sq and exp_avg_sq_scale")
+    for name, t in zip(names, state):
+        scale = name.endswith("scale")
+        allowed = (torch.uint8, torch.float8_e8m0fnu if scale else torch.float8_e4m3fn)
+        if t.dtype not in allowed:
+            raise TypeError(f"{name} must be one of {allowed}, got {t.dtype}")
+        if not t.is_contiguous() or t.numel() != (blocks if scale else n):
+            raise ValueError(f"{name} must be contiguous, with {blocks if scale else n} elements")
+    pd, gd = _dtype_code(param), _dtype_code(grad)
+    dev = _on_one_gpu(named + list(zip(names, state)))
+    t = muon_adamw8_tensor(param.data_ptr(), master.data_ptr() if master is not None else None, grad.data_ptr(),
+                           state[0].data_ptr(), state[2].data_ptr(), state[1].data_ptr(), state[3].data_ptr(), n,
+                           pd, gd)
+    return _owning(t, dev, named + list(zip(names, state)))
+
+
+def grad(t):
+    """muon_grad for a torch tensor (contiguous, float32 or bfloat16, on a GPU)."""
+    if not t.is_contiguous():
+        raise ValueError("a gradient must be contiguous")
+    code = _dtype_code(t)
+    named = [("grad", t)]
+    dev = _on_one_gpu(named)
+    return _owning(muon_grad(t.data_ptr(), t.numel(), code, 0), dev, named)

@@ -5,7 +5,8 @@
 //                      N_t written into the X workspace in the s x l orientation
 //                      (transposed through LDS when rows > cols) as fp32, or on the
 //                      bf16 path as the bf16 pair (hi, lo) the first Newton-Schulz
-//                      step reads directly, per-block sums of N_t^2 in fp64.
+//                      step reads directly, per-block sums of N_t^2 in fp64.  With a
+//                      clip factor c on the device, G_t is fl(c G_t).
 //  * norm_finalize   : ||N_t||_F^2 per matrix from the block sums, fixed order.
 //  * normalize       : X_0 = N_t / ||N_t||_F (book ch. 6 §5, normalisation line),
 //                      fp32 (fp32 path) or the bf16 pair (hi, lo), zero padding.
@@ -19,6 +20,7 @@
 // multiply and add rounds once, matching the fp32 bookkeeping reference.
 #include <algorithm>
 
+#include "adamw_math.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -33,30 +35,6 @@ template <typename T> __device__ __forceinline__ void store_val(T *p, int64_t i,
 template <> __device__ __forceinline__ void store_val<float>(float *p, int64_t i, float v) { p[i] = v; }
 template <> __device__ __forceinline__ void store_val<uint16_t>(uint16_t *p, int64_t i, float v) {
     p[i] = float_to_bf16_bits(v);
-}
-
-// Correctly rounded fp32 square root.  The hardware estimate v_sqrt_f32
-// (within 1 ulp) is corrected by the signs of the exact FMA residuals
-// x - s*pred(s) and x - s*succ(s): the true root lies below the midpoint
-// (s + pred(s))/2 iff x <= s*pred(s), because no float x falls strictly between
-// s*pred(s) and the square of that midpoint (Markstein's FMA-based square-root
-// rounding; Muller et al., Handbook of Floating-Point Arithmetic, square-root
-// chapter).  Inputs below 2^-96 are scaled by 2^32 so the residuals cannot
-// underflow; zeros, infinities, NaN and negative inputs take the hardware result.
-__device__ __forceinline__ float sqrt_rn(float x) {
-    if (!(x > 0.0f) || x == __builtin_inff()) return __builtin_amdgcn_sqrtf(x);
-    const bool tiny = x < 0x1p-96f;
-    const float xs = tiny ? x * 0x1p32f : x;
-    float s = __builtin_amdgcn_sqrtf(xs);
-    for (int i = 0; i < 2; ++i) {
-        const float dn = __uint_as_float(__float_as_uint(s) - 1u);
-        const float up = __uint_as_float(__float_as_uint(s) + 1u);
-        const float r_dn = __builtin_fmaf(-dn, s, xs);
-        const float r_up = __builtin_fmaf(-up, s, xs);
-        if (r_dn <= 0.0f) s = dn;
-        else if (r_up > 0.0f) s = up;
-    }
-    return tiny ? s * 0x1p-16f : s;
 }
 
 // Deterministic block reduction of one double per thread (fixed tree order).
@@ -103,8 +81,10 @@ constexpr int kMomElems = 4096;
 template <typename GradT, bool VEC>
 __global__ __launch_bounds__(256) void nesterov_rows_kernel(const MatDesc *__restrict__ descs,
                                                             Geom g, Work w, float mu,
-                                                            int nesterov, int blocks_per_mat) {
+                                                            int nesterov, int blocks_per_mat,
+                                                            const float *__restrict__ grad_factor) {
     __shared__ double sh[4];
+    const float f = grad_factor ? *as_global(grad_factor) : 1.0f;  // 1 leaves every value as it is
     const int64_t e = blockIdx.x / blocks_per_mat;
     const int64_t b = blockIdx.x % blocks_per_mat;
     const MatDesc d = descs[e];
@@ -152,8 +132,9 @@ __global__ __launch_bounds__(256) void nesterov_rows_kernel(const MatDesc *__res
             if (4 * t >= total) break;
             floatx4 mo, no;
             for (int q = 0; q < 4; ++q) {
-                const float m1 = mu * m[u][q] + gv[u][q];
-                const float n = nesterov ? (mu * m1 + gv[u][q]) : m1;
+                const float gq = f * gv[u][q];
+                const float m1 = mu * m[u][q] + gq;
+                const float n = nesterov ? (mu * m1 + gq) : m1;
                 mo[q] = m1;
                 no[q] = n;
                 acc += static_cast<double>(n) * static_cast<double>(n);
@@ -172,7 +153,7 @@ __global__ __launch_bounds__(256) void nesterov_rows_kernel(const MatDesc *__res
         }
     } else {
         for (int t = threadIdx.x; t < total; t += 256) {
-            const float gv = load_val<GradT>(gp, t);
+            const float gv = f * load_val<GradT>(gp, t);
             const float m1 = mu * mp[t] + gv;
             const float n = nesterov ? (mu * m1 + gv) : m1;
             mp[t] = m1;
@@ -220,9 +201,11 @@ template <typename GradT, bool VEC>
 __global__ __launch_bounds__(256) void nesterov_tile_kernel(const MatDesc *__restrict__ descs,
                                                             Geom g, Work w, float mu,
                                                             int nesterov, int tiles_c,
-                                                            int blocks_per_mat) {
+                                                            int blocks_per_mat,
+                                                            const float *__restrict__ grad_factor) {
     __shared__ float tile[64][65];
     __shared__ double sh[4];
+    const float f = grad_factor ? *as_global(grad_factor) : 1.0f;
     const int64_t e = blockIdx.x / blocks_per_mat;
     const int64_t t = blockIdx.x % blocks_per_mat;
     const int64_t i0 = (t / tiles_c) * 64;  // W row
@@ -252,8 +235,9 @@ __global__ __launch_bounds__(256) void nesterov_tile_kernel(const MatDesc *__res
             floatx4 m1;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                m1[q] = mu * m[r][q] + gv[r][q];
-                const float n = nesterov ? (mu * m1[q] + gv[r][q]) : m1[q];
+                const float gq = f * gv[r][q];
+                m1[q] = mu * m[r][q] + gq;
+                const float n = nesterov ? (mu * m1[q] + gq) : m1[q];
                 acc += static_cast<double>(n) * static_cast<double>(n);
                 tile[ii][q4 + q] = n;
             }
@@ -286,7 +270,7 @@ __global__ __launch_bounds__(256) void nesterov_tile_kernel(const MatDesc *__res
             float n = 0.0f;
             if (i < g.rows && j < g.cols) {
                 const int64_t src = i * g.cols + j;
-                const float gv = load_val<GradT>(gp, src);
+                const float gv = f * load_val<GradT>(gp, src);
                 const float m1 = mu * mp[src] + gv;
                 n = nesterov ? (mu * m1 + gv) : m1;
                 mp[src] = m1;
@@ -857,31 +841,39 @@ int nesterov_blocks_per_mat(const Geom &g, int *tiles_c) {
 }
 
 hipError_t launch_nesterov(const MatDesc *descs, int nmat, const Geom &g, const Work &w, float mu,
-                           int nesterov, int grad_bf16, bool vec_ok, hipStream_t st) {
+                           int nesterov, int grad_bf16, bool vec_ok, const float *grad_factor, hipStream_t st) {
     int tc = 0;
     const int bpm = nesterov_blocks_per_mat(g, &tc);
     const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(bpm) * nmat)), block(256);
     const bool vec = vec_ok && (g.cols % 4 == 0) && (g.lp % 4 == 0);
     if (g.transposed && vec) {
         if (grad_bf16)
-            hipLaunchKernelGGL((nesterov_tile_kernel<uint16_t, true>), grid, block, 0, st, descs, g, w, mu, nesterov, tc, bpm);
+            hipLaunchKernelGGL((nesterov_tile_kernel<uint16_t, true>), grid, block, 0, st, descs, g, w, mu, nesterov, tc, bpm,
+                               grad_factor);
         else
-            hipLaunchKernelGGL((nesterov_tile_kernel<float, true>), grid, block, 0, st, descs, g, w, mu, nesterov, tc, bpm);
+            hipLaunchKernelGGL((nesterov_tile_kernel<float, true>), grid, block, 0, st, descs, g, w, mu, nesterov, tc, bpm,
+                               grad_factor);
     } else if (g.transposed) {
         if (grad_bf16)
-            hipLaunchKernelGGL((nesterov_tile_kernel<uint16_t, false>), grid, block, 0, st, descs, g, w, mu, nesterov, tc, bpm);
+            hipLaunchKernelGGL((nesterov_tile_kernel<uint16_t, false>), grid, block, 0, st, descs, g, w, mu, nesterov, tc, bpm,
+                               grad_factor);
         else
-            hipLaunchKernelGGL((nesterov_tile_kernel<float, false>), grid, block, 0, st, descs, g, w, mu, nesterov, tc, bpm);
+            hipLaunchKernelGGL((nesterov_tile_kernel<float, false>), grid, block, 0, st, descs, g, w, mu, nesterov, tc, bpm,
+                               grad_factor);
     } else if (vec) {
         if (grad_bf16)
-            hipLaunchKernelGGL((nesterov_rows_kernel<uint16_t, true>), grid, block, 0, st, descs, g, w, mu, nesterov, bpm);
+            hipLaunchKernelGGL((nesterov_rows_kernel<uint16_t, true>), grid, block, 0, st, descs, g, w, mu, nesterov, bpm,
+                               grad_factor);
         else
-            hipLaunchKernelGGL((nesterov_rows_kernel<float, true>), grid, block, 0, st, descs, g, w, mu, nesterov, bpm);
+            hipLaunchKernelGGL((nesterov_rows_kernel<float, true>), grid, block, 0, st, descs, g, w, mu, nesterov, bpm,
+                               grad_factor);
     } else {
         if (grad_bf16)
-            hipLaunchKernelGGL((nesterov_rows_kernel<uint16_t, false>), grid, block, 0, st, descs, g, w, mu, nesterov, bpm);
+            hipLaunchKernelGGL((nesterov_rows_kernel<uint16_t, false>), grid, block, 0, st, descs, g, w, mu, nesterov, bpm,
+                               grad_factor);
         else
-            hipLaunchKernelGGL((nesterov_rows_kernel<float, false>), grid, block, 0, st, descs, g, w, mu, nesterov, bpm);
+            hipLaunchKernelGGL((nesterov_rows_kernel<float, false>), grid, block, 0, st, descs, g, w, mu, nesterov, bpm,
+                               grad_factor);
     }
     return hipGetLastError();
 }

@@ -12,6 +12,13 @@ struct AdamwScalars {
     float decay, beta1, beta2, one_minus_beta1, one_minus_beta2, bias_corr1, bias_corr2, lr, eps;
 };
 
+// Scalars of the 8-bit step: the bias corrections folded into one factor each
+// (the second one times 2^24), and the key of its stochastic rounding (adamw8_key).
+struct Adamw8Scalars {
+    float decay, beta1, beta2, one_minus_beta1, one_minus_beta2, lr_over_bias_corr1, scaled_inv_bias_corr2, eps;
+    uint32_t key;
+};
+
 // Newton-Schulz GEMM tile: every padded X dimension is a multiple of this.
 constexpr int kTile = 256;
 
@@ -26,8 +33,9 @@ hipError_t scratch_address(void **out);
 // per matrix: one per 4096 consecutive elements (rows <= cols), or one per
 // 64 x 64 tile of W when X is W transposed (*tiles_c: tiles per tile row).
 int nesterov_blocks_per_mat(const Geom &g, int *tiles_c);
+// grad_factor: a device float that multiplies every gradient value, or nullptr.
 hipError_t launch_nesterov(const MatDesc *descs, int nmat, const Geom &g, const Work &w, float mu,
-                           int nesterov, int grad_bf16, bool vec_ok, hipStream_t st);
+                           int nesterov, int grad_bf16, bool vec_ok, const float *grad_factor, hipStream_t st);
 hipError_t launch_norm_finalize(const MatDesc *descs, int nmat, const Work &w, int blocks_per_mat,
                                 hipStream_t st);
 hipError_t launch_import_n(const float *n_in, const Geom &g, const Work &w, hipStream_t st);
@@ -67,6 +75,66 @@ hipError_t launch_stream_probe(const void *src, void *dst, int64_t nvec, int64_t
                                hipStream_t st);
 void adamw_fill_desc(void *dst, float *param, const float *grad, float *m, float *v, int64_t numel,
                      int64_t first_block);
+
+// ---- AdamW in mixed types (adamw.hip)
+// Tensors of one launch, passed by value (tensor_table.hpp): a launch's
+// arguments stay below 4 KB.
+struct MixedDesc {
+    void *param;
+    float *master;  // or nullptr
+    const void *grad;
+    float *m, *v;
+    int64_t numel;
+};
+constexpr int kMixedTensors = 64;
+struct MixedTable {
+    uint32_t first[64];
+    MixedDesc d[kMixedTensors];
+};
+struct ByteDesc {
+    void *param;
+    float *master;  // or nullptr
+    const void *grad;
+    uint8_t *m, *v, *m_scale, *v_scale;
+    int64_t numel;
+};
+constexpr int kByteTensors = 48;
+struct ByteTable {
+    uint32_t first[64];
+    ByteDesc d[kByteTensors];
+};
+// What the tensors of one launch have in common.  A master copy goes with bf16
+// weights only.
+struct AdamwTypes {
+    bool param_bf16, master, grad_bf16;
+};
+// Workgroups of one tensor.
+int64_t adamw_mixed_blocks(int64_t numel);
+int64_t adamw8_blocks(int64_t numel);
+hipError_t launch_adamw_mixed(const MixedTable &t, uint32_t blocks, const AdamwTypes &y, const AdamwScalars &k,
+                              const float *factor, hipStream_t st);
+hipError_t launch_adamw8(const ByteTable &t, uint32_t blocks, const AdamwTypes &y, const Adamw8Scalars &k,
+                         const float *factor, hipStream_t st);
+uint32_t adamw8_key(uint64_t seed, int64_t step);
+
+// ---- gradient norm (grad_norm.hip)
+struct NormDesc {
+    const void *grad;
+    int64_t numel;
+};
+constexpr int kNormTensors = 128;
+struct NormTable {
+    uint32_t first[128];  // first chunk of each tensor
+    NormDesc d[kNormTensors];
+    uint64_t bf16[2];  // bit k of word k / 64: tensor k is bf16
+};
+constexpr int kNormBlocks = 2048;  // workgroups of one launch at most
+// Doubles of the workspace: one sum for each workgroup, and the running total.
+constexpr size_t kNormWorkspace = kNormBlocks + 1;
+int64_t grad_norm_chunks(int64_t numel);
+// One table of a call; the last one writes *norm and *factor.
+hipError_t launch_grad_norm(const NormTable &t, uint32_t chunks, double *ws, bool first, bool last, double max_norm,
+                            double *norm, float *factor, hipStream_t st);
 
 // ---- Newton-Schulz products (ns_bf16.hip, ns_f32.hip)
 // One Newton-Schulz step on every matrix of the chunk:

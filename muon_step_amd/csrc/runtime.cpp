@@ -106,6 +106,10 @@ muon_status check_hparams(const muon_hparams *hp, char *msg, size_t cap) {
         set_msg(msg, cap, "unknown scale_mode %d", hp->scale_mode);
         return MUON_ERR_INVALID_ARGUMENT;
     }
+    if (reinterpret_cast<uintptr_t>(hp->grad_factor) % 4 != 0) {
+        set_msg(msg, cap, "grad_factor is not 4-byte aligned");
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
     return MUON_OK;
 }
 
@@ -147,6 +151,10 @@ muon_status check_step(const muon_matrix *mats, int64_t count, const muon_hparam
         add(m.grad, dtype_size(m.grad_dtype), false, "grad");
         add(m.momentum, 4, true, "momentum");
         if (m.ns_out) add(m.ns_out, 4, true, "ns_out");
+    }
+    if (hp->grad_factor) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(hp->grad_factor);
+        iv.push_back(Interval{lo, lo + 4, false, -1, "grad_factor"});
     }
     const Interval *a = nullptr, *b = nullptr;
     if (find_overlap(iv, &a, &b)) {
@@ -206,6 +214,176 @@ muon_status check_adamw(const muon_adamw_tensor *ts, int64_t count, const muon_a
         return MUON_ERR_INVALID_ARGUMENT;
     }
     return MUON_OK;
+}
+
+bool known_dtype(int32_t dt) { return dt == MUON_F32 || dt == MUON_BF16; }
+bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// What the steps over mixed types ask of their hyper-parameters and the clip factor.
+muon_status check_mixed_hparams(const muon_adamw_hparams *hp, const float *factor, char *msg, size_t cap) {
+    if (!hp) { set_msg(msg, cap, "hparams is NULL"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (!finite(hp->lr) || !finite(hp->eps) || !finite(hp->weight_decay) || !(hp->eps >= 0)) {
+        set_msg(msg, cap, "lr, eps and weight_decay must be finite, eps not negative");
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
+    if (!(hp->beta1 >= 0 && hp->beta1 < 1) || !(hp->beta2 >= 0 && hp->beta2 < 1)) {
+        set_msg(msg, cap, "beta1 and beta2 must lie in [0, 1)");
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
+    if (hp->step < 1) { set_msg(msg, cap, "step must be >= 1"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (!aligned_to(factor, 4)) { set_msg(msg, cap, "grad_factor is not 4-byte aligned"); return MUON_ERR_INVALID_ARGUMENT; }
+    return MUON_OK;
+}
+
+muon_status check_list(const void *ts, int64_t count, char *msg, size_t cap) {
+    if (count < 0) { set_msg(msg, cap, "count < 0"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (count > 0 && !ts) { set_msg(msg, cap, "tensors is NULL"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (count > (int64_t(1) << 31) - 1) { set_msg(msg, cap, "too many tensors"); return MUON_ERR_INVALID_ARGUMENT; }
+    return MUON_OK;
+}
+
+// The ranges of a call's tensors, and the checks that each of them passes.
+struct Ranges {
+    std::vector<Interval> iv;
+    char *msg;
+    size_t cap;
+    // false: refused (the message is written).  A tensor of no elements has no range.
+    bool add(const void *p, int64_t n, size_t size, bool wr, int64_t owner, const char *what) {
+        if (n == 0) return true;
+        if (!p) {
+            set_msg(msg, cap, "tensor %lld: %s is NULL", (long long)owner, what);
+            return false;
+        }
+        if (!aligned_to(p, size)) {
+            set_msg(msg, cap, "tensor %lld: %s is not aligned to its %zu-byte elements", (long long)owner, what, size);
+            return false;
+        }
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        iv.push_back(Interval{lo, lo + static_cast<uintptr_t>(n) * size, wr, owner, what});
+        return true;
+    }
+    muon_status overlap() {
+        const Interval *a = nullptr, *b = nullptr;
+        if (!find_overlap(iv, &a, &b)) return MUON_OK;
+        set_msg(msg, cap, "memory of tensor %lld %s overlaps tensor %lld %s", (long long)a->owner, a->what,
+                (long long)b->owner, b->what);
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
+};
+
+// numel, dtypes and master of one tensor of a step over mixed types.
+template <class T> muon_status check_mixed_tensor(const T &t, int64_t i, char *msg, size_t cap) {
+    if (t.numel < 0 || t.numel > kMaxElems) {
+        set_msg(msg, cap, "tensor %lld: numel %lld out of range", (long long)i, (long long)t.numel);
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
+    if (!known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype)) {
+        set_msg(msg, cap, "tensor %lld: unknown dtype", (long long)i);
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
+    if (t.master && t.param_dtype != MUON_BF16) {
+        set_msg(msg, cap, "tensor %lld: a master copy goes with bf16 param only", (long long)i);
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
+    return MUON_OK;
+}
+
+template <class T> bool add_weights(Ranges &r, const T &t, int64_t i) {
+    return r.add(t.param, t.numel, dtype_size(t.param_dtype), true, i, "param") &&
+           (!t.master || r.add(t.master, t.numel, 4, true, i, "master")) &&
+           r.add(t.grad, t.numel, dtype_size(t.grad_dtype), false, i, "grad");
+}
+
+muon_status check_adamw_mixed(const muon_adamw_mixed_tensor *ts, int64_t count, const muon_adamw_hparams *hp,
+                              const float *factor, char *msg, size_t cap) {
+    muon_status s = check_list(ts, count, msg, cap);
+    if (s == MUON_OK) s = check_mixed_hparams(hp, factor, msg, cap);
+    if (s != MUON_OK) return s;
+    Ranges r{{}, msg, cap};
+    r.iv.reserve(static_cast<size_t>(count) * 5 + 1);
+    for (int64_t i = 0; i < count; ++i) {
+        const muon_adamw_mixed_tensor &t = ts[i];
+        if ((s = check_mixed_tensor(t, i, msg, cap)) != MUON_OK) return s;
+        if (!add_weights(r, t, i) || !r.add(t.exp_avg, t.numel, 4, true, i, "exp_avg") ||
+            !r.add(t.exp_avg_sq, t.numel, 4, true, i, "exp_avg_sq"))
+            return MUON_ERR_INVALID_ARGUMENT;
+    }
+    if (factor) (void)r.add(factor, 1, 4, false, -1, "grad_factor");
+    return r.overlap();
+}
+
+int64_t byte_blocks(int64_t numel) { return (numel + MUON_ADAMW8_BLOCK - 1) / MUON_ADAMW8_BLOCK; }
+
+muon_status check_adamw8(const muon_adamw8_tensor *ts, int64_t count, const muon_adamw_hparams *hp,
+                         const float *factor, char *msg, size_t cap) {
+    muon_status s = check_list(ts, count, msg, cap);
+    if (s == MUON_OK) s = check_mixed_hparams(hp, factor, msg, cap);
+    if (s != MUON_OK) return s;
+    // the hardware's reciprocal has no subnormal arguments
+    if (hp->eps > 0 && static_cast<float>(hp->eps) < std::numeric_limits<float>::min()) {
+        set_msg(msg, cap, "eps must be 0 or at least 2^-126");
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
+    Ranges r{{}, msg, cap};
+    r.iv.reserve(static_cast<size_t>(count) * 7 + 1);
+    for (int64_t i = 0; i < count; ++i) {
+        const muon_adamw8_tensor &t = ts[i];
+        if ((s = check_mixed_tensor(t, i, msg, cap)) != MUON_OK) return s;
+        const int64_t nb = byte_blocks(t.numel);
+        if (!add_weights(r, t, i) || !r.add(t.exp_avg, t.numel, 1, true, i, "exp_avg") ||
+            !r.add(t.exp_avg_sq, t.numel, 1, true, i, "exp_avg_sq") ||
+            !r.add(t.exp_avg_scale, nb, 1, true, i, "exp_avg_scale") ||
+            !r.add(t.exp_avg_sq_scale, nb, 1, true, i, "exp_avg_sq_scale"))
+            return MUON_ERR_INVALID_ARGUMENT;
+    }
+    if (factor) (void)r.add(factor, 1, 4, false, -1, "grad_factor");
+    return r.overlap();
+}
+
+muon_status check_grad_norm(const muon_grad *gs, int64_t count, double max_norm, const double *norm,
+                            const float *factor, char *msg, size_t cap) {
+    muon_status s = check_list(gs, count, msg, cap);
+    if (s != MUON_OK) return s;
+    if (!(max_norm > 0)) { set_msg(msg, cap, "max_norm must be positive"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (!norm || !factor || !aligned_to(norm, 8) || !aligned_to(factor, 4)) {
+        set_msg(msg, cap, "norm and factor must be non-NULL and aligned to their types");
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
+    // Gradients are only read and may share memory; no output may lie in one.
+    const uintptr_t n0 = reinterpret_cast<uintptr_t>(norm), f0 = reinterpret_cast<uintptr_t>(factor);
+    if (n0 < f0 + 4 && f0 < n0 + 8) { set_msg(msg, cap, "norm and factor overlap"); return MUON_ERR_INVALID_ARGUMENT; }
+    for (int64_t i = 0; i < count; ++i) {
+        const muon_grad &g = gs[i];
+        if (g.numel < 0 || g.numel > kMaxElems) {
+            set_msg(msg, cap, "tensor %lld: numel %lld out of range", (long long)i, (long long)g.numel);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        if (!known_dtype(g.dtype)) {
+            set_msg(msg, cap, "tensor %lld: unknown dtype", (long long)i);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        if (g.numel == 0) continue;
+        const size_t size = dtype_size(g.dtype);
+        if (!g.grad || !aligned_to(g.grad, size)) {
+            set_msg(msg, cap, "tensor %lld: grad is NULL or not aligned to its elements", (long long)i);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(g.grad), hi = lo + static_cast<uintptr_t>(g.numel) * size;
+        if ((lo < n0 + 8 && n0 < hi) || (lo < f0 + 4 && f0 < hi)) {
+            set_msg(msg, cap, "norm or factor lies in the memory of tensor %lld", (long long)i);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+    }
+    return MUON_OK;
+}
+
+// No C++ exception leaves the library: `fn` may fail for want of host memory.
+template <class F> muon_status guarded(F fn) {
+    try {
+        return fn();
+    } catch (...) {
+        return MUON_ERR_OUT_OF_MEMORY;
+    }
 }
 
 // ---------------------------------------------------------------- planning
@@ -480,6 +658,9 @@ struct muon_context {
     DevBuf call_nrm2; // per call matrix
     DevBuf mat_desc;  // MatDesc table
     DevBuf adamw_desc;
+    // muon_grad_norm's sums: of a fixed size and there from creation on, so that
+    // a captured call never points to memory that a later call replaced
+    double *norm_ws = nullptr;
     void *pinned = nullptr;
     size_t pinned_n = 0;
     hipEvent_t upload_done = nullptr;
@@ -545,11 +726,12 @@ muon_status hip_fail(muon_context *ctx, hipError_t e, const char *where) {
 
 enum Stage {
     ST_MOMENTUM = 0, ST_FINALIZE, ST_NORMALIZE, ST_GRAM, ST_POLY, ST_APPLY, ST_APPLY_UPDATE, ST_UPDATE,
-    ST_ADAMW, ST_IMPORT, ST_EXPORT, ST_UNIT_RMS, ST_PRENORM, ST_PROBE, ST_COUNT
+    ST_ADAMW, ST_IMPORT, ST_EXPORT, ST_UNIT_RMS, ST_PRENORM, ST_PROBE, ST_ADAMW_MIXED, ST_ADAMW8, ST_GRAD_NORM, ST_COUNT
 };
 const char *const kStageNames[ST_COUNT] = {"momentum_nesterov", "norm_finalize", "normalize", "gram", "poly",
                                            "apply", "apply_update", "update", "adamw", "import", "export",
-                                           "unit_rms", "prenormalize", "stream_probe"};
+                                           "unit_rms", "prenormalize", "stream_probe", "adamw_mixed", "adamw8",
+                                           "grad_norm"};
 
 hipError_t take_event(muon_context *ctx, hipEvent_t *ev) {
     if (ctx->ev_used == ctx->ev_pool.size()) {
@@ -1091,7 +1273,7 @@ muon_status step_impl(muon_context *ctx, const muon_matrix *mats, int64_t count,
                 // M read and written (8), N written: fp32 (4) or hi + residual (3)
                 hipError_t e = timed(ctx, ST_MOMENTUM, 0.0, elems * (gsz + (bf16 ? 11.0 : 12.0)), st, [&] {
                     return muon::launch_nesterov(dr, static_cast<int>(run.n), run.g, wr, mu, hp->nesterov,
-                                                 gp.grad_dtype == MUON_BF16, vec_ok, st);
+                                                 gp.grad_dtype == MUON_BF16, vec_ok, hp->grad_factor, st);
                 });
                 if (e != hipSuccess) return hip_fail(ctx, e, "momentum launch");
                 e = timed(ctx, ST_FINALIZE, 0.0, static_cast<double>(run.n) * bpm * 8.0, st,
@@ -1140,6 +1322,66 @@ muon_status step_impl(muon_context *ctx, const muon_matrix *mats, int64_t count,
     return MUON_OK;
 }
 
+muon::AdamwScalars adamw_scalars(const muon_adamw_hparams *hp) {
+    muon::AdamwScalars k{};
+    k.decay = static_cast<float>(1.0 - hp->lr * hp->weight_decay);
+    k.beta1 = static_cast<float>(hp->beta1);
+    k.beta2 = static_cast<float>(hp->beta2);
+    k.one_minus_beta1 = static_cast<float>(1.0 - hp->beta1);
+    k.one_minus_beta2 = static_cast<float>(1.0 - hp->beta2);
+    k.bias_corr1 = static_cast<float>(1.0 - std::pow(hp->beta1, static_cast<double>(hp->step)));
+    k.bias_corr2 = static_cast<float>(1.0 - std::pow(hp->beta2, static_cast<double>(hp->step)));
+    k.lr = static_cast<float>(hp->lr);
+    k.eps = static_cast<float>(hp->eps);
+    return k;
+}
+
+// Runs a step over tensors of mixed types: those of the same types together,
+// in the caller's order, as many to a launch as its table holds.  moment_bytes:
+// what the moments of one element move.
+template <class Table, int N, class T, class Blocks, class Fill, class Launch>
+muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage, double moment_bytes, hipStream_t st,
+                       Blocks blocks_of, Fill fill, Launch launch) {
+    DeviceGuard guard(ctx->device);
+    Table t;
+    for (int kind = 0; kind < 8; ++kind) {
+        const muon::AdamwTypes y{(kind & 1) != 0, (kind & 2) != 0, (kind & 4) != 0};
+        int n = 0;
+        int64_t blocks = 0;
+        double bytes = 0;
+        auto flush = [&]() -> hipError_t {
+            if (n == 0) return hipSuccess;
+            for (int j = n; j < 64; ++j) t.first[j] = 0xffffffffu;
+            const hipError_t e = timed(ctx, stage, 0.0, bytes, st,
+                                       [&] { return launch(t, static_cast<uint32_t>(blocks), y, st); });
+            n = 0;
+            blocks = 0;
+            bytes = 0;
+            return e;
+        };
+        for (int64_t i = 0; i < count; ++i) {
+            const T &x = ts[i];
+            if (x.numel == 0 || y.param_bf16 != (x.param_dtype == MUON_BF16) || y.master != (x.master != nullptr) ||
+                y.grad_bf16 != (x.grad_dtype == MUON_BF16))
+                continue;
+            const int64_t nb = blocks_of(x.numel);
+            if (n == N || blocks + nb >= (int64_t(1) << 31)) {
+                const hipError_t e = flush();
+                if (e != hipSuccess) return hip_fail(ctx, e, "AdamW launch");
+            }
+            t.first[n] = static_cast<uint32_t>(blocks);
+            fill(t.d[n], x);
+            ++n;
+            blocks += nb;
+            const double p = dtype_size(x.param_dtype), g = dtype_size(x.grad_dtype);
+            bytes += static_cast<double>(x.numel) * (moment_bytes + g + (x.master ? 8.0 + p : 2.0 * p));
+        }
+        const hipError_t e = flush();
+        if (e != hipSuccess) return hip_fail(ctx, e, "AdamW launch");
+    }
+    ctx->err.clear();
+    return MUON_OK;
+}
 
 }  // namespace
 
@@ -1197,6 +1439,25 @@ muon_status muon_check_adamw_args(const muon_adamw_tensor *ts, int64_t count, co
     return check_adamw(ts, count, hp, msg, msg_cap);
 }
 
+muon_status muon_check_adamw_mixed_args(const muon_adamw_mixed_tensor *ts, int64_t count,
+                                        const muon_adamw_hparams *hp, const float *grad_factor, char *msg,
+                                        size_t msg_cap) {
+    set_msg(msg, msg_cap, "%s", "");
+    return guarded([&] { return check_adamw_mixed(ts, count, hp, grad_factor, msg, msg_cap); });
+}
+
+muon_status muon_check_adamw8_args(const muon_adamw8_tensor *ts, int64_t count, const muon_adamw_hparams *hp,
+                                   const float *grad_factor, char *msg, size_t msg_cap) {
+    set_msg(msg, msg_cap, "%s", "");
+    return guarded([&] { return check_adamw8(ts, count, hp, grad_factor, msg, msg_cap); });
+}
+
+muon_status muon_check_grad_norm_args(const muon_grad *gs, int64_t count, double max_norm, const double *norm,
+                                      const float *factor, char *msg, size_t msg_cap) {
+    set_msg(msg, msg_cap, "%s", "");
+    return guarded([&] { return check_grad_norm(gs, count, max_norm, norm, factor, msg, msg_cap); });
+}
+
 muon_status muon_workspace_bytes(const muon_matrix *mats, int64_t count, const muon_hparams *hp,
                                  size_t *bytes_out) {
     if (!bytes_out) return MUON_ERR_INVALID_ARGUMENT;
@@ -1236,6 +1497,13 @@ muon_status muon_create(muon_context **out, int32_t hip_device, size_t workspace
         delete ctx;
         return MUON_ERR_DEVICE;
     }
+    if (hipMalloc(reinterpret_cast<void **>(&ctx->norm_ws), muon::kNormWorkspace * sizeof(double)) != hipSuccess) {
+        (void)hipGetLastError();
+        (void)hipEventDestroy(ctx->upload_done);
+        (void)hipEventDestroy(ctx->noalloc_upload_done);
+        delete ctx;
+        return MUON_ERR_OUT_OF_MEMORY;
+    }
     // The allocation-free step's memory: this device's copy of the static
     // scratch (its address, with this device current) and the pinned staging
     // of its descriptor table.  A failure here only disables that entry point.
@@ -1264,6 +1532,7 @@ muon_status muon_destroy(muon_context *ctx) {
     (void)hipDeviceSynchronize();
     for (DevBuf *b : {&ctx->ws, &ctx->tabs, &ctx->call_nrm2, &ctx->mat_desc, &ctx->adamw_desc})
         if (b->p) (void)hipFree(b->p);
+    if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
     if (ctx->pinned) (void)hipHostFree(ctx->pinned);
     if (ctx->noalloc_pinned) (void)hipHostFree(ctx->noalloc_pinned);
     if (ctx->upload_done) (void)hipEventDestroy(ctx->upload_done);
@@ -1394,16 +1663,7 @@ muon_status muon_adamw_step(muon_context *ctx, const muon_adamw_tensor *ts, int6
     char msg[512];
     muon_status s = check_adamw(ts, count, hp, msg, sizeof msg);
     if (s != MUON_OK) return fail(ctx, s, "%s", msg);
-    muon::AdamwScalars k{};
-    k.decay = static_cast<float>(1.0 - hp->lr * hp->weight_decay);
-    k.beta1 = static_cast<float>(hp->beta1);
-    k.beta2 = static_cast<float>(hp->beta2);
-    k.one_minus_beta1 = static_cast<float>(1.0 - hp->beta1);
-    k.one_minus_beta2 = static_cast<float>(1.0 - hp->beta2);
-    k.bias_corr1 = static_cast<float>(1.0 - std::pow(hp->beta1, static_cast<double>(hp->step)));
-    k.bias_corr2 = static_cast<float>(1.0 - std::pow(hp->beta2, static_cast<double>(hp->step)));
-    k.lr = static_cast<float>(hp->lr);
-    k.eps = static_cast<float>(hp->eps);
+    const muon::AdamwScalars k = adamw_scalars(hp);
     const size_t ds = muon::adamw_desc_size();
     std::vector<unsigned char> table;
     int64_t blocks = 0;
@@ -1430,6 +1690,100 @@ muon_status muon_adamw_step(muon_context *ctx, const muon_adamw_tensor *ts, int6
     if (e != hipSuccess) return hip_fail(ctx, e, "AdamW launch");
     ctx->err.clear();
     return MUON_OK;
+}
+
+muon_status muon_adamw_mixed_step(muon_context *ctx, const muon_adamw_mixed_tensor *ts, int64_t count,
+                                  const muon_adamw_hparams *hp, const float *grad_factor, void *hip_stream) {
+    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+    return guarded([&]() -> muon_status {
+        char msg[512];
+        const muon_status s = check_adamw_mixed(ts, count, hp, grad_factor, msg, sizeof msg);
+        if (s != MUON_OK) return fail(ctx, s, "%s", msg);
+        const muon::AdamwScalars k = adamw_scalars(hp);
+        auto fill = [](muon::MixedDesc &d, const muon_adamw_mixed_tensor &t) {
+            d = muon::MixedDesc{t.param, t.master, t.grad, t.exp_avg, t.exp_avg_sq, t.numel};
+        };
+        return run_tables<muon::MixedTable, muon::kMixedTensors>(
+            ctx, ts, count, ST_ADAMW_MIXED, 16.0, static_cast<hipStream_t>(hip_stream), muon::adamw_mixed_blocks, fill,
+            [&](const muon::MixedTable &t, uint32_t blocks, const muon::AdamwTypes &y, hipStream_t st) {
+                return muon::launch_adamw_mixed(t, blocks, y, k, grad_factor, st);
+            });
+    });
+}
+
+muon_status muon_adamw8_step(muon_context *ctx, const muon_adamw8_tensor *ts, int64_t count,
+                             const muon_adamw_hparams *hp, uint64_t seed, const float *grad_factor,
+                             void *hip_stream) {
+    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+    return guarded([&]() -> muon_status {
+        char msg[512];
+        const muon_status s = check_adamw8(ts, count, hp, grad_factor, msg, sizeof msg);
+        if (s != MUON_OK) return fail(ctx, s, "%s", msg);
+        const muon::AdamwScalars a = adamw_scalars(hp);
+        muon::Adamw8Scalars k{};
+        k.decay = a.decay;
+        k.beta1 = a.beta1;
+        k.beta2 = a.beta2;
+        k.one_minus_beta1 = a.one_minus_beta1;
+        k.one_minus_beta2 = a.one_minus_beta2;
+        k.eps = a.eps;
+        const double t = static_cast<double>(hp->step);
+        k.lr_over_bias_corr1 = static_cast<float>(hp->lr / (1.0 - std::pow(hp->beta1, t)));
+        k.scaled_inv_bias_corr2 = static_cast<float>(0x1p24 / (1.0 - std::pow(hp->beta2, t)));
+        k.key = muon::adamw8_key(seed, hp->step);
+        auto fill = [](muon::ByteDesc &d, const muon_adamw8_tensor &t) {
+            d = muon::ByteDesc{t.param,         t.master,          t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale,
+                               t.exp_avg_sq_scale, t.numel};
+        };
+        return run_tables<muon::ByteTable, muon::kByteTensors>(
+            ctx, ts, count, ST_ADAMW8, 4.0 + 4.0 / MUON_ADAMW8_BLOCK, static_cast<hipStream_t>(hip_stream),
+            muon::adamw8_blocks, fill,
+            [&](const muon::ByteTable &t, uint32_t blocks, const muon::AdamwTypes &y, hipStream_t st) {
+                return muon::launch_adamw8(t, blocks, y, k, grad_factor, st);
+            });
+    });
+}
+
+muon_status muon_grad_norm(muon_context *ctx, const muon_grad *gs, int64_t count, double max_norm, double *norm,
+                           float *factor, void *hip_stream) {
+    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+    return guarded([&]() -> muon_status {
+        char msg[512];
+        const muon_status s = check_grad_norm(gs, count, max_norm, norm, factor, msg, sizeof msg);
+        if (s != MUON_OK) return fail(ctx, s, "%s", msg);
+        DeviceGuard guard(ctx->device);
+        hipStream_t st = static_cast<hipStream_t>(hip_stream);
+        muon::NormTable t;
+        bool first = true;
+        int64_t i = 0;
+        do {  // at least one table: a call without elements writes norm 0 and factor 1
+            std::memset(&t, 0, sizeof t);
+            std::memset(t.first, 0xff, sizeof t.first);
+            int64_t chunks = 0;
+            double bytes = 0;
+            for (int n = 0; i < count && n < muon::kNormTensors; ++i) {
+                const muon_grad &g = gs[i];
+                const int64_t c = muon::grad_norm_chunks(g.numel);
+                if (c == 0) continue;
+                if (chunks + c >= (int64_t(1) << 31)) break;
+                t.first[n] = static_cast<uint32_t>(chunks);
+                t.d[n] = muon::NormDesc{g.grad, g.numel};
+                if (g.dtype == MUON_BF16) t.bf16[n / 64] |= uint64_t(1) << (n % 64);
+                chunks += c;
+                bytes += static_cast<double>(g.numel) * dtype_size(g.dtype);
+                ++n;
+            }
+            const bool last = i >= count;
+            const hipError_t e = timed(ctx, ST_GRAD_NORM, bytes, bytes, st, [&] {
+                return muon::launch_grad_norm(t, static_cast<uint32_t>(chunks), ctx->norm_ws, first, last, max_norm, norm,
+                                              factor, st);
+            });
+            if (e != hipSuccess) return hip_fail(ctx, e, "gradient norm launch");
+            first = false;
+        } while (i < count);
+        ctx->err.clear();
+        return MUON_OK;
+    });
 }
 
 muon_status muon_ns_stage(muon_context *ctx, int32_t stage, const float *x, const float *m, float *out, int64_t s,

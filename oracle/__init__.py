@@ -42,5 +42,6 @@ from .muon import (  # noqa: F401
     ns_flops_dense,
 )
 from .adamw import adamw_scalars_f32, adamw_step_f32  # noqa: F401
+from .adamw8 import adamw8_step, dither, e4m3_values, grad_norm, mix32, moment_values, quantise  # noqa: F401
 from .bf16 import bf16_round_f32, bf16_bits_to_f32, f32_to_bf16_bits  # noqa: F401
 from .jacobi import jacobi_svd, polar_factor  # noqa: F401
