@@ -174,25 +174,32 @@ def _clear_between(s, total):
 
 
 def _describe(s):
-    """The context and the descriptors that a program makes once and keeps."""
+    """The context and the descriptors that a program makes once and keeps.  The weights between the tensors of a
+    flattened buffer decay with the others: what lies behind a tensor is handed over as one without a gradient."""
     import muon_step_amd as ms
 
     case = s["case"]
     s["ctx"] = ms.Context(0)
     view = lambda name, at, n: None if s[name] is None else s[name][at:at + n]  # noqa: E731
-    scale = lambda name, at, n: s[name][at // BLOCK:at // BLOCK + (n + BLOCK - 1) // BLOCK]  # noqa: E731
     items = []
     for n, at in zip(s["numels"], s["starts"]):
-        grad = view("grad", at, n)
         if case["op"] == "norm":
-            items.append(ms.grad(grad))
-        elif case["op"] == "adamw32":
-            items.append(ms.adamw_mixed_tensor(view("param", at, n), grad, view("exp_avg", at, n),
-                                               view("exp_avg_sq", at, n), master=view("master", at, n)))
-        else:
-            state = (view("exp_avg", at, n), scale("exp_avg_scale", at, n), view("exp_avg_sq", at, n),
-                     scale("exp_avg_sq_scale", at, n))
-            items.append(ms.adamw8_tensor(view("param", at, n), grad, state, master=view("master", at, n)))
+            items.append(ms.grad(view("grad", at, n)))
+            continue
+        for first, count in ((at, n), (at + n, -n % 64)):
+            if count == 0:
+                continue
+            param, grad, master = (view(name, first, count) for name in ("param", "grad", "master"))
+            m, v = view("exp_avg", first, count), view("exp_avg_sq", first, count)
+            if case["op"] == "adamw32":
+                items.append(ms.adamw_mixed_tensor(param, grad, m, v, master=master))
+                continue
+            if first == at:
+                blocks = -(-n // BLOCK)
+                m_scale, v_scale = (view(name + "_scale", at // BLOCK, blocks) for name in ("exp_avg", "exp_avg_sq"))
+            else:  # moments of zero, whose exponents nothing else reads
+                m_scale, v_scale = (torch.zeros(2, dtype=torch.uint8, device="cuda")[:-(-count // BLOCK)] for _ in range(2))
+            items.append(ms.adamw8_tensor(param, grad, (m, m_scale, v, v_scale), master=master))
     s["table"] = ms.table(items)
     if case["op"] != "norm":
         s["hp"] = ms.adamw_hparams(lr=LR, beta1=BETA1, beta2=BETA2, eps=EPS, weight_decay=DECAY, step=case["step"])
