@@ -98,7 +98,7 @@ struct ByteDesc {
     uint8_t *m, *v, *m_scale, *v_scale;
     int64_t numel;
 };
-constexpr int kByteTensors = 48;
+constexpr int kByteTensors = 56;
 struct ByteTable {
     uint32_t first[64];
     ByteDesc d[kByteTensors];
