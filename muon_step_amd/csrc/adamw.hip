@@ -27,19 +27,36 @@ template <> __device__ __forceinline__ void store_one<uint16_t>(uint16_t *p, flo
     *as_global(p) = float_to_bf16_bits(v);
 }
 
+// Every tensor is read and written once: all accesses are non-temporal.  Where
+// the caches hold other data, as after a model's backward pass, that is what
+// counts: 128 MB take 27.6 us (32 MB 9.9, 1 GB 173; plain loads 32.0, 13.4 and
+// 193, plain stores 28.0, 10.7 and 186).  Only calls of some 64 to 128 MB in a
+// loop, which the Infinity Cache could hold, would gain from plain loads (128
+// MB 24.2 to 21.3 us).
+//
+// PACED (calls that move more than 512 MB): each tensor's load is waited for
+// before the next tensor's is issued.  With all of a lane's loads in flight on
+// every CU the HBM serves five to seven streams at once and gets slower: 5.9
+// GB of mixed-type AdamW take 968 us paced and 1018 not (210e6 elements), 1 GB
+// 168.6 and 173.4, 256 MB the same, 64 MB 0.3 us more paced.
+template <class T> __device__ __forceinline__ T nt_load(const T *p) { return __builtin_nontemporal_load(as_global(p)); }
+template <bool PACED> __device__ __forceinline__ void pace() {
+    if constexpr (PACED) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
 // V consecutive values as floats, in 16-byte accesses (8-byte ones for four
-// bf16), non-temporal: every tensor of the step is read and written once.
+// bf16).
 template <int V> __device__ __forceinline__ void load_vec(const float *p, float (&x)[V]) {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
-        const floatx4 r = __builtin_nontemporal_load(as_global(reinterpret_cast<const floatx4 *>(p + i)));
+        const floatx4 r = nt_load(reinterpret_cast<const floatx4 *>(p + i));
 #pragma unroll
         for (int q = 0; q < 4; ++q) x[i + q] = r[q];
     }
 }
 template <int V> __device__ __forceinline__ void load_vec(const uint16_t *p, float (&x)[V]) {
     typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
-    const words r = __builtin_nontemporal_load(as_global(reinterpret_cast<const words *>(p)));
+    const words r = nt_load(reinterpret_cast<const words *>(p));
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
         x[2 * i] = __uint_as_float(r[i] << 16);
@@ -60,28 +77,6 @@ template <int V> __device__ __forceinline__ void store_vec(uint16_t *p, const fl
     __builtin_nontemporal_store(r, as_global(reinterpret_cast<words *>(p)));
 }
 
-// Values i0 .. i0 + V - 1 of a tensor of n: in vectors (`vec`: its address and
-// i0 allow it and all of them are inside), or one by one, zero past the end.
-template <int V, typename T>
-__device__ __forceinline__ void load_some(const T *p, int64_t i0, int64_t n, bool vec, float (&x)[V]) {
-    if (vec) {
-        load_vec<V>(p + i0, x);
-    } else {
-#pragma unroll
-        for (int q = 0; q < V; ++q) x[q] = i0 + q < n ? load_one<T>(p + i0 + q) : 0.0f;
-    }
-}
-template <int V, typename T>
-__device__ __forceinline__ void store_some(T *p, int64_t i0, int64_t n, bool vec, const float (&x)[V]) {
-    if (vec) {
-        store_vec<V>(p + i0, x);
-    } else {
-#pragma unroll
-        for (int q = 0; q < V; ++q)
-            if (i0 + q < n) store_one<T>(p + i0 + q, x[q]);
-    }
-}
-
 // Multiplies by the clip factor (one rounding), when the call has one.
 template <int V> __device__ __forceinline__ void clip(const float *factor, float (&g)[V]) {
     if (!factor) return;
@@ -96,30 +91,9 @@ template <int V> __device__ __forceinline__ void clip(const float *factor, float
 constexpr int kMixedVec = 4;                       // elements of a lane
 constexpr int kMixedBlock = kThreads * kMixedVec;  // elements of a workgroup
 
-template <typename ParamT, typename GradT, bool MASTER>
-__global__ __launch_bounds__(kThreads) void adamw_mixed_kernel(const MixedTable t, uint32_t block0, AdamwScalars k,
-                                                               const float *factor) {
-    constexpr int V = kMixedVec;
-    const uint32_t b = block0 + blockIdx.x;
-    const int e = owner_of(t.first, b);
-    const MixedDesc d = t.d[e];
-    const int64_t i0 = static_cast<int64_t>(b - t.first[e]) * kMixedBlock + threadIdx.x * V;
-    if (i0 >= d.numel) return;
-    ParamT *param = static_cast<ParamT *>(d.param);
-    const GradT *grad = static_cast<const GradT *>(d.grad);
-    const uintptr_t low = reinterpret_cast<uintptr_t>(d.param) | reinterpret_cast<uintptr_t>(d.master) |
-                          reinterpret_cast<uintptr_t>(d.grad) | reinterpret_cast<uintptr_t>(d.m) |
-                          reinterpret_cast<uintptr_t>(d.v);
-    const bool vec = (low & 15) == 0 && i0 + V <= d.numel;
-    float p[V], g[V], m[V], v[V];
-    if constexpr (MASTER)
-        load_some<V>(d.master, i0, d.numel, vec, p);
-    else
-        load_some<V>(param, i0, d.numel, vec, p);
-    load_some<V>(grad, i0, d.numel, vec, g);
-    load_some<V>(d.m, i0, d.numel, vec, m);
-    load_some<V>(d.v, i0, d.numel, vec, v);
-    clip(factor, g);
+template <int V>
+__device__ __forceinline__ void adamw_exact(const AdamwScalars &k, float (&p)[V], const float (&g)[V], float (&m)[V],
+                                            float (&v)[V]) {
 #pragma unroll
     for (int q = 0; q < V; ++q) {
         const float p1 = k.decay * p[q];
@@ -128,10 +102,55 @@ __global__ __launch_bounds__(kThreads) void adamw_mixed_kernel(const MixedTable 
         const float den = sqrt_rn(__fdiv_rn(v[q], k.bias_corr2)) + k.eps;
         p[q] = p1 - k.lr * __fdiv_rn(__fdiv_rn(m[q], k.bias_corr1), den);
     }
-    store_some<V>(d.m, i0, d.numel, vec, m);
-    store_some<V>(d.v, i0, d.numel, vec, v);
-    if constexpr (MASTER) store_some<V>(d.master, i0, d.numel, vec, p);
-    store_some<V>(param, i0, d.numel, vec, p);
+}
+
+template <typename ParamT, typename GradT, bool MASTER, bool PACED>
+__global__ __launch_bounds__(kThreads) void adamw_mixed_kernel(const MixedTable t, uint32_t block0, AdamwScalars k,
+                                                               const float *factor) {
+    constexpr int V = kMixedVec;
+    const uint32_t b = block0 + blockIdx.x;
+    const int e = Owners<64>(t.first).of(b);
+    const MixedDesc d = t.d[e];
+    const int64_t k0 = static_cast<int64_t>(b - t.first[e]) * kMixedBlock;
+    ParamT *param = static_cast<ParamT *>(d.param) + k0;
+    const GradT *grad = static_cast<const GradT *>(d.grad) + k0;
+    float *master = MASTER ? d.master + k0 : nullptr, *dm = d.m + k0, *dv = d.v + k0;
+    const uintptr_t low = reinterpret_cast<uintptr_t>(d.param) | reinterpret_cast<uintptr_t>(d.master) |
+                          reinterpret_cast<uintptr_t>(d.grad) | reinterpret_cast<uintptr_t>(d.m) |
+                          reinterpret_cast<uintptr_t>(d.v);
+    const int64_t left = d.numel - k0;
+    if ((low & 15) == 0 && left >= kMixedBlock) {  // uniform: a whole block of aligned tensors
+        const int i = threadIdx.x * V;
+        float p[V], g[V], m[V], v[V];
+        if constexpr (MASTER)
+            load_vec(master + i, p);
+        else
+            load_vec(param + i, p);
+        pace<PACED>();
+        load_vec(grad + i, g);
+        pace<PACED>();
+        load_vec(dm + i, m);
+        pace<PACED>();
+        load_vec(dv + i, v);
+        clip(factor, g);
+        adamw_exact(k, p, g, m, v);
+        store_vec(dm + i, m);
+        store_vec(dv + i, v);
+        if constexpr (MASTER) store_vec(master + i, p);
+        store_vec(param + i, p);
+        return;
+    }
+    const int n = static_cast<int>(min<int64_t>(left, kMixedBlock));
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        float p[1] = {MASTER ? load_one(master + i) : load_one(param + i)};
+        float g[1] = {load_one(grad + i)}, m[1] = {load_one(dm + i)}, v[1] = {load_one(dv + i)};
+        clip(factor, g);
+        adamw_exact(k, p, g, m, v);
+        store_one(dm + i, m[0]);
+        store_one(dv + i, v[0]);
+        if constexpr (MASTER) store_one(master + i, p[0]);
+        store_one(param + i, p[0]);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -146,9 +165,6 @@ __global__ __launch_bounds__(kThreads) void adamw_mixed_kernel(const MixedTable 
 // value of the code here is the value itself.  v_cvt_sr_fp8_f32 rounds up where
 // the 20 bits of an fp32 significand that are cut off and the random operand's
 // top 20 bits carry.
-constexpr int kByteVec = 8;
-constexpr int kByteBlock = kThreads * kByteVec;
-
 // A 32-bit mixing function: two rounds of xor-shift and multiplication.
 __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     x ^= x >> 16;
@@ -158,12 +174,14 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     return x ^ (x >> 16);
 }
 
-// The largest of four neighbouring lanes' values (rows of a quad by DPP).
-__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
-    const uint32_t y = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xf, 0xf, true));
-    x = max(x, y);
-    const uint32_t z = static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xf, 0xf, true));
-    return max(x, z);
+// The largest value of the lanes that share a block of 32 elements: 32 / V
+// neighbours (DPP: within quads, then between the two quads of eight lanes).
+template <int V> __device__ __forceinline__ uint32_t block_max(uint32_t x) {
+    auto with = [](uint32_t a, int b) { return max(a, static_cast<uint32_t>(b)); };
+    x = with(x, __builtin_amdgcn_mov_dpp(static_cast<int>(x), 0xB1, 0xf, 0xf, true));             // lane ^ 1
+    x = with(x, __builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x4E, 0xf, 0xf, true));             // lane ^ 2
+    if (V == 4) x = with(x, __builtin_amdgcn_mov_dpp(static_cast<int>(x), 0x141, 0xf, 0xf, true));  // 7 - lane of 8
+    return x;
 }
 
 // The value of an e8m0 byte: 2^(e - 127), NaN for 255.
@@ -171,28 +189,10 @@ __device__ __forceinline__ float scale_value(uint32_t e) {
     return e == 255 ? __builtin_nanf("") : __uint_as_float(max(e << 23, 0x00400000u));
 }
 
-// Eight codes from memory.
-__device__ __forceinline__ u32x2 load_codes(const uint8_t *p, int64_t i0, int64_t n, bool vec) {
-    if (vec) return __builtin_nontemporal_load(as_global(reinterpret_cast<const u32x2 *>(p + i0)));
-    u32x2 w = {0u, 0u};
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-        if (i0 + q < n) w[q >> 2] |= static_cast<uint32_t>(*as_global(p + i0 + q)) << (8 * (q & 3));
-    return w;
-}
-__device__ __forceinline__ void store_codes(uint8_t *p, int64_t i0, int64_t n, bool vec, u32x2 w) {
-    if (vec) {
-        __builtin_nontemporal_store(w, as_global(reinterpret_cast<u32x2 *>(p + i0)));
-        return;
-    }
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-        if (i0 + q < n) *as_global(p + i0 + q) = static_cast<uint8_t>(w[q >> 2] >> (8 * (q & 3)));
-}
-__device__ __forceinline__ void decode(u32x2 w, float scale, float (&x)[8]) {
+template <int V> __device__ __forceinline__ void decode(const uint32_t (&w)[V / 4], float scale, float (&x)[V]) {
     typedef float floatx2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < V / 4; ++h) {
         const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[h]), false);
         const floatx2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w[h]), true);
         x[4 * h] = scale * a[0];
@@ -202,27 +202,27 @@ __device__ __forceinline__ void decode(u32x2 w, float scale, float (&x)[8]) {
     }
 }
 
-// Eight values of a block to codes.  The scale exponent e is the smallest that
+// V values of a block to codes.  The scale exponent e is the smallest that
 // brings the block's largest magnitude to 448 or less (to (224, 448], the upper
 // end of e4m3), 17 at least; the product with 2^(127 - e) is exact.  FLOOR: no
 // value of a block that holds anything but zeros is coded below 2^-9, the
 // smallest code above zero.  A block that holds an infinity or a NaN becomes
-// NaN throughout (e = 255).  hashed: the random words of the two groups of
+// NaN throughout (e = 255).  hashed: the random word of each group of
 // four; element j of a group takes it turned left by 8 j + TURN.
-template <bool FLOOR, int TURN>
-__device__ __forceinline__ u32x2 encode(const float (&x)[8], const uint32_t (&hashed)[2], uint32_t *e_out) {
+template <bool FLOOR, int TURN, int V>
+__device__ __forceinline__ void encode(const float (&x)[V], const uint32_t (&hashed)[V / 4], uint32_t (&w)[V / 4],
+                                       uint32_t &e_out) {
     uint32_t a = 0;  // as bit patterns NaN is above infinity, and infinity above every finite value
 #pragma unroll
-    for (int q = 0; q < 8; ++q) a = max(a, __float_as_uint(x[q]) & 0x7fffffffu);
-    a = quad_max(a);
+    for (int q = 0; q < V; ++q) a = max(a, __float_as_uint(x[q]) & 0x7fffffffu);
+    a = block_max<V>(a);
     const bool bad = a >= 0x7f800000u;
     const uint32_t e = max((a + 0x1fffffu) >> 23, 25u) - 8u;
     const float nan = __builtin_nanf("");
     const float inv = bad ? nan : __uint_as_float((254u - e) << 23);
     const float least = bad ? nan : (a != 0 ? 0x1p-9f : 0.0f);
-    u32x2 w;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < V / 4; ++h) {
         int word = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -239,62 +239,134 @@ __device__ __forceinline__ u32x2 encode(const float (&x)[8], const uint32_t (&ha
         }
         w[h] = static_cast<uint32_t>(word);
     }
-    *e_out = bad ? 255u : e;
-    return w;
+    e_out = bad ? 255u : e;
 }
 
-template <typename ParamT, typename GradT, bool MASTER>
-__global__ __launch_bounds__(kThreads) void adamw8_kernel(const ByteTable t, uint32_t block0, Adamw8Scalars k,
-                                                          const float *factor) {
-    constexpr int V = kByteVec;
-    const uint32_t b = block0 + blockIdx.x;
-    const int e = owner_of(t.first, b);
-    const ByteDesc d = t.d[e];
-    const int64_t i0 = static_cast<int64_t>(b - t.first[e]) * kByteBlock + threadIdx.x * V;
-    // Lanes past the tensor's end stay for the reduction over their quad: they
-    // hold zeros and store nothing.
-    ParamT *param = static_cast<ParamT *>(d.param);
-    const GradT *grad = static_cast<const GradT *>(d.grad);
-    const uintptr_t low = reinterpret_cast<uintptr_t>(d.param) | reinterpret_cast<uintptr_t>(d.master) |
-                          reinterpret_cast<uintptr_t>(d.grad);
-    const uintptr_t low8 = reinterpret_cast<uintptr_t>(d.m) | reinterpret_cast<uintptr_t>(d.v);
-    const bool vec = (low & 15) == 0 && (low8 & 7) == 0 && i0 + V <= d.numel;
-    float p[V], g[V], m[V], v[V];
-    if constexpr (MASTER)
-        load_some<V>(d.master, i0, d.numel, vec, p);
-    else
-        load_some<V>(param, i0, d.numel, vec, p);
-    load_some<V>(grad, i0, d.numel, vec, g);
-    const u32x2 mw = load_codes(d.m, i0, d.numel, vec), vw = load_codes(d.v, i0, d.numel, vec);
-    const bool inside = i0 < d.numel;
-    const int64_t blk = i0 >> 5;
-    const uint32_t me = inside ? *as_global(d.m_scale + blk) : 0u, ve = inside ? *as_global(d.v_scale + blk) : 0u;
-    decode(mw, scale_value(me), m);
-    decode(vw, scale_value(ve), v);
-    clip(factor, g);
+// Elements of a lane: 16 bytes of the widest tensor, so that a wave's load of
+// it is contiguous (eight elements of fp32 in two loads of every other 16 bytes
+// each: 5.4 instead of 5.9 TB/s with fp32 master weights and gradients; four
+// elements of bf16 in 8-byte loads: 6.0 instead of 6.3 TB/s).
+template <typename ParamT, typename GradT, bool MASTER> constexpr int byte_vec() {
+    return sizeof(ParamT) == 2 && sizeof(GradT) == 2 && !MASTER ? 8 : 4;
+}
+
+// What a lane holds of one vector: V elements and their block's scales.
+template <int V> struct ByteLane {
+    float p[V], g[V];
+    uint32_t m[V / 4], v[V / 4];  // codes
+    uint32_t m_scale, v_scale;
+};
+
+template <int V> __device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t (&w)[V / 4]) {
+    typedef uint32_t words __attribute__((ext_vector_type(V / 4)));
+    const words r = nt_load(reinterpret_cast<const words *>(p));
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) w[h] = r[h];
+}
+template <int V> __device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t (&w)[V / 4]) {
+    typedef uint32_t words __attribute__((ext_vector_type(V / 4)));
+    words r;
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) r[h] = w[h];
+    __builtin_nontemporal_store(r, as_global(reinterpret_cast<words *>(p)));
+}
+
+// The step on the V elements from `i0` of their tensor on.
+template <int V>
+__device__ __forceinline__ void adamw8_lane(const Adamw8Scalars &k, const float *factor, int64_t i0, ByteLane<V> &x) {
+    float m[V], v[V];
+    decode<V>(x.m, scale_value(x.m_scale), m);
+    decode<V>(x.v, scale_value(x.v_scale), v);
+    clip(factor, x.g);
 #pragma unroll
     for (int q = 0; q < V; ++q) {
-        m[q] = k.beta1 * m[q] + k.one_minus_beta1 * g[q];
-        v[q] = k.beta2 * v[q] + (k.one_minus_beta2 * g[q]) * g[q];
+        m[q] = k.beta1 * m[q] + k.one_minus_beta1 * x.g[q];
+        v[q] = k.beta2 * v[q] + (k.one_minus_beta2 * x.g[q]) * x.g[q];
         // 2^24 v / (1 - b2^step): v_sqrt_f32 takes subnormal values for zero
         const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v[q] * k.scaled_inv_bias_corr2), 0x1p-12f, k.eps);
         // the moment comes in last: neither product leaves fp32's range before the result does
-        p[q] = __builtin_fmaf(-k.lr_over_bias_corr1 * __builtin_amdgcn_rcpf(den), m[q], k.decay * p[q]);
+        x.p[q] = __builtin_fmaf(-k.lr_over_bias_corr1 * __builtin_amdgcn_rcpf(den), m[q], k.decay * x.p[q]);
     }
     const uint64_t group = static_cast<uint64_t>(i0) >> 2;
     const uint32_t key = k.key ^ (static_cast<uint32_t>(group >> 32) * 0x9E3779B9u);
-    const uint32_t hashed[2] = {mix32(static_cast<uint32_t>(group) ^ key), mix32(static_cast<uint32_t>(group + 1) ^ key)};
-    uint32_t me1, ve1;
-    const u32x2 mc = encode<false, 0>(m, hashed, &me1), vc = encode<true, 16>(v, hashed, &ve1);
-    if (!inside) return;
-    store_codes(d.m, i0, d.numel, vec, mc);
-    store_codes(d.v, i0, d.numel, vec, vc);
-    if ((threadIdx.x & 3) == 0) {
-        *as_global(d.m_scale + blk) = static_cast<uint8_t>(me1);
-        *as_global(d.v_scale + blk) = static_cast<uint8_t>(ve1);
+    uint32_t hashed[V / 4];
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) hashed[h] = mix32((static_cast<uint32_t>(group) + h) ^ key);
+    encode<false, 0>(m, hashed, x.m, x.m_scale);
+    encode<true, 16>(v, hashed, x.v, x.v_scale);
+}
+
+template <typename ParamT, typename GradT, bool MASTER, bool PACED>
+__global__ __launch_bounds__(kThreads) void adamw8_kernel(const ByteTable t, uint32_t block0, Adamw8Scalars k,
+                                                          const float *factor) {
+    constexpr int V = byte_vec<ParamT, GradT, MASTER>();
+    constexpr int kBlock = kThreads * V;
+    const uint32_t b = block0 + blockIdx.x;
+    const int e = Owners<64>(t.first).of(b);
+    const ByteDesc d = t.d[e];
+    const int64_t k0 = static_cast<int64_t>(b - t.first[e]) * kBlock;
+    ParamT *param = static_cast<ParamT *>(d.param) + k0;
+    const GradT *grad = static_cast<const GradT *>(d.grad) + k0;
+    float *master = MASTER ? d.master + k0 : nullptr;
+    uint8_t *dm = d.m + k0, *dv = d.v + k0, *ms = d.m_scale + (k0 >> 5), *vs = d.v_scale + (k0 >> 5);
+    const uintptr_t low = reinterpret_cast<uintptr_t>(d.param) | reinterpret_cast<uintptr_t>(d.master) |
+                          reinterpret_cast<uintptr_t>(d.grad);
+    const uintptr_t low8 = reinterpret_cast<uintptr_t>(d.m) | reinterpret_cast<uintptr_t>(d.v);
+    const int64_t left = d.numel - k0;
+    const int i = threadIdx.x * V;
+    ByteLane<V> x;
+    if ((low & 15) == 0 && (low8 & 7) == 0 && left >= kBlock) {  // uniform: a whole block of aligned tensors
+        if constexpr (MASTER)
+            load_vec(master + i, x.p);
+        else
+            load_vec(param + i, x.p);
+        pace<PACED>();
+        load_vec(grad + i, x.g);
+        pace<PACED>();
+        load_codes<V>(dm + i, x.m);
+        pace<PACED>();
+        load_codes<V>(dv + i, x.v);
+        x.m_scale = *as_global(ms + (i >> 5));
+        x.v_scale = *as_global(vs + (i >> 5));
+        adamw8_lane<V>(k, factor, k0 + i, x);
+        store_codes<V>(dm + i, x.m);
+        store_codes<V>(dv + i, x.v);
+        if ((i & 31) == 0) {
+            *as_global(ms + (i >> 5)) = static_cast<uint8_t>(x.m_scale);
+            *as_global(vs + (i >> 5)) = static_cast<uint8_t>(x.v_scale);
+        }
+        if constexpr (MASTER) store_vec(master + i, x.p);
+        store_vec(param + i, x.p);
+        return;
     }
-    if constexpr (MASTER) store_some<V>(d.master, i0, d.numel, vec, p);
-    store_some<V>(param, i0, d.numel, vec, p);
+    // One element at a time; lanes past the end stay for the reduction over
+    // their block: they hold zeros and store nothing.
+    const int n = static_cast<int>(min<int64_t>(left, kBlock));
+    x.m_scale = i < n ? *as_global(ms + (i >> 5)) : 0u;
+    x.v_scale = i < n ? *as_global(vs + (i >> 5)) : 0u;
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) x.m[h] = x.v[h] = 0u;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+        const bool in = i + q < n;
+        x.p[q] = in ? (MASTER ? load_one(master + i + q) : load_one(param + i + q)) : 0.0f;
+        x.g[q] = in ? load_one(grad + i + q) : 0.0f;
+        x.m[q >> 2] |= in ? static_cast<uint32_t>(*as_global(dm + i + q)) << (8 * (q & 3)) : 0u;
+        x.v[q >> 2] |= in ? static_cast<uint32_t>(*as_global(dv + i + q)) << (8 * (q & 3)) : 0u;
+    }
+    adamw8_lane<V>(k, factor, k0 + i, x);
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+        if (i + q >= n) break;
+        *as_global(dm + i + q) = static_cast<uint8_t>(x.m[q >> 2] >> (8 * (q & 3)));
+        *as_global(dv + i + q) = static_cast<uint8_t>(x.v[q >> 2] >> (8 * (q & 3)));
+        if constexpr (MASTER) store_one(master + i + q, x.p[q]);
+        store_one(param + i + q, x.p[q]);
+    }
+    if (i < n && (i & 31) == 0) {
+        *as_global(ms + (i >> 5)) = static_cast<uint8_t>(x.m_scale);
+        *as_global(vs + (i >> 5)) = static_cast<uint8_t>(x.v_scale);
+    }
 }
 
 // The grid of one launch: a launch's work items are counted in 32 bits.
@@ -313,31 +385,51 @@ hipError_t launch_table(Kernel kernel, const Table &t, uint32_t blocks, const Sc
 
 }  // namespace
 
-int64_t adamw_mixed_blocks(int64_t numel) { return (numel + kMixedBlock - 1) / kMixedBlock; }
-int64_t adamw8_blocks(int64_t numel) { return (numel + kByteBlock - 1) / kByteBlock; }
-
-hipError_t launch_adamw_mixed(const MixedTable &t, uint32_t blocks, const AdamwTypes &y, const AdamwScalars &k,
-                              const float *factor, hipStream_t st) {
-    if (!y.param_bf16)
-        return y.grad_bf16 ? launch_table(adamw_mixed_kernel<float, uint16_t, false>, t, blocks, k, factor, st)
-                           : launch_table(adamw_mixed_kernel<float, float, false>, t, blocks, k, factor, st);
-    if (y.master)
-        return y.grad_bf16 ? launch_table(adamw_mixed_kernel<uint16_t, uint16_t, true>, t, blocks, k, factor, st)
-                           : launch_table(adamw_mixed_kernel<uint16_t, float, true>, t, blocks, k, factor, st);
-    return y.grad_bf16 ? launch_table(adamw_mixed_kernel<uint16_t, uint16_t, false>, t, blocks, k, factor, st)
-                       : launch_table(adamw_mixed_kernel<uint16_t, float, false>, t, blocks, k, factor, st);
+int64_t adamw_mixed_blocks(int64_t numel, const AdamwTypes &) { return (numel + kMixedBlock - 1) / kMixedBlock; }
+int64_t adamw8_blocks(int64_t numel, const AdamwTypes &y) {
+    const int block = kThreads * (y.param_bf16 && y.grad_bf16 && !y.master ? byte_vec<uint16_t, uint16_t, false>()
+                                                                           : byte_vec<float, float, false>());
+    return (numel + block - 1) / block;
 }
 
-hipError_t launch_adamw8(const ByteTable &t, uint32_t blocks, const AdamwTypes &y, const Adamw8Scalars &k,
-                         const float *factor, hipStream_t st) {
+namespace {
+
+template <bool PACED>
+hipError_t launch_mixed(const MixedTable &t, uint32_t blocks, const AdamwTypes &y, const AdamwScalars &k,
+                        const float *factor, hipStream_t st) {
     if (!y.param_bf16)
-        return y.grad_bf16 ? launch_table(adamw8_kernel<float, uint16_t, false>, t, blocks, k, factor, st)
-                           : launch_table(adamw8_kernel<float, float, false>, t, blocks, k, factor, st);
+        return y.grad_bf16 ? launch_table(adamw_mixed_kernel<float, uint16_t, false, PACED>, t, blocks, k, factor, st)
+                           : launch_table(adamw_mixed_kernel<float, float, false, PACED>, t, blocks, k, factor, st);
     if (y.master)
-        return y.grad_bf16 ? launch_table(adamw8_kernel<uint16_t, uint16_t, true>, t, blocks, k, factor, st)
-                           : launch_table(adamw8_kernel<uint16_t, float, true>, t, blocks, k, factor, st);
-    return y.grad_bf16 ? launch_table(adamw8_kernel<uint16_t, uint16_t, false>, t, blocks, k, factor, st)
-                       : launch_table(adamw8_kernel<uint16_t, float, false>, t, blocks, k, factor, st);
+        return y.grad_bf16 ? launch_table(adamw_mixed_kernel<uint16_t, uint16_t, true, PACED>, t, blocks, k, factor, st)
+                           : launch_table(adamw_mixed_kernel<uint16_t, float, true, PACED>, t, blocks, k, factor, st);
+    return y.grad_bf16 ? launch_table(adamw_mixed_kernel<uint16_t, uint16_t, false, PACED>, t, blocks, k, factor, st)
+                       : launch_table(adamw_mixed_kernel<uint16_t, float, false, PACED>, t, blocks, k, factor, st);
+}
+
+template <bool PACED>
+hipError_t launch_bytes(const ByteTable &t, uint32_t blocks, const AdamwTypes &y, const Adamw8Scalars &k,
+                        const float *factor, hipStream_t st) {
+    if (!y.param_bf16)
+        return y.grad_bf16 ? launch_table(adamw8_kernel<float, uint16_t, false, PACED>, t, blocks, k, factor, st)
+                           : launch_table(adamw8_kernel<float, float, false, PACED>, t, blocks, k, factor, st);
+    if (y.master)
+        return y.grad_bf16 ? launch_table(adamw8_kernel<uint16_t, uint16_t, true, PACED>, t, blocks, k, factor, st)
+                           : launch_table(adamw8_kernel<uint16_t, float, true, PACED>, t, blocks, k, factor, st);
+    return y.grad_bf16 ? launch_table(adamw8_kernel<uint16_t, uint16_t, false, PACED>, t, blocks, k, factor, st)
+                       : launch_table(adamw8_kernel<uint16_t, float, false, PACED>, t, blocks, k, factor, st);
+}
+
+}  // namespace
+
+hipError_t launch_adamw_mixed(const MixedTable &t, uint32_t blocks, const AdamwTypes &y, bool paced,
+                              const AdamwScalars &k, const float *factor, hipStream_t st) {
+    return paced ? launch_mixed<true>(t, blocks, y, k, factor, st) : launch_mixed<false>(t, blocks, y, k, factor, st);
+}
+
+hipError_t launch_adamw8(const ByteTable &t, uint32_t blocks, const AdamwTypes &y, bool paced, const Adamw8Scalars &k,
+                         const float *factor, hipStream_t st) {
+    return paced ? launch_bytes<true>(t, blocks, y, k, factor, st) : launch_bytes<false>(t, blocks, y, k, factor, st);
 }
 
 // The rounding's key for one step: the seed and the step count, mixed.

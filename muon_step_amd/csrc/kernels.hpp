@@ -109,32 +109,49 @@ struct AdamwTypes {
     bool param_bf16, master, grad_bf16;
 };
 // Workgroups of one tensor.
-int64_t adamw_mixed_blocks(int64_t numel);
-int64_t adamw8_blocks(int64_t numel);
-hipError_t launch_adamw_mixed(const MixedTable &t, uint32_t blocks, const AdamwTypes &y, const AdamwScalars &k,
-                              const float *factor, hipStream_t st);
-hipError_t launch_adamw8(const ByteTable &t, uint32_t blocks, const AdamwTypes &y, const Adamw8Scalars &k,
+int64_t adamw_mixed_blocks(int64_t numel, const AdamwTypes &y);
+int64_t adamw8_blocks(int64_t numel, const AdamwTypes &y);
+// paced: one tensor's loads at a time, for calls that move a lot (adamw.hip).
+hipError_t launch_adamw_mixed(const MixedTable &t, uint32_t blocks, const AdamwTypes &y, bool paced,
+                              const AdamwScalars &k, const float *factor, hipStream_t st);
+hipError_t launch_adamw8(const ByteTable &t, uint32_t blocks, const AdamwTypes &y, bool paced, const Adamw8Scalars &k,
                          const float *factor, hipStream_t st);
 uint32_t adamw8_key(uint64_t seed, int64_t step);
 
 // ---- gradient norm (grad_norm.hip)
-struct NormDesc {
-    const void *grad;
-    int64_t numel;
-};
-constexpr int kNormTensors = 128;
+// A table holds each gradient's address, its first chunk, and the elements of its
+// last one; every other chunk has kNormChunk bytes.
+constexpr int kNormChunk = 32768;
+constexpr int kNormTensors = 256;
+constexpr uint16_t kTailBf16 = 0x8000;  // the gradient is bf16, not fp32
 struct NormTable {
-    uint32_t first[128];  // first chunk of each tensor
-    NormDesc d[kNormTensors];
-    uint64_t bf16[2];  // bit k of word k / 64: tensor k is bf16
+    uint32_t first[kNormTensors];
+    const void *grad[kNormTensors];
+    uint16_t tail[kNormTensors];
 };
-constexpr int kNormBlocks = 2048;  // workgroups of one launch at most
-// Doubles of the workspace: one sum for each workgroup, and the running total.
-constexpr size_t kNormWorkspace = kNormBlocks + 1;
-int64_t grad_norm_chunks(int64_t numel);
+constexpr uint32_t kNormBlocks = 1024;  // workgroups of one launch at most: four on each CU
+// A call's last table of at most this many chunks joins the sums in its own
+// launch: 6.9 us a call at 128 chunks against 9.4 with a second launch, 9.6
+// against 9.4 at 256 and 27.8 against 9.3 at 1024 (each workgroup's release
+// writes back its XCD's L2).
+constexpr uint32_t kNormFused = 128;
+constexpr uint32_t kNormSums = 16 * kNormBlocks;
+struct NormWorkspace {
+    double sums[kNormSums];  // of the workgroups since the last joining
+    double total;            // of those before
+    uint32_t tickets[8];     // of the grids of 2^k workgroups up to kNormFused, zero at first
+};
+// The state of one call between its tables.
+struct NormCall {
+    NormWorkspace *ws;
+    double max_norm;
+    double *norm;
+    float *factor;
+    uint32_t at = 0;  // sums that wait to be joined
+    bool first = true;
+};
 // One table of a call; the last one writes *norm and *factor.
-hipError_t launch_grad_norm(const NormTable &t, uint32_t chunks, double *ws, bool first, bool last, double max_norm,
-                            double *norm, float *factor, hipStream_t st);
+hipError_t launch_grad_norm(const NormTable &t, uint32_t chunks, NormCall &call, bool last, hipStream_t st);
 
 // ---- Newton-Schulz products (ns_bf16.hip, ns_f32.hip)
 // One Newton-Schulz step on every matrix of the chunk:

@@ -660,7 +660,7 @@ struct muon_context {
     DevBuf adamw_desc;
     // muon_grad_norm's sums: of a fixed size and there from creation on, so that
     // a captured call never points to memory that a later call replaced
-    double *norm_ws = nullptr;
+    muon::NormWorkspace *norm_ws = nullptr;
     void *pinned = nullptr;
     size_t pinned_n = 0;
     hipEvent_t upload_done = nullptr;
@@ -1336,6 +1336,9 @@ muon::AdamwScalars adamw_scalars(const muon_adamw_hparams *hp) {
     return k;
 }
 
+// Bytes of a call from which its loads are paced (adamw.hip).
+constexpr double kPacedBytes = 512e6;
+
 // Runs a step over tensors of mixed types: those of the same types together,
 // in the caller's order, as many to a launch as its table holds.  moment_bytes:
 // what the moments of one element move.
@@ -1343,6 +1346,13 @@ template <class Table, int N, class T, class Blocks, class Fill, class Launch>
 muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage, double moment_bytes, hipStream_t st,
                        Blocks blocks_of, Fill fill, Launch launch) {
     DeviceGuard guard(ctx->device);
+    auto bytes_of = [&](const T &x) {
+        const double p = dtype_size(x.param_dtype), g = dtype_size(x.grad_dtype);
+        return static_cast<double>(x.numel) * (moment_bytes + g + (x.master ? 8.0 + p : 2.0 * p));
+    };
+    double total = 0;
+    for (int64_t i = 0; i < count; ++i) total += bytes_of(ts[i]);
+    const bool paced = total > kPacedBytes;
     Table t;
     for (int kind = 0; kind < 8; ++kind) {
         const muon::AdamwTypes y{(kind & 1) != 0, (kind & 2) != 0, (kind & 4) != 0};
@@ -1353,7 +1363,7 @@ muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage,
             if (n == 0) return hipSuccess;
             for (int j = n; j < 64; ++j) t.first[j] = 0xffffffffu;
             const hipError_t e = timed(ctx, stage, 0.0, bytes, st,
-                                       [&] { return launch(t, static_cast<uint32_t>(blocks), y, st); });
+                                       [&] { return launch(t, static_cast<uint32_t>(blocks), y, paced, st); });
             n = 0;
             blocks = 0;
             bytes = 0;
@@ -1364,7 +1374,7 @@ muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage,
             if (x.numel == 0 || y.param_bf16 != (x.param_dtype == MUON_BF16) || y.master != (x.master != nullptr) ||
                 y.grad_bf16 != (x.grad_dtype == MUON_BF16))
                 continue;
-            const int64_t nb = blocks_of(x.numel);
+            const int64_t nb = blocks_of(x.numel, y);
             if (n == N || blocks + nb >= (int64_t(1) << 31)) {
                 const hipError_t e = flush();
                 if (e != hipSuccess) return hip_fail(ctx, e, "AdamW launch");
@@ -1373,8 +1383,7 @@ muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage,
             fill(t.d[n], x);
             ++n;
             blocks += nb;
-            const double p = dtype_size(x.param_dtype), g = dtype_size(x.grad_dtype);
-            bytes += static_cast<double>(x.numel) * (moment_bytes + g + (x.master ? 8.0 + p : 2.0 * p));
+            bytes += bytes_of(x);
         }
         const hipError_t e = flush();
         if (e != hipSuccess) return hip_fail(ctx, e, "AdamW launch");
@@ -1497,8 +1506,11 @@ muon_status muon_create(muon_context **out, int32_t hip_device, size_t workspace
         delete ctx;
         return MUON_ERR_DEVICE;
     }
-    if (hipMalloc(reinterpret_cast<void **>(&ctx->norm_ws), muon::kNormWorkspace * sizeof(double)) != hipSuccess) {
+    if (hipMalloc(reinterpret_cast<void **>(&ctx->norm_ws), sizeof(muon::NormWorkspace)) != hipSuccess ||
+        hipMemset(ctx->norm_ws, 0, sizeof(muon::NormWorkspace)) != hipSuccess ||
+        hipDeviceSynchronize() != hipSuccess) {  // the clearing is done before any stream reads it
         (void)hipGetLastError();
+        if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
         (void)hipEventDestroy(ctx->upload_done);
         (void)hipEventDestroy(ctx->noalloc_upload_done);
         delete ctx;
@@ -1705,8 +1717,8 @@ muon_status muon_adamw_mixed_step(muon_context *ctx, const muon_adamw_mixed_tens
         };
         return run_tables<muon::MixedTable, muon::kMixedTensors>(
             ctx, ts, count, ST_ADAMW_MIXED, 16.0, static_cast<hipStream_t>(hip_stream), muon::adamw_mixed_blocks, fill,
-            [&](const muon::MixedTable &t, uint32_t blocks, const muon::AdamwTypes &y, hipStream_t st) {
-                return muon::launch_adamw_mixed(t, blocks, y, k, grad_factor, st);
+            [&](const muon::MixedTable &t, uint32_t blocks, const muon::AdamwTypes &y, bool paced, hipStream_t st) {
+                return muon::launch_adamw_mixed(t, blocks, y, paced, k, grad_factor, st);
             });
     });
 }
@@ -1738,8 +1750,8 @@ muon_status muon_adamw8_step(muon_context *ctx, const muon_adamw8_tensor *ts, in
         return run_tables<muon::ByteTable, muon::kByteTensors>(
             ctx, ts, count, ST_ADAMW8, 4.0 + 4.0 / MUON_ADAMW8_BLOCK, static_cast<hipStream_t>(hip_stream),
             muon::adamw8_blocks, fill,
-            [&](const muon::ByteTable &t, uint32_t blocks, const muon::AdamwTypes &y, hipStream_t st) {
-                return muon::launch_adamw8(t, blocks, y, k, grad_factor, st);
+            [&](const muon::ByteTable &t, uint32_t blocks, const muon::AdamwTypes &y, bool paced, hipStream_t st) {
+                return muon::launch_adamw8(t, blocks, y, paced, k, grad_factor, st);
             });
     });
 }
@@ -1754,32 +1766,33 @@ muon_status muon_grad_norm(muon_context *ctx, const muon_grad *gs, int64_t count
         DeviceGuard guard(ctx->device);
         hipStream_t st = static_cast<hipStream_t>(hip_stream);
         muon::NormTable t;
-        bool first = true;
+        muon::NormCall call{ctx->norm_ws, max_norm, norm, factor};
         int64_t i = 0;
         do {  // at least one table: a call without elements writes norm 0 and factor 1
-            std::memset(&t, 0, sizeof t);
-            std::memset(t.first, 0xff, sizeof t.first);
             int64_t chunks = 0;
             double bytes = 0;
-            for (int n = 0; i < count && n < muon::kNormTensors; ++i) {
+            int n = 0;
+            for (; i < count && n < muon::kNormTensors; ++i) {
                 const muon_grad &g = gs[i];
-                const int64_t c = muon::grad_norm_chunks(g.numel);
-                if (c == 0) continue;
+                if (g.numel == 0) continue;
+                const int64_t full = muon::kNormChunk / static_cast<int64_t>(dtype_size(g.dtype));
+                const int64_t c = (g.numel + full - 1) / full;
                 if (chunks + c >= (int64_t(1) << 31)) break;
                 t.first[n] = static_cast<uint32_t>(chunks);
-                t.d[n] = muon::NormDesc{g.grad, g.numel};
-                if (g.dtype == MUON_BF16) t.bf16[n / 64] |= uint64_t(1) << (n % 64);
+                t.grad[n] = g.grad;
+                t.tail[n] = static_cast<uint16_t>((g.numel - 1) % full + 1) |
+                            (g.dtype == MUON_BF16 ? muon::kTailBf16 : uint16_t(0));
                 chunks += c;
                 bytes += static_cast<double>(g.numel) * dtype_size(g.dtype);
                 ++n;
             }
+            for (; n < muon::kNormTensors; ++n) t.first[n] = 0xffffffffu;
+            while (i < count && gs[i].numel == 0) ++i;  // nothing is left behind the last table
             const bool last = i >= count;
             const hipError_t e = timed(ctx, ST_GRAD_NORM, bytes, bytes, st, [&] {
-                return muon::launch_grad_norm(t, static_cast<uint32_t>(chunks), ctx->norm_ws, first, last, max_norm, norm,
-                                              factor, st);
+                return muon::launch_grad_norm(t, static_cast<uint32_t>(chunks), call, last, st);
             });
             if (e != hipSuccess) return hip_fail(ctx, e, "gradient norm launch");
-            first = false;
         } while (i < count);
         ctx->err.clear();
         return MUON_OK;

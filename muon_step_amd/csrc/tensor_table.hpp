@@ -10,16 +10,22 @@
 
 namespace muon {
 
-// The tensor that owns block b: the last k with first[k] <= b.  Each lane
-// compares 64 entries of the table at once, so the search is one load and one
-// ballot instead of a chain of dependent loads.  Uniform over the wave.
-template <int N>
-__device__ __forceinline__ int owner_of(const uint32_t (&first)[N], uint32_t b) {
+// Finds the tensor that owns a block: the last k with first[k] <= b.  Each lane
+// holds N / 64 entries of the table, so the search is one load and N / 64
+// ballots instead of a chain of dependent loads.  Uniform over the wave.
+template <int N> struct Owners {
     static_assert(N % 64 == 0, "whole waves");
-    int k = -1;
+    uint32_t mine[N / 64];
+    __device__ __forceinline__ explicit Owners(const uint32_t (&first)[N]) {
 #pragma unroll
-    for (int i = 0; i < N / 64; ++i) k += __popcll(__ballot(first[i * 64 + (threadIdx.x & 63)] <= b));
-    return __builtin_amdgcn_readfirstlane(k);
-}
+        for (int i = 0; i < N / 64; ++i) mine[i] = first[i * 64 + (threadIdx.x & 63)];
+    }
+    __device__ __forceinline__ int of(uint32_t b) const {
+        int k = -1;
+#pragma unroll
+        for (int i = 0; i < N / 64; ++i) k += __popcll(__ballot(mine[i] <= b));
+        return __builtin_amdgcn_readfirstlane(k);
+    }
+};
 
 }  // namespace muon
