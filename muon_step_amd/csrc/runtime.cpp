@@ -242,32 +242,81 @@ muon_status check_list(const void *ts, int64_t count, char *msg, size_t cap) {
     return MUON_OK;
 }
 
-// The ranges of a call's tensors, and the checks that each of them passes.
+// The memory of a call's tensors.  add() takes one kind after the other (every
+// param, every grad, ...): buffers that a program allocated in order, or views
+// of one flat buffer, then form few ascending runs, which overlap() merges in
+// few passes where a sort would take one for each doubling.
+struct Range {
+    uintptr_t lo, hi;
+    uint32_t owner;
+    uint8_t kind;
+    bool writable;
+};
 struct Ranges {
-    std::vector<Interval> iv;
+    std::vector<Range> all, spare;
+    std::vector<const char *> kinds;
     char *msg;
     size_t cap;
-    // false: refused (the message is written).  A tensor of no elements has no range.
-    bool add(const void *p, int64_t n, size_t size, bool wr, int64_t owner, const char *what) {
-        if (n == 0) return true;
-        if (!p) {
-            set_msg(msg, cap, "tensor %lld: %s is NULL", (long long)owner, what);
-            return false;
+    Ranges(char *m, size_t c) : msg(m), cap(c) {}
+
+    // at(i): address, elements and element size of tensor i's memory of this
+    // kind (no elements: none).  False: refused, with the message written.
+    template <class At> bool add(const char *kind, bool writable, int64_t count, At at) {
+        kinds.push_back(kind);
+        const uint8_t k = static_cast<uint8_t>(kinds.size() - 1);
+        for (int64_t i = 0; i < count; ++i) {
+            const Memory m = at(i);
+            if (m.n == 0) continue;
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(m.p);
+            if (!m.p || lo % m.size != 0) {
+                set_msg(msg, cap, m.p ? "tensor %lld: %s is not aligned to its elements" : "tensor %lld: %s is NULL",
+                        (long long)i, kind);
+                return false;
+            }
+            all.push_back(Range{lo, lo + static_cast<uintptr_t>(m.n) * m.size, static_cast<uint32_t>(i), k, writable});
         }
-        if (!aligned_to(p, size)) {
-            set_msg(msg, cap, "tensor %lld: %s is not aligned to its %zu-byte elements", (long long)owner, what, size);
-            return false;
-        }
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-        iv.push_back(Interval{lo, lo + static_cast<uintptr_t>(n) * size, wr, owner, what});
         return true;
     }
+    struct Memory {
+        const void *p;
+        int64_t n;
+        size_t size;
+    };
+
+    void sort() {
+        std::vector<size_t> runs{0};  // where each ascending run starts, and the end
+        for (size_t i = 1; i < all.size(); ++i)
+            if (all[i].lo < all[i - 1].lo) runs.push_back(i);
+        runs.push_back(all.size());
+        spare.resize(all.size());
+        while (runs.size() > 2) {
+            std::vector<size_t> next{0};
+            for (size_t r = 0; r + 1 < runs.size(); r += 2) {
+                const size_t mid = runs[r + 1], end = r + 2 < runs.size() ? runs[r + 2] : mid;
+                std::merge(all.begin() + runs[r], all.begin() + mid, all.begin() + mid, all.begin() + end,
+                           spare.begin() + runs[r], [](const Range &x, const Range &y) { return x.lo < y.lo; });
+                next.push_back(end);
+            }
+            std::swap(all, spare);
+            runs = std::move(next);
+        }
+    }
+
+    // INVALID_ARGUMENT where a written range overlaps any other.
     muon_status overlap() {
-        const Interval *a = nullptr, *b = nullptr;
-        if (!find_overlap(iv, &a, &b)) return MUON_OK;
-        set_msg(msg, cap, "memory of tensor %lld %s overlaps tensor %lld %s", (long long)a->owner, a->what,
-                (long long)b->owner, b->what);
-        return MUON_ERR_INVALID_ARGUMENT;
+        sort();
+        const Range *top = nullptr, *top_w = nullptr;  // the furthest ends so far: of all, of the written
+        for (const Range &r : all) {
+            const Range *hit = r.writable ? top : top_w;
+            if (hit && r.lo < hit->hi) {
+                set_msg(msg, cap, "memory of tensor %lld %s overlaps tensor %lld %s", (long long)hit->owner,
+                        kinds[hit->kind], (long long)r.owner, kinds[r.kind]);
+                return MUON_ERR_INVALID_ARGUMENT;
+            }
+            if (!top || r.hi > top->hi) top = &r;
+            if (r.writable && (!top_w || r.hi > top_w->hi)) top_w = &r;
+        }
+        return MUON_OK;
     }
 };
 
@@ -288,10 +337,12 @@ template <class T> muon_status check_mixed_tensor(const T &t, int64_t i, char *m
     return MUON_OK;
 }
 
-template <class T> bool add_weights(Ranges &r, const T &t, int64_t i) {
-    return r.add(t.param, t.numel, dtype_size(t.param_dtype), true, i, "param") &&
-           (!t.master || r.add(t.master, t.numel, 4, true, i, "master")) &&
-           r.add(t.grad, t.numel, dtype_size(t.grad_dtype), false, i, "grad");
+template <class T> bool add_weights(Ranges &r, const T *ts, int64_t count, const float *factor) {
+    using M = Ranges::Memory;
+    return r.add("param", true, count, [&](int64_t i) { return M{ts[i].param, ts[i].numel, dtype_size(ts[i].param_dtype)}; }) &&
+           r.add("master", true, count, [&](int64_t i) { return M{ts[i].master, ts[i].master ? ts[i].numel : 0, 4}; }) &&
+           r.add("grad", false, count, [&](int64_t i) { return M{ts[i].grad, ts[i].numel, dtype_size(ts[i].grad_dtype)}; }) &&
+           r.add("grad_factor", false, factor ? 1 : 0, [&](int64_t) { return M{factor, 1, 4}; });
 }
 
 muon_status check_adamw_mixed(const muon_adamw_mixed_tensor *ts, int64_t count, const muon_adamw_hparams *hp,
@@ -299,16 +350,15 @@ muon_status check_adamw_mixed(const muon_adamw_mixed_tensor *ts, int64_t count, 
     muon_status s = check_list(ts, count, msg, cap);
     if (s == MUON_OK) s = check_mixed_hparams(hp, factor, msg, cap);
     if (s != MUON_OK) return s;
-    Ranges r{{}, msg, cap};
-    r.iv.reserve(static_cast<size_t>(count) * 5 + 1);
-    for (int64_t i = 0; i < count; ++i) {
-        const muon_adamw_mixed_tensor &t = ts[i];
-        if ((s = check_mixed_tensor(t, i, msg, cap)) != MUON_OK) return s;
-        if (!add_weights(r, t, i) || !r.add(t.exp_avg, t.numel, 4, true, i, "exp_avg") ||
-            !r.add(t.exp_avg_sq, t.numel, 4, true, i, "exp_avg_sq"))
-            return MUON_ERR_INVALID_ARGUMENT;
-    }
-    if (factor) (void)r.add(factor, 1, 4, false, -1, "grad_factor");
+    for (int64_t i = 0; i < count; ++i)
+        if ((s = check_mixed_tensor(ts[i], i, msg, cap)) != MUON_OK) return s;
+    using M = Ranges::Memory;
+    Ranges r(msg, cap);
+    r.all.reserve(static_cast<size_t>(count) * 5 + 1);
+    if (!add_weights(r, ts, count, factor) ||
+        !r.add("exp_avg", true, count, [&](int64_t i) { return M{ts[i].exp_avg, ts[i].numel, 4}; }) ||
+        !r.add("exp_avg_sq", true, count, [&](int64_t i) { return M{ts[i].exp_avg_sq, ts[i].numel, 4}; }))
+        return MUON_ERR_INVALID_ARGUMENT;
     return r.overlap();
 }
 
@@ -324,19 +374,18 @@ muon_status check_adamw8(const muon_adamw8_tensor *ts, int64_t count, const muon
         set_msg(msg, cap, "eps must be 0 or at least 2^-126");
         return MUON_ERR_INVALID_ARGUMENT;
     }
-    Ranges r{{}, msg, cap};
-    r.iv.reserve(static_cast<size_t>(count) * 7 + 1);
-    for (int64_t i = 0; i < count; ++i) {
-        const muon_adamw8_tensor &t = ts[i];
-        if ((s = check_mixed_tensor(t, i, msg, cap)) != MUON_OK) return s;
-        const int64_t nb = byte_blocks(t.numel);
-        if (!add_weights(r, t, i) || !r.add(t.exp_avg, t.numel, 1, true, i, "exp_avg") ||
-            !r.add(t.exp_avg_sq, t.numel, 1, true, i, "exp_avg_sq") ||
-            !r.add(t.exp_avg_scale, nb, 1, true, i, "exp_avg_scale") ||
-            !r.add(t.exp_avg_sq_scale, nb, 1, true, i, "exp_avg_sq_scale"))
-            return MUON_ERR_INVALID_ARGUMENT;
-    }
-    if (factor) (void)r.add(factor, 1, 4, false, -1, "grad_factor");
+    for (int64_t i = 0; i < count; ++i)
+        if ((s = check_mixed_tensor(ts[i], i, msg, cap)) != MUON_OK) return s;
+    using M = Ranges::Memory;
+    Ranges r(msg, cap);
+    r.all.reserve(static_cast<size_t>(count) * 7 + 1);
+    if (!add_weights(r, ts, count, factor) ||
+        !r.add("exp_avg", true, count, [&](int64_t i) { return M{ts[i].exp_avg, ts[i].numel, 1}; }) ||
+        !r.add("exp_avg_sq", true, count, [&](int64_t i) { return M{ts[i].exp_avg_sq, ts[i].numel, 1}; }) ||
+        !r.add("exp_avg_scale", true, count, [&](int64_t i) { return M{ts[i].exp_avg_scale, byte_blocks(ts[i].numel), 1}; }) ||
+        !r.add("exp_avg_sq_scale", true, count,
+               [&](int64_t i) { return M{ts[i].exp_avg_sq_scale, byte_blocks(ts[i].numel), 1}; }))
+        return MUON_ERR_INVALID_ARGUMENT;
     return r.overlap();
 }
 
