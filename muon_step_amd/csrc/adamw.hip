@@ -9,6 +9,7 @@
 #include "adamw_math.hpp"
 #include "kernels.hpp"
 #include "tensor_table.hpp"
+#include "vector_access.hpp"
 
 namespace muon {
 
@@ -39,7 +40,6 @@ template <> __device__ __forceinline__ void store_one<uint16_t>(uint16_t *p, flo
 // every CU the HBM serves five to seven streams at once and gets slower: 5.9
 // GB of mixed-type AdamW take 968 us paced and 1018 not (210e6 elements), 1 GB
 // 168.6 and 173.4, 256 MB the same, 64 MB 0.3 us more paced.
-template <class T> __device__ __forceinline__ T nt_load(const T *p) { return __builtin_nontemporal_load(as_global(p)); }
 template <bool PACED> __device__ __forceinline__ void pace() {
     if constexpr (PACED) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
@@ -47,34 +47,42 @@ template <bool PACED> __device__ __forceinline__ void pace() {
 // V consecutive values as floats, in 16-byte accesses (8-byte ones for four
 // bf16).
 template <int V> __device__ __forceinline__ void load_vec(const float *p, float (&x)[V]) {
+    static_assert(V == 4, "one access");
+    uint32_t w[4];
+    load_words<4, 4>(p, w);
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-        const floatx4 r = nt_load(reinterpret_cast<const floatx4 *>(p + i));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) x[i + q] = r[q];
-    }
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
 }
 template <int V> __device__ __forceinline__ void load_vec(const uint16_t *p, float (&x)[V]) {
-    typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
-    const words r = nt_load(reinterpret_cast<const words *>(p));
+    uint32_t w[V / 2];
+    load_words<V / 2, 2>(p, w);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
-        x[2 * i] = __uint_as_float(r[i] << 16);
-        x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
 template <int V> __device__ __forceinline__ void store_vec(float *p, const float (&x)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4)
-        __builtin_nontemporal_store(floatx4{x[i], x[i + 1], x[i + 2], x[i + 3]},
-                                    as_global(reinterpret_cast<floatx4 *>(p + i)));
+    static_assert(V == 4, "one access");
+    const uint32_t w[4] = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+    store_words<4, 4>(p, w);
 }
 template <int V> __device__ __forceinline__ void store_vec(uint16_t *p, const float (&x)[V]) {
-    typedef uint32_t words __attribute__((ext_vector_type(V / 2)));
-    words r;
+    uint32_t w[V / 2];
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) r[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    __builtin_nontemporal_store(r, as_global(reinterpret_cast<words *>(p)));
+    for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    store_words<V / 2, 2>(p, w);
+}
+
+// The first n of V values (a tensor's last ones), the others zero.
+template <int V, class T> __device__ __forceinline__ void load_first(const T *p, int n, float (&x)[V]) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) x[q] = q < n ? load_one(p + q) : 0.0f;
+}
+template <int V, class T> __device__ __forceinline__ void store_first(T *p, int n, const float (&x)[V]) {
+#pragma unroll
+    for (int q = 0; q < V; ++q)
+        if (q < n) store_one(p + q, x[q]);
 }
 
 // Multiplies by the clip factor (one rounding), when the call has one.
@@ -115,13 +123,10 @@ __global__ __launch_bounds__(kThreads) void adamw_mixed_kernel(const MixedTable 
     ParamT *param = static_cast<ParamT *>(d.param) + k0;
     const GradT *grad = static_cast<const GradT *>(d.grad) + k0;
     float *master = MASTER ? d.master + k0 : nullptr, *dm = d.m + k0, *dv = d.v + k0;
-    const uintptr_t low = reinterpret_cast<uintptr_t>(d.param) | reinterpret_cast<uintptr_t>(d.master) |
-                          reinterpret_cast<uintptr_t>(d.grad) | reinterpret_cast<uintptr_t>(d.m) |
-                          reinterpret_cast<uintptr_t>(d.v);
-    const int64_t left = d.numel - k0;
-    if ((low & 15) == 0 && left >= kMixedBlock) {  // uniform: a whole block of aligned tensors
-        const int i = threadIdx.x * V;
-        float p[V], g[V], m[V], v[V];
+    const int i = threadIdx.x * V;
+    const int n = static_cast<int>(min<int64_t>(d.numel - k0, kMixedBlock)) - i;  // elements from this lane's first on
+    float p[V], g[V], m[V], v[V];
+    if (n >= V) {
         if constexpr (MASTER)
             load_vec(master + i, p);
         else
@@ -132,24 +137,27 @@ __global__ __launch_bounds__(kThreads) void adamw_mixed_kernel(const MixedTable 
         load_vec(dm + i, m);
         pace<PACED>();
         load_vec(dv + i, v);
-        clip(factor, g);
-        adamw_exact(k, p, g, m, v);
+    } else {
+        if constexpr (MASTER)
+            load_first(master + i, n, p);
+        else
+            load_first(param + i, n, p);
+        load_first(grad + i, n, g);
+        load_first(dm + i, n, m);
+        load_first(dv + i, n, v);
+    }
+    clip(factor, g);
+    adamw_exact(k, p, g, m, v);
+    if (n >= V) {
         store_vec(dm + i, m);
         store_vec(dv + i, v);
         if constexpr (MASTER) store_vec(master + i, p);
         store_vec(param + i, p);
-        return;
-    }
-    const int n = static_cast<int>(min<int64_t>(left, kMixedBlock));
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        float p[1] = {MASTER ? load_one(master + i) : load_one(param + i)};
-        float g[1] = {load_one(grad + i)}, m[1] = {load_one(dm + i)}, v[1] = {load_one(dv + i)};
-        clip(factor, g);
-        adamw_exact(k, p, g, m, v);
-        store_one(dm + i, m[0]);
-        store_one(dv + i, v[0]);
-        if constexpr (MASTER) store_one(master + i, p[0]);
-        store_one(param + i, p[0]);
+    } else {
+        store_first(dm + i, n, m);
+        store_first(dv + i, n, v);
+        if constexpr (MASTER) store_first(master + i, n, p);
+        store_first(param + i, n, p);
     }
 }
 
@@ -257,18 +265,18 @@ template <int V> struct ByteLane {
     uint32_t m_scale, v_scale;
 };
 
-template <int V> __device__ __forceinline__ void load_codes(const uint8_t *p, uint32_t (&w)[V / 4]) {
-    typedef uint32_t words __attribute__((ext_vector_type(V / 4)));
-    const words r = nt_load(reinterpret_cast<const words *>(p));
+// The codes of V elements, or of the first n of them.
+template <int V> __device__ __forceinline__ void load_first_codes(const uint8_t *p, int n, uint32_t (&w)[V / 4]) {
 #pragma unroll
-    for (int h = 0; h < V / 4; ++h) w[h] = r[h];
+    for (int h = 0; h < V / 4; ++h) w[h] = 0u;
+#pragma unroll
+    for (int q = 0; q < V; ++q)
+        if (q < n) w[q >> 2] |= static_cast<uint32_t>(*as_global(p + q)) << (8 * (q & 3));
 }
-template <int V> __device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t (&w)[V / 4]) {
-    typedef uint32_t words __attribute__((ext_vector_type(V / 4)));
-    words r;
+template <int V> __device__ __forceinline__ void store_first_codes(uint8_t *p, int n, const uint32_t (&w)[V / 4]) {
 #pragma unroll
-    for (int h = 0; h < V / 4; ++h) r[h] = w[h];
-    __builtin_nontemporal_store(r, as_global(reinterpret_cast<words *>(p)));
+    for (int q = 0; q < V; ++q)
+        if (q < n) *as_global(p + q) = static_cast<uint8_t>(w[q >> 2] >> (8 * (q & 3)));
 }
 
 // The step on the V elements from `i0` of their tensor on.
@@ -309,13 +317,14 @@ __global__ __launch_bounds__(kThreads) void adamw8_kernel(const ByteTable t, uin
     const GradT *grad = static_cast<const GradT *>(d.grad) + k0;
     float *master = MASTER ? d.master + k0 : nullptr;
     uint8_t *dm = d.m + k0, *dv = d.v + k0, *ms = d.m_scale + (k0 >> 5), *vs = d.v_scale + (k0 >> 5);
-    const uintptr_t low = reinterpret_cast<uintptr_t>(d.param) | reinterpret_cast<uintptr_t>(d.master) |
-                          reinterpret_cast<uintptr_t>(d.grad);
-    const uintptr_t low8 = reinterpret_cast<uintptr_t>(d.m) | reinterpret_cast<uintptr_t>(d.v);
-    const int64_t left = d.numel - k0;
     const int i = threadIdx.x * V;
+    // Elements from this lane's first on.  Lanes past the end stay for the
+    // reduction over their block: they hold zeros and store nothing.
+    const int n = static_cast<int>(min<int64_t>(d.numel - k0, kBlock)) - i;
     ByteLane<V> x;
-    if ((low & 15) == 0 && (low8 & 7) == 0 && left >= kBlock) {  // uniform: a whole block of aligned tensors
+    x.m_scale = n > 0 ? *as_global(ms + (i >> 5)) : 0u;
+    x.v_scale = n > 0 ? *as_global(vs + (i >> 5)) : 0u;
+    if (n >= V) {
         if constexpr (MASTER)
             load_vec(master + i, x.p);
         else
@@ -323,47 +332,31 @@ __global__ __launch_bounds__(kThreads) void adamw8_kernel(const ByteTable t, uin
         pace<PACED>();
         load_vec(grad + i, x.g);
         pace<PACED>();
-        load_codes<V>(dm + i, x.m);
+        load_words<V / 4, 1>(dm + i, x.m);
         pace<PACED>();
-        load_codes<V>(dv + i, x.v);
-        x.m_scale = *as_global(ms + (i >> 5));
-        x.v_scale = *as_global(vs + (i >> 5));
-        adamw8_lane<V>(k, factor, k0 + i, x);
-        store_codes<V>(dm + i, x.m);
-        store_codes<V>(dv + i, x.v);
-        if ((i & 31) == 0) {
-            *as_global(ms + (i >> 5)) = static_cast<uint8_t>(x.m_scale);
-            *as_global(vs + (i >> 5)) = static_cast<uint8_t>(x.v_scale);
-        }
-        if constexpr (MASTER) store_vec(master + i, x.p);
-        store_vec(param + i, x.p);
-        return;
-    }
-    // One element at a time; lanes past the end stay for the reduction over
-    // their block: they hold zeros and store nothing.
-    const int n = static_cast<int>(min<int64_t>(left, kBlock));
-    x.m_scale = i < n ? *as_global(ms + (i >> 5)) : 0u;
-    x.v_scale = i < n ? *as_global(vs + (i >> 5)) : 0u;
-#pragma unroll
-    for (int h = 0; h < V / 4; ++h) x.m[h] = x.v[h] = 0u;
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-        const bool in = i + q < n;
-        x.p[q] = in ? (MASTER ? load_one(master + i + q) : load_one(param + i + q)) : 0.0f;
-        x.g[q] = in ? load_one(grad + i + q) : 0.0f;
-        x.m[q >> 2] |= in ? static_cast<uint32_t>(*as_global(dm + i + q)) << (8 * (q & 3)) : 0u;
-        x.v[q >> 2] |= in ? static_cast<uint32_t>(*as_global(dv + i + q)) << (8 * (q & 3)) : 0u;
+        load_words<V / 4, 1>(dv + i, x.v);
+    } else {
+        if constexpr (MASTER)
+            load_first(master + i, n, x.p);
+        else
+            load_first(param + i, n, x.p);
+        load_first(grad + i, n, x.g);
+        load_first_codes<V>(dm + i, n, x.m);
+        load_first_codes<V>(dv + i, n, x.v);
     }
     adamw8_lane<V>(k, factor, k0 + i, x);
-#pragma unroll
-    for (int q = 0; q < V; ++q) {
-        if (i + q >= n) break;
-        *as_global(dm + i + q) = static_cast<uint8_t>(x.m[q >> 2] >> (8 * (q & 3)));
-        *as_global(dv + i + q) = static_cast<uint8_t>(x.v[q >> 2] >> (8 * (q & 3)));
-        if constexpr (MASTER) store_one(master + i + q, x.p[q]);
-        store_one(param + i + q, x.p[q]);
+    if (n >= V) {
+        store_words<V / 4, 1>(dm + i, x.m);
+        store_words<V / 4, 1>(dv + i, x.v);
+        if constexpr (MASTER) store_vec(master + i, x.p);
+        store_vec(param + i, x.p);
+    } else {
+        store_first_codes<V>(dm + i, n, x.m);
+        store_first_codes<V>(dv + i, n, x.v);
+        if constexpr (MASTER) store_first(master + i, n, x.p);
+        store_first(param + i, n, x.p);
     }
-    if (i < n && (i & 31) == 0) {
+    if (n > 0 && (i & 31) == 0) {
         *as_global(ms + (i >> 5)) = static_cast<uint8_t>(x.m_scale);
         *as_global(vs + (i >> 5)) = static_cast<uint8_t>(x.v_scale);
     }

@@ -13,6 +13,7 @@
 
 #include "kernels.hpp"
 #include "tensor_table.hpp"
+#include "vector_access.hpp"
 
 namespace muon {
 
@@ -36,10 +37,10 @@ __device__ __forceinline__ void add_square(float x, double &acc) {
     acc = __builtin_fma(d, d, acc);  // the product is exact: one rounding
 }
 
-__device__ __forceinline__ void add_squares(u32x4 w, bool bf16, double &acc) {
+template <bool BF16> __device__ __forceinline__ void add_squares(const uint32_t (&w)[4], double &acc) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        if (bf16) {
+        if constexpr (BF16) {
             add_square(__uint_as_float(w[q] << 16), acc);
             add_square(__uint_as_float(w[q] & 0xffff0000u), acc);
         } else {
@@ -48,31 +49,38 @@ __device__ __forceinline__ void add_squares(u32x4 w, bool bf16, double &acc) {
     }
 }
 
-// A whole chunk of an aligned gradient: every load of the lane first.
+// A whole chunk: every load of the lane first.
 template <bool BF16> __device__ __forceinline__ void add_whole(const char *p, double &acc) {
     constexpr int kLoads = kNormChunk / 16 / kThreads;
-    const u32x4 *v = reinterpret_cast<const u32x4 *>(p) + threadIdx.x;
-    u32x4 w[kLoads];
+    uint32_t w[kLoads][4];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) w[i] = __builtin_nontemporal_load(as_global(v + i * kThreads));
+    for (int i = 0; i < kLoads; ++i) load_words<4, BF16 ? 2 : 4>(p + 16 * (threadIdx.x + i * kThreads), w[i]);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) add_squares(w[i], BF16, acc);
+    for (int i = 0; i < kLoads; ++i) add_squares<BF16>(w[i], acc);
 }
 
-// n elements: in 16-byte loads from the first aligned one on, the others one by one.
-__device__ __forceinline__ void add_part(const char *p, int n, bool bf16, double &acc) {
-    const int size = bf16 ? 2 : 4, per = 16 / size;
-    const int head = min(n, static_cast<int>(-reinterpret_cast<uintptr_t>(p) & 15) / size), vectors = (n - head) / per;
-    const u32x4 *v = reinterpret_cast<const u32x4 *>(p + head * size);
-    for (int i = threadIdx.x; i < vectors; i += kThreads)
-        add_squares(__builtin_nontemporal_load(as_global(v + i)), bf16, acc);
-    const int rest = n - per * vectors;  // the head's elements, then those behind the last vector
-    for (int j = threadIdx.x; j < rest; j += kThreads) {
-        const int i = j < head ? j : j + per * vectors;
-        add_square(bf16 ? bf16_bits_to_float(*as_global(reinterpret_cast<const uint16_t *>(p) + i))
-                        : *as_global(reinterpret_cast<const float *>(p) + i),
-                   acc);
+// n elements: in 16-byte loads, and one by one what is left behind them.
+template <bool BF16> __device__ __forceinline__ void add_part(const char *p, int n, double &acc) {
+    constexpr int kSize = BF16 ? 2 : 4, kPer = 16 / kSize;
+    for (int i = threadIdx.x; i < n / kPer; i += kThreads) {
+        uint32_t w[4];
+        load_words<4, kSize>(p + 16 * i, w);
+        add_squares<BF16>(w, acc);
     }
+    for (int i = n / kPer * kPer + threadIdx.x; i < n; i += kThreads) {
+        if constexpr (BF16)
+            add_square(bf16_bits_to_float(*as_global(reinterpret_cast<const uint16_t *>(p) + i)), acc);
+        else
+            add_square(*as_global(reinterpret_cast<const float *>(p) + i), acc);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void add_chunk(const char *p, int n, double &acc) {
+    if (n == kNormChunk / (BF16 ? 2 : 4))
+        add_whole<BF16>(p, acc);
+    else
+        add_part<BF16>(p, n, acc);
 }
 
 // Joins the first `count` workgroups' sums, in their order, with the total of
@@ -129,16 +137,13 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const NormTable t, 
         const bool bf16 = (t.tail[e] & kTailBf16) != 0;
         const int full = kNormChunk / (bf16 ? 2 : 4);
         const char *g = static_cast<const char *>(t.grad[e]);
-        const bool aligned = (reinterpret_cast<uintptr_t>(g) & 15) == 0;
         for (; c < min(end, stop); ++c) {
             const char *p = g + static_cast<int64_t>(c - begin) * kNormChunk;
             const int n = c + 1 == end ? tail : full;
-            if (!aligned || n < full)
-                add_part(p, n, bf16, acc);
-            else if (bf16)
-                add_whole<true>(p, acc);
+            if (bf16)
+                add_chunk<true>(p, n, acc);
             else
-                add_whole<false>(p, acc);
+                add_chunk<false>(p, n, acc);
         }
     }
     const double s = block_total(acc, sh);
