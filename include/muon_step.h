@@ -403,7 +403,7 @@ muon_status muon_adamw8_step(muon_context *ctx, const muon_adamw8_tensor *ts, in
  *           norm is infinite or NaN (a step that reads it then writes NaN
  *           everywhere).
  * norm and factor are device memory outside every gradient; no gradient is
- * written.  The sums pass through memory of the context: as for every entry
+ * written, and one that is listed twice counts twice.  The sums pass through memory of the context: as for every entry
  * point, calls on one context (and replays of graphs that captured it) must be
  * ordered. */
 muon_status muon_grad_norm(muon_context *ctx, const muon_grad *gs, int64_t count, double max_norm, double *norm,

@@ -340,15 +340,22 @@ class Context:
         if _on_one_gpu(named) != self.device:
             raise ValueError(f"tensors live on another GPU than the context (cuda:{self.device})")
 
+    def _check_hp_factor(self, hp):
+        factor = getattr(hp, "_factor", None)
+        if factor is not None:
+            _factor_ptr(factor, self.device)
+
     # The methods below keep the C ABI's names.
     def muon_step(self, mats, hp, stream=None):
         self._check_device(mats, "matrix")
+        self._check_hp_factor(hp)
         arr = (muon_matrix * len(mats))(*mats)
         st = self.lib.muon_step(self.handle, arr, len(mats), ctypes.byref(hp), _stream_handle(stream))
         _check(self.lib, self.handle, st, "muon_step")
 
     def muon_step_noalloc(self, mats, hp, stream=None):
         self._check_device(mats, "matrix")
+        self._check_hp_factor(hp)
         arr = (muon_matrix * len(mats))(*mats)
         st = self.lib.muon_step_noalloc(self.handle, arr, len(mats), ctypes.byref(hp), _stream_handle(stream))
         _check(self.lib, self.handle, st, "muon_step_noalloc")

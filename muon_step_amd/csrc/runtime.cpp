@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <limits>
 #include <map>
@@ -1555,16 +1556,18 @@ muon_status muon_create(muon_context **out, int32_t hip_device, size_t workspace
         delete ctx;
         return MUON_ERR_DEVICE;
     }
-    if (hipMalloc(reinterpret_cast<void **>(&ctx->norm_ws), sizeof(muon::NormWorkspace)) != hipSuccess ||
-        hipMemset(ctx->norm_ws, 0, sizeof(muon::NormWorkspace)) != hipSuccess ||
-        hipDeviceSynchronize() != hipSuccess) {  // the clearing is done before any stream reads it
+    void *zeros = std::calloc(1, sizeof(muon::NormWorkspace));
+    if (!zeros || hipMalloc(reinterpret_cast<void **>(&ctx->norm_ws), sizeof(muon::NormWorkspace)) != hipSuccess ||
+        hipMemcpy(ctx->norm_ws, zeros, sizeof(muon::NormWorkspace), hipMemcpyHostToDevice) != hipSuccess) {
         (void)hipGetLastError();
+        std::free(zeros);
         if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
         (void)hipEventDestroy(ctx->upload_done);
         (void)hipEventDestroy(ctx->noalloc_upload_done);
         delete ctx;
         return MUON_ERR_OUT_OF_MEMORY;
     }
+    std::free(zeros);
     // The allocation-free step's memory: this device's copy of the static
     // scratch (its address, with this device current) and the pinned staging
     // of its descriptor table.  A failure here only disables that entry point.

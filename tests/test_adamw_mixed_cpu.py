@@ -141,6 +141,52 @@ def test_adamw8_refuses_more(lib):
     assert _check(lib, [_mixed()], hp=ms.adamw_hparams(eps=1e-39))[0] == ms.MUON_OK
 
 
+@pytest.mark.parametrize("eight", [False, True])
+def test_overlap_check_against_brute_force(lib, eight):
+    """Random layouts of a few dozen tensors, in and out of address order, some with one range moved onto another's
+    last or first byte: refused exactly where two ranges share a byte and one of them is written."""
+    rng = np.random.default_rng(4)
+    fields = (["param", "master", "grad", "exp_avg", "exp_avg_sq"] +
+              (["exp_avg_scale", "exp_avg_sq_scale"] if eight else []))
+    refused = 0
+    for trial in range(300):
+        count = int(rng.integers(1, 30))
+        ts = []
+        for _ in range(count):
+            t = (ms.muon_adamw8_tensor if eight else ms.muon_adamw_mixed_tensor)()
+            t.numel = int(rng.choice([0, 1, 31, 32, 33, 1000]))
+            t.param_dtype, t.grad_dtype = BF16, int(rng.integers(0, 2))
+            ts.append(t)
+        has_master = rng.random(count) < 0.5
+
+        def size(t, f):
+            if f == "param": return 2 * t.numel
+            if f == "grad": return (2 if t.grad_dtype == BF16 else 4) * t.numel
+            if f.endswith("scale"): return -(-t.numel // 32)
+            return t.numel if eight and f != "master" else 4 * t.numel
+
+        slots = [(i, f) for i in range(count) for f in fields if f != "master" or has_master[i]]
+        if trial % 2: rng.shuffle(slots)
+        at = BASE
+        for i, f in slots:
+            setattr(ts[int(i)], str(f), at)
+            at += -(-size(ts[int(i)], str(f)) // 4) * 4 + int(rng.choice([0, 0, 4, 64]))
+        if trial % 3 == 0:                       # move one range to another's end or start
+            (i, f), (j, h) = (slots[k] for k in rng.integers(0, len(slots), 2))
+            i, f, j, h = int(i), str(f), int(j), str(h)
+            addr = getattr(ts[j], h) + int(rng.choice([0, max(0, size(ts[j], h) - 4), size(ts[j], h)]))
+            setattr(ts[i], f, -(-addr // 4) * 4)
+        spans = [(getattr(ts[int(i)], str(f)), size(ts[int(i)], str(f)), f != "grad") for i, f in slots]
+        spans = [s for s in spans if s[1] > 0]
+        hit = any(a[0] < b[0] + b[1] and b[0] < a[0] + a[1] and (a[2] or b[2])
+                  for k, a in enumerate(spans) for b in spans[:k])
+        st, msg = _check(lib, ts)
+        assert st == (ms.MUON_ERR_INVALID_ARGUMENT if hit else ms.MUON_OK), (trial, msg)
+        assert ("overlaps" in msg) == hit
+        refused += hit
+    assert 20 < refused < 200
+
+
 def test_grad_norm_refuses(lib):
     g = ms.muon_grad(BASE, 1000, BF16, 0)
     norm, factor = BASE - 16, BASE - 8
