@@ -154,7 +154,9 @@ def moe16b_step(args):
     """Times the full synthetic 16B-MoE optimizer step (27 layers: 4 x 2048^2
     attention matrices and 64 experts x (2048x1408 up, gate; 1408x2048 down),
     Muon on all 5292 matrices in one call, then AdamW on the 102400x2048
-    embedding and head) and prints one JSON line of its own."""
+    embedding and head) and prints one JSON line of its own.  --clip-norm
+    measures the norm of all gradients first and clips every step with it;
+    --adamw8 holds the embedding's and the head's moments in 8 bits."""
     import torch
 
     import muon_step_amd as ms
@@ -182,16 +184,34 @@ def moe16b_step(args):
         p = torch.randn(n, generator=gen, device="cuda") * synth.gen.PARAM_STD
         adamw_bufs.append((p, torch.randn(n, generator=gen, device="cuda") * 1e-3, torch.zeros_like(p),
                            torch.zeros_like(p)))
-    tensors = [ms.adamw_tensor(*b) for b in adamw_bufs]
-    hp = ms.make_hparams(lr=0.02, momentum=0.95, weight_decay=0.1, gamma=0.2, nesterov=True,
+    if args.adamw8:
+        tensors = ms.table(ms.adamw8_tensor(p, g, ms.adamw8_state(p)) for p, g, _, _ in adamw_bufs)
+    elif args.clip_norm:
+        tensors = ms.table(ms.adamw_mixed_tensor(*b) for b in adamw_bufs)
+    else:
+        tensors = [ms.adamw_tensor(*b) for b in adamw_bufs]
+    norm, factor, all_grads = None, None, None
+    if args.clip_norm:
+        norm = torch.zeros(1, dtype=torch.float64, device="cuda")
+        factor = torch.ones(1, device="cuda")
+        all_grads = ms.table([ms.grad(g) for g in grads] + [ms.grad(b[1]) for b in adamw_bufs])
+    hp = ms.make_hparams(grad_factor=factor, lr=0.02, momentum=0.95, weight_decay=0.1, gamma=0.2, nesterov=True,
                          ns_precision=ms.MUON_NS_BF16,
                          scale_mode=ms.MUON_SCALE_UNIT_RMS if args.scale_mode == "unit_rms" else ms.MUON_SCALE_SQRT_MAX)
     ctx = ms.Context(0, args.workspace_gib << 30)
     stream = torch.cuda.current_stream()
 
     def step(i):
+        if args.clip_norm:
+            ctx.muon_grad_norm(all_grads, args.clip_norm, norm, factor, stream)
         ctx.muon_step(mats, hp, stream)
-        ctx.muon_adamw_step(tensors, ms.adamw_hparams(step=i + 1), stream)
+        ahp = ms.adamw_hparams(step=i + 1)
+        if args.adamw8:
+            ctx.muon_adamw8_step(tensors, ahp, seed=5, grad_factor=factor, stream=stream)
+        elif args.clip_norm:
+            ctx.muon_adamw_mixed_step(tensors, ahp, grad_factor=factor, stream=stream)
+        else:
+            ctx.muon_adamw_step(tensors, ahp, stream)
 
     for i in range(args.warmup):
         step(i)
@@ -217,7 +237,8 @@ def moe16b_step(args):
         "value": round(1000.0 / ms_per_step, 4), "unit": "steps/s", "ms_per_step": round(ms_per_step, 3),
         "steps": args.steps, "warmup": args.warmup, "n_gpus": 1, "dtype": "bf16", "data": "synthetic",
         "config": {"workload": "moe16b_full_step", "muon_matrices": len(specs),
-                   "workspace_cap_gib": args.workspace_gib, "scale_mode": args.scale_mode},
+                   "workspace_cap_gib": args.workspace_gib, "scale_mode": args.scale_mode,
+                   "clip_norm": args.clip_norm, "adamw_moments": "8 bits" if args.adamw8 else "fp32"},
         "ns_tflops": round(ns_flops / ns_ms / 1e9, 2) if ns_ms else None,
         "ns_frac_bf16_peak": round(ns_flops / ns_ms / 1e9 / PEAK_BF16_TFLOPS, 4) if ns_ms else None,
         "stage_ms_per_step": breakdown}), flush=True)
@@ -355,6 +376,9 @@ def main():
     ap.add_argument("--workspace-gib", type=int, default=64, help="NS workspace cap for --workload moe16b")
     ap.add_argument("--scale-mode", default="sqrt_max", choices=["sqrt_max", "unit_rms"],
                     help="update scale: sqrt(max(n,m))*gamma (DeepSeek-V4) or the unit-RMS mode")
+    ap.add_argument("--clip-norm", type=float, default=None,
+                    help="moe16b: measure the norm of all gradients and clip them to this one in every step")
+    ap.add_argument("--adamw8", action="store_true", help="moe16b: AdamW moments of embedding and head in 8 bits")
     ap.add_argument("--library-baseline", action="store_true",
                     help="only time torch bf16 batched products of the same shapes (64 matrices)")
     ap.add_argument("--hbm-probe", action="store_true",
