@@ -4,6 +4,17 @@
 //
 // Compiled with -ffp-contract=off: a multiply and an add round once each unless
 // the code says fma.
+//
+// Both kernels are bound by HBM: they read and write every byte once (by
+// counter: 2.94 GB each way for the 28-byte step on 210e6 elements; 1.28 and
+// 0.85 GB for the 8-bit step on bf16 weights and gradients, 10.1 bytes an
+// element).  A plain copy moves 6.4 TB/s on the same card; 210e6 elements take
+//   32-bit moments, bf16 weights + fp32 master, bf16 gradients   975 us  6.0 TB/s
+//   8-bit moments, bf16 weights and gradients                    332 us  6.4 TB/s
+//   8-bit moments, bf16 weights + fp32 master, fp32 gradients    612 us  6.2 TB/s
+// One vector a lane and a workgroup for each 1024 (2048) elements: with two or
+// four vectors a lane the first takes 1056 and 1018 us, in workgroups of 512
+// threads 2% more.
 #include <algorithm>
 
 #include "adamw_math.hpp"
@@ -94,8 +105,11 @@ template <int V> __device__ __forceinline__ void clip(const float *factor, float
 }
 
 // ---------------------------------------------------------------------------
-// Moments in 32 bits.  Per element the nine fp32 operations of muon_adamw_step
-// in their order, each rounded once (division and square root correctly).
+// Moments in 32 bits.  Per element the fp32 operations of muon_adamw_step in
+// their order, each rounded once (division and square root correctly).  Some 80
+// vector instructions an element for that hide behind the memory: with
+// approximate division and root a call of 92 MB takes 17.4 us instead of 18.2,
+// one of 5.9 GB the same.
 constexpr int kMixedVec = 4;                       // elements of a lane
 constexpr int kMixedBlock = kThreads * kMixedVec;  // elements of a workgroup
 
@@ -163,16 +177,20 @@ __global__ __launch_bounds__(kThreads) void adamw_mixed_kernel(const MixedTable 
 
 // ---------------------------------------------------------------------------
 // Moments in 8 bits: e4m3 codes with an e8m0 scale for each 32 elements, which
-// four neighbouring lanes of eight elements hold.  The moments' new values are
-// fp32 with each operation rounded once, so that the codes are defined bit for
-// bit; the weights are computed from those values (not from their codes) in
-// fp32 with the hardware's square root and reciprocal.
+// four (eight) neighbouring lanes of eight (four) elements hold.  The moments'
+// new values are fp32 with each operation rounded once, so that the codes are
+// defined bit for bit; the weights are computed from those values (not from
+// their codes) in fp32 with the hardware's square root and reciprocal: the
+// correctly rounded ones would take more time than the 10 bytes an element.
 //
 // Rounding is stochastic: with three mantissa bits a moving average rounded to
 // nearest stops moving (0.95 x 1.125 rounds back to 1.125), while the expected
 // value of the code here is the value itself.  v_cvt_sr_fp8_f32 rounds up where
 // the 20 bits of an fp32 significand that are cut off and the random operand's
-// top 20 bits carry.
+// top 20 bits carry.  One hash serves four elements, turned by a byte for each
+// and by two more for the second moment: each of its bytes leads one rounding of
+// either moment.
+
 // A 32-bit mixing function: two rounds of xor-shift and multiplication.
 __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     x ^= x >> 16;
