@@ -186,9 +186,9 @@ typedef struct muon_adamw_hparams {
  *               step is applied to param itself, and rounded to its type.
  *   grad        device, grad_dtype, read only
  *   exp_avg, exp_avg_sq  device fp32, in and out
- * Every address must be a multiple of its element's size.  Pointers of a tensor
- * with numel 0 are not looked at.  No written range may overlap any other range of
- * the call; gradients may share memory. */
+ * numel is at most 2^38.  Every address must be a multiple of its element's
+ * size.  Pointers of a tensor with numel 0 are not looked at.  No written range
+ * may overlap any other range of the call; gradients may share memory. */
 typedef struct muon_adamw_mixed_tensor {
     void *param;
     float *master;

@@ -9,12 +9,12 @@
 // counter: 2.94 GB each way for the 28-byte step on 210e6 elements; 1.28 and
 // 0.85 GB for the 8-bit step on bf16 weights and gradients, 10.1 bytes an
 // element).  A plain copy moves 6.4 TB/s on the same card; 210e6 elements take
-//   32-bit moments, bf16 weights + fp32 master, bf16 gradients   975 us  6.0 TB/s
-//   8-bit moments, bf16 weights and gradients                    332 us  6.4 TB/s
-//   8-bit moments, bf16 weights + fp32 master, fp32 gradients    612 us  6.2 TB/s
-// One vector a lane and a workgroup for each 1024 (2048) elements: with two or
-// four vectors a lane the first takes 1056 and 1018 us, in workgroups of 512
-// threads 2% more.
+//   32-bit moments, bf16 weights + fp32 master, bf16 gradients   931 us  6.3 TB/s
+//   8-bit moments, bf16 weights and gradients                    327 us  6.5 TB/s
+//   8-bit moments, bf16 weights + fp32 master, fp32 gradients    606 us  6.3 TB/s
+// One vector a lane and one wave a workgroup: in workgroups of 128, 256 and 512
+// threads the first takes 946, 983 and 1018 us (smaller calls the same), with
+// two or four vectors a lane (256 threads) 1056 and 1018.
 #include <algorithm>
 
 #include "adamw_math.hpp"
@@ -26,7 +26,7 @@ namespace muon {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;  // one wave: see below
 
 template <typename T> __device__ __forceinline__ float load_one(const T *p);
 template <> __device__ __forceinline__ float load_one<float>(const float *p) { return *as_global(p); }
@@ -48,9 +48,9 @@ template <> __device__ __forceinline__ void store_one<uint16_t>(uint16_t *p, flo
 //
 // PACED (calls that move more than 512 MB): each tensor's load is waited for
 // before the next tensor's is issued.  With all of a lane's loads in flight on
-// every CU the HBM serves five to seven streams at once and gets slower: 5.9
-// GB of mixed-type AdamW take 968 us paced and 1018 not (210e6 elements), 1 GB
-// 168.6 and 173.4, 256 MB the same, 64 MB 0.3 us more paced.
+// every CU the HBM serves five to seven streams at once and gets slower: the
+// first of the steps above takes 931 us paced and 958 not, the second 327 and
+// 336; calls of 256 MB and less gain nothing.
 template <bool PACED> __device__ __forceinline__ void pace() {
     if constexpr (PACED) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }

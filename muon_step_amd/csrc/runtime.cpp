@@ -29,6 +29,9 @@ namespace {
 constexpr int64_t kMaxNsSteps = 64;
 constexpr int64_t kMaxDim = int64_t(1) << 31;   // rows, cols
 constexpr int64_t kMaxElems = int64_t(1) << 40; // rows * cols
+// Elements of one tensor of the mixed-type AdamW steps: their workgroups of 256
+// elements or more are counted in 32 bits.
+constexpr int64_t kMaxMixedElems = int64_t(1) << 38;
 // Groups whose smaller side is at most this run the fp32 Newton-Schulz
 // products even when bf16 is requested: with so few singular directions the
 // bf16 rounding of X does not average out, and their cost is negligible.
@@ -323,7 +326,7 @@ struct Ranges {
 
 // numel, dtypes and master of one tensor of a step over mixed types.
 template <class T> muon_status check_mixed_tensor(const T &t, int64_t i, char *msg, size_t cap) {
-    if (t.numel < 0 || t.numel > kMaxElems) {
+    if (t.numel < 0 || t.numel > kMaxMixedElems) {
         set_msg(msg, cap, "tensor %lld: numel %lld out of range", (long long)i, (long long)t.numel);
         return MUON_ERR_INVALID_ARGUMENT;
     }

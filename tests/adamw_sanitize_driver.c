@@ -81,7 +81,7 @@ int main(void) {
     }
     muon_adamw8_tensor big;
     memset(&big, 0, sizeof big);
-    big.numel = (int64_t)1 << 40; /* the largest: ranges of 2^42 bytes */
+    big.numel = (int64_t)1 << 38; /* the largest */
     big.param_dtype = big.grad_dtype = MUON_F32;
     big.param = (void *)((uintptr_t)1 << 43);
     big.grad = (void *)((uintptr_t)2 << 43);
