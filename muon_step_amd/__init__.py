@@ -272,7 +272,7 @@ def table(items):
     if not items:
         raise ValueError("a table needs at least one descriptor")
     arr = _array(items, type(items[0]))
-    devices = {d for d in (getattr(it, "_device", None) for it in items) if d is not None}
+    devices = {getattr(it, "_device", None) for it in items} - {None}
     if len(devices) > 1:
         raise ValueError(f"the descriptors live on several GPUs: {sorted(devices)}")
     arr._device = devices.pop() if devices else None
@@ -499,42 +499,56 @@ def adamw_hparams(lr=0.02, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, st
     return muon_adamw_hparams(lr, beta1, beta2, eps, weight_decay, step)
 
 
-def _owning(desc, device, named):
+def _gpu_index(names, tensors):
+    """The GPU that all the tensors are on; raises where there is none, or more than one."""
+    dev = tensors[0].get_device()
+    for name, t in zip(names, tensors):
+        if t.get_device() != dev or dev < 0:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a GPU tensor, got device {t.device}")
+            raise ValueError(f"{name} is on {t.device}, {names[0]} on {tensors[0].device}")
+    return dev
+
+
+def _owning(desc, device, tensors):
     """Notes a descriptor's device, and keeps its tensors alive with it."""
     desc._device = device
-    desc._tensors = [t for _, t in named]
+    desc._tensors = tensors
     return desc
 
 
 def _weights(param, grad, master):
-    """The checks that the mixed-type AdamW descriptors share; returns their (name, tensor) pairs."""
-    named = [("param", param), ("grad", grad)]
-    if master is not None:
-        import torch
-        if param.dtype != torch.bfloat16:
-            raise TypeError("a master copy goes with a bfloat16 param")
-        named.append(("master", master))
-        _require_f32(named[2:])
-    for name, t in named:
-        if not t.is_contiguous() or t.numel() != param.numel():
+    """The checks that the mixed-type AdamW descriptors share; returns param's and grad's type codes."""
+    pd, gd = _dtype_code(param), _dtype_code(grad)
+    n = param.numel()
+    for name, t in (("param", param), ("grad", grad), ("master", param if master is None else master)):
+        if not t.is_contiguous() or t.numel() != n:
             raise ValueError(f"{name} must be contiguous, with param's number of elements")
-    return named
+    if master is not None:
+        if pd != MUON_BF16:
+            raise TypeError("a master copy goes with a bfloat16 param")
+        _require_f32((("master", master),))
+    return pd, gd
+
+
+_MIXED_NAMES = ("param", "grad", "exp_avg", "exp_avg_sq", "master")
 
 
 def adamw_mixed_tensor(param, grad, exp_avg, exp_avg_sq, master=None):
     """muon_adamw_mixed_tensor for torch tensors (contiguous, equal numel, one GPU; param and grad float32 or
     bfloat16, the others float32; master only with a bfloat16 param)."""
-    named = _weights(param, grad, master)
-    moments = [("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)]
+    pd, gd = _weights(param, grad, master)
+    n = param.numel()
+    moments = (("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq))
     for name, t in moments:
-        if not t.is_contiguous() or t.numel() != param.numel():
+        if not t.is_contiguous() or t.numel() != n:
             raise ValueError(f"{name} must be contiguous, with param's number of elements")
     _require_f32(moments)
-    pd, gd = _dtype_code(param), _dtype_code(grad)
-    dev = _on_one_gpu(named + moments)
-    t = muon_adamw_mixed_tensor(param.data_ptr(), master.data_ptr() if master is not None else None,
-                                grad.data_ptr(), exp_avg.data_ptr(), exp_avg_sq.data_ptr(), param.numel(), pd, gd)
-    return _owning(t, dev, named + moments)
+    tensors = (param, grad, exp_avg, exp_avg_sq) if master is None else (param, grad, exp_avg, exp_avg_sq, master)
+    dev = _gpu_index(_MIXED_NAMES, tensors)
+    t = muon_adamw_mixed_tensor(param.data_ptr(), None if master is None else master.data_ptr(), grad.data_ptr(),
+                                exp_avg.data_ptr(), exp_avg_sq.data_ptr(), n, pd, gd)
+    return _owning(t, dev, tensors)
 
 
 def adamw8_state(param):
@@ -565,29 +579,31 @@ def adamw8_moments(state):
     return tuple(out)
 
 
+_STATE_NAMES = ("exp_avg", "exp_avg_scale", "exp_avg_sq", "exp_avg_sq_scale")
+_BYTE_NAMES = ("param", "grad") + _STATE_NAMES + ("master",)
+
+
 def adamw8_tensor(param, grad, state, master=None):
     """muon_adamw8_tensor for torch tensors; state as adamw8_state() makes it (codes of one byte an element,
     float8_e4m3fn or uint8, and uint8 or float8_e8m0fnu scales of one byte for 32 elements)."""
     import torch
-    named = _weights(param, grad, master)
+    pd, gd = _weights(param, grad, master)
     n = param.numel()
     blocks = (n + MUON_ADAMW8_BLOCK - 1) // MUON_ADAMW8_BLOCK
-    names = ("exp_avg", "exp_avg_scale", "exp_avg_sq", "exp_avg_sq_scale")
     if len(state) != 4:
         raise ValueError("state must hold exp_avg, exp_avg_scale, exp_avg_sq and exp_avg_sq_scale")
-    for name, t in zip(names, state):
-        scale = name.endswith("scale")
-        allowed = (torch.uint8, torch.float8_e8m0fnu if scale else torch.float8_e4m3fn)
+    m, ms, v, vs = state
+    codes, scales = (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu)
+    for name, t, count, allowed in zip(_STATE_NAMES, state, (n, blocks, n, blocks), (codes, scales, codes, scales)):
         if t.dtype not in allowed:
             raise TypeError(f"{name} must be one of {allowed}, got {t.dtype}")
-        if not t.is_contiguous() or t.numel() != (blocks if scale else n):
-            raise ValueError(f"{name} must be contiguous, with {blocks if scale else n} elements")
-    pd, gd = _dtype_code(param), _dtype_code(grad)
-    dev = _on_one_gpu(named + list(zip(names, state)))
-    t = muon_adamw8_tensor(param.data_ptr(), master.data_ptr() if master is not None else None, grad.data_ptr(),
-                           state[0].data_ptr(), state[2].data_ptr(), state[1].data_ptr(), state[3].data_ptr(), n,
-                           pd, gd)
-    return _owning(t, dev, named + list(zip(names, state)))
+        if not t.is_contiguous() or t.numel() != count:
+            raise ValueError(f"{name} must be contiguous, with {count} elements")
+    tensors = (param, grad, m, ms, v, vs) if master is None else (param, grad, m, ms, v, vs, master)
+    dev = _gpu_index(_BYTE_NAMES, tensors)
+    t = muon_adamw8_tensor(param.data_ptr(), None if master is None else master.data_ptr(), grad.data_ptr(),
+                           m.data_ptr(), v.data_ptr(), ms.data_ptr(), vs.data_ptr(), n, pd, gd)
+    return _owning(t, dev, tensors)
 
 
 def grad(t):
@@ -595,6 +611,5 @@ def grad(t):
     if not t.is_contiguous():
         raise ValueError("a gradient must be contiguous")
     code = _dtype_code(t)
-    named = [("grad", t)]
-    dev = _on_one_gpu(named)
-    return _owning(muon_grad(t.data_ptr(), t.numel(), code, 0), dev, named)
+    dev = _gpu_index(("grad",), (t,))
+    return _owning(muon_grad(t.data_ptr(), t.numel(), code, 0), dev, (t,))
