@@ -371,8 +371,9 @@ muon_status muon_adamw_mixed_step(muon_context *ctx, const muon_adamw_mixed_tens
  *   p <- (1 - lr wd) p - (lr / (1 - b1^step)) m1 / (sqrt(v1 / (1 - b2^step)) + eps)
  * in fp32 within 2^-20 of the update's and 2^-22 of p's magnitude (1 / (1 -
  * b2^step) as a factor, square root and reciprocal within 1 ulp; v1 / (1 -
- * b2^step) of 2^104 or more counts as infinite; eps must be 0 or at least
- * 2^-126).  The moments are then coded block by block:
+ * b2^step) of 2^104 or more counts as infinite, and so does lr / (1 - b1^step)
+ * over the denominator from 2^128 on; eps must be 0 or at least 2^-126).  The
+ * moments are then coded block by block:
  *   e     the smallest exponent byte, 17 at least, with |x| 2^(127-e) <= 448
  *         for every value x of the block; y = x 2^(127-e)
  *   v1    a value below 2^-9 counts as y = 2^-9 (the smallest code above zero)
@@ -403,9 +404,9 @@ muon_status muon_adamw8_step(muon_context *ctx, const muon_adamw8_tensor *ts, in
  *           norm is infinite or NaN (a step that reads it then writes NaN
  *           everywhere).
  * norm and factor are device memory outside every gradient; no gradient is
- * written, and one that is listed twice counts twice.  The sums pass through memory of the context: as for every entry
- * point, calls on one context (and replays of graphs that captured it) must be
- * ordered. */
+ * written, and one that is listed twice counts twice.  The sums pass through
+ * memory of the context: as for every entry point, calls on one context (and
+ * replays of graphs that captured it) must be ordered. */
 muon_status muon_grad_norm(muon_context *ctx, const muon_grad *gs, int64_t count, double max_norm, double *norm,
                            float *factor, void *hip_stream);
 

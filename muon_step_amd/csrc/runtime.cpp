@@ -1844,7 +1844,7 @@ muon_status muon_grad_norm(muon_context *ctx, const muon_grad *gs, int64_t count
             for (; n < muon::kNormTensors; ++n) t.first[n] = 0xffffffffu;
             while (i < count && gs[i].numel == 0) ++i;  // nothing is left behind the last table
             const bool last = i >= count;
-            const hipError_t e = timed(ctx, ST_GRAD_NORM, bytes, bytes, st, [&] {
+            const hipError_t e = timed(ctx, ST_GRAD_NORM, 0.0, bytes, st, [&] {
                 return muon::launch_grad_norm(t, static_cast<uint32_t>(chunks), call, last, st);
             });
             if (e != hipSuccess) return hip_fail(ctx, e, "gradient norm launch");

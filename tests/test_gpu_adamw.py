@@ -457,6 +457,38 @@ def test_grad_norm_large(ctx, torch, ms):
     assert norm == math.sqrt(n * 0.25)   # every partial sum is exact
 
 
+def test_grad_norm_many_tables(torch, ms):
+    """More tensors than the sums' memory holds tables of, eager and captured: the sums are joined on the way, and the
+    last, small table joins what is left.  Multiples of 1/8 below 2^7, so every partial sum is exact."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(33)
+    x = torch.randint(-500, 501, (32768,), generator=gen, device="cuda") / 8.0      # four chunks
+    last = torch.full((3,), 2.0, device="cuda")
+    count = 17 * 256 + 2
+    ctxs = ms.Context(0), ms.Context(0)
+    try:
+        grads = ms.table([ms.grad(x)] * count + [ms.grad(last)])
+
+        def expected():
+            return math.sqrt(count * float((x.double() ** 2).sum()) + float((last.double() ** 2).sum()))
+
+        assert _norm(torch, ctxs[0], ms, grads)[0] == expected()
+        norm, factor = torch.zeros(1, dtype=torch.float64, device="cuda"), torch.zeros(1, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            ctxs[1].muon_grad_norm(grads, 1.0, norm, factor, torch.cuda.current_stream())
+        for k in range(3):
+            x.mul_(0.5)
+            graph.replay()
+            eager = _norm(torch, ctxs[0], ms, grads)
+            assert (float(norm), np.float32(float(factor))) == eager and eager[0] == expected(), f"replay {k}"
+    finally:
+        torch.cuda.synchronize()
+        for c in ctxs:
+            c.close()
+
+
 # -------------------------------------------------------------------------------- muon_step with the clip factor
 
 @pytest.mark.parametrize("shift", [0, 1])
