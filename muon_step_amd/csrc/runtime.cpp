@@ -247,9 +247,11 @@ muon_status check_list(const void *ts, int64_t count, char *msg, size_t cap) {
 }
 
 // The memory of a call's tensors.  add() takes one kind after the other (every
-// param, every grad, ...): buffers that a program allocated in order, or views
-// of one flat buffer, then form few ascending runs, which overlap() merges in
-// few passes where a sort would take one for each doubling.
+// param, every grad, ...).  Views of flat buffers, one buffer for each kind, are
+// told apart by where each kind begins and ends, which spares the call
+// the list of all ranges (55 tensors: 0.6 us instead of 1.6).  Otherwise
+// overlap() merges the ascending runs that buffers allocated in order form, in
+// few passes where a sort would take one for each doubling (2.6 us).
 struct Range {
     uintptr_t lo, hi;
     uint32_t owner;
@@ -257,28 +259,43 @@ struct Range {
     bool writable;
 };
 struct Ranges {
-    std::vector<Range> all, spare;
-    std::vector<const char *> kinds;
+    static constexpr int kKinds = 8;
+    std::vector<Range> all, spare;  // filled where listing
+    struct Kind {
+        const char *name;
+        uintptr_t lo, hi;  // of all its ranges
+    } kinds[kKinds];
+    int n_kinds = 0;
+    bool listing, apart = true;  // apart: no two ranges so far share memory, as far as their kinds tell
     char *msg;
     size_t cap;
-    Ranges(char *m, size_t c) : msg(m), cap(c) {}
+    Ranges(bool list, int64_t most, char *m, size_t c) : listing(list), msg(m), cap(c) {
+        if (list) all.reserve(static_cast<size_t>(most));
+    }
 
     // at(i): address, elements and element size of tensor i's memory of this
     // kind (no elements: none).  False: refused, with the message written.
-    template <class At> bool add(const char *kind, bool writable, int64_t count, At at) {
-        kinds.push_back(kind);
-        const uint8_t k = static_cast<uint8_t>(kinds.size() - 1);
+    template <class At> bool add(const char *name, bool writable, int64_t count, At at) {
+        if (!listing && !apart) return true;  // the listing comes next
+        Kind k{name, 0, 0};
         for (int64_t i = 0; i < count; ++i) {
             const Memory m = at(i);
             if (m.n == 0) continue;
             const uintptr_t lo = reinterpret_cast<uintptr_t>(m.p);
             if (!m.p || lo % m.size != 0) {
                 set_msg(msg, cap, m.p ? "tensor %lld: %s is not aligned to its elements" : "tensor %lld: %s is NULL",
-                        (long long)i, kind);
+                        (long long)i, name);
                 return false;
             }
-            all.push_back(Range{lo, lo + static_cast<uintptr_t>(m.n) * m.size, static_cast<uint32_t>(i), k, writable});
+            const uintptr_t hi = lo + static_cast<uintptr_t>(m.n) * m.size;
+            if (listing)
+                all.push_back(Range{lo, hi, static_cast<uint32_t>(i), static_cast<uint8_t>(n_kinds), writable});
+            apart &= lo >= k.hi;
+            if (k.hi == 0) k.lo = lo;
+            k.hi = hi;
         }
+        for (int j = 0; j < n_kinds; ++j) apart &= k.lo >= kinds[j].hi || kinds[j].lo >= k.hi;
+        kinds[n_kinds++] = k;
         return true;
     }
     struct Memory {
@@ -314,7 +331,7 @@ struct Ranges {
             const Range *hit = r.writable ? top : top_w;
             if (hit && r.lo < hit->hi) {
                 set_msg(msg, cap, "memory of tensor %lld %s overlaps tensor %lld %s", (long long)hit->owner,
-                        kinds[hit->kind], (long long)r.owner, kinds[r.kind]);
+                        kinds[hit->kind].name, (long long)r.owner, kinds[r.kind].name);
                 return MUON_ERR_INVALID_ARGUMENT;
             }
             if (!top || r.hi > top->hi) top = &r;
@@ -323,6 +340,16 @@ struct Ranges {
         return MUON_OK;
     }
 };
+
+// INVALID_ARGUMENT where memory that `each` adds is missing, misaligned, or
+// written and shared; most: its ranges at most.
+template <class Each> muon_status check_memory(int64_t most, char *msg, size_t cap, Each each) {
+    Ranges quick(false, 0, msg, cap);
+    if (!each(quick)) return MUON_ERR_INVALID_ARGUMENT;
+    if (quick.apart) return MUON_OK;
+    Ranges r(true, most, msg, cap);
+    return each(r) ? r.overlap() : MUON_ERR_INVALID_ARGUMENT;
+}
 
 // numel, dtypes and master of one tensor of a step over mixed types.
 template <class T> muon_status check_mixed_tensor(const T &t, int64_t i, char *msg, size_t cap) {
@@ -357,13 +384,11 @@ muon_status check_adamw_mixed(const muon_adamw_mixed_tensor *ts, int64_t count, 
     for (int64_t i = 0; i < count; ++i)
         if ((s = check_mixed_tensor(ts[i], i, msg, cap)) != MUON_OK) return s;
     using M = Ranges::Memory;
-    Ranges r(msg, cap);
-    r.all.reserve(static_cast<size_t>(count) * 5 + 1);
-    if (!add_weights(r, ts, count, factor) ||
-        !r.add("exp_avg", true, count, [&](int64_t i) { return M{ts[i].exp_avg, ts[i].numel, 4}; }) ||
-        !r.add("exp_avg_sq", true, count, [&](int64_t i) { return M{ts[i].exp_avg_sq, ts[i].numel, 4}; }))
-        return MUON_ERR_INVALID_ARGUMENT;
-    return r.overlap();
+    return check_memory(count * 5 + 1, msg, cap, [&](Ranges &r) {
+        return add_weights(r, ts, count, factor) &&
+               r.add("exp_avg", true, count, [&](int64_t i) { return M{ts[i].exp_avg, ts[i].numel, 4}; }) &&
+               r.add("exp_avg_sq", true, count, [&](int64_t i) { return M{ts[i].exp_avg_sq, ts[i].numel, 4}; });
+    });
 }
 
 int64_t byte_blocks(int64_t numel) { return (numel + MUON_ADAMW8_BLOCK - 1) / MUON_ADAMW8_BLOCK; }
@@ -381,16 +406,15 @@ muon_status check_adamw8(const muon_adamw8_tensor *ts, int64_t count, const muon
     for (int64_t i = 0; i < count; ++i)
         if ((s = check_mixed_tensor(ts[i], i, msg, cap)) != MUON_OK) return s;
     using M = Ranges::Memory;
-    Ranges r(msg, cap);
-    r.all.reserve(static_cast<size_t>(count) * 7 + 1);
-    if (!add_weights(r, ts, count, factor) ||
-        !r.add("exp_avg", true, count, [&](int64_t i) { return M{ts[i].exp_avg, ts[i].numel, 1}; }) ||
-        !r.add("exp_avg_sq", true, count, [&](int64_t i) { return M{ts[i].exp_avg_sq, ts[i].numel, 1}; }) ||
-        !r.add("exp_avg_scale", true, count, [&](int64_t i) { return M{ts[i].exp_avg_scale, byte_blocks(ts[i].numel), 1}; }) ||
-        !r.add("exp_avg_sq_scale", true, count,
-               [&](int64_t i) { return M{ts[i].exp_avg_sq_scale, byte_blocks(ts[i].numel), 1}; }))
-        return MUON_ERR_INVALID_ARGUMENT;
-    return r.overlap();
+    return check_memory(count * 7 + 1, msg, cap, [&](Ranges &r) {
+        return add_weights(r, ts, count, factor) &&
+               r.add("exp_avg", true, count, [&](int64_t i) { return M{ts[i].exp_avg, ts[i].numel, 1}; }) &&
+               r.add("exp_avg_sq", true, count, [&](int64_t i) { return M{ts[i].exp_avg_sq, ts[i].numel, 1}; }) &&
+               r.add("exp_avg_scale", true, count,
+                     [&](int64_t i) { return M{ts[i].exp_avg_scale, byte_blocks(ts[i].numel), 1}; }) &&
+               r.add("exp_avg_sq_scale", true, count,
+                     [&](int64_t i) { return M{ts[i].exp_avg_sq_scale, byte_blocks(ts[i].numel), 1}; });
+    });
 }
 
 muon_status check_grad_norm(const muon_grad *gs, int64_t count, double max_norm, const double *norm,
@@ -1403,11 +1427,19 @@ muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage,
         const double p = dtype_size(x.param_dtype), g = dtype_size(x.grad_dtype);
         return static_cast<double>(x.numel) * (moment_bytes + g + (x.master ? 8.0 + p : 2.0 * p));
     };
+    auto kind_of = [](const T &x) {
+        return (x.param_dtype == MUON_BF16 ? 1 : 0) | (x.master ? 2 : 0) | (x.grad_dtype == MUON_BF16 ? 4 : 0);
+    };
     double total = 0;
-    for (int64_t i = 0; i < count; ++i) total += bytes_of(ts[i]);
+    unsigned kinds = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        total += bytes_of(ts[i]);
+        if (ts[i].numel > 0) kinds |= 1u << kind_of(ts[i]);
+    }
     const bool paced = total > kPacedBytes;
     Table t;
     for (int kind = 0; kind < 8; ++kind) {
+        if (!(kinds >> kind & 1)) continue;
         const muon::AdamwTypes y{(kind & 1) != 0, (kind & 2) != 0, (kind & 4) != 0};
         int n = 0;
         int64_t blocks = 0;
@@ -1424,9 +1456,7 @@ muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage,
         };
         for (int64_t i = 0; i < count; ++i) {
             const T &x = ts[i];
-            if (x.numel == 0 || y.param_bf16 != (x.param_dtype == MUON_BF16) || y.master != (x.master != nullptr) ||
-                y.grad_bf16 != (x.grad_dtype == MUON_BF16))
-                continue;
+            if (x.numel == 0 || kind_of(x) != kind) continue;
             const int64_t nb = blocks_of(x.numel, y);
             if (n == N || blocks + nb >= (int64_t(1) << 31)) {
                 const hipError_t e = flush();
