@@ -575,7 +575,7 @@ def adamw8_moments(state):
         e = scale.view(torch.uint8).int()
         s = torch.where(e == 255, float("nan"), (e << 23).clamp(min=1 << 22).view(torch.float32))  # 2^(e - 127)
         s = s.repeat_interleave(MUON_ADAMW8_BLOCK)[:codes.numel()]
-        out.append(codes.float() * s.view(codes.shape))
+        out.append(codes.view(torch.float8_e4m3fn).float() * s.view(codes.shape))
     return tuple(out)
 
 
