@@ -235,7 +235,11 @@ typedef struct muon_grad {
 
 typedef struct muon_context muon_context; /* opaque */
 
-/* ABI version of the loaded library (MUON_STEP_ABI_VERSION it was built with). */
+/* ABI version of the loaded library (MUON_STEP_ABI_VERSION it was built with).
+ * A caller compares it with its own before the first call: the structures of
+ * two versions differ.  Zero a structure before its fields are set (= {0}):
+ * fields that a later version adds then hold their "none" (muon_hparams has
+ * grad_factor since version 5). */
 int32_t muon_abi_version(void);
 
 /* Static, never-NULL description of a status code. */

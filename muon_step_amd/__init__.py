@@ -15,6 +15,8 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmuon_step.so")
 
+MUON_STEP_ABI_VERSION = 5  # of the header that the structures below mirror
+
 MUON_OK = 0
 MUON_ERR_INVALID_ARGUMENT = 1
 MUON_ERR_UNSUPPORTED = 2
@@ -108,7 +110,7 @@ _lib = None
 
 
 def load(path=LIB_PATH):
-    """Loads libmuon_step.so and declares its signatures.  Raises if missing."""
+    """Loads libmuon_step.so and declares its signatures.  Raises if it is missing or of another ABI version."""
     global _lib
     if _lib is not None:
         return _lib
@@ -116,6 +118,10 @@ def load(path=LIB_PATH):
         raise ImportError(f"{path} is not built; run `python -m muon_step_amd.build` "
                           "(or __graft_entry__.build()) first")
     lib = ctypes.CDLL(path)
+    version = lib.muon_abi_version()  # before any structure is passed: another version lays them out differently
+    if version != MUON_STEP_ABI_VERSION:
+        raise ImportError(f"{path} has ABI version {version}, this package needs {MUON_STEP_ABI_VERSION}; build it "
+                          "again with `python -m muon_step_amd.build`")
     c = ctypes
     vp, i32, i64, sz = c.c_void_p, c.c_int32, c.c_int64, c.c_size_t
     sig = {

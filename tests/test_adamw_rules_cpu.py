@@ -1,6 +1,10 @@
 """Calls of the mixed-type AdamW steps, the gradient norm and the clip factor that their documentation allows or rules
 out, where one was once answered wrongly; needs no GPU."""
 
+import os
+import re
+import subprocess
+
 import numpy as np
 import pytest
 
@@ -22,3 +26,22 @@ def test_moments_of_every_type_a_state_may_have(codes, scales):
         ref = oracle.moment_values(c, e).astype(np.float32)
     for x in ms.adamw8_moments(state):
         assert x.dtype == torch.float32 and np.array_equal(x.numpy(), ref, equal_nan=True)
+
+
+def test_load_refuses_another_abi(tmp_path, monkeypatch):
+    """A library built from another version of the header lays its structures out differently: it is not loaded."""
+    src = tmp_path / "old.c"
+    src.write_text("int muon_abi_version(void) { return 4; }\n")
+    so = str(tmp_path / "old.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", so], check=True)
+    monkeypatch.setattr(ms, "_lib", None)
+    with pytest.raises(ImportError, match=r"ABI version 4.*needs 5"):
+        ms.load(so)
+    assert ms._lib is None
+
+
+def test_abi_version_is_the_headers():
+    """The version that load() asks for is the one of the header that the structures mirror."""
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "muon_step.h")
+    m = re.search(r"#define MUON_STEP_ABI_VERSION (\d+)", open(header).read())
+    assert ms.MUON_STEP_ABI_VERSION == int(m.group(1))
