@@ -361,7 +361,7 @@ template <class T> muon_status check_mixed_tensor(const T &t, int64_t i, char *m
         set_msg(msg, cap, "tensor %lld: unknown dtype", (long long)i);
         return MUON_ERR_INVALID_ARGUMENT;
     }
-    if (t.master && t.param_dtype != MUON_BF16) {
+    if (t.numel > 0 && t.master && t.param_dtype != MUON_BF16) {
         set_msg(msg, cap, "tensor %lld: a master copy goes with bf16 param only", (long long)i);
         return MUON_ERR_INVALID_ARGUMENT;
     }

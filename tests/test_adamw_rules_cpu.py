@@ -1,6 +1,7 @@
 """Calls of the mixed-type AdamW steps, the gradient norm and the clip factor that their documentation allows or rules
 out, where one was once answered wrongly; needs no GPU."""
 
+import ctypes
 import os
 import re
 import subprocess
@@ -45,3 +46,22 @@ def test_abi_version_is_the_headers():
     header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "muon_step.h")
     m = re.search(r"#define MUON_STEP_ABI_VERSION (\d+)", open(header).read())
     assert ms.MUON_STEP_ABI_VERSION == int(m.group(1))
+
+
+def _status(fn, ts, *args):
+    arr = (type(ts[0]) * len(ts))(*ts)
+    buf = ctypes.create_string_buffer(512)
+    return fn(arr, len(ts), *args, buf, 512), buf.value.decode()
+
+
+@pytest.mark.parametrize("kind", [ms.muon_adamw_mixed_tensor, ms.muon_adamw8_tensor])
+@pytest.mark.parametrize("dtype", [ms.MUON_F32, ms.MUON_BF16])
+def test_pointers_of_an_empty_tensor_are_not_looked_at(kind, dtype):
+    """Not the master copy's either, whatever the weights' type; a tensor with elements is refused as before."""
+    lib = ms.load()
+    fn = lib.muon_check_adamw_mixed_args if kind is ms.muon_adamw_mixed_tensor else lib.muon_check_adamw8_args
+    hp = ms.adamw_hparams()
+    t = kind(param=3, master=5, grad=7, exp_avg=9, exp_avg_sq=11, numel=0, param_dtype=dtype, grad_dtype=ms.MUON_F32)
+    assert _status(fn, [t], ctypes.byref(hp), None) == (ms.MUON_OK, "")
+    t.numel = 1
+    assert _status(fn, [t], ctypes.byref(hp), None)[0] == ms.MUON_ERR_INVALID_ARGUMENT
