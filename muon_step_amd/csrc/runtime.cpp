@@ -57,9 +57,18 @@ bool finite(double v) { return std::isfinite(v); }
 struct Interval {
     uintptr_t lo, hi;
     bool writable;
-    int64_t owner;
+    int64_t owner;  // kNoOwner: of the call, not of one of its items
     const char *what;
 };
+constexpr int64_t kNoOwner = -1;
+
+// How messages name memory: "matrix 3 param", or "grad_factor" where it has no owner.
+std::string memory_name(const char *items, int64_t owner, const char *what) {
+    return owner == kNoOwner ? std::string(what) : std::string(items) + " " + std::to_string(owner) + " " + what;
+}
+void set_overlap_msg(char *msg, size_t cap, const std::string &a, const std::string &b) {
+    set_msg(msg, cap, "memory of %s overlaps %s", a.c_str(), b.c_str());
+}
 
 // Returns the index pair of the first conflicting overlap (a writable range
 // overlapping any other range), or false.
@@ -158,12 +167,11 @@ muon_status check_step(const muon_matrix *mats, int64_t count, const muon_hparam
     }
     if (hp->grad_factor) {
         const uintptr_t lo = reinterpret_cast<uintptr_t>(hp->grad_factor);
-        iv.push_back(Interval{lo, lo + 4, false, -1, "grad_factor"});
+        iv.push_back(Interval{lo, lo + 4, false, kNoOwner, "grad_factor"});
     }
     const Interval *a = nullptr, *b = nullptr;
     if (find_overlap(iv, &a, &b)) {
-        set_msg(msg, cap, "memory of matrix %lld %s overlaps matrix %lld %s", (long long)a->owner, a->what,
-                (long long)b->owner, b->what);
+        set_overlap_msg(msg, cap, memory_name("matrix", a->owner, a->what), memory_name("matrix", b->owner, b->what));
         return MUON_ERR_INVALID_ARGUMENT;
     }
     return MUON_OK;
@@ -213,8 +221,7 @@ muon_status check_adamw(const muon_adamw_tensor *ts, int64_t count, const muon_a
     }
     const Interval *a = nullptr, *b = nullptr;
     if (find_overlap(iv, &a, &b)) {
-        set_msg(msg, cap, "memory of tensor %lld %s overlaps tensor %lld %s", (long long)a->owner, a->what,
-                (long long)b->owner, b->what);
+        set_overlap_msg(msg, cap, memory_name("tensor", a->owner, a->what), memory_name("tensor", b->owner, b->what));
         return MUON_ERR_INVALID_ARGUMENT;
     }
     return MUON_OK;
@@ -264,6 +271,7 @@ struct Ranges {
     struct Kind {
         const char *name;
         uintptr_t lo, hi;  // of all its ranges
+        bool of_tensors;   // not of the call
     } kinds[kKinds];
     int n_kinds = 0;
     bool listing, apart = true;  // apart: no two ranges so far share memory, as far as their kinds tell
@@ -275,9 +283,9 @@ struct Ranges {
 
     // at(i): address, elements and element size of tensor i's memory of this
     // kind (no elements: none).  False: refused, with the message written.
-    template <class At> bool add(const char *name, bool writable, int64_t count, At at) {
+    template <class At> bool add(const char *name, bool writable, int64_t count, At at, bool of_tensors = true) {
         if (!listing && !apart) return true;  // the listing comes next
-        Kind k{name, 0, 0};
+        Kind k{name, 0, 0, of_tensors};
         for (int64_t i = 0; i < count; ++i) {
             const Memory m = at(i);
             if (m.n == 0) continue;
@@ -323,6 +331,11 @@ struct Ranges {
         }
     }
 
+    std::string name_of(const Range &r) const {
+        const Kind &k = kinds[r.kind];
+        return memory_name("tensor", k.of_tensors ? static_cast<int64_t>(r.owner) : kNoOwner, k.name);
+    }
+
     // INVALID_ARGUMENT where a written range overlaps any other.
     muon_status overlap() {
         sort();
@@ -330,8 +343,7 @@ struct Ranges {
         for (const Range &r : all) {
             const Range *hit = r.writable ? top : top_w;
             if (hit && r.lo < hit->hi) {
-                set_msg(msg, cap, "memory of tensor %lld %s overlaps tensor %lld %s", (long long)hit->owner,
-                        kinds[hit->kind].name, (long long)r.owner, kinds[r.kind].name);
+                set_overlap_msg(msg, cap, name_of(*hit), name_of(r));
                 return MUON_ERR_INVALID_ARGUMENT;
             }
             if (!top || r.hi > top->hi) top = &r;
@@ -373,7 +385,7 @@ template <class T> bool add_weights(Ranges &r, const T *ts, int64_t count, const
     return r.add("param", true, count, [&](int64_t i) { return M{ts[i].param, ts[i].numel, dtype_size(ts[i].param_dtype)}; }) &&
            r.add("master", true, count, [&](int64_t i) { return M{ts[i].master, ts[i].master ? ts[i].numel : 0, 4}; }) &&
            r.add("grad", false, count, [&](int64_t i) { return M{ts[i].grad, ts[i].numel, dtype_size(ts[i].grad_dtype)}; }) &&
-           r.add("grad_factor", false, factor ? 1 : 0, [&](int64_t) { return M{factor, 1, 4}; });
+           r.add("grad_factor", false, factor ? 1 : 0, [&](int64_t) { return M{factor, 1, 4}; }, false);
 }
 
 muon_status check_adamw_mixed(const muon_adamw_mixed_tensor *ts, int64_t count, const muon_adamw_hparams *hp,

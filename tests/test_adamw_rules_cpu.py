@@ -65,3 +65,36 @@ def test_pointers_of_an_empty_tensor_are_not_looked_at(kind, dtype):
     assert _status(fn, [t], ctypes.byref(hp), None) == (ms.MUON_OK, "")
     t.numel = 1
     assert _status(fn, [t], ctypes.byref(hp), None)[0] == ms.MUON_ERR_INVALID_ARGUMENT
+
+
+def test_overlap_messages_name_the_factor():
+    """The clip factor belongs to no matrix or tensor: the message names it without a number."""
+    lib = ms.load()
+    base = 1 << 40
+    mats = [ms.muon_matrix(base + (i << 36), base + (i << 36) + (1 << 30), base + (i << 36) + (2 << 30), None, 64, 128,
+                           ms.MUON_BF16, ms.MUON_BF16) for i in range(2)]
+    hp = ms.make_hparams()
+    for at, what in ((mats[1].momentum + 16, "matrix 1 momentum"), (mats[1].param, "matrix 1 param"),
+                     (mats[0].momentum + 4 * 64 * 128 - 4, "matrix 0 momentum")):
+        hp.grad_factor = at
+        st, msg = _status(lib.muon_check_step_args, mats, ctypes.byref(hp))
+        assert st == ms.MUON_ERR_INVALID_ARGUMENT
+        assert msg in (f"memory of {what} overlaps grad_factor", f"memory of grad_factor overlaps {what}")
+    mats[1].param = mats[0].momentum
+    hp.grad_factor = None
+    st, msg = _status(lib.muon_check_step_args, mats, ctypes.byref(hp))
+    assert st == ms.MUON_ERR_INVALID_ARGUMENT
+    assert sorted(msg[len("memory of "):].split(" overlaps ")) == ["matrix 0 momentum", "matrix 1 param"]
+
+    def tensor(kind, i):
+        names = [f for f, t in kind._fields_ if t is ctypes.c_void_p and f != "master"]
+        at = {f: base + (i << 36) + (k << 20) for k, f in enumerate(names)}
+        return kind(**at, numel=1000, param_dtype=ms.MUON_F32, grad_dtype=ms.MUON_F32)
+
+    for kind, fn in ((ms.muon_adamw_mixed_tensor, lib.muon_check_adamw_mixed_args),
+                     (ms.muon_adamw8_tensor, lib.muon_check_adamw8_args)):
+        ts = [tensor(kind, i) for i in range(3)]
+        st, msg = _status(fn, ts, ctypes.byref(ms.adamw_hparams()), ts[2].exp_avg_sq + 4)
+        assert st == ms.MUON_ERR_INVALID_ARGUMENT
+        assert msg in ("memory of tensor 2 exp_avg_sq overlaps grad_factor",
+                       "memory of grad_factor overlaps tensor 2 exp_avg_sq")
