@@ -186,12 +186,12 @@ def moe16b_step(args):
                            torch.zeros_like(p)))
     if args.adamw8:
         tensors = ms.table(ms.adamw8_tensor(p, g, ms.adamw8_state(p)) for p, g, _, _ in adamw_bufs)
-    elif args.clip_norm:
+    elif args.clip_norm is not None:
         tensors = ms.table(ms.adamw_mixed_tensor(*b) for b in adamw_bufs)
     else:
         tensors = [ms.adamw_tensor(*b) for b in adamw_bufs]
     norm, factor, all_grads = None, None, None
-    if args.clip_norm:
+    if args.clip_norm is not None:
         norm = torch.zeros(1, dtype=torch.float64, device="cuda")
         factor = torch.ones(1, device="cuda")
         all_grads = ms.table([ms.grad(g) for g in grads] + [ms.grad(b[1]) for b in adamw_bufs])
@@ -202,13 +202,13 @@ def moe16b_step(args):
     stream = torch.cuda.current_stream()
 
     def step(i):
-        if args.clip_norm:
+        if args.clip_norm is not None:
             ctx.muon_grad_norm(all_grads, args.clip_norm, norm, factor, stream)
         ctx.muon_step(mats, hp, stream)
         ahp = ms.adamw_hparams(step=i + 1)
         if args.adamw8:
             ctx.muon_adamw8_step(tensors, ahp, seed=5, grad_factor=factor, stream=stream)
-        elif args.clip_norm:
+        elif args.clip_norm is not None:
             ctx.muon_adamw_mixed_step(tensors, ahp, grad_factor=factor, stream=stream)
         else:
             ctx.muon_adamw_step(tensors, ahp, stream)
@@ -384,6 +384,10 @@ def main():
     ap.add_argument("--hbm-probe", action="store_true",
                     help="only time the library's streaming probe at the elementwise kernels' read:write mixes")
     args = ap.parse_args()
+    if args.workload != "moe16b" and (args.clip_norm is not None or args.adamw8):
+        ap.error("--clip-norm and --adamw8 go with --workload moe16b")
+    if args.clip_norm is not None and not args.clip_norm > 0:
+        ap.error("--clip-norm must be positive")
     if args.copy_calibration:
         copy_calibration()
         return

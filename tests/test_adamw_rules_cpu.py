@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -98,3 +99,17 @@ def test_overlap_messages_name_the_factor():
         assert st == ms.MUON_ERR_INVALID_ARGUMENT
         assert msg in ("memory of tensor 2 exp_avg_sq overlaps grad_factor",
                        "memory of grad_factor overlaps tensor 2 exp_avg_sq")
+
+
+@pytest.mark.parametrize("args", [["--workload", "moe16b", "--clip-norm", "0"],
+                                  ["--workload", "moe16b", "--clip-norm", "-1"],
+                                  ["--workload", "moe16b", "--clip-norm", "nan"],
+                                  ["--clip-norm", "1"], ["--adamw8"],
+                                  ["--workload", "dense_block_bf16", "--clip-norm", "1"]])
+def test_bench_refuses_options_that_would_do_nothing(args):
+    """A norm that the library refuses, and options of another workload, end the run before it starts."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, os.path.join(root, "bench.py"), *args], capture_output=True, text=True,
+                         timeout=100)
+    assert res.returncode == 2 and res.stdout == ""
+    assert "--clip-norm" in res.stderr.splitlines()[-1] or "--adamw8" in res.stderr.splitlines()[-1]
