@@ -374,10 +374,11 @@ muon_status muon_adamw_mixed_step(muon_context *ctx, const muon_adamw_mixed_tens
  * and from them, before they are coded,
  *   p <- (1 - lr wd) p - (lr / (1 - b1^step)) m1 / (sqrt(v1 / (1 - b2^step)) + eps)
  * in fp32 within 2^-20 of the update's and 2^-22 of p's magnitude (1 / (1 -
- * b2^step) as a factor, square root and reciprocal within 1 ulp; v1 / (1 -
- * b2^step) of 2^104 or more counts as infinite, and so does lr / (1 - b1^step)
- * over the denominator from 2^128 on; eps must be 0 or at least 2^-126).  The
- * moments are then coded block by block:
+ * b2^step) as a factor, square root and reciprocal within 1 ulp).  v1 / (1 -
+ * b2^step) past fp32's largest value is infinite, as in the step above.  lr /
+ * (1 - b1^step) over the denominator is infinite from 2^128 on, and below
+ * 2^-126 its last bits are lost, all of them at worst.  eps must be 0 or at
+ * least 2^-126.  The moments are then coded block by block:
  *   e     the smallest exponent byte, 17 at least, with |x| 2^(127-e) <= 448
  *         for every value x of the block; y = x 2^(127-e)
  *   v1    a value below 2^-9 counts as y = 2^-9 (the smallest code above zero)

@@ -297,8 +297,22 @@ template <int V> __device__ __forceinline__ void store_first_codes(uint8_t *p, i
         if (q < n) *as_global(p + q) = static_cast<uint8_t>(w[q >> 2] >> (8 * (q & 3)));
 }
 
+constexpr float kSmallEps = 0x1p-38f;
+
+// sqrt(v / (1 - b2^step)) + eps.  v_sqrt_f32 takes subnormal values, whose roots
+// are below 2^-63, for zero: against kSmallEps that is less than 2^-25 of
+// the sum.  SMALL_EPS: under a smaller eps values below 2^-96 are lifted by 2^32.
+// It has kernels of its own: a branch on eps in one kernel costs bf16 weights and
+// gradients 1 to 2% (210e6 elements 328 to 331 and 335 us, by how it is placed).
+template <bool SMALL_EPS> __device__ __forceinline__ float denominator(const Adamw8Scalars &k, float v) {
+    if constexpr (!SMALL_EPS) return __builtin_amdgcn_sqrtf(v * k.inv_bias_corr2) + k.eps;
+    const bool low = v < 0x1p-96f;
+    const float root = __builtin_amdgcn_sqrtf(v * (low ? 0x1p32f * k.inv_bias_corr2 : k.inv_bias_corr2));
+    return __builtin_fmaf(root, low ? 0x1p-16f : 1.0f, k.eps);
+}
+
 // The step on the V elements from `i0` of their tensor on.
-template <int V>
+template <int V, bool SMALL_EPS>
 __device__ __forceinline__ void adamw8_lane(const Adamw8Scalars &k, const float *factor, int64_t i0, ByteLane<V> &x) {
     float m[V], v[V];
     decode<V>(x.m, scale_value(x.m_scale), m);
@@ -308,8 +322,7 @@ __device__ __forceinline__ void adamw8_lane(const Adamw8Scalars &k, const float 
     for (int q = 0; q < V; ++q) {
         m[q] = k.beta1 * m[q] + k.one_minus_beta1 * x.g[q];
         v[q] = k.beta2 * v[q] + (k.one_minus_beta2 * x.g[q]) * x.g[q];
-        // 2^24 v / (1 - b2^step): v_sqrt_f32 takes subnormal values for zero
-        const float den = __builtin_fmaf(__builtin_amdgcn_sqrtf(v[q] * k.scaled_inv_bias_corr2), 0x1p-12f, k.eps);
+        const float den = denominator<SMALL_EPS>(k, v[q]);
         // the moment comes in last: neither product leaves fp32's range before the result does
         x.p[q] = __builtin_fmaf(-k.lr_over_bias_corr1 * __builtin_amdgcn_rcpf(den), m[q], k.decay * x.p[q]);
     }
@@ -322,7 +335,7 @@ __device__ __forceinline__ void adamw8_lane(const Adamw8Scalars &k, const float 
     encode<true, 16>(v, hashed, x.v, x.v_scale);
 }
 
-template <typename ParamT, typename GradT, bool MASTER, bool PACED>
+template <typename ParamT, typename GradT, bool MASTER, bool PACED, bool SMALL_EPS>
 __global__ __launch_bounds__(kThreads) void adamw8_kernel(const ByteTable t, uint32_t block0, Adamw8Scalars k,
                                                           const float *factor) {
     constexpr int V = byte_vec<ParamT, GradT, MASTER>();
@@ -362,7 +375,7 @@ __global__ __launch_bounds__(kThreads) void adamw8_kernel(const ByteTable t, uin
         load_first_codes<V>(dm + i, n, x.m);
         load_first_codes<V>(dv + i, n, x.v);
     }
-    adamw8_lane<V>(k, factor, k0 + i, x);
+    adamw8_lane<V, SMALL_EPS>(k, factor, k0 + i, x);
     if (n >= V) {
         store_words<V / 4, 1>(dm + i, x.m);
         store_words<V / 4, 1>(dv + i, x.v);
@@ -418,17 +431,17 @@ hipError_t launch_mixed(const MixedTable &t, uint32_t blocks, const AdamwTypes &
                        : launch_table(adamw_mixed_kernel<uint16_t, float, false, PACED>, t, blocks, k, factor, st);
 }
 
-template <bool PACED>
+template <bool PACED, bool SMALL_EPS>
 hipError_t launch_bytes(const ByteTable &t, uint32_t blocks, const AdamwTypes &y, const Adamw8Scalars &k,
                         const float *factor, hipStream_t st) {
     if (!y.param_bf16)
-        return y.grad_bf16 ? launch_table(adamw8_kernel<float, uint16_t, false, PACED>, t, blocks, k, factor, st)
-                           : launch_table(adamw8_kernel<float, float, false, PACED>, t, blocks, k, factor, st);
+        return y.grad_bf16 ? launch_table(adamw8_kernel<float, uint16_t, false, PACED, SMALL_EPS>, t, blocks, k, factor, st)
+                           : launch_table(adamw8_kernel<float, float, false, PACED, SMALL_EPS>, t, blocks, k, factor, st);
     if (y.master)
-        return y.grad_bf16 ? launch_table(adamw8_kernel<uint16_t, uint16_t, true, PACED>, t, blocks, k, factor, st)
-                           : launch_table(adamw8_kernel<uint16_t, float, true, PACED>, t, blocks, k, factor, st);
-    return y.grad_bf16 ? launch_table(adamw8_kernel<uint16_t, uint16_t, false, PACED>, t, blocks, k, factor, st)
-                       : launch_table(adamw8_kernel<uint16_t, float, false, PACED>, t, blocks, k, factor, st);
+        return y.grad_bf16 ? launch_table(adamw8_kernel<uint16_t, uint16_t, true, PACED, SMALL_EPS>, t, blocks, k, factor, st)
+                           : launch_table(adamw8_kernel<uint16_t, float, true, PACED, SMALL_EPS>, t, blocks, k, factor, st);
+    return y.grad_bf16 ? launch_table(adamw8_kernel<uint16_t, uint16_t, false, PACED, SMALL_EPS>, t, blocks, k, factor, st)
+                       : launch_table(adamw8_kernel<uint16_t, float, false, PACED, SMALL_EPS>, t, blocks, k, factor, st);
 }
 
 }  // namespace
@@ -440,7 +453,11 @@ hipError_t launch_adamw_mixed(const MixedTable &t, uint32_t blocks, const AdamwT
 
 hipError_t launch_adamw8(const ByteTable &t, uint32_t blocks, const AdamwTypes &y, bool paced, const Adamw8Scalars &k,
                          const float *factor, hipStream_t st) {
-    return paced ? launch_bytes<true>(t, blocks, y, k, factor, st) : launch_bytes<false>(t, blocks, y, k, factor, st);
+    if (k.eps < kSmallEps)
+        return paced ? launch_bytes<true, true>(t, blocks, y, k, factor, st)
+                     : launch_bytes<false, true>(t, blocks, y, k, factor, st);
+    return paced ? launch_bytes<true, false>(t, blocks, y, k, factor, st)
+                 : launch_bytes<false, false>(t, blocks, y, k, factor, st);
 }
 
 // The rounding's key for one step: the seed and the step count, mixed.

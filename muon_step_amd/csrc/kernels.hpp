@@ -12,10 +12,10 @@ struct AdamwScalars {
     float decay, beta1, beta2, one_minus_beta1, one_minus_beta2, bias_corr1, bias_corr2, lr, eps;
 };
 
-// Scalars of the 8-bit step: the bias corrections folded into one factor each
-// (the second one times 2^24), and the key of its stochastic rounding (adamw8_key).
+// Scalars of the 8-bit step: the bias corrections folded into one factor each,
+// and the key of its stochastic rounding (adamw8_key).
 struct Adamw8Scalars {
-    float decay, beta1, beta2, one_minus_beta1, one_minus_beta2, lr_over_bias_corr1, scaled_inv_bias_corr2, eps;
+    float decay, beta1, beta2, one_minus_beta1, one_minus_beta2, lr_over_bias_corr1, inv_bias_corr2, eps;
     uint32_t key;
 };
 

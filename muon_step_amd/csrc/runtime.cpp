@@ -1838,7 +1838,7 @@ muon_status muon_adamw8_step(muon_context *ctx, const muon_adamw8_tensor *ts, in
         k.eps = a.eps;
         const double t = static_cast<double>(hp->step);
         k.lr_over_bias_corr1 = static_cast<float>(hp->lr / (1.0 - std::pow(hp->beta1, t)));
-        k.scaled_inv_bias_corr2 = static_cast<float>(0x1p24 / (1.0 - std::pow(hp->beta2, t)));
+        k.inv_bias_corr2 = static_cast<float>(1.0 / (1.0 - std::pow(hp->beta2, t)));
         k.key = muon::adamw8_key(seed, hp->step);
         auto fill = [](muon::ByteDesc &d, const muon_adamw8_tensor &t) {
             d = muon::ByteDesc{t.param,         t.master,          t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale,

@@ -110,7 +110,7 @@ def adamw8_step(p, g, state, lr, beta1, beta2, eps, weight_decay, step, seed=0, 
     v1 = (k["beta2"] * v) + ((k["one_minus_beta2"] * g) * g)
     m64, v64 = m1.astype(np.float64), v1.astype(np.float64)
     v_hat = v64 / (1 - beta2 ** step)
-    v_hat = np.where(v_hat >= 2.0 ** 104, np.inf, v_hat)
+    v_hat = np.where(np.isinf(v_hat.astype(np.float32)), np.inf, v_hat)  # as the quotient in float32, in both steps
     update = lr * (m64 / (1 - beta1 ** step)) / (np.sqrt(v_hat) + eps)
     p_new = (1 - lr * weight_decay) * np.asarray(p, dtype=np.float64) - update
     index = np.arange(g.size)

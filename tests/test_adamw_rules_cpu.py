@@ -113,3 +113,24 @@ def test_bench_refuses_options_that_would_do_nothing(args):
                          timeout=100)
     assert res.returncode == 2 and res.stdout == ""
     assert "--clip-norm" in res.stderr.splitlines()[-1] or "--adamw8" in res.stderr.splitlines()[-1]
+
+
+def test_oracle_8_bit_weights_are_those_of_the_32_bit_step():
+    """From the same moments the weights of the two steps differ by fp32 roundings alone, at second moments up to
+    fp32's largest value.  In units of 2^-24: the 32-bit step rounds v / (1 - b2^t) (halved by the root), the root, the
+    sum with eps, two quotients, the product with lr and three constants: at most 9 of the update; the decay's constant
+    and product and the difference: at most 3 of the larger weight."""
+    rng = np.random.default_rng(22)
+    n = 64 * 32
+    for step in (1, 3, 1000):
+        e = np.repeat(np.linspace(20, 240, 64).astype(np.uint8), 1)          # v from 2^-116 to past 2^120
+        state = (rng.integers(0, 127, n).astype(np.uint8), ((e.astype(int) + 127) // 2).astype(np.uint8),
+                 rng.integers(8, 127, n).astype(np.uint8), e)
+        m, v = (oracle.moment_values(c, s).astype(np.float32) for c, s in (state[:2], state[2:]))
+        p, g = rng.standard_normal(n).astype(np.float32), np.zeros(n, np.float32)
+        args = (0.02, 0.9, 0.95, 1e-8, 0.1, step)
+        with np.errstate(over="ignore"):
+            p32, m32, v32 = oracle.adamw_step_f32(p, g, m, v, *args)
+            p8, update, _ = oracle.adamw8_step(p, g, state, *args)
+        assert np.isfinite(v32).all() and v32.max() > 2.0 ** 120
+        assert (np.abs(p8 - p32) <= 2.0 ** -24 * (9 * np.abs(update) + 3 * np.maximum(np.abs(p), np.abs(p32)))).all()
