@@ -48,3 +48,90 @@ def test_adamw8_small_second_moments(ctx, torch, ms, eps):
     torch.cuda.synchronize()
     for c in cases:
         c.check(1, eps=eps, what=f"eps {eps}")
+
+
+SIZES = (1, 31, 32, 33, 64, 100, 255, 256, 1000, 1025, 4099)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("eight", [False, True])
+def test_nan_factor_adamw(ctx, torch, ms, eight, shift):
+    """The factor of a norm that is not finite leaves NaN in every weight and moment, partial blocks and gradients of
+    zero among them, and touches nothing else."""
+    rng = np.random.default_rng(53)
+
+    def change(p, g, m, v):
+        g[::3] = 0
+    cases = [Case(torch, ms, eight, rng, n, t, 5, shift, change) for n in SIZES for t in TYPES]
+    _step(ctx, ms, cases, 5, torch.full((1,), math.nan, device="cuda"))
+    torch.cuda.synchronize()
+    for c in cases:
+        what = f"n={c.n} {c.pd} {c.master}"
+        for x in c.all:
+            x.check(what)
+        assert np.array_equal(c.dg.np(), c.g), what
+        for x in (c.dp, c.dm) if c.master else (c.dp,):
+            assert np.isnan(x.np()).all(), what
+        for d, scale in zip(c.ds, (False, True, False, True)):
+            if not eight:
+                assert np.isnan(d.np()).all(), what
+            elif scale:
+                assert (d.np() == 255).all(), what
+            else:
+                assert (d.np() & 0x7F == 0x7F).all(), what
+
+
+@pytest.mark.parametrize("scale_mode", ["sqrt_max", "unit_rms"])
+@pytest.mark.parametrize("precision", ["bf16", "f32"])
+@pytest.mark.parametrize("entry", ["muon_step", "muon_step_noalloc"])
+def test_nan_factor_muon(ctx, torch, ms, entry, precision, scale_mode):
+    """The same of a Muon step, shapes that pad among them; the context's next step is not affected."""
+    rng = np.random.default_rng(54)
+    shapes = [(64, 128), (128, 64), (33, 65), (65, 33), (200, 300), (256, 256), (8, 40), (1, 5)]
+    kw = {"ns_precision": ms.MUON_NS_BF16 if precision == "bf16" else ms.MUON_NS_F32,
+          "scale_mode": ms.MUON_SCALE_UNIT_RMS if scale_mode == "unit_rms" else ms.MUON_SCALE_SQRT_MAX}
+
+    def new():
+        out = []
+        for k, (rows, cols) in enumerate(shapes):
+            g = rng.standard_normal((rows, cols)).astype(np.float32)
+            g[rows // 2] = 0
+            host = ((rng.standard_normal((rows, cols)) * 0.02).astype(np.float32), g,
+                    rng.standard_normal((rows, cols)).astype(np.float32))
+            types = (torch.bfloat16 if k % 2 else torch.float32, torch.bfloat16 if k % 3 else torch.float32, torch.float32)
+            out.append([Guarded(torch, _bf16(x).ravel(), d) for x, d in zip(host, types)])
+        return out
+
+    def step(tensors, factor):
+        mats = [ms.matrix(*(x.t.view(s) for x in ts)) for ts, s in zip(tensors, shapes)]
+        getattr(ctx, entry)(mats, ms.make_hparams(grad_factor=factor, **kw))
+
+    bad, good, again = new(), new(), []
+    for ts in good:
+        again.append([Guarded(torch, x.np(), x.t.dtype) for x in ts])
+    step(good, None)
+    step(bad, torch.full((1,), math.nan, device="cuda"))
+    step(again, None)
+    torch.cuda.synchronize()
+    for ts, s in zip(bad, shapes):
+        for x, name in zip(ts, ("param", "grad", "momentum")):
+            x.check(f"{s} {name}")
+            assert np.isnan(x.np()).all() == (name != "grad"), f"{s} {name}"
+    for a, b in zip(good, again):
+        for x, y in zip(a, b):
+            assert np.array_equal(x.np(), y.np())
+
+
+def test_nan_factor_comes_from_the_norm(ctx, torch, ms):
+    """An infinity in one gradient of one tensor: the norm's factor, read on the device, leaves NaN in all of them."""
+    rng = np.random.default_rng(55)
+    cases = [Case(torch, ms, eight, rng, n, t, 2) for eight in (False, True) for n in (33, 300) for t in TYPES]
+    cases[3].dg.t[7] = -math.inf
+    norm, factor = torch.zeros(1, dtype=torch.float64, device="cuda"), torch.ones(1, device="cuda")
+    ctx.muon_grad_norm([ms.grad(c.dg.t) for c in cases], 1.0, norm, factor)
+    for eight in (False, True):
+        _step(ctx, ms, [c for c in cases if c.eight == eight], 2, factor)
+    torch.cuda.synchronize()
+    assert float(norm) == math.inf and math.isnan(float(factor))
+    for c in cases:
+        assert np.isnan(c.dp.np()).all()
