@@ -352,9 +352,16 @@ muon_status muon_adamw_step(muon_context *ctx, const muon_adamw_tensor *ts, int6
 /* The three entry points below upload nothing and allocate nothing: their
  * descriptors travel as kernel arguments.  They may be captured into a graph,
  * on their first call too; a replay uses the addresses and the host scalars of
- * the capture (lr, step and the rounding's key with it) and reads grad_factor
- * anew.  As everywhere, tensors, norm and factor must stay allocated until the
- * work has run. */
+ * the capture and reads grad_factor anew.  For the two AdamW steps those
+ * scalars are lr, the step number and the rounding's key: replays of one
+ * capture repeat ONE step number, with its bias corrections, and in the 8-bit
+ * step round each element by the same random number every time, which is no
+ * longer unbiased.  A loop of training steps therefore captures an AdamW call
+ * anew for every step number (or updates its graph with such a capture), or
+ * calls it outside its graph; muon_grad_norm may be replayed as it is.  As
+ * everywhere, tensors, norm and factor must stay allocated until the work has
+ * run, and the context until the last replay: a captured muon_grad_norm
+ * works in its memory. */
 
 /* AdamW over `count` tensors (host array ts) of mixed types, with moments in
  * 32 bits: per element the operations of muon_adamw_step in the same order and

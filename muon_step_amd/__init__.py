@@ -375,7 +375,8 @@ class Context:
 
     def muon_adamw_mixed_step(self, tensors, hp, grad_factor=None, stream=None):
         """tensors: a list of adamw_mixed_tensor() or a table() of them; hp: adamw_hparams(); grad_factor: a
-        one-element float32 GPU tensor (muon_grad_norm's factor), read when the step runs."""
+        one-element float32 GPU tensor (muon_grad_norm's factor), read when the step runs.  hp is read at the call:
+        a captured call repeats its lr and step number at every replay, so it is captured anew for every step."""
         self._check_device(tensors, "tensor")
         arr, factor = _array(tensors, muon_adamw_mixed_tensor), _factor_ptr(grad_factor, self.device)
         st = self.lib.muon_adamw_mixed_step(self.handle, arr, len(arr), ctypes.byref(hp), factor,
@@ -384,7 +385,8 @@ class Context:
 
     def muon_adamw8_step(self, tensors, hp, seed=0, grad_factor=None, stream=None):
         """tensors: a list of adamw8_tensor() or a table() of them; seed: of the moments' stochastic rounding,
-        one for a run (0 <= seed < 2^64)."""
+        one for a run (0 <= seed < 2^64).  A captured call repeats its step number and its random numbers at every
+        replay, so it is captured anew for every step."""
         if not 0 <= seed < 1 << 64:
             raise ValueError(f"seed must lie in [0, 2^64), got {seed}")
         self._check_device(tensors, "tensor")

@@ -135,3 +135,39 @@ def test_nan_factor_comes_from_the_norm(ctx, torch, ms):
     assert float(norm) == math.inf and math.isnan(float(factor))
     for c in cases:
         assert np.isnan(c.dp.np()).all()
+
+
+def test_training_steps_captured_one_by_one(torch, ms):
+    """The steps' scalars are the capture's, so a loop that replays graphs captures each step number anew: the same
+    bits as eager calls, in fresh and in kept graphs, with eager work of another context between."""
+    from test_gpu_adamw import _model
+    captured, eager, between = ms.Context(0), ms.Context(0), ms.Context(0)
+    try:
+        a, b, other = (_model(torch, ms, seed) for seed in (61, 61, 62))
+
+        def run(c, t, step):
+            hp = ms.adamw_hparams(step=step)
+            c.muon_grad_norm(t["grads"], 1.0, t["norm"], t["factor"])
+            c.muon_adamw_mixed_step(t["mixed"], hp, grad_factor=t["factor"])
+            c.muon_adamw8_step(t["eight"], hp, seed=SEED, grad_factor=t["factor"])
+
+        graphs = []
+        for step in range(1, 5):
+            torch.cuda.synchronize()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                run(captured, a, step)
+        for step, graph in enumerate(graphs, 1):
+            for x, y in zip(a["g"], b["g"]):
+                x.mul_(1.0 - 0.1 * step)
+                y.copy_(x)
+            graph.replay()
+            run(between, other, step)
+            run(eager, b, step)
+            torch.cuda.synchronize()
+            for x, y in zip(a["state"], b["state"]):
+                assert bool((x.view(torch.uint8) == y.view(torch.uint8)).all()), f"step {step}"
+    finally:
+        torch.cuda.synchronize()
+        for c in (captured, eager, between):
+            c.close()
