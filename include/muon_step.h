@@ -32,7 +32,7 @@
  *   - A context is not thread-safe; calls on one context must be ordered by
  *     the caller (one stream at a time, or explicit synchronisation).
  *   - Results are deterministic: identical inputs give bit-identical outputs
- *     (no atomics in any reduction).
+ *     (no atomic adds up values; muon_grad_norm's one counts workgroups).
  */
 #ifndef MUON_STEP_H
 #define MUON_STEP_H
