@@ -340,8 +340,11 @@ muon_status muon_set_concurrent_groups(muon_context *ctx, int32_t enable);
  * Every call on one GPU shares that GPU's array (across contexts too), and
  * calls that overlap on one GPU race: order them on one stream or
  * synchronise.  muon_last_norms reads from the array, so it is valid until
- * the next muon_step_noalloc on that GPU.  With per-stage timing enabled
- * (muon_profile_enable) the call may create HIP events. */
+ * the next muon_step_noalloc on that GPU.  Under capture the matrices'
+ * addresses become part of the graph, and a replay steps them whatever the
+ * context was called with since; it counts as a call on the GPU's array.  With
+ * per-stage timing enabled (muon_profile_enable) the call may create HIP
+ * events: not under capture. */
 muon_status muon_step_noalloc(muon_context *ctx, const muon_matrix *mats, int64_t count,
                               const muon_hparams *hp, void *hip_stream);
 

@@ -27,6 +27,9 @@ constexpr int kTile = 256;
 constexpr size_t kScratchBytes = size_t(128) << 20;
 // Device address of the current device's copy of the array.
 hipError_t scratch_address(void **out);
+// Writes a host table of descriptors to the device by kernels that carry it as
+// arguments, for calls under graph capture.
+hipError_t launch_write_descs(MatDesc *dst, const MatDesc *src, int64_t count, hipStream_t st);
 
 // ---- elementwise (elementwise.hip)
 // Workgroups per matrix of the momentum pass, and so its ||N||^2 partial sums

@@ -1195,16 +1195,32 @@ Lanes plan_lanes(const std::vector<GroupPlan> &plan, int max_lanes, size_t cap) 
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Whether the stream is being captured into a graph.
+bool capturing(hipStream_t st) {
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(st, &status) != hipSuccess) {
+        (void)hipGetLastError();
+        return false;
+    }
+    return status != hipStreamCaptureStatusNone;
+}
+
 // Copies the descriptor table into the fixed scratch through the context's
 // pinned staging buffer (allocated by muon_create), once the previous copy
-// from it has been consumed.  Nothing is allocated.
-muon_status upload_fixed(muon_context *ctx, void *dst, const void *src, size_t n, hipStream_t st) {
+// from it has been consumed.  Under capture the table is part of the graph
+// (launch_write_descs).  Nothing is allocated.
+muon_status upload_fixed(muon_context *ctx, MatDesc *dst, const std::vector<MatDesc> &descs, hipStream_t st) {
     hipError_t e;
+    if (capturing(st)) {
+        e = muon::launch_write_descs(dst, descs.data(), static_cast<int64_t>(descs.size()), st);
+        return e == hipSuccess ? MUON_OK : hip_fail(ctx, e, "descriptor launch");
+    }
     if (ctx->noalloc_upload_recorded) {
         e = hipEventSynchronize(ctx->noalloc_upload_done);
         if (e != hipSuccess) return hip_fail(ctx, e, "hipEventSynchronize");
     }
-    std::memcpy(ctx->noalloc_pinned, src, n);
+    const size_t n = descs.size() * sizeof(MatDesc);
+    std::memcpy(ctx->noalloc_pinned, descs.data(), n);
     e = hipMemcpyAsync(dst, ctx->noalloc_pinned, n, hipMemcpyHostToDevice, st);
     if (e != hipSuccess) return hip_fail(ctx, e, "hipMemcpyAsync");
     e = hipEventRecord(ctx->noalloc_upload_done, st);
@@ -1307,12 +1323,12 @@ muon_status step_impl(muon_context *ctx, const muon_matrix *mats, int64_t count,
             d.call_index = i;
             descs.push_back(d);
         }
-    const size_t desc_bytes = descs.size() * sizeof(MatDesc);
     if (fixed) {
-        s = upload_fixed(ctx, desc_dst, descs.data(), desc_bytes, st);
+        s = upload_fixed(ctx, desc_dst, descs, st);
         if (s != MUON_OK) return s;
     } else {
-        s = upload(ctx, ctx->mat_desc, ctx->mat_cache, descs.data(), desc_bytes, st, "matrix descriptors");
+        s = upload(ctx, ctx->mat_desc, ctx->mat_cache, descs.data(), descs.size() * sizeof(MatDesc), st,
+                   "matrix descriptors");
         if (s != MUON_OK) return s;
         desc_dst = static_cast<MatDesc *>(ctx->mat_desc.p);
     }

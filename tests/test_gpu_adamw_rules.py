@@ -171,3 +171,56 @@ def test_training_steps_captured_one_by_one(torch, ms):
         torch.cuda.synchronize()
         for c in (captured, eager, between):
             c.close()
+
+
+def test_clipped_noalloc_steps_captured(torch, ms):
+    """The norm and two muon_step_noalloc calls that read its factor in one graph, more matrices than one descriptor
+    launch carries among them.  Between the replays the same context steps other, smaller matrices eagerly: a replay
+    goes on with its own, bit for bit as eager calls do."""
+    rng = np.random.default_rng(63)
+
+    def matrices(shapes):
+        return [[torch.from_numpy(rng.standard_normal(s).astype(np.float32) * k).cuda().to(d)
+                 for k, d in ((0.02, torch.bfloat16), (1, torch.bfloat16), (1, torch.float32))] for s in shapes]
+
+    def copy(ts):
+        return [[x.clone() for x in t] for t in ts]
+
+    def run(c, t):
+        c.muon_grad_norm([ms.grad(g) for part in t["parts"] for _, g, _ in part], 1.0, t["norm"], t["factor"])
+        for part in t["parts"]:
+            c.muon_step_noalloc([ms.matrix(*x) for x in part], ms.make_hparams(grad_factor=t["factor"]))
+
+    def state(t):
+        return [x for part in t["parts"] for w, _, m in part for x in (w, m)]
+
+    a = {"parts": [matrices([(64, 128)] * 100 + [(128, 64)] * 70), matrices([(300, 200), (5, 3)])]}
+    b = {"parts": [copy(part) for part in a["parts"]]}
+    for t in (a, b):
+        t["norm"], t["factor"] = torch.zeros(1, dtype=torch.float64, device="cuda"), torch.zeros(1, device="cuda")
+    small = matrices([(2, 2), (3, 5)])
+    graph_ctx, eager_ctx = ms.Context(0), ms.Context(0)
+    try:
+        graph_ctx.muon_step_noalloc([ms.matrix(*x) for x in small], ms.make_hparams())
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(graph_ctx, a)
+        for x, y in zip(state(a), state(b)):
+            assert torch.equal(x, y), "a capture runs nothing"
+        for k in range(4):
+            for p, q in zip(a["parts"], b["parts"]):
+                for (_, g, _), (_, h, _) in zip(p, q):
+                    g.mul_(0.9)
+                    h.copy_(g)
+            graph_ctx.muon_step_noalloc([ms.matrix(*x) for x in small[k % 2:]], ms.make_hparams())
+            graph.replay()
+            run(eager_ctx, b)
+            torch.cuda.synchronize()
+            assert float(a["norm"]) == float(b["norm"])
+            for x, y in zip(state(a), state(b)):
+                assert torch.equal(x, y), f"replay {k}"
+    finally:
+        torch.cuda.synchronize()
+        for c in (graph_ctx, eager_ctx):
+            c.close()
