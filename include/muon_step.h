@@ -316,7 +316,12 @@ const char *muon_last_error(const muon_context *ctx);
  * it before the call returns, each lane of groups in a workspace slice of
  * its own; a nonzero workspace cap that those slices together would exceed
  * runs the groups in turn instead.  Either way the results are the same,
- * bit for bit. */
+ * bit for bit.  Under graph capture the call works where the context's last
+ * call had the same list (its buffers and tables are then in place: a graph
+ * can neither allocate nor upload them), and is refused with
+ * MUON_ERR_UNSUPPORTED otherwise; later calls with other lists take new
+ * tables and, where they need more of it, a new workspace, and the graph's
+ * stay until muon_destroy.  A replay counts as a call on the context. */
 muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
                       const muon_hparams *hp, void *hip_stream);
 
@@ -348,7 +353,8 @@ muon_status muon_set_concurrent_groups(muon_context *ctx, int32_t enable);
 muon_status muon_step_noalloc(muon_context *ctx, const muon_matrix *mats, int64_t count,
                               const muon_hparams *hp, void *hip_stream);
 
-/* One AdamW step over `count` tensors (host array ts), one launch. */
+/* One AdamW step over `count` tensors (host array ts), one launch.  Under graph
+ * capture as muon_step; a replay repeats the step number. */
 muon_status muon_adamw_step(muon_context *ctx, const muon_adamw_tensor *ts, int64_t count,
                             const muon_adamw_hparams *hp, void *hip_stream);
 

@@ -736,6 +736,7 @@ muon_status plan_groups(const muon_matrix *mats, int64_t count, int32_t precisio
 struct DevBuf {
     void *p = nullptr;
     size_t n = 0;
+    bool in_graph = false;  // a captured call holds it
 };
 
 struct muon_context {
@@ -747,6 +748,7 @@ struct muon_context {
     DevBuf call_nrm2; // per call matrix
     DevBuf mat_desc;  // MatDesc table
     DevBuf adamw_desc;
+    std::vector<void *> retired;  // buffers that graphs may hold, and calls no longer
     // muon_grad_norm's sums: of a fixed size and there from creation on, so that
     // a captured call never points to memory that a later call replaced
     muon::NormWorkspace *norm_ws = nullptr;
@@ -851,10 +853,40 @@ hipError_t timed(muon_context *ctx, int stage, double flops, double bytes, hipSt
     return hipSuccess;
 }
 
+// Whether the stream is being captured into a graph.
+bool capturing(hipStream_t st) {
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(st, &status) != hipSuccess) {
+        (void)hipGetLastError();
+        return false;
+    }
+    return status != hipStreamCaptureStatusNone;
+}
+
+// Entry points that keep buffers and tables in the context may be captured once
+// these are as the call needs them: a graph cannot allocate or upload them.
+// What a graph holds is not changed or freed before muon_destroy (in_graph).
+muon_status refuse_capture(muon_context *ctx, const char *what) {
+    return fail(ctx, MUON_ERR_UNSUPPORTED,
+                "under graph capture the %s cannot change: call it with the same arguments before, or use "
+                "muon_step_noalloc", what);
+}
+
+// Puts a buffer that a graph may hold aside and leaves none in its place.
+void retire(muon_context *ctx, DevBuf &b) {
+    ctx->retired.push_back(b.p);
+    b = DevBuf{};
+}
+
 // Grows a device buffer to at least n bytes.  Outstanding work may still use
 // the old buffer, so the device is synchronised before it is freed.
-muon_status ensure(muon_context *ctx, DevBuf &b, size_t n, const char *what) {
-    if (b.n >= n && b.p) return MUON_OK;
+muon_status ensure(muon_context *ctx, DevBuf &b, size_t n, const char *what, bool in_graph) {
+    if (b.n >= n && b.p) {
+        b.in_graph |= in_graph;
+        return MUON_OK;
+    }
+    if (in_graph) return refuse_capture(ctx, what);
+    if (b.in_graph) retire(ctx, b);
     if (b.p) {
         hipError_t e = hipDeviceSynchronize();
         if (e != hipSuccess) return hip_fail(ctx, e, "hipDeviceSynchronize");
@@ -876,10 +908,16 @@ muon_status ensure(muon_context *ctx, DevBuf &b, size_t n, const char *what) {
 // Uploads a host table to a device buffer through pinned staging, skipping the
 // copy when the bytes equal the previous upload of the same table.
 muon_status upload(muon_context *ctx, DevBuf &dst, std::vector<unsigned char> &cache, const void *src, size_t n,
-                   hipStream_t st, const char *what) {
+                   hipStream_t st, const char *what, bool in_graph) {
     if (n == 0) return MUON_OK;
-    if (cache.size() == n && dst.p && dst.n >= n && std::memcmp(cache.data(), src, n) == 0) return MUON_OK;
-    muon_status s = ensure(ctx, dst, n, what);
+    if (cache.size() == n && dst.p && dst.n >= n && std::memcmp(cache.data(), src, n) == 0) {
+        dst.in_graph |= in_graph;
+        return MUON_OK;
+    }
+    if (in_graph) return refuse_capture(ctx, what);
+    cache.clear();  // until the new table is on its way
+    if (dst.in_graph) retire(ctx, dst);
+    muon_status s = ensure(ctx, dst, n, what, false);
     if (s != MUON_OK) return s;
     hipError_t e;
     if (ctx->upload_recorded) {
@@ -1195,16 +1233,6 @@ Lanes plan_lanes(const std::vector<GroupPlan> &plan, int max_lanes, size_t cap) 
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Whether the stream is being captured into a graph.
-bool capturing(hipStream_t st) {
-    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
-    if (hipStreamIsCapturing(st, &status) != hipSuccess) {
-        (void)hipGetLastError();
-        return false;
-    }
-    return status != hipStreamCaptureStatusNone;
-}
-
 // Copies the descriptor table into the fixed scratch through the context's
 // pinned staging buffer (allocated by muon_create), once the previous copy
 // from it has been consumed.  Under capture the table is part of the graph
@@ -1280,6 +1308,7 @@ muon_status step_impl(muon_context *ctx, const muon_matrix *mats, int64_t count,
     }
     DeviceGuard guard(ctx->device);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
+    const bool in_graph = capturing(st);
     // groups on concurrent lanes (plan_lanes), except in the allocation-free
     // step and under per-stage timing, which run them in turn
     Lanes lanes;
@@ -1303,10 +1332,10 @@ muon_status step_impl(muon_context *ctx, const muon_matrix *mats, int64_t count,
     const size_t tabs_total = nlanes > 1 ? lanes.tb_off.back() : tabs_bytes(parts, max_chunk);
     if (nlanes > 1) ws = lanes.ws_off.back();
     if (!fixed) {
-        if ((s = ensure(ctx, ctx->ws, ws, "workspace")) != MUON_OK) return s;
-        if ((s = ensure(ctx, ctx->tabs, tabs_total, "norm tables")) != MUON_OK) return s;
-        if ((s = ensure(ctx, ctx->call_nrm2, static_cast<size_t>(count) * sizeof(double), "norm output")) != MUON_OK)
-            return s;
+        if ((s = ensure(ctx, ctx->ws, ws, "workspace", in_graph)) != MUON_OK) return s;
+        if ((s = ensure(ctx, ctx->tabs, tabs_total, "norm tables", in_graph)) != MUON_OK) return s;
+        const size_t nrm2 = static_cast<size_t>(count) * sizeof(double);
+        if ((s = ensure(ctx, ctx->call_nrm2, nrm2, "norm output", in_graph)) != MUON_OK) return s;
         mem = CallMem{static_cast<char *>(ctx->ws.p), static_cast<char *>(ctx->tabs.p),
                       static_cast<double *>(ctx->call_nrm2.p)};
     }
@@ -1328,7 +1357,7 @@ muon_status step_impl(muon_context *ctx, const muon_matrix *mats, int64_t count,
         if (s != MUON_OK) return s;
     } else {
         s = upload(ctx, ctx->mat_desc, ctx->mat_cache, descs.data(), descs.size() * sizeof(MatDesc), st,
-                   "matrix descriptors");
+                   "matrix descriptors", in_graph);
         if (s != MUON_OK) return s;
         desc_dst = static_cast<MatDesc *>(ctx->mat_desc.p);
     }
@@ -1657,6 +1686,7 @@ muon_status muon_destroy(muon_context *ctx) {
     (void)hipDeviceSynchronize();
     for (DevBuf *b : {&ctx->ws, &ctx->tabs, &ctx->call_nrm2, &ctx->mat_desc, &ctx->adamw_desc})
         if (b->p) (void)hipFree(b->p);
+    for (void *p : ctx->retired) (void)hipFree(p);
     if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
     if (ctx->pinned) (void)hipHostFree(ctx->pinned);
     if (ctx->noalloc_pinned) (void)hipHostFree(ctx->noalloc_pinned);
@@ -1703,14 +1733,15 @@ muon_status muon_ns_only(muon_context *ctx, const float *n_in, float *x_out, int
         return fail(ctx, MUON_ERR_OUT_OF_MEMORY, "matrix needs %zu bytes of workspace, above the cap", need);
     DeviceGuard guard(ctx->device);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
+    const bool in_graph = capturing(st);
     const int tc = static_cast<int>((cols + 63) / 64);
     const int nb_blocks = static_cast<int>(((rows + 63) / 64) * tc);
-    if ((s = ensure(ctx, ctx->ws, need, "workspace")) != MUON_OK) return s;
-    if ((s = ensure(ctx, ctx->tabs, tabs_bytes(static_cast<size_t>(nb_blocks), 1), "norm tables")) != MUON_OK)
+    if ((s = ensure(ctx, ctx->ws, need, "workspace", in_graph)) != MUON_OK) return s;
+    if ((s = ensure(ctx, ctx->tabs, tabs_bytes(static_cast<size_t>(nb_blocks), 1), "norm tables", in_graph)) != MUON_OK)
         return s;
-    if ((s = ensure(ctx, ctx->call_nrm2, sizeof(double), "norm output")) != MUON_OK) return s;
+    if ((s = ensure(ctx, ctx->call_nrm2, sizeof(double), "norm output", in_graph)) != MUON_OK) return s;
     MatDesc d{};
-    s = upload(ctx, ctx->mat_desc, ctx->mat_cache, &d, sizeof d, st, "matrix descriptors");
+    s = upload(ctx, ctx->mat_desc, ctx->mat_cache, &d, sizeof d, st, "matrix descriptors", in_graph);
     if (s != MUON_OK) return s;
     const MatDesc *ddev = static_cast<const MatDesc *>(ctx->mat_desc.p);
     Work w = chunk_work(CallMem{static_cast<char *>(ctx->ws.p), static_cast<char *>(ctx->tabs.p),
@@ -1752,6 +1783,7 @@ muon_status muon_apply_update(muon_context *ctx, void *param, int32_t param_dtyp
     muon_scalars(hp, rows, cols, &d, &sc);
     DeviceGuard guard(ctx->device);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
+    const bool in_graph = capturing(st);
     const double by = static_cast<double>(rows) * cols * (4.0 + 2.0 * dtype_size(param_dtype));
     const float *s_dev = nullptr;
     hipError_t e = hipSuccess;
@@ -1760,7 +1792,7 @@ muon_status muon_apply_update(muon_context *ctx, void *param, int32_t param_dtyp
         // blocks, the scale written after the partial sums.
         const int nbx = static_cast<int>(std::min<int64_t>(rows, 1024));
         const size_t part = align_up(static_cast<size_t>(nbx) * sizeof(double));
-        if ((s = ensure(ctx, ctx->tabs, part + sizeof(float), "norm tables")) != MUON_OK) return s;
+        if ((s = ensure(ctx, ctx->tabs, part + sizeof(float), "norm tables", in_graph)) != MUON_OK) return s;
         Geom g{};
         g.rows = g.s = g.sp = rows;
         g.cols = g.l = g.lp = cols;
@@ -1806,7 +1838,8 @@ muon_status muon_adamw_step(muon_context *ctx, const muon_adamw_tensor *ts, int6
     if (blocks > (int64_t(1) << 31) - 1) return fail(ctx, MUON_ERR_UNSUPPORTED, "AdamW call too large for one grid");
     DeviceGuard guard(ctx->device);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    s = upload(ctx, ctx->adamw_desc, ctx->adamw_cache, table.data(), table.size(), st, "AdamW descriptors");
+    const bool in_graph = capturing(st);
+    s = upload(ctx, ctx->adamw_desc, ctx->adamw_cache, table.data(), table.size(), st, "AdamW descriptors", in_graph);
     if (s != MUON_OK) return s;
     double elems = 0;
     for (int64_t i = 0; i < count; ++i) elems += static_cast<double>(ts[i].numel);
@@ -1939,10 +1972,11 @@ muon_status muon_ns_stage(muon_context *ctx, int32_t stage, const float *x, cons
         return fail(ctx, MUON_ERR_OUT_OF_MEMORY, "matrix needs %zu bytes of workspace, above the cap", need);
     DeviceGuard guard(ctx->device);
     hipStream_t st = static_cast<hipStream_t>(hip_stream);
+    const bool in_graph = capturing(st);
     muon_status rs;
-    if ((rs = ensure(ctx, ctx->ws, need, "workspace")) != MUON_OK) return rs;
-    if ((rs = ensure(ctx, ctx->tabs, tabs_bytes(1, 1), "norm tables")) != MUON_OK) return rs;
-    if ((rs = ensure(ctx, ctx->call_nrm2, sizeof(double), "norm output")) != MUON_OK) return rs;
+    if ((rs = ensure(ctx, ctx->ws, need, "workspace", in_graph)) != MUON_OK) return rs;
+    if ((rs = ensure(ctx, ctx->tabs, tabs_bytes(1, 1), "norm tables", in_graph)) != MUON_OK) return rs;
+    if ((rs = ensure(ctx, ctx->call_nrm2, sizeof(double), "norm output", in_graph)) != MUON_OK) return rs;
     Work w = chunk_work(CallMem{static_cast<char *>(ctx->ws.p), static_cast<char *>(ctx->tabs.p),
                                 static_cast<double *>(ctx->call_nrm2.p)},
                         g, true, 1, 1, sp.kpart(1));

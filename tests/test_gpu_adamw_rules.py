@@ -224,3 +224,59 @@ def test_clipped_noalloc_steps_captured(torch, ms):
         torch.cuda.synchronize()
         for c in (graph_ctx, eager_ctx):
             c.close()
+
+
+def test_clipped_muon_and_adamw_steps_captured(torch, ms):
+    """muon_step and muon_adamw_step under capture: refused on a context whose last call had another list, with the
+    next eager call unharmed; otherwise the replays go on with their own tensors, whatever lists and sizes the context
+    steps eagerly between them."""
+    rng = np.random.default_rng(64)
+
+    def matrices(shapes):
+        return [[torch.from_numpy(rng.standard_normal(s).astype(np.float32) * k).cuda().to(d)
+                 for k, d in ((0.02, torch.bfloat16), (1, torch.bfloat16), (1, torch.float32))] for s in shapes]
+
+    def vectors(sizes):
+        return [[torch.from_numpy((rng.standard_normal(n) ** 2).astype(np.float32)).cuda() for _ in range(4)] for n in sizes]
+
+    def run(c, mats, tensors, factor):
+        c.muon_step([ms.matrix(*x) for x in mats], ms.make_hparams(grad_factor=factor))
+        c.muon_adamw_step([ms.adamw_tensor(*x) for x in tensors], ms.adamw_hparams(step=3))
+
+    a = matrices([(64, 128), (128, 64), (40, 40)]), vectors([100, 7])
+    b = tuple([[x.clone() for x in t] for t in part] for part in a)
+    others = [(matrices(s), vectors(n)) for s, n in (([(2, 3)], [1]), ([(512, 700)] * 3 + [(64, 64)], [9, 5000, 3]))]
+    factor = torch.full((1,), 0.25, device="cuda")
+    graph_ctx, eager_ctx = ms.Context(0), ms.Context(0)
+    try:
+        for warm in (None, others[0]):
+            if warm:
+                run(graph_ctx, *warm, None)
+            torch.cuda.synchronize()
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                for call in (lambda: graph_ctx.muon_step([ms.matrix(*x) for x in a[0]], ms.make_hparams()),
+                             lambda: graph_ctx.muon_adamw_step([ms.adamw_tensor(*x) for x in a[1]], ms.adamw_hparams())):
+                    with pytest.raises(ms.MuonError) as err:
+                        call()
+                    assert err.value.status == ms.MUON_ERR_UNSUPPORTED and "capture" in str(err.value)
+                factor.add_(0)   # a graph that holds something
+        run(graph_ctx, *a, factor)
+        run(eager_ctx, *b, factor)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(graph_ctx, *a, factor)
+        for k in range(4):
+            factor.fill_(0.5 + 0.125 * k)
+            run(graph_ctx, *others[k % 2], factor)
+            graph.replay()
+            run(eager_ctx, *b, factor)
+            torch.cuda.synchronize()
+            for p, q in zip(a, b):
+                for t, u in zip(p, q):
+                    for x, y in zip(t, u):
+                        assert torch.equal(x, y), f"replay {k}"
+    finally:
+        torch.cuda.synchronize()
+        for c in (graph_ctx, eager_ctx):
+            c.close()
