@@ -141,7 +141,7 @@ muon_status check_step(const muon_matrix *mats, int64_t count, const muon_hparam
     muon_status s = check_hparams(hp, msg, cap);
     if (s != MUON_OK) return s;
     std::vector<Interval> iv;
-    iv.reserve(static_cast<size_t>(count) * 4);
+    iv.reserve(static_cast<size_t>(std::min(count, std::numeric_limits<int64_t>::max() / 4)) * 4);
     for (int64_t i = 0; i < count; ++i) {
         const muon_matrix &m = mats[i];
         if (!m.param || !m.grad || !m.momentum) {
@@ -466,11 +466,14 @@ muon_status check_grad_norm(const muon_grad *gs, int64_t count, double max_norm,
     return MUON_OK;
 }
 
-// No C++ exception leaves the library: `fn` may fail for want of host memory.
-template <class F> muon_status guarded(F fn) {
+// No C++ exception leaves the library: every entry point that may ask for host
+// memory runs in one of these.
+constexpr const char *kNoHostMemory = "out of host memory";
+template <class F> muon_status guarded(char *msg, size_t cap, F fn) {
     try {
         return fn();
     } catch (...) {
+        set_msg(msg, cap, "%s", kNoHostMemory);
         return MUON_ERR_OUT_OF_MEMORY;
     }
 }
@@ -800,6 +803,18 @@ struct DeviceGuard {
         if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
     }
 };
+
+template <class F> muon_status guarded(muon_context *ctx, F fn) {
+    try {
+        return fn();
+    } catch (...) {
+        try {
+            if (ctx) ctx->err = kNoHostMemory;
+        } catch (...) {
+        }
+        return MUON_ERR_OUT_OF_MEMORY;
+    }
+}
 
 muon_status fail(muon_context *ctx, muon_status st, const char *fmt, ...) {
     char buf[512];
@@ -1579,105 +1594,109 @@ int64_t muon_schedule(const char *name, muon_ns_coeff *out, int64_t capacity) {
 muon_status muon_check_step_args(const muon_matrix *mats, int64_t count, const muon_hparams *hp, char *msg,
                                  size_t msg_cap) {
     set_msg(msg, msg_cap, "%s", "");
-    return check_step(mats, count, hp, msg, msg_cap);
+    return guarded(msg, msg_cap, [&] { return check_step(mats, count, hp, msg, msg_cap); });
 }
 
 muon_status muon_check_adamw_args(const muon_adamw_tensor *ts, int64_t count, const muon_adamw_hparams *hp,
                                   char *msg, size_t msg_cap) {
     set_msg(msg, msg_cap, "%s", "");
-    return check_adamw(ts, count, hp, msg, msg_cap);
+    return guarded(msg, msg_cap, [&] { return check_adamw(ts, count, hp, msg, msg_cap); });
 }
 
 muon_status muon_check_adamw_mixed_args(const muon_adamw_mixed_tensor *ts, int64_t count,
                                         const muon_adamw_hparams *hp, const float *grad_factor, char *msg,
                                         size_t msg_cap) {
     set_msg(msg, msg_cap, "%s", "");
-    return guarded([&] { return check_adamw_mixed(ts, count, hp, grad_factor, msg, msg_cap); });
+    return guarded(msg, msg_cap, [&] { return check_adamw_mixed(ts, count, hp, grad_factor, msg, msg_cap); });
 }
 
 muon_status muon_check_adamw8_args(const muon_adamw8_tensor *ts, int64_t count, const muon_adamw_hparams *hp,
                                    const float *grad_factor, char *msg, size_t msg_cap) {
     set_msg(msg, msg_cap, "%s", "");
-    return guarded([&] { return check_adamw8(ts, count, hp, grad_factor, msg, msg_cap); });
+    return guarded(msg, msg_cap, [&] { return check_adamw8(ts, count, hp, grad_factor, msg, msg_cap); });
 }
 
 muon_status muon_check_grad_norm_args(const muon_grad *gs, int64_t count, double max_norm, const double *norm,
                                       const float *factor, char *msg, size_t msg_cap) {
     set_msg(msg, msg_cap, "%s", "");
-    return guarded([&] { return check_grad_norm(gs, count, max_norm, norm, factor, msg, msg_cap); });
+    return guarded(msg, msg_cap, [&] { return check_grad_norm(gs, count, max_norm, norm, factor, msg, msg_cap); });
 }
 
 muon_status muon_workspace_bytes(const muon_matrix *mats, int64_t count, const muon_hparams *hp,
                                  size_t *bytes_out) {
-    if (!bytes_out) return MUON_ERR_INVALID_ARGUMENT;
-    muon_status s = check_step(mats, count, hp, nullptr, 0);
-    if (s != MUON_OK) return s;
-    std::vector<GroupPlan> plan;
-    size_t ws = 0, parts = 0;
-    int64_t mc = 0;
-    s = plan_groups(mats, count, hp->ns_precision, 0, &plan, &ws, &parts, &mc, nullptr, 0);
-    if (s != MUON_OK) return s;
-    const Lanes lanes = plan_lanes(plan, 1 + muon_context::kSide, 0);
-    const size_t tabs = lanes.n > 1 ? lanes.tb_off.back() : tabs_bytes(parts, mc);
-    if (lanes.n > 1) ws = lanes.ws_off.back();
-    *bytes_out = ws + tabs + align_up(static_cast<size_t>(count) * sizeof(double)) +
-                 align_up(static_cast<size_t>(count) * sizeof(MatDesc));
-    return MUON_OK;
+    return guarded(nullptr, 0, [&]() -> muon_status {
+        if (!bytes_out) return MUON_ERR_INVALID_ARGUMENT;
+        muon_status s = check_step(mats, count, hp, nullptr, 0);
+        if (s != MUON_OK) return s;
+        std::vector<GroupPlan> plan;
+        size_t ws = 0, parts = 0;
+        int64_t mc = 0;
+        s = plan_groups(mats, count, hp->ns_precision, 0, &plan, &ws, &parts, &mc, nullptr, 0);
+        if (s != MUON_OK) return s;
+        const Lanes lanes = plan_lanes(plan, 1 + muon_context::kSide, 0);
+        const size_t tabs = lanes.n > 1 ? lanes.tb_off.back() : tabs_bytes(parts, mc);
+        if (lanes.n > 1) ws = lanes.ws_off.back();
+        *bytes_out = ws + tabs + align_up(static_cast<size_t>(count) * sizeof(double)) +
+                     align_up(static_cast<size_t>(count) * sizeof(MatDesc));
+        return MUON_OK;
+    });
 }
 
 muon_status muon_create(muon_context **out, int32_t hip_device, size_t workspace_cap_bytes) {
-    if (!out) return MUON_ERR_INVALID_ARGUMENT;
-    *out = nullptr;
-    int n = 0;
-    if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) {
-        (void)hipGetLastError();
-        return MUON_ERR_DEVICE;
-    }
-    if (hip_device < 0 || hip_device >= n) return MUON_ERR_INVALID_ARGUMENT;
-    muon_context *ctx = new (std::nothrow) muon_context();
-    if (!ctx) return MUON_ERR_OUT_OF_MEMORY;
-    ctx->device = hip_device;
-    ctx->cap = workspace_cap_bytes;
-    DeviceGuard guard(hip_device);
-    if (hipEventCreateWithFlags(&ctx->upload_done, hipEventDisableTiming) != hipSuccess ||
-        hipEventCreateWithFlags(&ctx->noalloc_upload_done, hipEventDisableTiming) != hipSuccess) {
-        (void)hipGetLastError();
-        if (ctx->upload_done) (void)hipEventDestroy(ctx->upload_done);
-        delete ctx;
-        return MUON_ERR_DEVICE;
-    }
-    void *zeros = std::calloc(1, sizeof(muon::NormWorkspace));
-    if (!zeros || hipMalloc(reinterpret_cast<void **>(&ctx->norm_ws), sizeof(muon::NormWorkspace)) != hipSuccess ||
-        hipMemcpy(ctx->norm_ws, zeros, sizeof(muon::NormWorkspace), hipMemcpyHostToDevice) != hipSuccess) {
-        (void)hipGetLastError();
+    return guarded(nullptr, 0, [&]() -> muon_status {
+        if (!out) return MUON_ERR_INVALID_ARGUMENT;
+        *out = nullptr;
+        int n = 0;
+        if (hipGetDeviceCount(&n) != hipSuccess || n <= 0) {
+            (void)hipGetLastError();
+            return MUON_ERR_DEVICE;
+        }
+        if (hip_device < 0 || hip_device >= n) return MUON_ERR_INVALID_ARGUMENT;
+        muon_context *ctx = new (std::nothrow) muon_context();
+        if (!ctx) return MUON_ERR_OUT_OF_MEMORY;
+        ctx->device = hip_device;
+        ctx->cap = workspace_cap_bytes;
+        DeviceGuard guard(hip_device);
+        if (hipEventCreateWithFlags(&ctx->upload_done, hipEventDisableTiming) != hipSuccess ||
+            hipEventCreateWithFlags(&ctx->noalloc_upload_done, hipEventDisableTiming) != hipSuccess) {
+            (void)hipGetLastError();
+            if (ctx->upload_done) (void)hipEventDestroy(ctx->upload_done);
+            delete ctx;
+            return MUON_ERR_DEVICE;
+        }
+        void *zeros = std::calloc(1, sizeof(muon::NormWorkspace));
+        if (!zeros || hipMalloc(reinterpret_cast<void **>(&ctx->norm_ws), sizeof(muon::NormWorkspace)) != hipSuccess ||
+            hipMemcpy(ctx->norm_ws, zeros, sizeof(muon::NormWorkspace), hipMemcpyHostToDevice) != hipSuccess) {
+            (void)hipGetLastError();
+            std::free(zeros);
+            if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
+            (void)hipEventDestroy(ctx->upload_done);
+            (void)hipEventDestroy(ctx->noalloc_upload_done);
+            delete ctx;
+            return MUON_ERR_OUT_OF_MEMORY;
+        }
         std::free(zeros);
-        if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
-        (void)hipEventDestroy(ctx->upload_done);
-        (void)hipEventDestroy(ctx->noalloc_upload_done);
-        delete ctx;
-        return MUON_ERR_OUT_OF_MEMORY;
-    }
-    std::free(zeros);
-    // The allocation-free step's memory: this device's copy of the static
-    // scratch (its address, with this device current) and the pinned staging
-    // of its descriptor table.  A failure here only disables that entry point.
-    void *sp = nullptr;
-    hipError_t e = muon::scratch_address(&sp);
-    if (e != hipSuccess) {
-        (void)hipGetLastError();
-        ctx->scratch_err = std::string("hipGetSymbolAddress: ") + hipGetErrorString(e);
-    } else {
-        ctx->scratch = static_cast<char *>(sp);
-        e = hipHostMalloc(&ctx->noalloc_pinned, static_cast<size_t>(kNoAllocMaxMatrices) * sizeof(MatDesc),
-                          hipHostMallocDefault);
+        // The allocation-free step's memory: this device's copy of the static
+        // scratch (its address, with this device current) and the pinned staging
+        // of its descriptor table.  A failure here only disables that entry point.
+        void *sp = nullptr;
+        hipError_t e = muon::scratch_address(&sp);
         if (e != hipSuccess) {
             (void)hipGetLastError();
-            ctx->noalloc_pinned = nullptr;
-            ctx->scratch_err = std::string("hipHostMalloc: ") + hipGetErrorString(e);
+            ctx->scratch_err = std::string("hipGetSymbolAddress: ") + hipGetErrorString(e);
+        } else {
+            ctx->scratch = static_cast<char *>(sp);
+            e = hipHostMalloc(&ctx->noalloc_pinned, static_cast<size_t>(kNoAllocMaxMatrices) * sizeof(MatDesc),
+                              hipHostMallocDefault);
+            if (e != hipSuccess) {
+                (void)hipGetLastError();
+                ctx->noalloc_pinned = nullptr;
+                ctx->scratch_err = std::string("hipHostMalloc: ") + hipGetErrorString(e);
+            }
         }
-    }
-    *out = ctx;
-    return MUON_OK;
+        *out = ctx;
+        return MUON_OK;
+    });
 }
 
 muon_status muon_destroy(muon_context *ctx) {
@@ -1706,154 +1725,160 @@ const char *muon_last_error(const muon_context *ctx) { return ctx ? ctx->err.c_s
 
 muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count, const muon_hparams *hp,
                       void *hip_stream) {
-    return step_impl(ctx, mats, count, hp, hip_stream, false);
+    return guarded(ctx, [&] { return step_impl(ctx, mats, count, hp, hip_stream, false); });
 }
 
 muon_status muon_step_noalloc(muon_context *ctx, const muon_matrix *mats, int64_t count, const muon_hparams *hp,
                               void *hip_stream) {
-    return step_impl(ctx, mats, count, hp, hip_stream, true);
+    return guarded(ctx, [&] { return step_impl(ctx, mats, count, hp, hip_stream, true); });
 }
 
 muon_status muon_ns_only(muon_context *ctx, const float *n_in, float *x_out, int64_t rows, int64_t cols,
                          const muon_hparams *hp, void *hip_stream) {
-    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
-    char msg[512];
-    if (!n_in || !x_out) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "n_in and x_out must be non-NULL");
-    muon_status s = check_shape(rows, cols, msg, sizeof msg, 0);
-    if (s != MUON_OK) return fail(ctx, s, "%s", msg);
-    if ((s = check_hparams(hp, msg, sizeof msg)) != MUON_OK) return fail(ctx, s, "%s", msg);
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(n_in), b0 = reinterpret_cast<uintptr_t>(x_out);
-    const uintptr_t nb = static_cast<uintptr_t>(rows * cols) * 4;
-    if (a0 < b0 + nb && b0 < a0 + nb) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "n_in and x_out overlap");
-    const Geom g = make_geom(rows, cols);
-    const bool bf16 = use_bf16(hp->ns_precision, g.s);
-    const Splits sp = plan_splits(g, bf16, 1);
-    const size_t need = chunk_layout(g, bf16, 1, sp.kpart(1)).total;
-    if (ctx->cap && need > ctx->cap)
-        return fail(ctx, MUON_ERR_OUT_OF_MEMORY, "matrix needs %zu bytes of workspace, above the cap", need);
-    DeviceGuard guard(ctx->device);
-    hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    const bool in_graph = capturing(st);
-    const int tc = static_cast<int>((cols + 63) / 64);
-    const int nb_blocks = static_cast<int>(((rows + 63) / 64) * tc);
-    if ((s = ensure(ctx, ctx->ws, need, "workspace", in_graph)) != MUON_OK) return s;
-    if ((s = ensure(ctx, ctx->tabs, tabs_bytes(static_cast<size_t>(nb_blocks), 1), "norm tables", in_graph)) != MUON_OK)
-        return s;
-    if ((s = ensure(ctx, ctx->call_nrm2, sizeof(double), "norm output", in_graph)) != MUON_OK) return s;
-    MatDesc d{};
-    s = upload(ctx, ctx->mat_desc, ctx->mat_cache, &d, sizeof d, st, "matrix descriptors", in_graph);
-    if (s != MUON_OK) return s;
-    const MatDesc *ddev = static_cast<const MatDesc *>(ctx->mat_desc.p);
-    Work w = chunk_work(CallMem{static_cast<char *>(ctx->ws.p), static_cast<char *>(ctx->tabs.p),
-                                static_cast<double *>(ctx->call_nrm2.p)},
-                        g, bf16, 1, nb_blocks, sp.kpart(1));
-    const double elems = static_cast<double>(rows) * cols;
-    hipError_t e = timed(ctx, ST_IMPORT, 0.0, elems * 8.0, st, [&] { return muon::launch_import_n(n_in, g, w, st); });
-    if (e != hipSuccess) return hip_fail(ctx, e, "import launch");
-    e = timed(ctx, ST_FINALIZE, 0.0, nb_blocks * 8.0, st,
-              [&] { return muon::launch_norm_finalize(ddev, 1, w, nb_blocks, st); });
-    if (e != hipSuccess) return hip_fail(ctx, e, "norm launch");
-    const Run run{0, 1, g};
-    s = run_ns(ctx, ddev, 1, g, w, bf16, hp, false, 0, false, 0.f, 0.f, st, sp, &run, 1);
-    if (s != MUON_OK) return s;
-    e = timed(ctx, ST_EXPORT, 0.0, elems * 8.0, st, [&] { return muon::launch_export_x(g, w, x_out, st); });
-    if (e != hipSuccess) return hip_fail(ctx, e, "export launch");
-    ctx->last_stream = st;
-    ctx->last_count = 1;
-    ctx->last_nrm2 = w.call_nrm2;
-    ctx->err.clear();
-    return MUON_OK;
+    return guarded(ctx, [&]() -> muon_status {
+        if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+        char msg[512];
+        if (!n_in || !x_out) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "n_in and x_out must be non-NULL");
+        muon_status s = check_shape(rows, cols, msg, sizeof msg, 0);
+        if (s != MUON_OK) return fail(ctx, s, "%s", msg);
+        if ((s = check_hparams(hp, msg, sizeof msg)) != MUON_OK) return fail(ctx, s, "%s", msg);
+        const uintptr_t a0 = reinterpret_cast<uintptr_t>(n_in), b0 = reinterpret_cast<uintptr_t>(x_out);
+        const uintptr_t nb = static_cast<uintptr_t>(rows * cols) * 4;
+        if (a0 < b0 + nb && b0 < a0 + nb) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "n_in and x_out overlap");
+        const Geom g = make_geom(rows, cols);
+        const bool bf16 = use_bf16(hp->ns_precision, g.s);
+        const Splits sp = plan_splits(g, bf16, 1);
+        const size_t need = chunk_layout(g, bf16, 1, sp.kpart(1)).total;
+        if (ctx->cap && need > ctx->cap)
+            return fail(ctx, MUON_ERR_OUT_OF_MEMORY, "matrix needs %zu bytes of workspace, above the cap", need);
+        DeviceGuard guard(ctx->device);
+        hipStream_t st = static_cast<hipStream_t>(hip_stream);
+        const bool in_graph = capturing(st);
+        const int tc = static_cast<int>((cols + 63) / 64);
+        const int nb_blocks = static_cast<int>(((rows + 63) / 64) * tc);
+        if ((s = ensure(ctx, ctx->ws, need, "workspace", in_graph)) != MUON_OK) return s;
+        if ((s = ensure(ctx, ctx->tabs, tabs_bytes(static_cast<size_t>(nb_blocks), 1), "norm tables", in_graph)) != MUON_OK)
+            return s;
+        if ((s = ensure(ctx, ctx->call_nrm2, sizeof(double), "norm output", in_graph)) != MUON_OK) return s;
+        MatDesc d{};
+        s = upload(ctx, ctx->mat_desc, ctx->mat_cache, &d, sizeof d, st, "matrix descriptors", in_graph);
+        if (s != MUON_OK) return s;
+        const MatDesc *ddev = static_cast<const MatDesc *>(ctx->mat_desc.p);
+        Work w = chunk_work(CallMem{static_cast<char *>(ctx->ws.p), static_cast<char *>(ctx->tabs.p),
+                                    static_cast<double *>(ctx->call_nrm2.p)},
+                            g, bf16, 1, nb_blocks, sp.kpart(1));
+        const double elems = static_cast<double>(rows) * cols;
+        hipError_t e = timed(ctx, ST_IMPORT, 0.0, elems * 8.0, st, [&] { return muon::launch_import_n(n_in, g, w, st); });
+        if (e != hipSuccess) return hip_fail(ctx, e, "import launch");
+        e = timed(ctx, ST_FINALIZE, 0.0, nb_blocks * 8.0, st,
+                  [&] { return muon::launch_norm_finalize(ddev, 1, w, nb_blocks, st); });
+        if (e != hipSuccess) return hip_fail(ctx, e, "norm launch");
+        const Run run{0, 1, g};
+        s = run_ns(ctx, ddev, 1, g, w, bf16, hp, false, 0, false, 0.f, 0.f, st, sp, &run, 1);
+        if (s != MUON_OK) return s;
+        e = timed(ctx, ST_EXPORT, 0.0, elems * 8.0, st, [&] { return muon::launch_export_x(g, w, x_out, st); });
+        if (e != hipSuccess) return hip_fail(ctx, e, "export launch");
+        ctx->last_stream = st;
+        ctx->last_count = 1;
+        ctx->last_nrm2 = w.call_nrm2;
+        ctx->err.clear();
+        return MUON_OK;
+    });
 }
 
 muon_status muon_apply_update(muon_context *ctx, void *param, int32_t param_dtype, const float *x, int64_t rows,
                               int64_t cols, const muon_hparams *hp, void *hip_stream) {
-    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
-    char msg[512];
-    if (!param || !x) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "param and x must be non-NULL");
-    if (param_dtype != MUON_F32 && param_dtype != MUON_BF16)
-        return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "unknown param dtype");
-    muon_status s = check_shape(rows, cols, msg, sizeof msg, 0);
-    if (s != MUON_OK) return fail(ctx, s, "%s", msg);
-    if ((s = check_hparams(hp, msg, sizeof msg)) != MUON_OK) return fail(ctx, s, "%s", msg);
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(param), b0 = reinterpret_cast<uintptr_t>(x);
-    const uintptr_t na = static_cast<uintptr_t>(rows * cols) * dtype_size(param_dtype);
-    const uintptr_t nx = static_cast<uintptr_t>(rows * cols) * 4;
-    if (a0 < b0 + nx && b0 < a0 + na) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "param and x overlap");
-    float d = 0.f, sc = 0.f;
-    muon_scalars(hp, rows, cols, &d, &sc);
-    DeviceGuard guard(ctx->device);
-    hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    const bool in_graph = capturing(st);
-    const double by = static_cast<double>(rows) * cols * (4.0 + 2.0 * dtype_size(param_dtype));
-    const float *s_dev = nullptr;
-    hipError_t e = hipSuccess;
-    if (hp->scale_mode == MUON_SCALE_UNIT_RMS) {
-        // ||x||^2 over the plain rows x cols matrix: rows reduced in up to 1024
-        // blocks, the scale written after the partial sums.
-        const int nbx = static_cast<int>(std::min<int64_t>(rows, 1024));
-        const size_t part = align_up(static_cast<size_t>(nbx) * sizeof(double));
-        if ((s = ensure(ctx, ctx->tabs, part + sizeof(float), "norm tables", in_graph)) != MUON_OK) return s;
-        Geom g{};
-        g.rows = g.s = g.sp = rows;
-        g.cols = g.l = g.lp = cols;
-        Work w{};
-        w.partials = static_cast<double *>(ctx->tabs.p);
-        float *sd = reinterpret_cast<float *>(static_cast<char *>(ctx->tabs.p) + part);
-        const double gsq = hp->gamma * std::sqrt(static_cast<double>(rows) * static_cast<double>(cols));
-        e = timed(ctx, ST_UNIT_RMS, 0.0, static_cast<double>(rows) * cols * 4.0, st, [&] {
-            return muon::launch_unit_rms_scale(1, g, w, x, nbx, hp->lr, gsq, sd, st);
+    return guarded(ctx, [&]() -> muon_status {
+        if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+        char msg[512];
+        if (!param || !x) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "param and x must be non-NULL");
+        if (param_dtype != MUON_F32 && param_dtype != MUON_BF16)
+            return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "unknown param dtype");
+        muon_status s = check_shape(rows, cols, msg, sizeof msg, 0);
+        if (s != MUON_OK) return fail(ctx, s, "%s", msg);
+        if ((s = check_hparams(hp, msg, sizeof msg)) != MUON_OK) return fail(ctx, s, "%s", msg);
+        const uintptr_t a0 = reinterpret_cast<uintptr_t>(param), b0 = reinterpret_cast<uintptr_t>(x);
+        const uintptr_t na = static_cast<uintptr_t>(rows * cols) * dtype_size(param_dtype);
+        const uintptr_t nx = static_cast<uintptr_t>(rows * cols) * 4;
+        if (a0 < b0 + nx && b0 < a0 + na) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "param and x overlap");
+        float d = 0.f, sc = 0.f;
+        muon_scalars(hp, rows, cols, &d, &sc);
+        DeviceGuard guard(ctx->device);
+        hipStream_t st = static_cast<hipStream_t>(hip_stream);
+        const bool in_graph = capturing(st);
+        const double by = static_cast<double>(rows) * cols * (4.0 + 2.0 * dtype_size(param_dtype));
+        const float *s_dev = nullptr;
+        hipError_t e = hipSuccess;
+        if (hp->scale_mode == MUON_SCALE_UNIT_RMS) {
+            // ||x||^2 over the plain rows x cols matrix: rows reduced in up to 1024
+            // blocks, the scale written after the partial sums.
+            const int nbx = static_cast<int>(std::min<int64_t>(rows, 1024));
+            const size_t part = align_up(static_cast<size_t>(nbx) * sizeof(double));
+            if ((s = ensure(ctx, ctx->tabs, part + sizeof(float), "norm tables", in_graph)) != MUON_OK) return s;
+            Geom g{};
+            g.rows = g.s = g.sp = rows;
+            g.cols = g.l = g.lp = cols;
+            Work w{};
+            w.partials = static_cast<double *>(ctx->tabs.p);
+            float *sd = reinterpret_cast<float *>(static_cast<char *>(ctx->tabs.p) + part);
+            const double gsq = hp->gamma * std::sqrt(static_cast<double>(rows) * static_cast<double>(cols));
+            e = timed(ctx, ST_UNIT_RMS, 0.0, static_cast<double>(rows) * cols * 4.0, st, [&] {
+                return muon::launch_unit_rms_scale(1, g, w, x, nbx, hp->lr, gsq, sd, st);
+            });
+            if (e != hipSuccess) return hip_fail(ctx, e, "unit-RMS norm launch");
+            s_dev = sd;
+        }
+        e = timed(ctx, ST_UPDATE, 0.0, by, st, [&] {
+            return muon::launch_update_plain(param, param_dtype == MUON_BF16, x, rows * cols, d, sc, s_dev, st);
         });
-        if (e != hipSuccess) return hip_fail(ctx, e, "unit-RMS norm launch");
-        s_dev = sd;
-    }
-    e = timed(ctx, ST_UPDATE, 0.0, by, st, [&] {
-        return muon::launch_update_plain(param, param_dtype == MUON_BF16, x, rows * cols, d, sc, s_dev, st);
+        if (e != hipSuccess) return hip_fail(ctx, e, "update launch");
+        ctx->err.clear();
+        return MUON_OK;
     });
-    if (e != hipSuccess) return hip_fail(ctx, e, "update launch");
-    ctx->err.clear();
-    return MUON_OK;
 }
 
 muon_status muon_adamw_step(muon_context *ctx, const muon_adamw_tensor *ts, int64_t count,
                             const muon_adamw_hparams *hp, void *hip_stream) {
-    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
-    char msg[512];
-    muon_status s = check_adamw(ts, count, hp, msg, sizeof msg);
-    if (s != MUON_OK) return fail(ctx, s, "%s", msg);
-    const muon::AdamwScalars k = adamw_scalars(hp);
-    const size_t ds = muon::adamw_desc_size();
-    std::vector<unsigned char> table;
-    int64_t blocks = 0;
-    int n = 0;
-    for (int64_t i = 0; i < count; ++i) {
-        if (ts[i].numel == 0) continue;
-        table.resize(table.size() + ds);
-        muon::adamw_fill_desc(table.data() + table.size() - ds, static_cast<float *>(ts[i].param),
-                              static_cast<const float *>(ts[i].grad), ts[i].exp_avg, ts[i].exp_avg_sq, ts[i].numel,
-                              blocks);
-        blocks += muon::adamw_blocks(ts[i].numel);
-        ++n;
-    }
-    if (n == 0) { ctx->err.clear(); return MUON_OK; }
-    if (blocks > (int64_t(1) << 31) - 1) return fail(ctx, MUON_ERR_UNSUPPORTED, "AdamW call too large for one grid");
-    DeviceGuard guard(ctx->device);
-    hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    const bool in_graph = capturing(st);
-    s = upload(ctx, ctx->adamw_desc, ctx->adamw_cache, table.data(), table.size(), st, "AdamW descriptors", in_graph);
-    if (s != MUON_OK) return s;
-    double elems = 0;
-    for (int64_t i = 0; i < count; ++i) elems += static_cast<double>(ts[i].numel);
-    hipError_t e = timed(ctx, ST_ADAMW, 0.0, elems * 28.0, st,
-                         [&] { return muon::launch_adamw(ctx->adamw_desc.p, n, blocks, k, st); });
-    if (e != hipSuccess) return hip_fail(ctx, e, "AdamW launch");
-    ctx->err.clear();
-    return MUON_OK;
+    return guarded(ctx, [&]() -> muon_status {
+        if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+        char msg[512];
+        muon_status s = check_adamw(ts, count, hp, msg, sizeof msg);
+        if (s != MUON_OK) return fail(ctx, s, "%s", msg);
+        const muon::AdamwScalars k = adamw_scalars(hp);
+        const size_t ds = muon::adamw_desc_size();
+        std::vector<unsigned char> table;
+        int64_t blocks = 0;
+        int n = 0;
+        for (int64_t i = 0; i < count; ++i) {
+            if (ts[i].numel == 0) continue;
+            table.resize(table.size() + ds);
+            muon::adamw_fill_desc(table.data() + table.size() - ds, static_cast<float *>(ts[i].param),
+                                  static_cast<const float *>(ts[i].grad), ts[i].exp_avg, ts[i].exp_avg_sq, ts[i].numel,
+                                  blocks);
+            blocks += muon::adamw_blocks(ts[i].numel);
+            ++n;
+        }
+        if (n == 0) { ctx->err.clear(); return MUON_OK; }
+        if (blocks > (int64_t(1) << 31) - 1) return fail(ctx, MUON_ERR_UNSUPPORTED, "AdamW call too large for one grid");
+        DeviceGuard guard(ctx->device);
+        hipStream_t st = static_cast<hipStream_t>(hip_stream);
+        const bool in_graph = capturing(st);
+        s = upload(ctx, ctx->adamw_desc, ctx->adamw_cache, table.data(), table.size(), st, "AdamW descriptors", in_graph);
+        if (s != MUON_OK) return s;
+        double elems = 0;
+        for (int64_t i = 0; i < count; ++i) elems += static_cast<double>(ts[i].numel);
+        hipError_t e = timed(ctx, ST_ADAMW, 0.0, elems * 28.0, st,
+                             [&] { return muon::launch_adamw(ctx->adamw_desc.p, n, blocks, k, st); });
+        if (e != hipSuccess) return hip_fail(ctx, e, "AdamW launch");
+        ctx->err.clear();
+        return MUON_OK;
+    });
 }
 
 muon_status muon_adamw_mixed_step(muon_context *ctx, const muon_adamw_mixed_tensor *ts, int64_t count,
                                   const muon_adamw_hparams *hp, const float *grad_factor, void *hip_stream) {
     if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
-    return guarded([&]() -> muon_status {
+    return guarded(ctx, [&]() -> muon_status {
         char msg[512];
         const muon_status s = check_adamw_mixed(ts, count, hp, grad_factor, msg, sizeof msg);
         if (s != MUON_OK) return fail(ctx, s, "%s", msg);
@@ -1873,7 +1898,7 @@ muon_status muon_adamw8_step(muon_context *ctx, const muon_adamw8_tensor *ts, in
                              const muon_adamw_hparams *hp, uint64_t seed, const float *grad_factor,
                              void *hip_stream) {
     if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
-    return guarded([&]() -> muon_status {
+    return guarded(ctx, [&]() -> muon_status {
         char msg[512];
         const muon_status s = check_adamw8(ts, count, hp, grad_factor, msg, sizeof msg);
         if (s != MUON_OK) return fail(ctx, s, "%s", msg);
@@ -1905,7 +1930,7 @@ muon_status muon_adamw8_step(muon_context *ctx, const muon_adamw8_tensor *ts, in
 muon_status muon_grad_norm(muon_context *ctx, const muon_grad *gs, int64_t count, double max_norm, double *norm,
                            float *factor, void *hip_stream) {
     if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
-    return guarded([&]() -> muon_status {
+    return guarded(ctx, [&]() -> muon_status {
         char msg[512];
         const muon_status s = check_grad_norm(gs, count, max_norm, norm, factor, msg, sizeof msg);
         if (s != MUON_OK) return fail(ctx, s, "%s", msg);
@@ -1947,108 +1972,114 @@ muon_status muon_grad_norm(muon_context *ctx, const muon_grad *gs, int64_t count
 
 muon_status muon_ns_stage(muon_context *ctx, int32_t stage, const float *x, const float *m, float *out, int64_t s,
                           int64_t l, double a, double b, double c, void *hip_stream) {
-    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
-    if (stage != MUON_STAGE_GRAM && stage != MUON_STAGE_POLY && stage != MUON_STAGE_APPLY)
-        return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "unknown stage %d", stage);
-    if (!out || (stage != MUON_STAGE_POLY && !x) || (stage != MUON_STAGE_GRAM && !m))
-        return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "missing operand or output");
-    if (s < 1 || l < s || l > kMaxDim || s * l > kMaxElems)
-        return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "unsupported shape %lld x %lld (need 1 <= s <= l)", (long long)s,
-                    (long long)l);
-    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
-        return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "non-finite coefficient");
-    const uintptr_t o0 = reinterpret_cast<uintptr_t>(out);
-    const uintptr_t on = static_cast<uintptr_t>(stage == MUON_STAGE_APPLY ? s * l : s * s) * 4;
-    for (const float *in : {x, m}) {
-        if (!in) continue;
-        const uintptr_t i0 = reinterpret_cast<uintptr_t>(in);
-        const uintptr_t in_n = static_cast<uintptr_t>(in == x ? s * l : s * s) * 4;
-        if (i0 < o0 + on && o0 < i0 + in_n) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "an operand overlaps out");
-    }
-    const Geom g = make_geom(s, l);
-    const Splits sp = plan_splits(g, true, 1);
-    const size_t need = chunk_layout(g, true, 1, sp.kpart(1)).total;
-    if (ctx->cap && need > ctx->cap)
-        return fail(ctx, MUON_ERR_OUT_OF_MEMORY, "matrix needs %zu bytes of workspace, above the cap", need);
-    DeviceGuard guard(ctx->device);
-    hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    const bool in_graph = capturing(st);
-    muon_status rs;
-    if ((rs = ensure(ctx, ctx->ws, need, "workspace", in_graph)) != MUON_OK) return rs;
-    if ((rs = ensure(ctx, ctx->tabs, tabs_bytes(1, 1), "norm tables", in_graph)) != MUON_OK) return rs;
-    if ((rs = ensure(ctx, ctx->call_nrm2, sizeof(double), "norm output", in_graph)) != MUON_OK) return rs;
-    Work w = chunk_work(CallMem{static_cast<char *>(ctx->ws.p), static_cast<char *>(ctx->tabs.p),
-                                static_cast<double *>(ctx->call_nrm2.p)},
-                        g, true, 1, 1, sp.kpart(1));
-    muon::NsStep p{};
-    p.a = static_cast<float>(a);
-    p.b = static_cast<float>(b);
-    p.c = static_cast<float>(c);
-    p.gram_splits = sp.gram;
-    p.gram_units = sp.gram_units;
-    p.poly_splits = sp.poly;
-    p.poly_units = sp.poly_units;
-    p.split_from = sp.from;
-    p.apply_splits = sp.apply;
-    p.apply_units = sp.apply_units;
-    p.apply_split_from = sp.apply_from;
-    hipError_t e = hipSuccess;
-    if (stage != MUON_STAGE_POLY) e = muon::launch_import_pair(g, x, w, st);
-    if (e == hipSuccess && stage != MUON_STAGE_GRAM)
-        e = muon::launch_import_bf16_square(s, g.sp, m, stage == MUON_STAGE_POLY ? w.ab : w.bb, st);
-    if (e != hipSuccess) return hip_fail(ctx, e, "operand import");
-    const int kind = stage == MUON_STAGE_GRAM ? 0 : stage == MUON_STAGE_POLY ? 1 : 2;
-    double fl = 0, by = 0;
-    ns_work(kind == 0 ? ST_GRAM : kind == 1 ? ST_POLY : ST_APPLY, g, true, 1, false, 2, &fl, &by);
-    e = timed(ctx, kind == 0 ? ST_GRAM : kind == 1 ? ST_POLY : ST_APPLY, fl, by, st,
-              [&] { return muon::launch_ns_stage_bf16(kind, nullptr, 1, g, w, p, st); });
-    if (e != hipSuccess) return hip_fail(ctx, e, "Newton-Schulz launch");
-    if (stage == MUON_STAGE_APPLY) {
-        std::swap(w.xb, w.xb_next);
-        e = muon::launch_export_x(g, w, out, st);
-    } else {
-        e = muon::launch_export_bf16_square(s, g.sp, stage == MUON_STAGE_GRAM ? w.ab : w.bb, out, st);
-    }
-    if (e != hipSuccess) return hip_fail(ctx, e, "export launch");
-    ctx->err.clear();
-    return MUON_OK;
+    return guarded(ctx, [&]() -> muon_status {
+        if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+        if (stage != MUON_STAGE_GRAM && stage != MUON_STAGE_POLY && stage != MUON_STAGE_APPLY)
+            return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "unknown stage %d", stage);
+        if (!out || (stage != MUON_STAGE_POLY && !x) || (stage != MUON_STAGE_GRAM && !m))
+            return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "missing operand or output");
+        if (s < 1 || l < s || l > kMaxDim || s * l > kMaxElems)
+            return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "unsupported shape %lld x %lld (need 1 <= s <= l)", (long long)s,
+                        (long long)l);
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+            return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "non-finite coefficient");
+        const uintptr_t o0 = reinterpret_cast<uintptr_t>(out);
+        const uintptr_t on = static_cast<uintptr_t>(stage == MUON_STAGE_APPLY ? s * l : s * s) * 4;
+        for (const float *in : {x, m}) {
+            if (!in) continue;
+            const uintptr_t i0 = reinterpret_cast<uintptr_t>(in);
+            const uintptr_t in_n = static_cast<uintptr_t>(in == x ? s * l : s * s) * 4;
+            if (i0 < o0 + on && o0 < i0 + in_n) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "an operand overlaps out");
+        }
+        const Geom g = make_geom(s, l);
+        const Splits sp = plan_splits(g, true, 1);
+        const size_t need = chunk_layout(g, true, 1, sp.kpart(1)).total;
+        if (ctx->cap && need > ctx->cap)
+            return fail(ctx, MUON_ERR_OUT_OF_MEMORY, "matrix needs %zu bytes of workspace, above the cap", need);
+        DeviceGuard guard(ctx->device);
+        hipStream_t st = static_cast<hipStream_t>(hip_stream);
+        const bool in_graph = capturing(st);
+        muon_status rs;
+        if ((rs = ensure(ctx, ctx->ws, need, "workspace", in_graph)) != MUON_OK) return rs;
+        if ((rs = ensure(ctx, ctx->tabs, tabs_bytes(1, 1), "norm tables", in_graph)) != MUON_OK) return rs;
+        if ((rs = ensure(ctx, ctx->call_nrm2, sizeof(double), "norm output", in_graph)) != MUON_OK) return rs;
+        Work w = chunk_work(CallMem{static_cast<char *>(ctx->ws.p), static_cast<char *>(ctx->tabs.p),
+                                    static_cast<double *>(ctx->call_nrm2.p)},
+                            g, true, 1, 1, sp.kpart(1));
+        muon::NsStep p{};
+        p.a = static_cast<float>(a);
+        p.b = static_cast<float>(b);
+        p.c = static_cast<float>(c);
+        p.gram_splits = sp.gram;
+        p.gram_units = sp.gram_units;
+        p.poly_splits = sp.poly;
+        p.poly_units = sp.poly_units;
+        p.split_from = sp.from;
+        p.apply_splits = sp.apply;
+        p.apply_units = sp.apply_units;
+        p.apply_split_from = sp.apply_from;
+        hipError_t e = hipSuccess;
+        if (stage != MUON_STAGE_POLY) e = muon::launch_import_pair(g, x, w, st);
+        if (e == hipSuccess && stage != MUON_STAGE_GRAM)
+            e = muon::launch_import_bf16_square(s, g.sp, m, stage == MUON_STAGE_POLY ? w.ab : w.bb, st);
+        if (e != hipSuccess) return hip_fail(ctx, e, "operand import");
+        const int kind = stage == MUON_STAGE_GRAM ? 0 : stage == MUON_STAGE_POLY ? 1 : 2;
+        double fl = 0, by = 0;
+        ns_work(kind == 0 ? ST_GRAM : kind == 1 ? ST_POLY : ST_APPLY, g, true, 1, false, 2, &fl, &by);
+        e = timed(ctx, kind == 0 ? ST_GRAM : kind == 1 ? ST_POLY : ST_APPLY, fl, by, st,
+                  [&] { return muon::launch_ns_stage_bf16(kind, nullptr, 1, g, w, p, st); });
+        if (e != hipSuccess) return hip_fail(ctx, e, "Newton-Schulz launch");
+        if (stage == MUON_STAGE_APPLY) {
+            std::swap(w.xb, w.xb_next);
+            e = muon::launch_export_x(g, w, out, st);
+        } else {
+            e = muon::launch_export_bf16_square(s, g.sp, stage == MUON_STAGE_GRAM ? w.ab : w.bb, out, st);
+        }
+        if (e != hipSuccess) return hip_fail(ctx, e, "export launch");
+        ctx->err.clear();
+        return MUON_OK;
+    });
 }
 
 muon_status muon_stream_probe(muon_context *ctx, const void *src, void *dst, int64_t stream_bytes,
                               int64_t pitch_bytes, int32_t reads, int32_t writes, void *hip_stream) {
-    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
-    if (!src || !dst || stream_bytes <= 0 || stream_bytes % 16 != 0 || pitch_bytes < stream_bytes ||
-        pitch_bytes % 16 != 0 || (reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) % 16 != 0)
-        return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "src and dst must be 16-byte aligned, stream_bytes a positive "
-                                                    "multiple of 16, pitch_bytes a multiple of 16 >= stream_bytes");
-    if (!((reads == 6 && writes == 7) || (reads == 4 && writes == 3) || (reads == 5 && writes == 2) ||
-          (reads == 1 && writes == 1)))
-        return fail(ctx, MUON_ERR_UNSUPPORTED, "no probe for %d reads : %d writes", reads, writes);
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(src), b0 = reinterpret_cast<uintptr_t>(dst);
-    const uintptr_t na = static_cast<uintptr_t>(pitch_bytes) * (reads - 1) + static_cast<uintptr_t>(stream_bytes);
-    const uintptr_t nb = static_cast<uintptr_t>(pitch_bytes) * (writes - 1) + static_cast<uintptr_t>(stream_bytes);
-    if (a0 < b0 + nb && b0 < a0 + na) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "src and dst overlap");
-    DeviceGuard guard(ctx->device);
-    hipStream_t st = static_cast<hipStream_t>(hip_stream);
-    hipError_t e = timed(ctx, ST_PROBE, 0.0, static_cast<double>(stream_bytes) * (reads + writes), st, [&] {
-        return muon::launch_stream_probe(src, dst, stream_bytes / 16, pitch_bytes / 16, reads, writes, st);
+    return guarded(ctx, [&]() -> muon_status {
+        if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+        if (!src || !dst || stream_bytes <= 0 || stream_bytes % 16 != 0 || pitch_bytes < stream_bytes ||
+            pitch_bytes % 16 != 0 || (reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) % 16 != 0)
+            return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "src and dst must be 16-byte aligned, stream_bytes a positive "
+                                                        "multiple of 16, pitch_bytes a multiple of 16 >= stream_bytes");
+        if (!((reads == 6 && writes == 7) || (reads == 4 && writes == 3) || (reads == 5 && writes == 2) ||
+              (reads == 1 && writes == 1)))
+            return fail(ctx, MUON_ERR_UNSUPPORTED, "no probe for %d reads : %d writes", reads, writes);
+        const uintptr_t a0 = reinterpret_cast<uintptr_t>(src), b0 = reinterpret_cast<uintptr_t>(dst);
+        const uintptr_t na = static_cast<uintptr_t>(pitch_bytes) * (reads - 1) + static_cast<uintptr_t>(stream_bytes);
+        const uintptr_t nb = static_cast<uintptr_t>(pitch_bytes) * (writes - 1) + static_cast<uintptr_t>(stream_bytes);
+        if (a0 < b0 + nb && b0 < a0 + na) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "src and dst overlap");
+        DeviceGuard guard(ctx->device);
+        hipStream_t st = static_cast<hipStream_t>(hip_stream);
+        hipError_t e = timed(ctx, ST_PROBE, 0.0, static_cast<double>(stream_bytes) * (reads + writes), st, [&] {
+            return muon::launch_stream_probe(src, dst, stream_bytes / 16, pitch_bytes / 16, reads, writes, st);
+        });
+        if (e != hipSuccess) return hip_fail(ctx, e, "probe launch");
+        ctx->err.clear();
+        return MUON_OK;
     });
-    if (e != hipSuccess) return hip_fail(ctx, e, "probe launch");
-    ctx->err.clear();
-    return MUON_OK;
 }
 
 muon_status muon_last_norms(muon_context *ctx, double *out, int64_t capacity, int64_t *count_out) {
-    if (!ctx || !count_out || capacity < 0 || (capacity > 0 && !out)) return MUON_ERR_INVALID_ARGUMENT;
-    *count_out = ctx->last_count;
-    const int64_t n = std::min(capacity, ctx->last_count);
-    if (n == 0) return MUON_OK;
-    DeviceGuard guard(ctx->device);
-    hipError_t e = hipStreamSynchronize(ctx->last_stream);
-    if (e != hipSuccess) return hip_fail(ctx, e, "hipStreamSynchronize");
-    e = hipMemcpy(out, ctx->last_nrm2, static_cast<size_t>(n) * sizeof(double), hipMemcpyDeviceToHost);
-    if (e != hipSuccess) return hip_fail(ctx, e, "hipMemcpy");
-    return MUON_OK;
+    return guarded(ctx, [&]() -> muon_status {
+        if (!ctx || !count_out || capacity < 0 || (capacity > 0 && !out)) return MUON_ERR_INVALID_ARGUMENT;
+        *count_out = ctx->last_count;
+        const int64_t n = std::min(capacity, ctx->last_count);
+        if (n == 0) return MUON_OK;
+        DeviceGuard guard(ctx->device);
+        hipError_t e = hipStreamSynchronize(ctx->last_stream);
+        if (e != hipSuccess) return hip_fail(ctx, e, "hipStreamSynchronize");
+        e = hipMemcpy(out, ctx->last_nrm2, static_cast<size_t>(n) * sizeof(double), hipMemcpyDeviceToHost);
+        if (e != hipSuccess) return hip_fail(ctx, e, "hipMemcpy");
+        return MUON_OK;
+    });
 }
 
 muon_status muon_set_concurrent_groups(muon_context *ctx, int32_t enable) {
@@ -2066,31 +2097,33 @@ muon_status muon_profile_enable(muon_context *ctx, int32_t enable) {
 }
 
 muon_status muon_profile_read(muon_context *ctx, muon_stage_stats *out, int32_t capacity, int32_t *count) {
-    if (!ctx || !count || capacity < 0 || (capacity > 0 && !out)) return MUON_ERR_INVALID_ARGUMENT;
-    DeviceGuard guard(ctx->device);
-    std::vector<int> order;
-    std::vector<muon_stage_stats> agg(ST_COUNT);
-    for (int i = 0; i < ST_COUNT; ++i) {
-        std::memset(&agg[i], 0, sizeof agg[i]);
-        std::snprintf(agg[i].name, sizeof agg[i].name, "%s", kStageNames[i]);
-    }
-    for (const auto &r : ctx->recs) {
-        hipError_t e = hipEventSynchronize(r.b);
-        if (e != hipSuccess) return hip_fail(ctx, e, "hipEventSynchronize");
-        float ms = 0.f;
-        e = hipEventElapsedTime(&ms, r.a, r.b);
-        if (e != hipSuccess) return hip_fail(ctx, e, "hipEventElapsedTime");
-        if (agg[r.stage].launches == 0) order.push_back(r.stage);
-        agg[r.stage].launches += 1;
-        agg[r.stage].total_ms += ms;
-        agg[r.stage].flops += r.flops;
-        agg[r.stage].bytes += r.bytes;
-    }
-    *count = static_cast<int32_t>(order.size());
-    for (int i = 0; i < static_cast<int>(order.size()) && i < capacity; ++i) out[i] = agg[order[i]];
-    ctx->recs.clear();
-    ctx->ev_used = 0;
-    return MUON_OK;
+    return guarded(ctx, [&]() -> muon_status {
+        if (!ctx || !count || capacity < 0 || (capacity > 0 && !out)) return MUON_ERR_INVALID_ARGUMENT;
+        DeviceGuard guard(ctx->device);
+        std::vector<int> order;
+        std::vector<muon_stage_stats> agg(ST_COUNT);
+        for (int i = 0; i < ST_COUNT; ++i) {
+            std::memset(&agg[i], 0, sizeof agg[i]);
+            std::snprintf(agg[i].name, sizeof agg[i].name, "%s", kStageNames[i]);
+        }
+        for (const auto &r : ctx->recs) {
+            hipError_t e = hipEventSynchronize(r.b);
+            if (e != hipSuccess) return hip_fail(ctx, e, "hipEventSynchronize");
+            float ms = 0.f;
+            e = hipEventElapsedTime(&ms, r.a, r.b);
+            if (e != hipSuccess) return hip_fail(ctx, e, "hipEventElapsedTime");
+            if (agg[r.stage].launches == 0) order.push_back(r.stage);
+            agg[r.stage].launches += 1;
+            agg[r.stage].total_ms += ms;
+            agg[r.stage].flops += r.flops;
+            agg[r.stage].bytes += r.bytes;
+        }
+        *count = static_cast<int32_t>(order.size());
+        for (int i = 0; i < static_cast<int>(order.size()) && i < capacity; ++i) out[i] = agg[order[i]];
+        ctx->recs.clear();
+        ctx->ev_used = 0;
+        return MUON_OK;
+    });
 }
 
 }  // extern "C"

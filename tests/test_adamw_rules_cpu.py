@@ -134,3 +134,22 @@ def test_oracle_8_bit_weights_are_those_of_the_32_bit_step():
             p8, update, _ = oracle.adamw8_step(p, g, state, *args)
         assert np.isfinite(v32).all() and v32.max() > 2.0 ** 120
         assert (np.abs(p8 - p32) <= 2.0 ** -24 * (9 * np.abs(update) + 3 * np.maximum(np.abs(p), np.abs(p32)))).all()
+
+
+def test_no_exception_leaves_the_checks():
+    """A count that no host memory could list is an error, not the end of the process."""
+    code = """if True:
+        import ctypes, muon_step_amd as ms
+        lib, buf = ms.load(), ctypes.create_string_buffer(100)
+        mats, need = (ms.muon_matrix * 1)(), ctypes.c_size_t()
+        for count in (1 << 62, 1 << 60, (1 << 63) - 1):
+            hp = ctypes.byref(ms.make_hparams())
+            print(lib.muon_check_step_args(mats, count, hp, buf, 100), buf.value.decode())
+            print(lib.muon_check_step_args(mats, count, hp, None, 0))
+            print(lib.muon_workspace_bytes(mats, count, hp, ctypes.byref(need)))
+        """
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=100)
+    assert res.returncode == 0, res.stderr
+    out = ms.MUON_ERR_OUT_OF_MEMORY
+    assert res.stdout.splitlines() == [f"{out} out of host memory", f"{out}", f"{out}"] * 3
