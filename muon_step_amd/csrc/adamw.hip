@@ -399,6 +399,7 @@ constexpr uint32_t kMaxGrid = 1u << 23;
 template <class Table, class Scalars, class Kernel>
 hipError_t launch_table(Kernel kernel, const Table &t, uint32_t blocks, const Scalars &k, const float *factor,
                         hipStream_t st) {
+    static_assert(sizeof(Table) <= kTableBytes && sizeof(Table) + sizeof(Scalars) + 16 <= 4096, "kernel arguments");
     for (uint32_t b0 = 0; b0 < blocks; b0 += kMaxGrid) {
         hipLaunchKernelGGL(kernel, dim3(std::min(kMaxGrid, blocks - b0)), dim3(kThreads), 0, st, t, b0, k, factor);
         const hipError_t err = hipGetLastError();

@@ -80,8 +80,14 @@ void adamw_fill_desc(void *dst, float *param, const float *grad, float *m, float
                      int64_t first_block);
 
 // ---- AdamW in mixed types (adamw.hip)
-// Tensors of one launch, passed by value (tensor_table.hpp): a launch's
-// arguments stay below 4 KB.
+// Tensors of one launch, passed by value (tensor_table.hpp): as many as the 4 KB
+// of a launch's arguments hold beside its scalars, 64 at most (the entries that
+// a wave looks up at once).
+constexpr int kTableBytes = 4096 - 64;
+constexpr int table_tensors(int desc_bytes) {
+    const int n = (kTableBytes - 64 * 4) / desc_bytes;
+    return n < 64 ? n : 64;
+}
 struct MixedDesc {
     void *param;
     float *master;  // or nullptr
@@ -89,7 +95,7 @@ struct MixedDesc {
     float *m, *v;
     int64_t numel;
 };
-constexpr int kMixedTensors = 64;
+constexpr int kMixedTensors = table_tensors(sizeof(MixedDesc));  // 64
 struct MixedTable {
     uint32_t first[64];
     MixedDesc d[kMixedTensors];
@@ -101,7 +107,7 @@ struct ByteDesc {
     uint8_t *m, *v, *m_scale, *v_scale;
     int64_t numel;
 };
-constexpr int kByteTensors = 56;
+constexpr int kByteTensors = table_tensors(sizeof(ByteDesc));  // 59
 struct ByteTable {
     uint32_t first[64];
     ByteDesc d[kByteTensors];

@@ -280,3 +280,15 @@ def test_clipped_muon_and_adamw_steps_captured(torch, ms):
         torch.cuda.synchronize()
         for c in (graph_ctx, eager_ctx):
             c.close()
+
+
+@pytest.mark.parametrize("count", [58, 59, 60, 64, 65, 130])
+@pytest.mark.parametrize("eight", [False, True])
+def test_more_tensors_of_one_kind_than_a_launch_takes(ctx, torch, ms, eight, count):
+    """Around the number of tensors that one launch's arguments hold, and past two of them."""
+    rng = np.random.default_rng(65)
+    cases = [Case(torch, ms, eight, rng, int(rng.integers(1, 700)), ("bf16", True, "bf16"), 2) for _ in range(count)]
+    _step(ctx, ms, cases, 2, torch.full((1,), 0.5, device="cuda"))
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check(2, 0.5)
