@@ -153,3 +153,33 @@ def test_no_exception_leaves_the_checks():
     assert res.returncode == 0, res.stderr
     out = ms.MUON_ERR_OUT_OF_MEMORY
     assert res.stdout.splitlines() == [f"{out} out of host memory", f"{out}", f"{out}"] * 3
+
+
+def test_slow_second_moment_over_many_steps():
+    """A second moment at b2 = 0.999 over 2000 steps of constant gradients: unbiased, and its noise stays within what
+    the rounding's variance gives.  A step moves a code c by d <= (1 - b2) c at most once it is settled, and rounds with
+    variance at most d x gap <= (1 - b2) c^2 / 8 (the gap is c / 8 at most); the sum over the steps, each weakened by
+    b2 a step, is at most 1 / (1 - b2^2) of that: c^2 / 16, a standard deviation of a quarter.  4096 elements are 1024
+    independent groups of four: their mean is within 5 x 1/4 / 32 = 4% of the exact one, and their deviation's estimate
+    within 5 / sqrt(2 x 1024) = 11% of the true one."""
+    n, steps, b2 = 4096, 2000, 0.999
+    rng = np.random.default_rng(23)
+    g = np.exp2(rng.uniform(-1, 1, n)).astype(np.float32)
+    k = oracle.adamw_scalars_f32(0.02, 0.9, b2, 1e-8, 0.1, 1)
+    codes, scale = np.zeros(n, np.uint8), np.zeros(n // 32, np.uint8)
+    index = np.arange(n)
+    for step in range(1, steps + 1):
+        v = oracle.moment_values(codes, scale).astype(np.float32)
+        v = (k["beta2"] * v) + ((k["one_minus_beta2"] * g) * g)
+        codes, scale = oracle.quantise(v, True, index, 99, step, 16)
+    ratio = oracle.moment_values(codes, scale) / ((1 - b2 ** steps) * g.astype(np.float64) ** 2)
+    assert abs(ratio.mean() - 1) <= 0.04
+    assert ratio.std() <= 0.25 * 1.11
+
+
+def test_words_of_the_two_moments():
+    """What the rounding's words share, as the format is defined: a group of four elements has one word, turned by a
+    byte for each, and an element's second moment takes the turn of the first moment of the element two further on."""
+    i = np.arange(64)
+    first, second = oracle.dither(i, 7, 3, 0), oracle.dither(i, 7, 3, 16)
+    assert np.array_equal(second, first[i // 4 * 4 + (i + 2) % 4])
