@@ -5,13 +5,15 @@
 // Compiled with -ffp-contract=off: a multiply and an add round once each unless
 // the code says fma.
 //
-// Both kernels are bound by HBM: they read and write every byte once (by
-// counter: 2.94 GB each way for the 28-byte step on 210e6 elements; 1.28 and
-// 0.85 GB for the 8-bit step on bf16 weights and gradients, 10.1 bytes an
-// element).  A plain copy moves 6.4 TB/s on the same card; 210e6 elements take
-//   32-bit moments, bf16 weights + fp32 master, bf16 gradients   931 us  6.3 TB/s
-//   8-bit moments, bf16 weights and gradients                    327 us  6.5 TB/s
-//   8-bit moments, bf16 weights + fp32 master, fp32 gradients    606 us  6.3 TB/s
+// Both kernels are bound by HBM.  The 32-bit step moves every byte once (by
+// counter 2.94 GB each way for its 28 bytes an element on 210e6 elements).  The
+// 8-bit step needs 1.27 GB in and 0.85 out for bf16 weights and gradients, 10.1
+// bytes an element, and by counter fetches 1.36 and writes 0.87: lines of scales
+// that workgroups on several XCDs share.  A plain copy moves 6.4 TB/s on the same
+// card; 210e6 elements take
+//   32-bit moments, bf16 weights + fp32 master, bf16 gradients   932 us  6.3 TB/s
+//   8-bit moments, bf16 weights and gradients                    328 us  6.5 TB/s
+//   8-bit moments, bf16 weights + fp32 master, fp32 gradients    607 us  6.3 TB/s
 // One vector a lane and one wave a workgroup: in workgroups of 128, 256 and 512
 // threads the first takes 946, 983 and 1018 us (smaller calls the same), with
 // two or four vectors a lane (256 threads) 1056 and 1018.
@@ -26,7 +28,7 @@ namespace muon {
 
 namespace {
 
-constexpr int kThreads = 64;  // one wave: see below
+constexpr int kThreads = 64;  // one wave: see above
 
 template <typename T> __device__ __forceinline__ float load_one(const T *p);
 template <> __device__ __forceinline__ float load_one<float>(const float *p) { return *as_global(p); }
