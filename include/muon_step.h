@@ -44,7 +44,7 @@
 extern "C" {
 #endif
 
-#define MUON_STEP_ABI_VERSION 5
+#define MUON_STEP_ABI_VERSION 6
 
 /* Bytes of the fixed per-GPU device scratch muon_step_noalloc works in. */
 #define MUON_NOALLOC_SCRATCH_BYTES 134217728
@@ -130,8 +130,8 @@ typedef struct muon_matrix {
  *   grad_factor   optional device float (muon_grad_norm's factor): G_t is then
  *                 fl32(factor * G_t), one rounding, wherever the step reads it.
  *                 It is read when the step runs.  NULL: no factor.  It must not
- *                 lie in memory that the step writes.  Read by muon_step and
- *                 muon_step_noalloc only.
+ *                 lie in memory that the step writes.  Read by muon_step,
+ *                 muon_step_noalloc and muon_blocks_step only.
  * lr, momentum, weight_decay and gamma must be finite. */
 typedef struct muon_hparams {
     double lr;
@@ -225,6 +225,31 @@ typedef struct muon_adamw8_tensor {
     int32_t grad_dtype;  /* muon_dtype */
 } muon_adamw8_tensor;
 
+/* One weight handed to muon_blocks_step: rows x cols, row-major, cut into a grid
+ * of blocks of block_rows x block_cols, each a matrix of its own for the method
+ * (the heads of an attention projection are row blocks of the query's weight and
+ * column blocks of the output's; an adapter's factor is one block).
+ *   param, grad, momentum, ns_out   as in muon_matrix
+ *   *_pitch      elements from one row to the next, at least cols; what lies
+ *                between the rows is neither read nor written
+ * block_rows and block_cols divide rows and cols; the smaller of them is at most
+ * MUON_BLOCK_SIDE, the larger at most 2^24; pitches are at most 2^27.  Addresses
+ * are multiples of their element's size.  No written element may be an element
+ * of another range of the call; ranges that interleave (two slices of the
+ * columns of one buffer) must have the same pitch in bytes. */
+#define MUON_BLOCK_SIDE 128
+typedef struct muon_block_matrix {
+    void *param;
+    const void *grad;
+    float *momentum;
+    float *ns_out;
+    int64_t rows, cols;
+    int64_t block_rows, block_cols;
+    int64_t param_pitch, grad_pitch, momentum_pitch, ns_out_pitch;
+    int32_t param_dtype; /* muon_dtype */
+    int32_t grad_dtype;  /* muon_dtype */
+} muon_block_matrix;
+
 /* One gradient of muon_grad_norm: numel contiguous elements, read only. */
 typedef struct muon_grad {
     const void *grad; /* device */
@@ -276,6 +301,10 @@ muon_status muon_check_adamw8_args(const muon_adamw8_tensor *ts, int64_t count, 
 muon_status muon_check_grad_norm_args(const muon_grad *gs, int64_t count, double max_norm, const double *norm,
                                       const float *factor, char *msg, size_t msg_cap);
 
+/* Host-only validation of a muon_blocks_step argument list. */
+muon_status muon_check_blocks_args(const muon_block_matrix *mats, int64_t count, const muon_hparams *hp, char *msg,
+                                   size_t msg_cap);
+
 /* Workspace the library would allocate for this argument list when nothing
  * caps it: the largest per-group chunk of Newton-Schulz buffers (with
  * concurrent groups, the largest of each lane's groups summed over the
@@ -324,6 +353,32 @@ const char *muon_last_error(const muon_context *ctx);
  * stay until muon_destroy.  A replay counts as a call on the context. */
 muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
                       const muon_hparams *hp, void *hip_stream);
+
+/* One Muon step over the blocks of `count` weights (host array mats): for each
+ * block W (n x m), with its own norm and its own max(n, m),
+ *     M <- mu M + G,  N = mu M + G (or M),  X = N / ||N||_F,
+ *     X <- a X + b (X X^T) X + c (X X^T)^2 X  for each step of the schedule,
+ *     W <- (1 - lr wd) W - lr O,  O as hp's scale_mode says, RMS block by block.
+ * M has muon_step's bits (and hp's grad_factor its meaning).  Operands of the
+ * products are fp32 values as pairs of 16-bit parts, so X is far closer to the
+ * exact iteration than MUON_NS_BF16's (relative Frobenius error 1e-6 to 1e-4,
+ * more only in directions whose singular value is below 1e-4 of ||N||); hp's
+ * ns_precision must be MUON_NS_BF16 (MUON_NS_F32: UNSUPPORTED).  The schedule
+ * must keep every singular value of [0, 1] within 3.9 at each step, with
+ * |a + b x + c x^2| and its product with x at most 60 on the x it meets
+ * (UNSUPPORTED otherwise; the named schedules stay within 1.3 and 4).  A block
+ * whose N is all zero gets the decay-only update, one with an infinity or a NaN
+ * in N becomes NaN in all its elements, and no other block does; the scale of N
+ * does not matter, from the smallest fp32 values to the largest.  A block's
+ * result does not depend on the other blocks of the call.
+ * Descriptors travel as kernel arguments; the step works in memory of the
+ * context, at most its workspace cap, which grows on first use: under graph
+ * capture the call works once a call with the same list has run, and is refused
+ * with MUON_ERR_UNSUPPORTED where the memory would have to grow.  A replay
+ * repeats the addresses and the host scalars of the capture, counts as a call on
+ * the context, and needs it until the last one. */
+muon_status muon_blocks_step(muon_context *ctx, const muon_block_matrix *mats, int64_t count,
+                             const muon_hparams *hp, void *hip_stream);
 
 /* Enables (1, the default) or disables (0) the concurrent execution of a
  * muon_step call's groups described above; disabled, every group runs in
@@ -501,7 +556,9 @@ muon_status muon_stream_probe(muon_context *ctx, const void *src, void *dst, int
  * A A, and the bytes it must move to and from HBM) is recorded with it.
  * Stage names: "momentum_nesterov", "norm_finalize", "normalize", "gram",
  * "poly", "apply", "apply_update" (the last product with the fused decay and
- * update), "update", "adamw", "adamw_mixed", "adamw8", "grad_norm", "import",
+ * update), "update", "adamw", "adamw_mixed", "adamw8", "grad_norm",
+ * "blocks_momentum", "blocks_chain", "blocks_regram", "blocks_update" (the four
+ * launches of muon_blocks_step), "import",
  * "export", "unit_rms" (the per-matrix ||X||^2 reduction and scale of the
  * unit-RMS mode), "stream_probe" (muon_stream_probe), "prenormalize" (the bf16
  * path's normalisation of the matrices whose ||N_t|| lies outside the range

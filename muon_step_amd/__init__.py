@@ -15,7 +15,7 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmuon_step.so")
 
-MUON_STEP_ABI_VERSION = 5  # of the header that the structures below mirror
+MUON_STEP_ABI_VERSION = 6  # of the header that the structures below mirror
 
 MUON_OK = 0
 MUON_ERR_INVALID_ARGUMENT = 1
@@ -38,7 +38,7 @@ EXPORTS = (
     "muon_last_norms", "muon_profile_enable", "muon_profile_read", "muon_step_noalloc",
     "muon_stream_probe", "muon_ns_stage", "muon_set_concurrent_groups",
     "muon_adamw_mixed_step", "muon_adamw8_step", "muon_grad_norm", "muon_check_adamw_mixed_args",
-    "muon_check_adamw8_args", "muon_check_grad_norm_args",
+    "muon_check_adamw8_args", "muon_check_grad_norm_args", "muon_blocks_step", "muon_check_blocks_args",
 )
 
 MUON_STAGE_GRAM = 0
@@ -46,6 +46,7 @@ MUON_STAGE_POLY = 1
 MUON_STAGE_APPLY = 2
 
 MUON_ADAMW8_BLOCK = 32
+MUON_BLOCK_SIDE = 128
 
 
 class MuonError(RuntimeError):
@@ -101,6 +102,14 @@ class muon_grad(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class muon_block_matrix(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p),
+                ("ns_out", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("block_rows", ctypes.c_int64), ("block_cols", ctypes.c_int64), ("param_pitch", ctypes.c_int64),
+                ("grad_pitch", ctypes.c_int64), ("momentum_pitch", ctypes.c_int64), ("ns_out_pitch", ctypes.c_int64),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
 class muon_stage_stats(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double),
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
@@ -151,6 +160,8 @@ def load(path=LIB_PATH):
         "muon_check_adamw8_args": (i32, [c.POINTER(muon_adamw8_tensor), i64, c.POINTER(muon_adamw_hparams), vp,
                                          c.c_char_p, sz]),
         "muon_check_grad_norm_args": (i32, [c.POINTER(muon_grad), i64, c.c_double, vp, vp, c.c_char_p, sz]),
+        "muon_blocks_step": (i32, [vp, c.POINTER(muon_block_matrix), i64, c.POINTER(muon_hparams), vp]),
+        "muon_check_blocks_args": (i32, [c.POINTER(muon_block_matrix), i64, c.POINTER(muon_hparams), c.c_char_p, sz]),
         "muon_ns_only": (i32, [vp, vp, vp, i64, i64, c.POINTER(muon_hparams), vp]),
         "muon_apply_update": (i32, [vp, vp, i32, vp, i64, i64, c.POINTER(muon_hparams), vp]),
         "muon_last_norms": (i32, [vp, c.POINTER(c.c_double), i64, c.POINTER(i64)]),
@@ -408,6 +419,14 @@ class Context:
                                      _stream_handle(stream, self.device))
         _check(self.lib, self.handle, st, "muon_grad_norm")
 
+    def muon_blocks_step(self, mats, hp, stream=None):
+        """mats: a list of block_matrix() or a table() of them; hp: make_hparams()."""
+        self._check_device(mats, "matrix")
+        self._check_hp_factor(hp)
+        arr = _array(mats, muon_block_matrix)
+        st = self.lib.muon_blocks_step(self.handle, arr, len(arr), ctypes.byref(hp), _stream_handle(stream, self.device))
+        _check(self.lib, self.handle, st, "muon_blocks_step")
+
     def muon_ns_only(self, n_in, x_out, hp, stream=None):
         named = [("n_in", n_in), ("x_out", x_out)]
         for name, t in named:
@@ -537,6 +556,32 @@ def _weights(param, grad, master):
             raise TypeError("a master copy goes with a bfloat16 param")
         _require_f32((("master", master),))
     return pd, gd
+
+
+_MATRIX_NAMES = ("param", "grad", "momentum", "ns_out")
+
+
+def block_matrix(param, grad, momentum, block_rows, block_cols, ns_out=None):
+    """muon_block_matrix for torch tensors: 2-D, of one shape, rows contiguous and any distance apart (views of a
+    larger tensor, too), one GPU; momentum and ns_out float32, param and grad float32 or bfloat16."""
+    tensors = (param, grad, momentum) if ns_out is None else (param, grad, momentum, ns_out)
+    rows, cols = param.shape if param.dim() == 2 else (0, 0)
+    pitches = []
+    for name, t in zip(_MATRIX_NAMES, tensors):
+        if t.dim() != 2 or t.shape != param.shape or rows == 0 or cols == 0:
+            raise ValueError("param, grad, momentum and ns_out must be 2-D, not empty and of one shape")
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows, got strides {tuple(t.stride())}")
+        pitches.append(max(t.stride(0), cols) if rows == 1 else t.stride(0))
+        if pitches[-1] < cols:
+            raise ValueError(f"{name}'s rows overlap: strides {tuple(t.stride())}")
+    _require_f32(list(zip(_MATRIX_NAMES, tensors))[2:])
+    pd, gd = _dtype_code(param), _dtype_code(grad)
+    dev = _gpu_index(_MATRIX_NAMES, tensors)
+    m = muon_block_matrix(param.data_ptr(), grad.data_ptr(), momentum.data_ptr(),
+                          None if ns_out is None else ns_out.data_ptr(), rows, cols, block_rows, block_cols, *pitches[:3],
+                          0 if ns_out is None else pitches[3], pd, gd)
+    return _owning(m, dev, tensors)
 
 
 _MIXED_NAMES = ("param", "grad", "exp_avg", "exp_avg_sq", "master")

@@ -1,0 +1,87 @@
+// Muon steps on the blocks of a weight (blocks.hip): what host and kernels share.
+#pragma once
+
+#include "common.hpp"
+
+namespace muon {
+
+// One weight of a launch: a grid of blocks, `across` of them beside each other.
+struct BlockDesc {
+    void *param;
+    const void *grad;
+    float *mom;
+    float *ns_out;  // or nullptr
+    uint32_t param_pitch, grad_pitch, mom_pitch, out_pitch;  // elements from row to row
+    uint32_t across;
+    uint32_t pad_;
+};
+// Weights of one launch, by value: 64 of 56 bytes, their first blocks, and the
+// call's scalars fill the 4 KB of a launch's arguments.
+constexpr int kBlockTensors = 64;
+struct BlockTable {
+    uint32_t first[kBlockTensors];  // blocks before each weight; 0xffffffff past the last
+    BlockDesc d[kBlockTensors];
+};
+
+constexpr int kBlockSide = 128;      // largest smaller side of a block: four tiles of 32
+constexpr int kBlockUnit = 128;      // columns of X that a workgroup takes at once: 32 for each wave
+constexpr int kMaxChainSteps = 64;
+
+// What one block needs between the launches (index: block of the launch).
+struct BlockScalars {
+    float inv_norm;   // 1 / ||N 2^shift||
+    int32_t shift;    // N 2^shift has an rms of 1/2 to 1
+    float update;     // lr x scale of the block's update
+    int32_t pad_;
+};
+// The sum of squares' range of one part of a block.
+struct BlockPart {
+    uint32_t largest;  // bits of max |N|
+    int32_t shift;     // its Gram is that of N 2^-shift
+};
+struct BlockWork {
+    float *gram;           // [block][part][tile][32 x 32], the lower triangle's tiles
+    BlockPart *parts;      // [block][part]
+    _Float16 *poly;        // [block]: P's rows as operand fragments, hi then lo
+    float *poly_own;       // [block]: P's columns as the chain holds them
+    BlockScalars *scalars; // [block]
+};
+
+struct BlockCall {
+    BlockWork w;
+    const float *factor;  // or nullptr
+    uint32_t base;                  // the launch's first block in the table
+    int32_t s, l;                   // smaller and larger side of a block
+    int32_t block_rows, block_cols;
+    int32_t parts, part_len;        // a block's l columns in `parts` ranges of part_len
+    float mu;
+    int32_t nesterov;
+    float poly_scale;               // what P's fragments are to be multiplied by
+    float decay;
+};
+
+// The polynomials of one segment of the schedule (between two Gram matrices
+// taken from X), and what surrounds them.
+struct BlockChain {
+    BlockWork w;
+    int32_t s, l, parts, steps;
+    int32_t first, last;       // segment
+    int32_t unit_rms;
+    float update;              // lr gamma sqrt(max(n, m)); unit RMS: lr gamma sqrt(n m)
+    struct Step {
+        float a, b, c;
+        int32_t exp_in, exp_out;  // P 2^-exp is what enters and leaves the step as fp16 pairs
+    } step[kMaxChainSteps];
+};
+
+inline int block_tiles(int64_t s) { return static_cast<int>((s + 31) / 32); }
+
+hipError_t launch_blocks_momentum(const BlockTable &t, const BlockCall &c, uint32_t blocks, bool tall, bool grad_bf16,
+                                  hipStream_t st);
+hipError_t launch_blocks_chain(const BlockChain &c, uint32_t blocks, hipStream_t st);
+hipError_t launch_blocks_regram(const BlockTable &t, const BlockCall &c, uint32_t blocks, bool tall, bool grad_bf16,
+                                hipStream_t st);
+hipError_t launch_blocks_update(const BlockTable &t, const BlockCall &c, uint32_t blocks, bool tall, bool grad_bf16,
+                                bool param_bf16, hipStream_t st);
+
+}  // namespace muon

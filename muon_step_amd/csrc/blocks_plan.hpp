@@ -1,0 +1,101 @@
+// Which schedules the block step can run, and where it cuts them (host only).
+//
+// The chain (blocks.hip) holds A, Q = a + b A + c A^2, A Q and P as scaled fp16
+// pairs, so a schedule has to keep them within bounds on every spectrum that a
+// normalised X can have, singular values in [0, 1].
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "../../include/muon_step.h"
+#include "blocks.hpp"
+
+namespace muon {
+
+struct BlockSegment {
+    int first, steps;
+};
+struct BlockSchedule {
+    bool fits = false;
+    std::vector<BlockSegment> segments;  // at least one
+    std::vector<int> exp_in;             // of each step; exp_out is the next one's, last_exp after the last
+    int last_exp = 0;
+};
+
+// Largest |c0 + c1 x + c2 x^2| x^power on [0, top], power 0 or 1.
+inline double polynomial_bound(double c0, double c1, double c2, int power, double top) {
+    auto value = [&](double x) { return std::fabs((c0 + (c1 + c2 * x) * x) * (power ? x : 1.0)); };
+    double best = std::max(value(0.0), value(top));
+    auto at = [&](double x) {
+        if (x > 0.0 && x < top) best = std::max(best, value(x));
+    };
+    if (power == 0) {
+        if (c2 != 0.0) at(-c1 / (2.0 * c2));
+    } else if (c2 == 0.0) {
+        if (c1 != 0.0) at(-c0 / (2.0 * c1));
+    } else {
+        const double d = c1 * c1 - 3.0 * c0 * c2;  // roots of c0 + 2 c1 x + 3 c2 x^2
+        if (d >= 0.0) {
+            at((-c1 + std::sqrt(d)) / (3.0 * c2));
+            at((-c1 - std::sqrt(d)) / (3.0 * c2));
+        }
+    }
+    return best;
+}
+
+// The exponent e that brings magnitudes up to `bound` to 2^11 at most as x 2^-e.
+inline int pair_exponent(double bound) {
+    return static_cast<int>(std::ceil(std::log2(std::max(bound, 0x1p-20)))) - 11;
+}
+
+inline BlockSchedule plan_blocks_schedule(const muon_ns_coeff *c, int n) {
+    BlockSchedule out;
+    if (n > kMaxChainSteps) return out;
+    double x = 1.0, p = 1.0;  // bounds of |X| and |P|
+    for (int k = 0; k < n; ++k) {
+        const double top = x * x;
+        const double q = polynomial_bound(c[k].a, c[k].b, c[k].c, 0, top);
+        const double r = polynomial_bound(c[k].a, c[k].b, c[k].c, 1, top);
+        out.exp_in.push_back(pair_exponent(p));
+        // |X'|^2 = |lambda Q^2|: the bound of Q lambda times that of Q, and the map's own at its grid's points
+        double next = 0.0;
+        constexpr int kGrid = 4096;
+        for (int i = 0; i <= kGrid; ++i) {
+            const double s = x * i / kGrid, l = s * s;
+            next = std::max(next, std::fabs(s * (c[k].a + (c[k].b + c[k].c * l) * l)));
+        }
+        next *= 1.01;  // between the points
+        p *= q;
+        if (!(q <= 60.0 && r <= 60.0 && next <= 3.9 && p <= 0x1p60)) return out;
+        x = std::max(next, 0x1p-20);
+    }
+    out.last_exp = pair_exponent(p);
+    out.fits = true;
+    // A step multiplies what noise has put in the directions of vanishing singular
+    // values by a^2, relative to what Q makes of them.  A segment goes on while
+    // that stays below 2^11 times fp32's rounding (1e-4 of a small direction's
+    // gain); the last one, whose noise no later step can grow, up to 2^17.
+    // Measured on spectra over three decades, error against 64 bits: the hybrid
+    // schedule as 4 + 6 steps 2.9e-5, as 5 + 5 6.0e-5, as 4 + 4 + 2 2.5e-5 (which
+    // is another pass over M and G), every step's A from X in fp32 4.8e-6.
+    auto gain = [&](int k) { return std::max(1.0, c[k].a * c[k].a); };
+    int at = 0;
+    while (at < n) {
+        double rest = 1.0;
+        for (int k = at; k + 1 < n; ++k) rest *= gain(k);
+        int steps = n - at;
+        if (rest > 0x1p17) {
+            double g = 1.0;
+            for (steps = 1; at + steps < n && (g *= gain(at + steps - 1)) <= 0x1p11; ++steps) {
+            }
+        }
+        out.segments.push_back(BlockSegment{at, steps});
+        at += steps;
+    }
+    if (out.segments.empty()) out.segments.push_back(BlockSegment{0, 0});
+    return out;
+}
+
+}  // namespace muon

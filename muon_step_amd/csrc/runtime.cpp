@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/muon_step.h"
+#include "blocks_plan.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -466,6 +467,101 @@ muon_status check_grad_norm(const muon_grad *gs, int64_t count, double max_norm,
     return MUON_OK;
 }
 
+// The memory of one strided matrix: `rows` rows of `width` bytes, `pitch` apart.
+struct Strided {
+    uintptr_t lo, hi;
+    uintptr_t pitch, width;
+    bool writable;
+    int64_t owner;
+    const char *what;
+};
+// Whether two of them, one of them written, share a byte.  Ranges that interleave
+// are told apart where their pitch is the same.
+bool share_memory(const Strided &a, const Strided &b) {
+    if ((!a.writable && !b.writable) || a.lo >= b.hi || b.lo >= a.hi) return false;
+    if (a.pitch != b.pitch) return true;
+    const uintptr_t ahead = (a.lo <= b.lo ? b.lo - a.lo : a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;  // b's columns after a's
+    return ahead < a.width || ahead + b.width > a.pitch;
+}
+
+constexpr int64_t kMaxBlockSide = int64_t(1) << 24;   // fp16 holds N 2^shift up to sqrt(128 2^24)
+constexpr int64_t kMaxBlockPitch = int64_t(1) << 27;
+
+muon_status check_blocks(const muon_block_matrix *mats, int64_t count, const muon_hparams *hp, char *msg, size_t cap) {
+    if (count < 0) { set_msg(msg, cap, "count < 0"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (count > 0 && !mats) { set_msg(msg, cap, "mats is NULL"); return MUON_ERR_INVALID_ARGUMENT; }
+    muon_status s = check_hparams(hp, msg, cap);
+    if (s != MUON_OK) return s;
+    std::vector<Strided> all;
+    for (int64_t i = 0; i < count; ++i) {
+        const muon_block_matrix &m = mats[i];
+        if (!known_dtype(m.param_dtype) || !known_dtype(m.grad_dtype)) {
+            set_msg(msg, cap, "matrix %lld: unknown dtype", (long long)i);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        s = check_shape(m.rows, m.cols, msg, cap, i);
+        if (s != MUON_OK) return s;
+        if (m.block_rows < 1 || m.block_cols < 1 || m.rows % m.block_rows != 0 || m.cols % m.block_cols != 0) {
+            set_msg(msg, cap, "matrix %lld: blocks of %lld x %lld do not divide %lld x %lld", (long long)i,
+                    (long long)m.block_rows, (long long)m.block_cols, (long long)m.rows, (long long)m.cols);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        if (std::min(m.block_rows, m.block_cols) > MUON_BLOCK_SIDE || std::max(m.block_rows, m.block_cols) > kMaxBlockSide) {
+            set_msg(msg, cap, "matrix %lld: blocks of %lld x %lld: the smaller side must be at most %d, the larger at most 2^24",
+                    (long long)i, (long long)m.block_rows, (long long)m.block_cols, MUON_BLOCK_SIDE);
+            return MUON_ERR_UNSUPPORTED;
+        }
+        auto add = [&](const void *p, size_t es, int64_t pitch, bool wr, const char *what) {
+            if (!p || !aligned_to(p, es)) {
+                set_msg(msg, cap, "matrix %lld: %s is NULL or not aligned to its elements", (long long)i, what);
+                return false;
+            }
+            if (pitch < m.cols || pitch > kMaxBlockPitch) {
+                set_msg(msg, cap, "matrix %lld: %s rows of %lld elements cannot lie %lld apart", (long long)i, what,
+                        (long long)m.cols, (long long)pitch);
+                return false;
+            }
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+            all.push_back(Strided{lo, lo + (static_cast<uintptr_t>(m.rows - 1) * pitch + m.cols) * es,
+                                  static_cast<uintptr_t>(pitch) * es, static_cast<uintptr_t>(m.cols) * es, wr, i, what});
+            return true;
+        };
+        if (!add(m.param, dtype_size(m.param_dtype), m.param_pitch, true, "param") ||
+            !add(m.grad, dtype_size(m.grad_dtype), m.grad_pitch, false, "grad") ||
+            !add(m.momentum, 4, m.momentum_pitch, true, "momentum") ||
+            (m.ns_out && !add(m.ns_out, 4, m.ns_out_pitch, true, "ns_out")))
+            return MUON_ERR_INVALID_ARGUMENT;
+    }
+    if (hp->grad_factor) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(hp->grad_factor);
+        all.push_back(Strided{lo, lo + 4, 0, 4, false, kNoOwner, "grad_factor"});
+    }
+    std::sort(all.begin(), all.end(), [](const Strided &x, const Strided &y) { return x.lo < y.lo; });
+    std::vector<const Strided *> open;  // those that reach past the current one's begin
+    for (const Strided &cur : all) {
+        size_t kept = 0;
+        for (const Strided *o : open) {
+            if (o->hi <= cur.lo) continue;
+            if (share_memory(*o, cur)) {
+                set_overlap_msg(msg, cap, memory_name("matrix", o->owner, o->what), memory_name("matrix", cur.owner, cur.what));
+                return MUON_ERR_INVALID_ARGUMENT;
+            }
+            open[kept++] = o;
+        }
+        open.resize(kept);
+        open.push_back(&cur);
+    }
+    if (hp->ns_precision != MUON_NS_BF16) {
+        set_msg(msg, cap, "the block step has no fp32 products: ns_precision must be MUON_NS_BF16");
+        return MUON_ERR_UNSUPPORTED;
+    }
+    if (!muon::plan_blocks_schedule(hp->schedule, hp->num_ns_steps).fits) {
+        set_msg(msg, cap, "the schedule leaves the range of the block step's products");
+        return MUON_ERR_UNSUPPORTED;
+    }
+    return MUON_OK;
+}
+
 // No C++ exception leaves the library: every entry point that may ask for host
 // memory runs in one of these.
 constexpr const char *kNoHostMemory = "out of host memory";
@@ -751,6 +847,7 @@ struct muon_context {
     DevBuf call_nrm2; // per call matrix
     DevBuf mat_desc;  // MatDesc table
     DevBuf adamw_desc;
+    DevBuf blocks;    // muon_blocks_step's sums, polynomials and scalars
     std::vector<void *> retired;  // buffers that graphs may hold, and calls no longer
     // muon_grad_norm's sums: of a fixed size and there from creation on, so that
     // a captured call never points to memory that a later call replaced
@@ -832,12 +929,14 @@ muon_status hip_fail(muon_context *ctx, hipError_t e, const char *where) {
 
 enum Stage {
     ST_MOMENTUM = 0, ST_FINALIZE, ST_NORMALIZE, ST_GRAM, ST_POLY, ST_APPLY, ST_APPLY_UPDATE, ST_UPDATE,
-    ST_ADAMW, ST_IMPORT, ST_EXPORT, ST_UNIT_RMS, ST_PRENORM, ST_PROBE, ST_ADAMW_MIXED, ST_ADAMW8, ST_GRAD_NORM, ST_COUNT
+    ST_ADAMW, ST_IMPORT, ST_EXPORT, ST_UNIT_RMS, ST_PRENORM, ST_PROBE, ST_ADAMW_MIXED, ST_ADAMW8, ST_GRAD_NORM,
+    ST_BLOCKS_MOMENTUM, ST_BLOCKS_CHAIN, ST_BLOCKS_REGRAM, ST_BLOCKS_UPDATE, ST_COUNT
 };
 const char *const kStageNames[ST_COUNT] = {"momentum_nesterov", "norm_finalize", "normalize", "gram", "poly",
                                            "apply", "apply_update", "update", "adamw", "import", "export",
                                            "unit_rms", "prenormalize", "stream_probe", "adamw_mixed", "adamw8",
-                                           "grad_norm"};
+                                           "grad_norm", "blocks_momentum", "blocks_chain", "blocks_regram",
+                                           "blocks_update"};
 
 hipError_t take_event(muon_context *ctx, hipEvent_t *ev) {
     if (ctx->ev_used == ctx->ev_pool.size()) {
@@ -1547,6 +1646,177 @@ muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage,
     return MUON_OK;
 }
 
+// ---- muon_blocks_step
+
+// Blocks with this many parts of their long side in all fill the card: 512
+// workgroups, two for each CU.
+constexpr int64_t kBlockWorkgroups = 512;
+constexpr int64_t kMaxBlockParts = 32;
+// What the blocks of one launch may hold in the context.
+constexpr size_t kBlockMemory = size_t(256) << 20;
+
+struct BlockShape {
+    int32_t s, l, parts, part_len;
+    bool tall;
+    size_t per_block;
+};
+BlockShape block_shape(const muon_block_matrix &m, int64_t blocks) {
+    BlockShape g{};
+    g.s = static_cast<int32_t>(std::min(m.block_rows, m.block_cols));
+    g.l = static_cast<int32_t>(std::max(m.block_rows, m.block_cols));
+    g.tall = m.block_rows > m.block_cols;
+    const int64_t most = std::min(kMaxBlockParts, (int64_t(g.l) + muon::kBlockUnit - 1) / muon::kBlockUnit);
+    const int64_t parts = std::max<int64_t>(1, std::min(most, (kBlockWorkgroups + blocks - 1) / blocks));
+    g.part_len = static_cast<int32_t>(round_up((g.l + parts - 1) / parts, muon::kBlockUnit));
+    g.parts = (g.l + g.part_len - 1) / g.part_len;
+    const size_t t = muon::block_tiles(g.s);
+    g.per_block = g.parts * (t * (t + 1) / 2 * 4096 + sizeof(muon::BlockPart)) + t * t * 8192 + sizeof(muon::BlockScalars);
+    return g;
+}
+
+// The launches of up to kBlockTensors weights with blocks of one shape and type.
+muon_status run_block_table(muon_context *ctx, const muon::BlockTable &t, int64_t total, const muon_block_matrix &like,
+                            const muon_hparams *hp, const muon::BlockSchedule &plan, hipStream_t st) {
+    size_t room = kBlockMemory;
+    if (ctx->cap > 0) room = std::min(room, ctx->cap);
+    const size_t slack = 8 * 256;
+    BlockShape g = block_shape(like, total);
+    int64_t most = room > slack ? static_cast<int64_t>((room - slack) / g.per_block) : 0;
+    if (most < total) {  // several launches after one another, of blocks enough for all CUs
+        g = block_shape(like, std::max<int64_t>(1, most));
+        most = room > slack ? static_cast<int64_t>((room - slack) / g.per_block) : 0;
+        if (most < 1)
+            return fail(ctx, MUON_ERR_OUT_OF_MEMORY, "workspace cap of %zu bytes: one block of %lld x %lld needs %zu", ctx->cap,
+                        (long long)like.block_rows, (long long)like.block_cols, g.per_block + slack);
+    }
+    const int64_t n = std::min(most, total);
+    muon_status s = ensure(ctx, ctx->blocks, g.per_block * n + slack, "block workspace", capturing(st));
+    if (s != MUON_OK) return s;
+    const size_t tiles = muon::block_tiles(g.s);
+    muon::BlockCall c{};
+    char *at = static_cast<char *>(ctx->blocks.p);
+    auto take = [&](size_t bytes) {
+        char *p = at;
+        at += align_up(bytes);
+        return p;
+    };
+    c.w.gram = reinterpret_cast<float *>(take(n * g.parts * tiles * (tiles + 1) / 2 * 4096));
+    c.w.poly = reinterpret_cast<_Float16 *>(take(n * tiles * tiles * 4096));
+    c.w.poly_own = reinterpret_cast<float *>(take(n * tiles * tiles * 4096));
+    c.w.parts = reinterpret_cast<muon::BlockPart *>(take(n * g.parts * sizeof(muon::BlockPart)));
+    c.w.scalars = reinterpret_cast<muon::BlockScalars *>(take(n * sizeof(muon::BlockScalars)));
+    c.factor = hp->grad_factor;
+    c.s = g.s;
+    c.l = g.l;
+    c.block_rows = static_cast<int32_t>(like.block_rows);
+    c.block_cols = static_cast<int32_t>(like.block_cols);
+    c.parts = g.parts;
+    c.part_len = g.part_len;
+    c.mu = static_cast<float>(hp->momentum);
+    c.nesterov = hp->nesterov;
+    float unused;
+    muon::BlockChain chain{};
+    muon_scalars(hp, like.block_rows, like.block_cols, &c.decay, hp->scale_mode == MUON_SCALE_UNIT_RMS ? &unused : &chain.update);
+    if (hp->scale_mode == MUON_SCALE_UNIT_RMS)
+        chain.update = static_cast<float>(hp->lr * (hp->gamma * std::sqrt(static_cast<double>(g.s) * g.l)));
+    chain.unit_rms = hp->scale_mode == MUON_SCALE_UNIT_RMS;
+    chain.w = c.w;
+    chain.s = g.s;
+    chain.l = g.l;
+    chain.parts = g.parts;
+    const bool gb = like.grad_dtype == MUON_BF16, pb = like.param_dtype == MUON_BF16;
+    const double gs = dtype_size(like.grad_dtype), ps = dtype_size(like.param_dtype);
+    for (int64_t base = 0; base < total; base += n) {
+        const int64_t now = std::min(n, total - base);
+        const double elems = static_cast<double>(now) * g.s * g.l, side = g.s;
+        c.base = static_cast<uint32_t>(base);
+        hipError_t e = timed(ctx, ST_BLOCKS_MOMENTUM, elems * (side + 1), elems * (8.0 + gs), st, [&] {
+            return muon::launch_blocks_momentum(t, c, static_cast<uint32_t>(now), g.tall, gb, st);
+        });
+        if (e != hipSuccess) return hip_fail(ctx, e, "block momentum launch");
+        for (size_t k = 0; k < plan.segments.size(); ++k) {
+            const muon::BlockSegment &seg = plan.segments[k];
+            if (k > 0) {
+                e = timed(ctx, ST_BLOCKS_REGRAM, elems * (3 * side + 1), elems * (4.0 + gs), st, [&] {
+                    return muon::launch_blocks_regram(t, c, static_cast<uint32_t>(now), g.tall, gb, st);
+                });
+                if (e != hipSuccess) return hip_fail(ctx, e, "block Gram launch");
+            }
+            chain.first = k == 0;
+            chain.last = k + 1 == plan.segments.size();
+            chain.steps = seg.steps;
+            int out = 0;
+            for (int i = 0; i < seg.steps; ++i) {
+                const muon_ns_coeff &co = hp->schedule[seg.first + i];
+                const size_t next = static_cast<size_t>(seg.first + i + 1);
+                out = next < plan.exp_in.size() ? plan.exp_in[next] : plan.last_exp;
+                chain.step[i] = muon::BlockChain::Step{static_cast<float>(co.a), static_cast<float>(co.b),
+                                                       static_cast<float>(co.c), plan.exp_in[seg.first + i], out};
+            }
+            e = timed(ctx, ST_BLOCKS_CHAIN, static_cast<double>(now) * seg.steps * 3 * side * side * (side + 1), 0.0, st, [&] {
+                return muon::launch_blocks_chain(chain, static_cast<uint32_t>(now), st);
+            });
+            if (e != hipSuccess) return hip_fail(ctx, e, "block polynomial launch");
+            c.poly_scale = std::ldexp(1.0f, out);
+        }
+        e = timed(ctx, ST_BLOCKS_UPDATE, elems * 2 * side, elems * (4.0 + gs + 2 * ps), st, [&] {
+            return muon::launch_blocks_update(t, c, static_cast<uint32_t>(now), g.tall, gb, pb, st);
+        });
+        if (e != hipSuccess) return hip_fail(ctx, e, "block update launch");
+    }
+    return MUON_OK;
+}
+
+muon_status blocks_impl(muon_context *ctx, const muon_block_matrix *mats, int64_t count, const muon_hparams *hp,
+                        hipStream_t st) {
+    char msg[512];
+    muon_status s = check_blocks(mats, count, hp, msg, sizeof msg);
+    if (s != MUON_OK) return fail(ctx, s, "%s", msg);
+    const muon::BlockSchedule plan = muon::plan_blocks_schedule(hp->schedule, hp->num_ns_steps);
+    DeviceGuard guard(ctx->device);
+    // Weights with the same blocks and types run together, in the caller's order.
+    auto key = [&](int64_t i) {
+        const muon_block_matrix &m = mats[i];
+        return std::make_tuple(m.block_rows, m.block_cols, m.param_dtype, m.grad_dtype);
+    };
+    std::vector<char> done(static_cast<size_t>(count), 0);
+    for (int64_t i = 0; i < count; ++i) {
+        if (done[i]) continue;
+        muon::BlockTable t;
+        int n = 0;
+        int64_t blocks = 0;
+        auto flush = [&]() -> muon_status {
+            for (int k = n; k < muon::kBlockTensors; ++k) t.first[k] = 0xffffffffu;
+            const muon_status r = run_block_table(ctx, t, blocks, mats[i], hp, plan, st);
+            n = 0;
+            blocks = 0;
+            return r;
+        };
+        for (int64_t j = i; j < count; ++j) {
+            if (done[j] || key(j) != key(i)) continue;
+            const muon_block_matrix &m = mats[j];
+            const int64_t across = m.cols / m.block_cols, nb = m.rows / m.block_rows * across;
+            if (nb >= int64_t(1) << 31) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "matrix %lld: too many blocks", (long long)j);
+            if (n == muon::kBlockTensors || blocks + nb >= int64_t(1) << 31) {
+                s = flush();
+                if (s != MUON_OK) return s;
+            }
+            t.first[n] = static_cast<uint32_t>(blocks);
+            t.d[n] = muon::BlockDesc{m.param, m.grad, m.momentum, m.ns_out,
+                                     static_cast<uint32_t>(m.param_pitch), static_cast<uint32_t>(m.grad_pitch),
+                                     static_cast<uint32_t>(m.momentum_pitch), static_cast<uint32_t>(m.ns_out ? m.ns_out_pitch : 0),
+                                     static_cast<uint32_t>(across), 0};
+            ++n;
+            blocks += nb;
+            done[j] = 1;
+        }
+        s = flush();
+        if (s != MUON_OK) return s;
+    }
+    ctx->err.clear();
+    return MUON_OK;
+}
+
 }  // namespace
 
 // ===================================================================== C ABI
@@ -1620,6 +1890,11 @@ muon_status muon_check_grad_norm_args(const muon_grad *gs, int64_t count, double
                                       const float *factor, char *msg, size_t msg_cap) {
     set_msg(msg, msg_cap, "%s", "");
     return guarded(msg, msg_cap, [&] { return check_grad_norm(gs, count, max_norm, norm, factor, msg, msg_cap); });
+}
+
+muon_status muon_check_blocks_args(const muon_block_matrix *mats, int64_t count, const muon_hparams *hp, char *msg,
+                                   size_t msg_cap) {
+    return guarded(msg, msg_cap, [&] { return check_blocks(mats, count, hp, msg, msg_cap); });
 }
 
 muon_status muon_workspace_bytes(const muon_matrix *mats, int64_t count, const muon_hparams *hp,
@@ -1703,7 +1978,7 @@ muon_status muon_destroy(muon_context *ctx) {
     if (!ctx) return MUON_OK;
     DeviceGuard guard(ctx->device);
     (void)hipDeviceSynchronize();
-    for (DevBuf *b : {&ctx->ws, &ctx->tabs, &ctx->call_nrm2, &ctx->mat_desc, &ctx->adamw_desc})
+    for (DevBuf *b : {&ctx->ws, &ctx->tabs, &ctx->call_nrm2, &ctx->mat_desc, &ctx->adamw_desc, &ctx->blocks})
         if (b->p) (void)hipFree(b->p);
     for (void *p : ctx->retired) (void)hipFree(p);
     if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
@@ -1731,6 +2006,12 @@ muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
 muon_status muon_step_noalloc(muon_context *ctx, const muon_matrix *mats, int64_t count, const muon_hparams *hp,
                               void *hip_stream) {
     return guarded(ctx, [&] { return step_impl(ctx, mats, count, hp, hip_stream, true); });
+}
+
+muon_status muon_blocks_step(muon_context *ctx, const muon_block_matrix *mats, int64_t count, const muon_hparams *hp,
+                             void *hip_stream) {
+    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+    return guarded(ctx, [&] { return blocks_impl(ctx, mats, count, hp, static_cast<hipStream_t>(hip_stream)); });
 }
 
 muon_status muon_ns_only(muon_context *ctx, const float *n_in, float *x_out, int64_t rows, int64_t cols,
