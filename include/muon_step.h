@@ -233,7 +233,7 @@ typedef struct muon_adamw8_tensor {
  *   *_pitch      elements from one row to the next, at least cols; what lies
  *                between the rows is neither read nor written
  * block_rows and block_cols divide rows and cols; the smaller of them is at most
- * MUON_BLOCK_SIDE, the larger at most 2^24; pitches are at most 2^27.  Addresses
+ * MUON_BLOCK_SIDE, the larger at most 2^24; pitches are at most 2^26.  Addresses
  * are multiples of their element's size.  No written element may be an element
  * of another range of the call; ranges that interleave (two slices of the
  * columns of one buffer) must have the same pitch in bytes. */

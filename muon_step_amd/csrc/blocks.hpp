@@ -1,4 +1,39 @@
-// Muon steps on the blocks of a weight (blocks.hip): what host and kernels share.
+// Muon steps on blocks with a smaller side of at most 128: the heads of an
+// attention projection, the factors of an adapter.
+//
+// X is s x l with s <= 128, so the iteration X <- (a + b A + c A^2) X, A = X X^T,
+// need not touch X's long rows at every step: X_k = P_k X_0 with P_k a product
+// of s x s polynomials, and A follows in s x s matrices as well,
+//     Q = a + b A + c A^2,   A <- Q A Q,   P <- Q P.
+// A's rounding noise sits in the directions of small singular values too, where
+// each step multiplies it by a^2 (11.9), so A is taken from X = P N again where
+// that has grown too far (the host cuts the schedule into segments; the hybrid
+// schedule into 4 + 6 steps).  One step over a block then is
+//     momentum:  M, N, the partial sums of N N^T                  (reads G, M; writes M)
+//     chain:     A = N N^T / ||N||^2, the first segment's P       (s x s, one workgroup a block)
+//     regram:    X = P N, the partial sums of X X^T               (reads G, M)
+//     chain:     the second segment's P
+//     update:    O = P N, W                                       (reads G, M, W; writes W)
+// N is formed from M and G wherever it is needed: 6 bytes read an element, where
+// a stored X would be 4 written and 4 read.
+//
+// Products run on the matrix cores with each fp32 operand as a sum of two
+// 16-bit parts, hi and lo, and three products hi hi + hi lo + lo hi in fp32
+// accumulators: bf16 parts (16 bits of significand) for the first N N^T, whose
+// scale is not known before it, fp16 parts (21 bits) of suitably scaled
+// matrices everywhere else.
+//
+// Index basis of the smaller side.  A wave reads 32 lanes x T tiles of it; where
+// memory is contiguous along the smaller side (tall blocks, X = N^T) lane i
+// takes elements T i .. T i + T - 1, one for each tile, so basis index 32 t + i
+// stands for element T i + t; in wide blocks it stands for itself.
+//
+// Fragments.  v_mfma_f32_32x32x16 wants of either operand, in lane (i, h), i < 32,
+// h < 2, eight k of row (column) i; the accumulator holds in lane (j, h) rows
+// 8 (r / 4) + 4 h + r % 4, r < 16, of column j.  The order of k is free as long
+// as both operands agree, so chunk q (of two) of a tile takes accumulator
+// registers 8 q .. 8 q + 7 as they are: an accumulator is the next product's
+// operand without leaving its lane.
 #pragma once
 
 #include "common.hpp"
@@ -66,7 +101,7 @@ struct BlockChain {
     BlockWork w;
     int32_t s, l, parts, steps;
     int32_t first, last;       // segment
-    int32_t unit_rms;
+    int32_t unit_rms, tall;
     float update;              // lr gamma sqrt(max(n, m)); unit RMS: lr gamma sqrt(n m)
     struct Step {
         float a, b, c;

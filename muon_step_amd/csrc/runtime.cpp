@@ -485,7 +485,7 @@ bool share_memory(const Strided &a, const Strided &b) {
 }
 
 constexpr int64_t kMaxBlockSide = int64_t(1) << 24;   // fp16 holds N 2^shift up to sqrt(128 2^24)
-constexpr int64_t kMaxBlockPitch = int64_t(1) << 27;
+constexpr int64_t kMaxBlockPitch = int64_t(1) << 26;   // lanes address 8 rows in 32 bits
 
 muon_status check_blocks(const muon_block_matrix *mats, int64_t count, const muon_hparams *hp, char *msg, size_t cap) {
     if (count < 0) { set_msg(msg, cap, "count < 0"); return MUON_ERR_INVALID_ARGUMENT; }
@@ -1720,6 +1720,7 @@ muon_status run_block_table(muon_context *ctx, const muon::BlockTable &t, int64_
     if (hp->scale_mode == MUON_SCALE_UNIT_RMS)
         chain.update = static_cast<float>(hp->lr * (hp->gamma * std::sqrt(static_cast<double>(g.s) * g.l)));
     chain.unit_rms = hp->scale_mode == MUON_SCALE_UNIT_RMS;
+    chain.tall = g.tall;
     chain.w = c.w;
     chain.s = g.s;
     chain.l = g.l;
