@@ -8,27 +8,30 @@ namespace {
 // ------------------------------------------------------------ products with N
 
 // M and G of 32 V columns of X as a wave loads them, and N from them.  A lane
-// holds column j (wide blocks: columns V j .. V j + V - 1) and, of the smaller
-// side, for chunk (t, q) basis indices 32 t + 16 q + 8 a + 4 h + b, a < 2, b < 4.
-// They come in phases: in wide blocks each chunk is one, eight rows that lanes
-// read side by side; in tall ones the T chunks of one q, as two runs of 4 T
-// elements that lie side by side in the lane's row of memory.  A phase's
-// registers are loaded for the next columns as soon as they are used up, so that
-// a wave always has most of a unit (24 KB at T = 4) on its way.
+// holds column j (wide blocks: columns V j .. V j + V - 1, in one access) and, of
+// the smaller side, for chunk (t, q) basis indices 32 t + 16 q + 8 a + 4 h + b,
+// a < 2, b < 4.  They come in phases: in wide blocks each chunk is one, eight rows
+// that lanes read side by side; in tall ones the T chunks of one q, as two runs of
+// 4 T elements that lie side by side in the lane's row of memory.  The registers
+// hold kSlots phases; one is loaded anew, for the phase kSlots further on, as soon
+// as it is used up, so that a wave always has loads on their way.
 //
 // Places outside of the block are read as others inside of it: what the products
 // make of them meets P's zeros (its rows and columns past the smaller side) or
-// belongs to columns that nobody stores or sums.  EVEN: a tall block's runs lie
-// inside or outside as a whole (4 T divides its smaller side).
+// belongs to columns that nobody stores or sums.  V > 1: all columns are inside.
+// EVEN: a tall block's runs lie inside or outside as a whole (4 T divides its
+// smaller side).
 template <int T, int V, bool TALL, bool BF16, bool EVEN> struct Stream {
     static_assert(!TALL || V == 1, "a tall block's lane holds one column");
     static constexpr int kPhases = TALL ? 2 : 2 * T, kChunks = TALL ? T : 1;
+    static constexpr int kSlots = V == 4 ? 2 : V == 2 && T == 4 ? 4 : kPhases;
     static constexpr int kValues = 8 * kChunks * V;              // of a phase
-    static constexpr int kGrads = BF16 && (TALL || V == 2) ? kValues / 2 : kValues;  // words of G
+    static constexpr int kGrads = BF16 && (TALL || V > 1) ? kValues / 2 : kValues;  // words of G
     static constexpr int kGSize = BF16 ? 2 : 4;
+    static_assert(kPhases % kSlots == 0, "a phase has the same slot in every unit");
     typedef const char *Bytes;
-    float m[kPhases][kValues];
-    uint32_t g[kPhases][kGrads];
+    float m[kSlots][kValues];
+    uint32_t g[kSlots][kGrads];
     const Place &at;
     const BlockCall &c;
     float factor;
@@ -38,51 +41,80 @@ template <int T, int V, bool TALL, bool BF16, bool EVEN> struct Stream {
     Bytes mom_row = nullptr, grad_row = nullptr, mom_first = nullptr, grad_first = nullptr;
     int left = 0;  // rows from there to the block's end
     uint32_t mom_lane = 0, grad_lane = 0, mom_part[4] = {}, grad_part[4] = {};
+    int64_t mom_at = 0, grad_at = 0;  // tall: the lane's row of memory
 
     __device__ __forceinline__ Stream(const Place &place, const BlockCall &call, float f, int lane, int sh)
-        : at(place), c(call), factor(f), j(lane & 31), h(lane >> 5), shift(sh) {}
-
+        : at(place), c(call), factor(f), j(lane & 31), h(lane >> 5), shift(sh) {
+        if constexpr (!TALL && V > 1) lanes(V * j);
+    }
     // Before the phases of columns x0 ..; `end`: the first column that is not there.
-    int64_t mom_at = 0, grad_at = 0;  // tall: the lane's row of memory
-    bool odd = false;                 // wide, V = 2: the lane's second column is what both loads hold
     __device__ __forceinline__ void begin(int x0, int end) {
         if constexpr (TALL) {
             const int64_t row = min(x0 + j, end - 1);
             mom_at = row * at.mom_pitch;
             grad_at = row * at.grad_pitch;
         } else {
-            // a pair that would reach past the end starts one column earlier (a
-            // single column: its own, twice)
-            const int x = x0 + V * j, last = max(end - V, 0);
-            const uint32_t col = min(x, last);
-            odd = V == 2 && x == last + 1;
-            const uint32_t mp = static_cast<uint32_t>(at.mom_pitch), gp = static_cast<uint32_t>(at.grad_pitch);
-            mom_lane = (4 * h * mp + col) * 4;
-            grad_lane = (4 * h * gp + col) * kGSize;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint32_t row = min(4 * h + b, (c.s & 7) - 1);  // unused where s % 8 == 0
-                mom_part[b] = (row * mp + col) * 4;
-                grad_part[b] = (row * gp + col) * kGSize;
-            }
-            mom_first = reinterpret_cast<Bytes>(at.mom);
-            grad_first = at.grad;
+            if constexpr (V == 1) lanes(min(j, end - 1 - x0));
+            mom_first = reinterpret_cast<Bytes>(at.mom + x0);
+            grad_first = at.grad + static_cast<int64_t>(x0) * kGSize;
             mom_row = mom_first;
             grad_row = grad_first;
             left = c.s;
         }
     }
+    // Columns x0 .. and their first kSlots phases.
+    __device__ __forceinline__ void start(int x0, int end) {
+        begin(x0, end);
+#pragma unroll
+        for (int ph = 0; ph < kSlots; ++ph) load(ph);
+    }
+    // Behind the use of phase ph of a unit: what takes its place, `next` being the next unit.
+    __device__ __forceinline__ void refill(int ph, int next, int end) {
+        if (ph + kSlots < kPhases) {
+            load(ph);
+        } else if (next < end) {
+            if (ph + kSlots == kPhases) begin(next, end);
+            load(ph);
+        }
+    }
+    // N 2^shift of chunk `sub` of a phase, column v, as fp16 pairs.
+    __device__ __forceinline__ void fragment(int ph, int sub, int v, half8 &hi, half8 &lo) const {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int i = TALL ? ((e >> 2) * 4 + (e & 3)) * T + sub : e * V + v;
+            float n = m[ph % kSlots][i];
+            if (c.nesterov) n = c.mu * n + grad_value(ph % kSlots, i) * factor;
+            x[e] = __builtin_amdgcn_ldexpf(n, shift);
+        }
+        split_half(x, hi, lo);
+    }
+
+  private:
+    __device__ __forceinline__ void lanes(uint32_t col) {
+        const uint32_t mp = static_cast<uint32_t>(at.mom_pitch), gp = static_cast<uint32_t>(at.grad_pitch);
+        mom_lane = (4 * h * mp + col) * 4;
+        grad_lane = (4 * h * gp + col) * kGSize;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t row = min(4 * h + b, max((c.s & 7) - 1, 0));  // unused where s % 8 == 0
+            mom_part[b] = (row * mp + col) * 4;
+            grad_part[b] = (row * gp + col) * kGSize;
+        }
+    }
+    // The next phase of the columns begun, into the slot of `ph`.
     __device__ __forceinline__ void load(int ph) {
+        const int k = ph % kSlots;
         if constexpr (TALL) {
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
                 const int run = T * (16 * ph + 8 * a + 4 * h);
                 if constexpr (EVEN) {
                     const int p = run < c.s ? run : 0;
-                    words<4 * T, 4>(at.mom + mom_at + p, reinterpret_cast<uint32_t *>(&m[ph][a * 4 * T]));
-                    words<(BF16 ? 2 : 4) * T, kGSize>(at.grad + (grad_at + p) * kGSize, &g[ph][a * (BF16 ? 2 : 4) * T]);
+                    words<4 * T, 4>(at.mom + mom_at + p, reinterpret_cast<uint32_t *>(&m[k][a * 4 * T]));
+                    words<(BF16 ? 2 : 4) * T, kGSize>(at.grad + (grad_at + p) * kGSize, &g[k][a * (BF16 ? 2 : 4) * T]);
                 } else {
-                    checked(ph, a, run);
+                    checked(k, a, run);
                 }
             }
         } else {
@@ -96,78 +128,50 @@ template <int T, int V, bool TALL, bool BF16, bool EVEN> struct Stream {
                     const Bytes mp = mr + (full ? b * at.mom_pitch * 4 : 0), gp = gr + (full ? b * at.grad_pitch * kGSize : 0);
                     const uint32_t ml = full ? mom_lane : mom_part[b], gl = full ? grad_lane : grad_part[b];
                     if constexpr (V == 1) {
-                        m[ph][e] = global<float>(mp, ml);
-                        g[ph][e] = BF16 ? static_cast<uint32_t>(global<uint16_t>(gp, gl)) : global<uint32_t>(gp, gl);
+                        m[k][e] = load_at<float>(mp, ml);
+                        g[k][e] = BF16 ? static_cast<uint32_t>(load_at<uint16_t>(gp, gl)) : load_at<uint32_t>(gp, gl);
                     } else {
-                        const auto v = global<FloatsAt<2>::type>(mp, ml);
-                        m[ph][2 * e] = v[0];
-                        m[ph][2 * e + 1] = v[1];
-                        if constexpr (BF16) {
-                            typedef uint32_t word __attribute__((aligned(2)));
-                            g[ph][e] = global<word>(gp, gl);
-                        } else {
-                            const auto u = global<FloatsAt<2>::type>(gp, gl);
-                            g[ph][2 * e] = __float_as_uint(u[0]);
-                            g[ph][2 * e + 1] = __float_as_uint(u[1]);
-                        }
+                        const auto v = load_at<typename WordsAt<V, 4>::type>(mp, ml);
+                        const auto u = load_at<typename WordsAt<BF16 ? V / 2 : V, kGSize>::type>(gp, gl);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) m[k][V * e + i] = __uint_as_float(v[i]);
+#pragma unroll
+                        for (int i = 0; i < (BF16 ? V / 2 : V); ++i) g[k][(BF16 ? V / 2 : V) * e + i] = u[i];
                     }
                 }
                 mom_row += 8 * at.mom_pitch * 4;
                 grad_row += 8 * at.grad_pitch * kGSize;
-                // the compiler would form every row's address ahead of the loop, and spill them
                 left -= 8;
+                // the compiler would form every row's address ahead of the loop, and spill them
                 asm volatile("" : "+s"(mom_row), "+s"(grad_row), "+s"(left));
             }
         }
     }
-    // N 2^shift of chunk `sub` of a phase, column v, as fp16 pairs.
-    __device__ __forceinline__ void fragment(int ph, int sub, int v, half8 &hi, half8 &lo) const {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int i = TALL ? ((e >> 2) * 4 + (e & 3)) * T + sub : e * V + v;
-            float n = m[ph][i];
-            if (c.nesterov) n = c.mu * n + grad_value(ph, i) * factor;
-            if (V == 2 && v == 0) {  // the block's last column alone: its lane holds it second
-                float other = m[ph][i + V - 1];
-                if (c.nesterov) other = c.mu * other + grad_value(ph, i + V - 1) * factor;
-                n = odd ? other : n;
-            }
-            x[e] = __builtin_amdgcn_ldexpf(n, shift);
-        }
-        split_half(x, hi, lo);
-    }
-
-  private:
-    __device__ __forceinline__ float grad_value(int ph, int i) const {
-        if constexpr (!BF16) return __uint_as_float(g[ph][i]);
-        if constexpr (kGrads == kValues) return __uint_as_float(g[ph][i] << 16);
-        return __uint_as_float(i % 2 ? g[ph][i / 2] & 0xffff0000u : g[ph][i / 2] << 16);
-    }
-    template <class W> __device__ __forceinline__ static W global(Bytes row, uint32_t lane) {
-        return *(const W __attribute__((address_space(1))) *)((const char __attribute__((address_space(1))) *)row + lane);
+    __device__ __forceinline__ float grad_value(int k, int i) const {
+        if constexpr (!BF16) return __uint_as_float(g[k][i]);
+        if constexpr (kGrads == kValues) return __uint_as_float(g[k][i] << 16);
+        return __uint_as_float(i % 2 ? g[k][i / 2] & 0xffff0000u : g[k][i / 2] << 16);
     }
     // Tall: a run that the smaller side's end may cut.
-    __device__ __forceinline__ void checked(int ph, int a, int p) {
+    __device__ __forceinline__ void checked(int k, int a, int p) {
 #pragma unroll
         for (int i = 0; i < 4 * T; ++i) {
             const int from = min(p + i, c.s - 1);
-            m[ph][a * 4 * T + i] = as_global(at.mom)[mom_at + from];
+            m[k][a * 4 * T + i] = as_global(at.mom)[mom_at + from];
             if constexpr (BF16) {
                 const uint32_t v = as_global(reinterpret_cast<const uint16_t *>(at.grad))[grad_at + from];
-                uint32_t &w = g[ph][a * 2 * T + i / 2];
+                uint32_t &w = g[k][a * 2 * T + i / 2];
                 w = i % 2 ? w | v << 16 : v;
             } else {
-                g[ph][a * 4 * T + i] = as_global(reinterpret_cast<const uint32_t *>(at.grad))[grad_at + from];
+                g[k][a * 4 * T + i] = as_global(reinterpret_cast<const uint32_t *>(at.grad))[grad_at + from];
             }
         }
     }
     template <int N, int A> __device__ __forceinline__ static void words(const void *p, uint32_t *to) {
         constexpr int W = N % 4 == 0 ? 4 : 2;
-        typedef uint32_t type __attribute__((ext_vector_type(W), aligned(A)));
 #pragma unroll
         for (int i = 0; i < N; i += W) {
-            const type v = ((const type __attribute__((address_space(1))) *)p)[i / W];
+            const auto v = ((const typename WordsAt<W, A>::type __attribute__((address_space(1))) *)p)[i / W];
 #pragma unroll
             for (int k = 0; k < W; ++k) to[i + k] = v[k];
         }
@@ -196,7 +200,6 @@ __device__ __forceinline__ void times_poly(floatx16 (&acc)[V][T], Stream<T, V, T
         for (int i = 0; i < T; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[v][i][r] = 0.0f;
-    if (next < end) in.begin(next, end);
 #pragma unroll
     for (int ph = 0; ph < S::kPhases; ++ph) {
 #pragma unroll
@@ -210,7 +213,7 @@ __device__ __forceinline__ void times_poly(floatx16 (&acc)[V][T], Stream<T, V, T
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) in.fragment(ph, sub, v, hi[v], lo[v]);
-            if (sub + 1 == S::kChunks && next < end) in.load(ph);
+            if (sub + 1 == S::kChunks) in.refill(ph, next, end);
 #pragma unroll
             for (int k = 0; k < 3; ++k)
 #pragma unroll
@@ -225,9 +228,41 @@ __device__ __forceinline__ void times_poly(floatx16 (&acc)[V][T], Stream<T, V, T
     }
 }
 
+// Columns x0, x0 + stride, ... below `end` of a wave: the sum of X X^T, X = P N 2^shift scale.
+template <int T, int V, bool TALL, bool BF16, bool EVEN>
+__device__ __forceinline__ void regram_columns(Triangle<T> &sum, Stream<T, V, TALL, BF16, EVEN> &in, const Poly<T> &poly, int lane,
+                                               float scale, int x0, int stride, int end) {
+    for (; x0 < end; x0 += stride) {
+        floatx16 acc[V][T];
+        times_poly<true>(acc, in, poly, lane, x0 + stride, end);
+        if (V == 1 && x0 + 32 > end) {  // columns that are not there
+#pragma unroll
+            for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[0][i][r] = x0 + acc_row(r, lane >> 5) < end ? acc[0][i][r] : 0.0f;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                half8 hi[T], lo[T];
+#pragma unroll
+                for (int i = 0; i < T; ++i) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = acc[v][i][8 * q + e] * scale;
+                    split_half(x, hi[i], lo[i]);
+                }
+                sum.add(hi, lo);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+}
+
 // One part of one block: the sum of X X^T, X = P N / ||N||, over the part's columns.
 template <int T, bool TALL, bool BF16, bool EVEN>
 __global__ __launch_bounds__(kThreads) void blocks_regram_kernel(const BlockTable t, const BlockCall c) {
+    constexpr int V = TALL ? 1 : 2;
     union Shared {
         Poly<T> poly;
         float sums[2 * kWaves * 1024];
@@ -238,168 +273,214 @@ __global__ __launch_bounds__(kThreads) void blocks_regram_kernel(const BlockTabl
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int begin = part * c.part_len, end = min(begin + c.part_len, c.l);
     const BlockScalars k = c.w.scalars[block];
-    const float scale = c.poly_scale * k.inv_norm * kScaleX;
-    Stream<T, 1, TALL, BF16, EVEN> in(at, c, c.factor ? *c.factor : 1.0f, lane, k.shift);
-    int x0 = begin + 32 * wave;
-    if (x0 < end) {
-        in.begin(x0, end);
-#pragma unroll
-        for (int ph = 0; ph < in.kPhases; ++ph) in.load(ph);
-    }
-    sh.poly.load(c.w.poly + static_cast<int64_t>(block) * (T * T * 2048));
-    __syncthreads();
+    const float scale = c.poly_scale * k.inv_norm * kScaleX, factor = c.factor ? *c.factor : 1.0f;
+    // whole units for all waves, V columns a lane; then what is left, one a lane
+    const int whole = V == 1 ? begin : begin + (end - begin) / (V * kBlockUnit) * (V * kBlockUnit);
+    Stream<T, V, TALL, BF16, EVEN> in(at, c, factor, lane, k.shift);
     Triangle<T> sum;
     sum.clear();
-    const int h = lane >> 5;
-    for (; x0 < end; x0 += kBlockUnit) {
-        floatx16 acc[1][T];
-        times_poly<true>(acc, in, sh.poly, lane, x0 + kBlockUnit, end);
-        if (x0 + 32 > end) {  // columns that are not there
-#pragma unroll
-            for (int i = 0; i < T; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[0][i][r] = x0 + acc_row(r, h) < end ? acc[0][i][r] : 0.0f;
+    const int x0 = begin + 32 * V * wave, x1 = whole + 32 * wave;
+    if (V > 1 && x0 < whole) in.start(x0, whole);
+    if (V == 1 && x1 < end) in.start(x1, end);
+    sh.poly.load(c.w.poly + static_cast<int64_t>(block) * (T * T * 2048));
+    __syncthreads();
+    if constexpr (V > 1) {
+        regram_columns(sum, in, sh.poly, lane, scale, x0, V * kBlockUnit, whole);
+        if (x1 < end) {
+            Stream<T, 1, TALL, BF16, EVEN> rest(at, c, factor, lane, k.shift);
+            rest.start(x1, end);
+            regram_columns(sum, rest, sh.poly, lane, scale, x1, kBlockUnit, end);
         }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            half8 hi[T], lo[T];
-#pragma unroll
-            for (int i = 0; i < T; ++i) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = acc[0][i][8 * q + e] * scale;
-                split_half(x, hi[i], lo[i]);
-            }
-            sum.add(hi, lo);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+    } else {
+        regram_columns(sum, in, sh.poly, lane, scale, x1, kBlockUnit, end);
     }
     __syncthreads();
     sum.reduce(c.w.gram + (static_cast<int64_t>(block) * c.parts + part) * tri(T) * 1024, sh.sums);
 }
 
-// W <- fl(fl(d W) - fl(s O)) and O to ns_out, of one row of memory: its uniform
-// begin and the lane's element behind it; N elements that lie side by side.
-struct Row {
-    char *param;
-    char *out;  // or nullptr
-    __device__ __forceinline__ void keep() { asm volatile("" : "+s"(param), "+s"(out)); }
-};
-template <bool PBF16, int N>
-__device__ __forceinline__ void update_run(char *param, char *out, uint32_t param_lane, uint32_t out_lane, const float (&o)[N],
-                                           float d, float s) {
-    typedef char __attribute__((address_space(1))) *place;
-    if constexpr (PBF16) {
-        const place p = (place)param + param_lane;
-        if constexpr (N == 1 || N == 3) {
-            typedef uint16_t __attribute__((address_space(1))) *halves;
+// Up to N elements of W side by side, as they lie in memory; `there` of them are.
+template <bool PBF16, int N> struct Run {
+    static constexpr int kWords = PBF16 ? (N + 1) / 2 : N;
+    uint32_t w[kWords];
+    typedef char __attribute__((address_space(1))) *Address;
+
+    __device__ __forceinline__ void load(const char *row, uint32_t lane, bool whole, int there) {
+        const Address p = (Address) const_cast<char *>(row) + lane;
+        if (whole) {
+            if constexpr (PBF16 && N % 2 == 0) {
+                typedef uint32_t type __attribute__((ext_vector_type(kWords), aligned(2)));
+                const type v = *(const type __attribute__((address_space(1))) *)p;
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                ((halves)p)[k] = float_to_bf16_bits(d * bf16_bits_to_float(((halves)p)[k]) - s * o[k]);
+                for (int k = 0; k < kWords; ++k) w[k] = v[k];
+            } else if constexpr (!PBF16 && N % 2 == 0) {
+                typedef uint32_t type __attribute__((ext_vector_type(N), aligned(4)));
+                const type v = *(const type __attribute__((address_space(1))) *)p;
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) w[k] = v[k];
+            } else {
+                single(p, N);
+            }
         } else {
-            typedef typename HalvesAt<N>::type __attribute__((address_space(1))) *halves;
-            auto v = *(halves)p;
-#pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = float_to_bf16_bits(d * bf16_bits_to_float(v[k]) - s * o[k]);
-            *(halves)p = v;
+            single(p, there);
         }
-    } else {
-        float *p = (float *)((place)param + param_lane);
-        float w[N];
-        load_floats<N>(p, w);
-#pragma unroll
-        for (int k = 0; k < N; ++k) w[k] = d * w[k] - s * o[k];
-        store_floats<N>(p, w);
     }
-    if (out) store_floats<N>((float *)((place)out + out_lane), o);
+    // W <- fl(fl(d W) - fl(s o)), and o to `out` unless it is null.
+    __device__ __forceinline__ void update(char *row, uint32_t lane, char *out, uint32_t out_lane, bool whole, int there,
+                                           const float (&o)[N], float d, float s) {
+        const Address p = (Address)row + lane;
+        float x[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float old = !PBF16 ? __uint_as_float(w[e]) : __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+            x[e] = d * old - s * o[e];
+        }
+        if (whole && N % 2 == 0) {
+            if constexpr (PBF16 && N % 2 == 0) {
+                typedef uint32_t type __attribute__((ext_vector_type(kWords), aligned(2)));
+                type v;
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) v[k] = pack_bf16x2(x[2 * k], x[2 * k + 1]);
+                *(type __attribute__((address_space(1))) *)p = v;
+            } else if constexpr (N % 2 == 0) {
+                typedef float type __attribute__((ext_vector_type(N), aligned(4)));
+                type v;
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[k] = x[k];
+                *(type __attribute__((address_space(1))) *)p = v;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                if (!whole && e >= there) continue;
+                if constexpr (PBF16)
+                    ((uint16_t __attribute__((address_space(1))) *)p)[e] = float_to_bf16_bits(x[e]);
+                else
+                    ((float __attribute__((address_space(1))) *)p)[e] = x[e];
+            }
+        }
+        if (out) {
+            const Address q = (Address)out + out_lane;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (whole || e < there) ((float __attribute__((address_space(1))) *)q)[e] = o[e];
+        }
+    }
+
+  private:
+    __device__ __forceinline__ void single(Address p, int there) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const bool in = e < there;
+            if constexpr (PBF16) {
+                const uint32_t v = in ? ((const uint16_t __attribute__((address_space(1))) *)p)[e] : 0;
+                w[e / 2] = e % 2 ? w[e / 2] | v << 16 : v;
+            } else {
+                w[e] = in ? ((const uint32_t __attribute__((address_space(1))) *)p)[e] : 0;
+            }
+        }
+    }
+};
+
+// What the last pass needs beside a Stream.
+struct Update {
+    const Place &at;
+    const BlockCall &c;
+    float scale, update;
+};
+
+// Columns x0, x0 + stride, ... below `end` of a wave: O = P N 2^shift scale, and W.
+// W's rows of the first tile are read before the products and those of a later
+// tile before the tile in front of it is written, so that they are there in time.
+template <int T, int V, bool TALL, bool BF16, bool PBF16, bool EVEN>
+__device__ __forceinline__ void update_columns(Stream<T, V, TALL, BF16, EVEN> &in, const Update &u, const Poly<T> &poly, int lane,
+                                               int x0, int stride, int end) {
+    constexpr int kPSize = PBF16 ? 2 : 4;
+    constexpr int N = TALL ? T : V;    // elements side by side
+    constexpr int kTiles = TALL ? 1 : T;  // of 32 rows of memory
+    const int j = lane & 31, h = lane >> 5;
+    const Place &at = u.at;
+    // the lane's place behind the begin of the first of eight rows
+    const int64_t pp = at.param_pitch * kPSize, op = at.out_pitch * 4;
+    const uint32_t across = N * j;
+    const uint32_t param_lane = 4 * h * static_cast<uint32_t>(pp) + across * kPSize;
+    const uint32_t out_lane = 4 * h * static_cast<uint32_t>(op) + across * 4;
+    for (; x0 < end; x0 += stride) {
+        // rows of memory from the first one to the end, and elements of a row from the lane's on
+        const int rows = TALL ? end - x0 : u.c.s, there = (TALL ? u.c.s : end - x0) - static_cast<int>(across);
+        const bool whole = TALL ? u.c.s % T == 0 : V > 1 || x0 + 32 <= end;
+        char *row = at.param + (TALL ? x0 * pp : static_cast<int64_t>(x0) * kPSize);
+        const char *ahead = row;
+        char *out = at.out ? reinterpret_cast<char *>(at.out) + (TALL ? x0 * op : static_cast<int64_t>(x0) * 4) : nullptr;
+        int left = rows, ahead_left = rows;
+        Run<PBF16, N> w[2][4][4];
+        auto fetch = [&](int tile) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (4 * h + b < ahead_left && there > 0) w[tile & 1][q][b].load(ahead + b * pp, param_lane, whole, there);
+                ahead += 8 * pp;
+                ahead_left -= 8;
+                asm volatile("" : "+s"(ahead), "+s"(ahead_left));
+            }
+        };
+        fetch(0);
+        floatx16 acc[V][T];
+        times_poly<TALL>(acc, in, poly, lane, x0 + stride, end);
+#pragma unroll
+        for (int tile = 0; tile < kTiles; ++tile) {
+            if (tile + 1 < kTiles) fetch(tile + 1);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float o[N];
+#pragma unroll
+                    for (int e = 0; e < N; ++e) o[e] = (TALL ? acc[0][e][4 * q + b] : acc[e][tile][4 * q + b]) * u.scale;
+                    if (4 * h + b < left && there > 0)
+                        w[tile & 1][q][b].update(row + b * pp, param_lane, out ? out + b * op : nullptr, out_lane, whole, there, o,
+                                                 u.c.decay, u.update);
+                }
+                row += 8 * pp;
+                out = out ? out + 8 * op : nullptr;
+                left -= 8;
+                asm volatile("" : "+s"(row), "+s"(out), "+s"(left));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
 }
 
 // The last pass: O = P N / ||N|| and W of one part of one block.
 template <int T, bool TALL, bool BF16, bool PBF16, bool EVEN>
 __global__ __launch_bounds__(kThreads) void blocks_update_kernel(const BlockTable t, const BlockCall c) {
-    // wide blocks: two columns a lane, so that bf16 gradients and weights move in words
-    constexpr int V = TALL ? 1 : 2, kPSize = PBF16 ? 2 : 4;
+    // four columns a lane, 16 and 8 bytes of fp32 and bf16 data, where the part is
+    // long enough for whole units of all waves
+    constexpr int V = TALL ? 1 : 2;
     __shared__ __attribute__((aligned(16))) Poly<T> poly;
     const uint32_t block = blockIdx.x / c.parts, part = blockIdx.x % c.parts;  // block: of the launch
-    const Place at = locate<BF16 ? 2 : 4, kPSize>(t, c, c.base + block);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, j = lane & 31, h = lane >> 5;
+    const Place at = locate<BF16 ? 2 : 4, PBF16 ? 2 : 4>(t, c, c.base + block);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int begin = part * c.part_len, end = min(begin + c.part_len, c.l);
     const BlockScalars k = c.w.scalars[block];
-    const float scale = c.poly_scale * k.inv_norm;
-    Stream<T, V, TALL, BF16, EVEN> in(at, c, c.factor ? *c.factor : 1.0f, lane, k.shift);
-    constexpr int kStride = V * kBlockUnit;
-    int x0 = begin + 32 * V * wave;
-    if (x0 < end) {
-        in.begin(x0, end);
-#pragma unroll
-        for (int ph = 0; ph < in.kPhases; ++ph) in.load(ph);
-    }
+    const float factor = c.factor ? *c.factor : 1.0f;
+    const Update u{at, c, c.poly_scale * k.inv_norm, k.update};
+    const int whole = V == 1 ? begin : begin + (end - begin) / (V * kBlockUnit) * (V * kBlockUnit);
+    Stream<T, V, TALL, BF16, EVEN> in(at, c, factor, lane, k.shift);
+    const int x0 = begin + 32 * V * wave, x1 = whole + 32 * wave;
+    if (V > 1 && x0 < whole) in.start(x0, whole);
+    if (V == 1 && x1 < end) in.start(x1, end);
     poly.load(c.w.poly + static_cast<int64_t>(block) * (T * T * 2048));
     __syncthreads();
-    // the lane's place behind the begin of the first of eight rows (wide: of the
-    // smaller side, tall: of the larger)
-    const int64_t pp = at.param_pitch * kPSize, op = at.out_pitch * 4;
-    const uint32_t across = TALL ? T * j : V * j;
-    const uint32_t param_lane = 4 * h * static_cast<uint32_t>(pp) + across * kPSize;
-    const uint32_t out_lane = 4 * h * static_cast<uint32_t>(op) + across * 4;
-    for (; x0 < end; x0 += kStride) {
-        floatx16 acc[V][T];
-        times_poly<TALL>(acc, in, poly, lane, x0 + kStride, end);
-        // `run` elements side by side of row 8 q + 4 h + b of the tiles
-        constexpr int N = TALL ? T : V;
-        auto store = [&](const Row &row, int b, const float (&o)[N], bool whole, int there) {
-            char *param = row.param + b * pp, *out = row.out ? row.out + b * op : nullptr;
-            if (whole) {
-                update_run<PBF16, N>(param, out, param_lane, out_lane, o, c.decay, k.update);
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float one[1] = {o[e]};
-                    if (e < there) update_run<PBF16, 1>(param, out, param_lane + e * kPSize, out_lane + e * 4, one, c.decay, k.update);
-                }
-            }
-        };
-        if constexpr (TALL) {
-            Row row{at.param + x0 * pp, at.out ? reinterpret_cast<char *>(at.out) + x0 * op : nullptr};
-            const bool whole = c.s % T == 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (x0 + 8 * q + 4 * h + b >= end || T * j >= c.s) continue;
-                    float o[T];
-#pragma unroll
-                    for (int i = 0; i < T; ++i) o[i] = acc[0][i][4 * q + b] * scale;
-                    store(row, b, o, whole, c.s - T * j);
-                }
-                row.param += 8 * pp;
-                row.out = row.out ? row.out + 8 * op : nullptr;
-                row.keep();
-            }
-        } else {
-            Row row{at.param + x0 * kPSize, at.out ? reinterpret_cast<char *>(at.out + x0) : nullptr};
-            const bool whole = x0 + 32 * V <= end;
-            int left = c.s;  // rows from `row` to the block's end
-#pragma unroll
-            for (int i = 0; i < T; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (left <= 0) continue;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        if (4 * h + b >= left) continue;
-                        float o[V];
-#pragma unroll
-                        for (int v = 0; v < V; ++v) o[v] = acc[v][i][4 * q + b] * scale;
-                        store(row, b, o, whole, end - x0 - V * j);
-                    }
-                    row.param += 8 * pp;
-                    row.out = row.out ? row.out + 8 * op : nullptr;
-                    row.keep();
-                    left -= 8;
-                    asm volatile("" : "+s"(left));
-                }
+    if constexpr (V > 1) {
+        update_columns<T, V, TALL, BF16, PBF16, EVEN>(in, u, poly, lane, x0, V * kBlockUnit, whole);
+        if (x1 < end) {
+            Stream<T, 1, TALL, BF16, EVEN> rest(at, c, factor, lane, k.shift);
+            rest.start(x1, end);
+            update_columns<T, 1, TALL, BF16, PBF16, EVEN>(rest, u, poly, lane, x1, kBlockUnit, end);
         }
+    } else {
+        update_columns<T, 1, TALL, BF16, PBF16, EVEN>(in, u, poly, lane, x1, kBlockUnit, end);
     }
 }
 

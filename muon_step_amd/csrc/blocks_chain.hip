@@ -20,58 +20,58 @@ template <int T> struct Slab {
 template <int T> struct Left {
     half8 hi[T][2 * T][64], lo[T][2 * T][64];
 };
-template <int T>
-__device__ __forceinline__ void put(Left<T> &left, int wave, int lane, const Slab<T> &m, float scale) {
+// One wave's columns as operand fragments.
+template <int T> struct Pairs {
+    half8 hi[2 * T], lo[2 * T];
+};
+template <int T> __device__ __forceinline__ void split_chunk(const Slab<T> &m, int c, half8 &hi, half8 &lo) {
+    float x[8];
 #pragma unroll
-    for (int c = 0; c < 2 * T; ++c) {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = m.v[c >> 1][8 * (c & 1) + e] * scale;
-        half8 hi, lo;
-        split_half(x, hi, lo);
-        left.hi[wave][c][lane] = hi;
-        left.lo[wave][c][lane] = lo;
-    }
+    for (int e = 0; e < 8; ++e) x[e] = m.v[c >> 1][8 * (c & 1) + e];
+    split_half(x, hi, lo);
 }
-// L^T B, scaled: L was put with its own scale, B is split as B scale, the result multiplied by `out`.
-template <int T>
-__device__ __forceinline__ Slab<T> product(const Left<T> &left, int lane, const Slab<T> &b, float scale, float out) {
-    floatx16 acc[T];
-#pragma unroll
-    for (int i = 0; i < T; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][r] = 0.0f;
-    half8 ah[2][T], al[2][T];
+// left^T times the columns whose fragments `right(b, c, hi, lo)` gives, for B
+// right operands at once; every chunk's fragments are fetched and split during
+// the chunk before it.
+template <int T, int B, class F>
+__device__ __forceinline__ void product(floatx16 (&acc)[B][T], const Left<T> &left, int lane, F right) {
+    half8 ah[2][T], al[2][T], bh[2][B], bl[2][B];
     auto fetch = [&](int c) {
 #pragma unroll
         for (int i = 0; i < T; ++i) {
             ah[c & 1][i] = left.hi[i][c][lane];
             al[c & 1][i] = left.lo[i][c][lane];
         }
+#pragma unroll
+        for (int b = 0; b < B; ++b) right(b, c, bh[c & 1][b], bl[c & 1][b]);
     };
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[b][i][r] = 0.0f;
     fetch(0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int c = 0; c < 2 * T; ++c) {
         if (c + 1 < 2 * T) fetch(c + 1);
-        float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = b.v[c >> 1][8 * (c & 1) + e] * scale;
-        half8 hi, lo;
-        split_half(x, hi, lo);
+        for (int k = 0; k < 3; ++k)
 #pragma unroll
-        for (int i = 0; i < T; ++i) acc[i] = mfma(ah[c & 1][i], hi, acc[i]);
+            for (int b = 0; b < B; ++b)
 #pragma unroll
-        for (int i = 0; i < T; ++i) acc[i] = mfma(ah[c & 1][i], lo, acc[i]);
+                for (int i = 0; i < T; ++i)
+                    acc[b][i] = mfma(k == 2 ? al[c & 1][i] : ah[c & 1][i], k == 1 ? bl[c & 1][b] : bh[c & 1][b], acc[b][i]);
+        // loads first, then the splits' instructions between those of the matrix core
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * T + 2 * B, 0);
 #pragma unroll
-        for (int i = 0; i < T; ++i) acc[i] = mfma(al[c & 1][i], hi, acc[i]);
+        for (int k = 0; k < 3 * B * T; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
     }
-    Slab<T> r;
-#pragma unroll
-    for (int i = 0; i < T; ++i)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) r.v[i][k] = acc[i][k] * out;
-    return r;
 }
 
 template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kernel(const BlockChain c) {
@@ -81,7 +81,7 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
     };
     __shared__ __attribute__((aligned(16))) Shared sh;
     __shared__ float sh_sum[T];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, j = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, j = lane & 31, h = lane >> 5;
     const int64_t block = blockIdx.x;
     const int col = 32 * wave + j;
 
@@ -118,45 +118,62 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
     for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) a.v[t][r] = 0.0f;
-    for (int k = 0; k < c.parts; ++k) {
-        const float *g = c.w.gram + (block * c.parts + k) * tri(T) * 1024;
-        if (c.first && parts[k].largest == 0) continue;
-        const float weight = c.first ? ldexpf(1.0f, 2 * (parts[k].shift - common)) : 1.0f;
+    auto add_parts = [&](int first, auto count) {
+        constexpr int N = count.value;
+        float v[N][T][16], weight[N];
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-            if (t >= wave) {
+        for (int n = 0; n < N; ++n) {
+            const float *g = c.w.gram + (block * c.parts + first + n) * tri(T) * 1024;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) a.v[t][r] += weight * g[(tri(t) + wave) * 1024 + acc_row(r, h) * 32 + j];
-            } else {
+            for (int t = 0; t < T; ++t) {
+                if (t >= wave) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const floatx4 v = *reinterpret_cast<const floatx4 *>(g + (tri(wave) + t) * 1024 + j * 32 + 8 * q + 4 * h);
+                    for (int r = 0; r < 16; ++r) v[n][t][r] = as_global(g)[(tri(t) + wave) * 1024 + acc_row(r, h) * 32 + j];
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) a.v[t][4 * q + e] += weight * v[e];
+                    for (int q = 0; q < 4; ++q) {
+                        const floatx4 u = *(const floatx4 __attribute__((address_space(1))) *)(
+                            g + (tri(wave) + t) * 1024 + j * 32 + 8 * q + 4 * h);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[n][t][4 * q + e] = u[e];
+                    }
                 }
             }
+            weight[n] = 1.0f;
+            if (c.first) weight[n] = parts[first + n].largest == 0 ? 0.0f : ldexpf(1.0f, 2 * (parts[first + n].shift - common));
         }
-    }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) a.v[t][r] = __builtin_fmaf(weight[n], v[n][t][r], a.v[t][r]);
+    };
+    // some parts' loads at once
+    int k = 0;
+    for (; k + 4 <= c.parts; k += 4) add_parts(k, std::integral_constant<int, 4>{});
+    for (; k < c.parts; ++k) add_parts(k, std::integral_constant<int, 1>{});
     if (c.first) {
         float trace = 0.0f;
 #pragma unroll
         for (int t = 0; t < T; ++t)
+            if (t == wave) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) trace += on_diagonal(t, r) ? a.v[t][r] : 0.0f;
+                for (int r = 0; r < 16; ++r) trace += acc_row(r, h) == j ? a.v[t][r] : 0.0f;
+            }
         trace = total(trace);
-        const double n = sqrt(static_cast<double>(trace));
-        const float inv = static_cast<float>(1.0 / (n * n));
+        const float n = sqrtf(trace), inv = 1.0f / trace;
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
             for (int r = 0; r < 16; ++r) a.v[t][r] *= inv;
         if (threadIdx.x == 0) {
             int e = 0;  // 2^e <= sqrt(s l) / norm < 2^(e + 1)
-            (void)frexp(sqrt(static_cast<double>(c.s) * c.l) / n, &e);
+            (void)frexpf(sqrtf(static_cast<float>(c.s) * static_cast<float>(c.l)) / n, &e);
             --e;
             BlockScalars out;
             out.shift = zero || bad ? 0 : e - common;
-            out.inv_norm = zero || bad ? 1.0f : static_cast<float>(1.0 / ldexp(n, e));
+            out.inv_norm = zero || bad ? 1.0f : 1.0f / ldexpf(n, e);
             out.update = c.update;
             out.pad_ = 0;
             c.w.scalars[block] = out;
@@ -178,46 +195,106 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
     for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-            p.v[t][r] = c.first ? (on_diagonal(t, r) && there ? 1.0f : 0.0f) : own[(t * 16 + r) * 64 + lane];
+            p.v[t][r] = c.first ? (on_diagonal(t, r) && there ? 1.0f : 0.0f) : as_global(own)[(t * 16 + r) * 64 + lane];
 
-    Slab<T> q = p;  // the last step's Q, for the norm of what it makes of X
-    Slab<T> last_r = a;
+    // A, Q and P as they enter the products: A 64, Q 16, P 2^-exp_in, A Q 1024.
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            a.v[t][r] *= kScaleA;
+            p.v[t][r] *= c.steps > 0 ? ldexpf(1.0f, -c.step[0].exp_in) : 1.0f;
+        }
+    float square = 1.0f;  // ||O||^2
     for (int k = 0; k < c.steps; ++k) {
         const BlockChain::Step step = c.step[k];
-        put(sh.left, wave, lane, a, kScaleA);
+        const bool more = k + 1 < c.steps, norm = !more && c.last && c.unit_rms;
+#pragma unroll
+        for (int i = 0; i < 2 * T; ++i) {
+            half8 hi, lo;
+            split_chunk(a, i, hi, lo);
+            sh.left.hi[wave][i][lane] = hi;
+            sh.left.lo[wave][i][lane] = lo;
+        }
         __syncthreads();
-        const Slab<T> s = product(sh.left, lane, a, kScaleA, 1.0f / (kScaleA * kScaleA));
+        floatx16 s[1][T];
+        // A^T A: the wave's own columns of A are among the rows of A^T
+        product<T, 1>(s, sh.left, lane, [&](int, int i, half8 &hi, half8 &lo) {
+            hi = sh.left.hi[wave][i][lane];
+            lo = sh.left.lo[wave][i][lane];
+        });
+        const float qa = kScaleQ * step.a, qb = kScaleQ / kScaleA * step.b, qc = kScaleQ / (kScaleA * kScaleA) * step.c;
+        Slab<T> q;
 #pragma unroll
-        for (int t = 0; t < T; ++t)
+        for (int t = 0; t < T; ++t) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float diagonal = on_diagonal(t, r) ? step.a : 0.0f;
-                q.v[t][r] = diagonal + step.b * a.v[t][r] + step.c * s.v[t][r];
+            for (int r = 0; r < 16; ++r) q.v[t][r] = __builtin_fmaf(qc, s[0][t][r], qb * a.v[t][r]);
+            if (t == wave) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) q.v[t][r] += acc_row(r, h) == j ? qa : 0.0f;
             }
-        const bool more = k + 1 < c.steps;
-        if (more || (c.last && c.unit_rms)) last_r = product(sh.left, lane, q, kScaleQ, 1.0f / (kScaleA * kScaleQ));
+        }
+        Pairs<T> pairs;
+        Slab<T> ar;  // A^T Q
+        if (more || norm) {
+            floatx16 acc[1][T];
+            product<T, 1>(acc, sh.left, lane, [&](int, int i, half8 &hi, half8 &lo) {
+                split_chunk(q, i, hi, lo);
+                pairs.hi[i] = hi;
+                pairs.lo[i] = lo;
+            });
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) ar.v[t][r] = acc[0][t][r];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * T; ++i) split_chunk(q, i, pairs.hi[i], pairs.lo[i]);
+        }
+        if (norm) {  // ||O||^2 = tr Q A Q
+            float sq = 0.0f;
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sq += q.v[t][r] * ar.v[t][r];
+            square = total(sq) / (kScaleA * kScaleQ * kScaleQ);
+        }
         __syncthreads();
-        put(sh.left, wave, lane, q, kScaleQ);
+#pragma unroll
+        for (int i = 0; i < 2 * T; ++i) {
+            sh.left.hi[wave][i][lane] = pairs.hi[i];
+            sh.left.lo[wave][i][lane] = pairs.lo[i];
+        }
         __syncthreads();
-        p = product(sh.left, lane, p, ldexpf(1.0f, -step.exp_in), ldexpf(1.0f / kScaleQ, step.exp_in));
-        if (more) a = product(sh.left, lane, last_r, kScaleR, 1.0f / (kScaleQ * kScaleR));
+        const float rescale = ldexpf(1.0f / kScaleQ, step.exp_in - step.exp_out);
+        if (more) {
+            floatx16 acc[2][T];
+            product<T, 2>(acc, sh.left, lane, [&](int b, int i, half8 &hi, half8 &lo) { split_chunk(b ? ar : p, i, hi, lo); });
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    p.v[t][r] = acc[0][t][r] * rescale;
+                    a.v[t][r] = acc[1][t][r] * (1.0f / (kScaleQ * kScaleQ));
+                }
+        } else {
+            floatx16 acc[1][T];
+            product<T, 1>(acc, sh.left, lane, [&](int, int i, half8 &hi, half8 &lo) { split_chunk(p, i, hi, lo); });
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) p.v[t][r] = acc[0][t][r] * rescale;
+        }
         __syncthreads();
     }
 
-    if (c.last && c.unit_rms) {
-        // ||O||^2 = tr Q A Q, or 1 where there was no step
-        float sq = 0.0f;
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sq += q.v[t][r] * last_r.v[t][r];
-        sq = total(sq);
-        const double o = c.steps > 0 ? sqrt(static_cast<double>(sq)) : 1.0;
-        if (threadIdx.x == 0) c.w.scalars[block].update = zero || !(o > 0) ? 0.0f : static_cast<float>(c.update / o);
+    if (c.last && c.unit_rms && threadIdx.x == 0) {
+        const double o = sqrt(static_cast<double>(square));
+        c.w.scalars[block].update = zero || !(o > 0) ? 0.0f : static_cast<float>(c.update / o);
     }
 
     // P's columns for the next segment, and its rows as fragments for the products with N.
-    const float out = c.steps > 0 ? ldexpf(1.0f, -c.step[c.steps - 1].exp_out) : 1.0f;
+    const float whole = c.steps > 0 ? ldexpf(1.0f, c.step[c.steps - 1].exp_out) : 1.0f;  // what P is held short of
     const float nan = __builtin_nanf("");
     __syncthreads();
 #pragma unroll
@@ -225,8 +302,8 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const float x = zero ? 0.0f : bad ? nan : p.v[t][r];
-            if (!c.last) own[(t * 16 + r) * 64 + lane] = x;
-            sh.rows[32 * t + acc_row(r, h)][col] = x * out;
+            if (!c.last) own[(t * 16 + r) * 64 + lane] = x * whole;
+            sh.rows[32 * t + acc_row(r, h)][col] = x;
         }
     __syncthreads();
     half8 *frag = reinterpret_cast<half8 *>(c.w.poly) + block * (T * T * 256);

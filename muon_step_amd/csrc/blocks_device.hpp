@@ -27,15 +27,20 @@ __device__ __forceinline__ floatx16 mfma(bf16x8 a, bf16x8 b, floatx16 c) {
 // The row of an accumulator's register r in lane half h.
 __device__ __forceinline__ int acc_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
-// x = hi + lo to 2^-21 of x (both parts truncated), |x| below 65504; parts below 2^-24 are lost.
+// x = hi + lo to 2^-21 of x (both parts truncated, two values an instruction),
+// |x| below 65504; parts below 2^-24 are lost.
 __device__ __forceinline__ void split_half(const float (&x)[8], half8 &hi, half8 &lo) {
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
-        const half2_t h = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(x[k], x[k + 1]));
-        const half2_t l = __builtin_bit_cast(
-            half2_t, __builtin_amdgcn_cvt_pkrtz(x[k] - static_cast<float>(h[0]), x[k + 1] - static_cast<float>(h[1])));
-        hi[k] = h[0];
-        hi[k + 1] = h[1];
+        const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(x[k], x[k + 1]));
+        // x - hi, with the conversion of hi in the same instruction
+        float d0, d1;
+        asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel_hi:[1,0,0]" : "=v"(d0) : "v"(h), "v"(x[k]));
+        asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(d1) : "v"(h), "v"(x[k + 1]));
+        const half2_t l = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(d0, d1));
+        const half2_t hh = __builtin_bit_cast(half2_t, h);
+        hi[k] = hh[0];
+        hi[k + 1] = hh[1];
         lo[k] = l[0];
         lo[k + 1] = l[1];
     }
@@ -49,9 +54,9 @@ __device__ __forceinline__ void split_bf(const float (&x)[8], bf16x8 &hi, bf16x8
     }
 }
 
-// Scales of the fp16 pairs: A up to 16 (the host admits schedules that keep
-// |X| <= 4), Q up to 64, R up to 64 in magnitude.
-constexpr float kScaleA = 256.0f, kScaleQ = 16.0f, kScaleR = 256.0f;
+// Scales of the fp16 pairs: |A| <= 16, |Q| <= 60 and |A Q| <= 60 in the schedules
+// that the host admits, so A Q's product of scales, 1024, keeps it below 65504 too.
+constexpr float kScaleA = 64.0f, kScaleQ = 16.0f;
 // X of the second and later segments' Gram, |X| <= 4.
 constexpr float kScaleX = 8192.0f;
 
@@ -90,62 +95,34 @@ template <bool BF16> __device__ __forceinline__ float load_grad(const char *p, i
     return *as_global(reinterpret_cast<const float *>(p) + at);
 }
 
-// N floats / bf16 values at an address that only their size aligns.
-template <int N> struct FloatsAt {
-    typedef float type __attribute__((ext_vector_type(N), aligned(4)));
-};
-template <int N> __device__ __forceinline__ void load_floats(const float *p, float (&x)[N]) {
-    static_assert(N == 1 || N == 2 || N == 3 || N % 4 == 0, "whole vectors");
-    if constexpr (N == 1) {
-        x[0] = *as_global(p);
-    } else if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const auto v = *(const typename FloatsAt<4>::type __attribute__((address_space(1))) *)(p + i);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[i + k] = v[k];
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = as_global(p)[k];
-    }
+// A value at a uniform address and a lane's bytes behind it.
+template <class W> __device__ __forceinline__ W load_at(const char *row, uint32_t lane) {
+    return *(const W __attribute__((address_space(1))) *)((const char __attribute__((address_space(1))) *)row + lane);
 }
-template <int N> __device__ __forceinline__ void store_floats(float *p, const float (&x)[N]) {
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            typename FloatsAt<4>::type v;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = x[i + k];
-            *(typename FloatsAt<4>::type __attribute__((address_space(1))) *)(p + i) = v;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) as_global(p)[k] = x[k];
-    }
+template <class W> __device__ __forceinline__ void store_at(char *row, uint32_t lane, const W &v) {
+    *(W __attribute__((address_space(1))) *)((char __attribute__((address_space(1))) *)row + lane) = v;
 }
-template <int N> struct HalvesAt {
-    typedef uint16_t type __attribute__((ext_vector_type(N), aligned(2)));
+// N words at an address that A divides.
+template <int N, int A> struct WordsAt {
+    typedef uint32_t type __attribute__((ext_vector_type(N), aligned(A)));
 };
-template <bool BF16, int N> __device__ __forceinline__ void load_grads(const char *p, int64_t at, float (&x)[N]) {
-    if constexpr (!BF16) {
-        load_floats<N>(reinterpret_cast<const float *>(p) + at, x);
-    } else if constexpr (N % 8 == 0 || N == 4 || N == 2) {
-        constexpr int V = N % 8 == 0 ? 8 : N;
+
+// Sum of a value over the waves of a workgroup, 1024 values of each, to dst: `put`
+// writes a wave's own to the buffer it is given.  k alternates between two buffers
+// of sh (4 KB for each wave each), so that one barrier a tile suffices.
+template <class F> __device__ __forceinline__ void sum_tile(float *dst, float *sh, int k, F put) {
+    const int wave = threadIdx.x >> 6;
+    float *buf = sh + (k & 1) * kWaves * 1024;
+    put(buf + wave * 1024);
+    __syncthreads();
+    floatx4 v = *reinterpret_cast<const floatx4 *>(buf + threadIdx.x * 4);
 #pragma unroll
-        for (int i = 0; i < N; i += V) {
-            const auto v = *(const typename HalvesAt<V>::type __attribute__((address_space(1))) *)(
-                reinterpret_cast<const uint16_t *>(p) + at + i);
-#pragma unroll
-            for (int k = 0; k < V; ++k) x[i + k] = bf16_bits_to_float(v[k]);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) x[k] = load_grad<true>(p, at + k);
-    }
+    for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const floatx4 *>(buf + w * 1024 + threadIdx.x * 4);
+    *(floatx4 __attribute__((address_space(1))) *)(dst + threadIdx.x * 4) = v;
 }
 
-// The lower triangle's tiles of a sum of X X^T over columns of X.
+// The lower triangle's 32 x 32 tiles of a sum of X X^T over columns of X, from
+// fragments of 32 rows and 16 columns.
 template <int T> struct Triangle {
     floatx16 tile[tri(T)];
     __device__ __forceinline__ void clear() {
@@ -157,33 +134,68 @@ template <int T> struct Triangle {
     // Adds 16 columns, given as hi and lo fragments of each of X's T row blocks.
     template <class V> __device__ __forceinline__ void add(const V (&hi)[T], const V (&lo)[T]) {
 #pragma unroll
-        for (int i = 0; i < T; ++i)
+        for (int k = 0; k < 3; ++k)
 #pragma unroll
-            for (int j = 0; j <= i; ++j) tile[tri(i) + j] = mfma(hi[i], hi[j], tile[tri(i) + j]);
+            for (int i = 0; i < T; ++i)
 #pragma unroll
-        for (int i = 0; i < T; ++i)
-#pragma unroll
-            for (int j = 0; j <= i; ++j) tile[tri(i) + j] = mfma(hi[i], lo[j], tile[tri(i) + j]);
-#pragma unroll
-        for (int i = 0; i < T; ++i)
-#pragma unroll
-            for (int j = 0; j <= i; ++j) tile[tri(i) + j] = mfma(lo[i], hi[j], tile[tri(i) + j]);
+                for (int j = 0; j <= i; ++j) {
+                    floatx16 &t = tile[tri(i) + j];
+                    t = mfma(k == 2 ? lo[i] : hi[i], k == 1 ? lo[j] : hi[j], t);
+                }
     }
-    // The workgroup's waves' sum, row-major tile by tile, to dst.  sh: two times
-    // 4 KB for each wave; entered behind a barrier.
+    // The workgroup's sum, row-major tile by tile, to dst; entered behind a barrier.
     __device__ __forceinline__ void reduce(float *dst, float *sh) const {
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int k = 0; k < tri(T); ++k) {
-            float *buf = sh + (k & 1) * kWaves * 1024;
+        for (int k = 0; k < tri(T); ++k)
+            sum_tile(dst + k * 1024, sh, k, [&](float *buf) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) buf[wave * 1024 + acc_row(r, lane >> 5) * 32 + (lane & 31)] = tile[k][r];
-            __syncthreads();
-            floatx4 v = *reinterpret_cast<const floatx4 *>(buf + threadIdx.x * 4);
+                for (int r = 0; r < 16; ++r) buf[acc_row(r, lane >> 5) * 32 + (lane & 31)] = tile[k][r];
+            });
+    }
+};
+
+// The same from fragments of 16 rows and 32 columns (v_mfma_f32_16x16x32, whose
+// accumulator holds in lane (j, h), j < 16, h < 4, rows 4 h .. 4 h + 3 of column j).
+template <int T> struct FineTriangle {
+    floatx4 tile[tri(2 * T)];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const floatx4 *>(buf + w * 1024 + threadIdx.x * 4);
-            *(floatx4 __attribute__((address_space(1))) *)(dst + k * 1024 + threadIdx.x * 4) = v;
-        }
+        for (int k = 0; k < tri(2 * T); ++k) tile[k] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __device__ __forceinline__ void add(const bf16x8 (&hi)[2 * T], const bf16x8 (&lo)[2 * T]) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int i = 0; i < 2 * T; ++i)
+#pragma unroll
+                for (int j = 0; j <= i; ++j) {
+                    floatx4 &t = tile[tri(i) + j];
+                    t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k == 2 ? lo[i] : hi[i], k == 1 ? lo[j] : hi[j], t, 0, 0, 0);
+                }
+    }
+    __device__ __forceinline__ void reduce(float *dst, float *sh) const {
+        const int j = threadIdx.x & 15, h = threadIdx.x >> 4 & 3;
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int k = 0; k <= i; ++k)
+                sum_tile(dst + (tri(i) + k) * 1024, sh, tri(i) + k, [&](float *buf) {
+#pragma unroll
+                    for (int a = 0; a < 2; ++a)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const bool mirror = i == k && b > a;  // of a diagonal tile, the part above the diagonal
+                            const floatx4 &t = mirror ? tile[tri(2 * i + b) + 2 * k + a] : tile[tri(2 * i + a) + 2 * k + b];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                if (mirror)
+                                    buf[(16 * a + j) * 32 + 16 * b + 4 * h + r] = t[r];
+                                else
+                                    buf[(16 * a + 4 * h + r) * 32 + 16 * b + j] = t[r];
+                            }
+                        }
+                });
     }
 };
 

@@ -1,9 +1,173 @@
 // The first pass of the block step: momentum, N, and the sums of N N^T (blocks.hpp).
+//
+// Bound by memory (10 bytes an element, and 3 s / 2 products of 16-bit parts for
+// each, a fifth of the matrix cores' rate at s = 128).  What counts is that a
+// wave's accesses cover whole stretches of memory: 64 bytes of M for each row in
+// wide blocks (16 rows by 4 lanes: with 32 rows by 2 lanes, M's stores reached the
+// L2 in pieces of 16 bytes, four times as many, and the pass ran at 3.7 TB/s), and
+// T elements of a row for each of 32 lanes in tall ones; and that the next 32
+// columns are on their way while the present ones are worked on.
 #include "blocks_device.hpp"
 
 namespace muon {
 
 namespace {
+
+// M and G of 32 columns of X, and what a lane does with them.
+//   wide  lane (i, h), i < 16, h < 4: of rows 16 b + i, columns 16 e + 4 h + k, e < 2, k < 4
+//   tall  lane (i, h), i < 32, h < 2: of columns 16 q + 8 h + e, e < 8, the T entries from T i on
+template <int T, bool TALL, bool BF16> struct Columns {
+    static constexpr int kSteps = TALL ? 2 : 2 * T;         // parts of the unit, loaded and used in turn
+    static constexpr int kValues = TALL ? 8 * T : 8;
+    static constexpr bool kPacked = BF16 && (!TALL || T % 2 == 0);
+    static constexpr int kGrads = kPacked ? kValues / 2 : kValues;
+    static constexpr int kGSize = BF16 ? 2 : 4;
+    typedef char *Bytes;
+    float m[kSteps][kValues];
+    uint32_t g[kSteps][kGrads];
+    const Place &at;
+    int s, i, h;
+    Bytes mom_row = nullptr, put_row = nullptr;
+    const char *grad_row = nullptr;
+    int left = 0, put_left = 0;
+    uint32_t mom_lane, grad_lane, mom_part, grad_part;
+
+    __device__ __forceinline__ Columns(const Place &place, int side, int lane) : at(place), s(side) {
+        const uint32_t mp = static_cast<uint32_t>(at.mom_pitch), gp = static_cast<uint32_t>(at.grad_pitch);
+        if constexpr (TALL) {
+            i = lane & 31;
+            h = lane >> 5;
+            const uint32_t p = T * i < s ? T * i : 0;
+            mom_lane = mom_part = (8 * h * mp + p) * 4;
+            grad_lane = grad_part = (8 * h * gp + p) * kGSize;
+        } else {
+            i = lane & 15;
+            h = lane >> 4;
+            const uint32_t row = min(i, s - 1), part = (s & 15) ? min(i, (s & 15) - 1) : row;
+            mom_lane = (row * mp + 4 * h) * 4;
+            grad_lane = (row * gp + 4 * h) * kGSize;
+            mom_part = (part * mp + 4 * h) * 4;
+            grad_part = (part * gp + 4 * h) * kGSize;
+        }
+    }
+    // Whether the lane's entries of a step belong to the block (wide: `rows` from the step's first on are there).
+    __device__ __forceinline__ bool mine(int rows) const { return TALL ? T * i < s : i < rows; }
+    __device__ __forceinline__ void begin(int x0) {
+        mom_row = reinterpret_cast<Bytes>(at.mom + (TALL ? x0 * at.mom_pitch : x0));
+        grad_row = at.grad + (TALL ? x0 * at.grad_pitch : x0) * kGSize;
+        left = s;
+    }
+    __device__ __forceinline__ void begin_store(int x0) {
+        put_row = reinterpret_cast<Bytes>(at.mom + (TALL ? x0 * at.mom_pitch : x0));
+        put_left = s;
+    }
+    __device__ __forceinline__ void load(int step) {
+        if constexpr (TALL) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const Bytes mr = mom_row + e * at.mom_pitch * 4;
+                const char *gr = grad_row + e * at.grad_pitch * kGSize;
+                floats(mr, &m[step][e * T]);
+                if constexpr (kPacked) {
+                    const auto v = load_at<typename WordsAt<T / 2, 2>::type>(gr, grad_lane);
+#pragma unroll
+                    for (int k = 0; k < T / 2; ++k) g[step][e * T / 2 + k] = v[k];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < T; ++k)
+                        g[step][e * T + k] = BF16 ? static_cast<uint32_t>(load_at<uint16_t>(gr, grad_lane + 2 * k))
+                                                  : load_at<uint32_t>(gr, grad_lane + 4 * k);
+                }
+            }
+            mom_row += 16 * at.mom_pitch * 4;
+            grad_row += 16 * at.grad_pitch * kGSize;
+            asm volatile("" : "+s"(mom_row), "+s"(grad_row));
+        } else {
+            const bool full = left >= 16;
+            const uint32_t ml = full ? mom_lane : mom_part, gl = full ? grad_lane : grad_part;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const auto v = load_at<WordsAt<4, 4>::type>(mom_row + 64 * e, ml);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) m[step][4 * e + k] = __uint_as_float(v[k]);
+                if constexpr (BF16) {
+                    const auto u = load_at<WordsAt<2, 2>::type>(grad_row + 32 * e, gl);
+                    g[step][2 * e] = u[0];
+                    g[step][2 * e + 1] = u[1];
+                } else {
+                    const auto u = load_at<WordsAt<4, 4>::type>(grad_row + 64 * e, gl);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) g[step][4 * e + k] = u[k];
+                }
+            }
+            left -= 16;
+            if (left > 0) {  // steps past the last row read that step again
+                mom_row += 16 * at.mom_pitch * 4;
+                grad_row += 16 * at.grad_pitch * kGSize;
+            } else {
+                left += 16;
+            }
+            asm volatile("" : "+s"(mom_row), "+s"(grad_row), "+s"(left));
+        }
+    }
+    // N of a step's values, zero where there is nothing; M's new ones take the old ones' place.
+    __device__ __forceinline__ void input(int step, float factor, float mu, bool nesterov, float (&n)[kValues]) {
+        const bool in = mine(s - 16 * step);
+#pragma unroll
+        for (int k = 0; k < kValues; ++k) {
+            float gf;
+            if constexpr (!BF16)
+                gf = __uint_as_float(g[step][k]);
+            else if constexpr (kPacked)
+                gf = __uint_as_float(k % 2 ? g[step][k / 2] & 0xffff0000u : g[step][k / 2] << 16);
+            else
+                gf = __uint_as_float(g[step][k] << 16);
+            gf *= factor;
+            float &v = m[step][k];
+            v = mu * v + gf;
+            const float x = nesterov ? mu * v + gf : v;
+            n[k] = in ? x : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void store(int step) {
+        if constexpr (TALL) {
+            if (mine(0)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) put_floats<T>(put_row + e * at.mom_pitch * 4, mom_lane, &m[step][e * T]);
+            }
+            put_row += 16 * at.mom_pitch * 4;
+        } else {
+            if (mine(put_left)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) put_floats<4>(put_row + 64 * e, mom_lane, &m[step][4 * e]);
+            }
+            put_left -= 16;
+            put_row += 16 * at.mom_pitch * 4;
+        }
+        asm volatile("" : "+s"(put_row), "+s"(put_left));
+    }
+
+  private:
+    __device__ __forceinline__ void floats(Bytes row, float *to) const {
+        if constexpr (T == 1) {
+            to[0] = load_at<float>(row, mom_lane);
+        } else {
+            const auto v = load_at<typename WordsAt<T, 4>::type>(row, mom_lane);
+#pragma unroll
+            for (int k = 0; k < T; ++k) to[k] = __uint_as_float(v[k]);
+        }
+    }
+    template <int N> __device__ __forceinline__ static void put_floats(Bytes row, uint32_t lane, const float *from) {
+        if constexpr (N == 1) {
+            store_at<float>(row, lane, from[0]);
+        } else {
+            typename WordsAt<N, 4>::type v;
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = __float_as_uint(from[k]);
+            store_at(row, lane, v);
+        }
+    }
+};
 
 // One part of one block: M <- mu M + G and the sum of N N^T over the part's
 // columns.  Outside 2^-40 <= max |N| <= 2^40, where squares could leave fp32's
@@ -14,130 +178,123 @@ __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTa
     __shared__ uint32_t sh_largest[kWaves];
     const uint32_t block = blockIdx.x / c.parts, part = blockIdx.x % c.parts;  // block: of the launch
     const Place at = locate<BF16 ? 2 : 4, 2>(t, c, c.base + block);
-    const int wave = threadIdx.x >> 6, i = threadIdx.x & 31, h = threadIdx.x >> 5 & 1;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int begin = part * c.part_len, end = min(begin + c.part_len, c.l);
     const float factor = c.factor ? *c.factor : 1.0f;
     const float mu = c.mu;
     const bool nesterov = c.nesterov != 0;
     uint32_t largest = 0;
-    Triangle<T> sum;
+    typename std::conditional<TALL, Triangle<T>, FineTriangle<T>>::type sum;
+    Columns<T, TALL, BF16> in(at, c.s, lane);
 
     auto note = [&](float n) { largest = max(largest, __float_as_uint(n) & 0x7fffffffu); };
 
     // 32 columns from x0 on, element by element, past-the-end ones as zeros;
     // again: M is up to date, and N is scaled by 2^-shift.
-    auto each = [&](int x0, bool again, int shift) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            bf16x8 hi[T], lo[T];
-#pragma unroll
-            for (int k = 0; k < T; ++k) {
-                const int p = TALL ? T * i + k : 32 * k + i;
-                float n[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int x = TALL ? x0 + 16 * q + 8 * h + e : x0 + 16 * h + 8 * q + e;
-                    n[e] = 0.0f;
-                    if (p < c.s && x < end) {
-                        const int64_t row = TALL ? x : p, col = TALL ? p : x;
-                        float *m = at.mom + row * at.mom_pitch + col;
-                        const float g = load_grad<BF16>(at.grad, row * at.grad_pitch + col) * factor;
-                        float v = *as_global(m);
-                        if (!again) {
-                            v = mu * v + g;
-                            *as_global(m) = v;
-                        }
-                        n[e] = nesterov ? mu * v + g : v;
-                    }
-                    if (again)
-                        n[e] = ldexpf(n[e], -shift);
-                    else
-                        note(n[e]);
-                }
-                split_bf(n, hi[k], lo[k]);
+    auto one = [&](int p, int x, bool again, int shift) {
+        float n = 0.0f;
+        if (p < c.s && x < end) {
+            const int64_t row = TALL ? x : p, col = TALL ? p : x;
+            float *m = at.mom + row * at.mom_pitch + col;
+            const float g = load_grad<BF16>(at.grad, row * at.grad_pitch + col) * factor;
+            float v = *as_global(m);
+            if (!again) {
+                v = mu * v + g;
+                *as_global(m) = v;
             }
-            sum.add(hi, lo);
+            n = nesterov ? mu * v + g : v;
         }
+        if (again)
+            n = ldexpf(n, -shift);
+        else
+            note(n);
+        return n;
     };
-    // 32 columns, all of them inside.
-    auto whole = [&](int x0) {
+    auto each = [&](int x0, bool again, int shift) {
         if constexpr (TALL) {
-            const bool mine = T * i < c.s;
-            const int p = mine ? T * i : 0;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                float m[8][T], g[8][T];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t row = x0 + 16 * q + 8 * h + e;
-                    load_floats<T>(at.mom + row * at.mom_pitch + p, m[e]);
-                    load_grads<BF16, T>(at.grad, row * at.grad_pitch + p, g[e]);
-                }
                 bf16x8 hi[T], lo[T];
 #pragma unroll
                 for (int k = 0; k < T; ++k) {
                     float n[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float gf = g[e][k] * factor;
-                        m[e][k] = mu * m[e][k] + gf;
-                        n[e] = nesterov ? mu * m[e][k] + gf : m[e][k];
-                        n[e] = mine ? n[e] : 0.0f;
-                        note(n[e]);
-                    }
+                    for (int e = 0; e < 8; ++e) n[e] = one(T * in.i + k, x0 + 16 * q + 8 * in.h + e, again, shift);
                     split_bf(n, hi[k], lo[k]);
-                }
-                if (mine) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        store_floats<T>(at.mom + (x0 + 16 * q + 8 * h + e) * at.mom_pitch + p, m[e]);
                 }
                 sum.add(hi, lo);
             }
         } else {
-            bf16x8 hi[2][T], lo[2][T];
-            float m[T][16], g[T][16];
+            bf16x8 hi[2 * T], lo[2 * T];
 #pragma unroll
-            for (int k = 0; k < T; ++k) {
-                const int64_t row = min(32 * k + i, c.s - 1);
-                load_floats<16>(at.mom + row * at.mom_pitch + x0 + 16 * h, m[k]);
-                load_grads<BF16, 16>(at.grad, row * at.grad_pitch + x0 + 16 * h, g[k]);
+            for (int b = 0; b < 2 * T; ++b) {
+                float n[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    n[e] = one(16 * b + in.i, x0 + 16 * (e >> 2) + 4 * in.h + (e & 3), again, shift);
+                split_bf(n, hi[b], lo[b]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-            for (int k = 0; k < T; ++k) {
-                const bool mine = 32 * k + i < c.s;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float n[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float gf = g[k][8 * q + e] * factor;
-                        float &v = m[k][8 * q + e];
-                        v = mu * v + gf;
-                        n[e] = nesterov ? mu * v + gf : v;
-                        n[e] = mine ? n[e] : 0.0f;
-                        note(n[e]);
-                    }
-                    split_bf(n, hi[q][k], lo[q][k]);
-                }
-                if (mine) store_floats<16>(at.mom + (32 * k + i) * at.mom_pitch + x0 + 16 * h, m[k]);
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q) sum.add(hi[q], lo[q]);
+            sum.add(hi, lo);
         }
     };
 
     sum.clear();
-    const bool vec = !TALL || c.s % T == 0;
-    for (int x0 = begin + 32 * wave; x0 < end; x0 += kBlockUnit) {
-        if (vec && x0 + 32 <= end)
-            whole(x0);
-        else
-            each(x0, false, 0);
-    }
+    // units that lie inside as a whole; in tall blocks lanes that do, too
+    const int whole = (TALL && c.s % T != 0) ? begin : begin + (end - begin) / 32 * 32;
+    int x0 = begin + 32 * wave;
+    if (x0 < whole) {
+        in.begin(x0);
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) largest = max(largest, static_cast<uint32_t>(__shfl_xor(static_cast<int>(largest), off, 64)));
-    if ((threadIdx.x & 63) == 0) sh_largest[wave] = largest;
+        for (int k = 0; k < in.kSteps; ++k) in.load(k);
+    }
+    for (; x0 < whole; x0 += kBlockUnit) {
+        const int next = x0 + kBlockUnit;
+        if (next < whole) in.begin(next);
+        in.begin_store(x0);
+        if constexpr (TALL) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float n[8 * T];
+                in.input(q, factor, mu, nesterov, n);
+                in.store(q);
+                if (next < whole) in.load(q);
+                bf16x8 hi[T], lo[T];
+#pragma unroll
+                for (int k = 0; k < T; ++k) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = n[e * T + k];
+                        note(x[e]);
+                    }
+                    split_bf(x, hi[k], lo[k]);
+                }
+                sum.add(hi, lo);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            bf16x8 hi[2 * T], lo[2 * T];
+#pragma unroll
+            for (int b = 0; b < 2 * T; ++b) {
+                float n[8];
+                in.input(b, factor, mu, nesterov, n);
+                in.store(b);
+                if (next < whole) in.load(b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) note(n[e]);
+                split_bf(n, hi[b], lo[b]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            sum.add(hi, lo);
+        }
+    }
+    // (the wave's next unit, so that every unit has one owner)
+    for (; x0 < end; x0 += kBlockUnit) each(x0, false, 0);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        largest = max(largest, static_cast<uint32_t>(__shfl_xor(static_cast<int>(largest), off, 64)));
+    if (lane == 0) sh_largest[wave] = largest;
     __syncthreads();
     largest = max(max(sh_largest[0], sh_largest[1]), max(sh_largest[2], sh_largest[3]));
     int shift = 0;
@@ -148,7 +305,7 @@ __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTa
     }
     if (shift != 0) {
         sum.clear();
-        for (int x0 = begin + 32 * wave; x0 < end; x0 += kBlockUnit) each(x0, true, shift);
+        for (x0 = begin + 32 * wave; x0 < end; x0 += kBlockUnit) each(x0, true, shift);
     }
     const int64_t slot = static_cast<int64_t>(block) * c.parts + part;
     sum.reduce(c.w.gram + slot * tri(T) * 1024, sh);
