@@ -389,8 +389,7 @@ struct Update {
 };
 
 // Columns x0, x0 + stride, ... below `end` of a wave: O = P N 2^shift scale, and W.
-// W's rows of the first tile are read before the products and those of a later
-// tile before the tile in front of it is written, so that they are there in time.
+// W is read before the products, so that it is there behind them.
 template <int T, int V, bool TALL, bool BF16, bool PBF16, bool EVEN>
 __device__ __forceinline__ void update_columns(Stream<T, V, TALL, BF16, EVEN> &in, const Update &u, const Poly<T> &poly, int lane,
                                                int x0, int stride, int end) {
@@ -412,24 +411,22 @@ __device__ __forceinline__ void update_columns(Stream<T, V, TALL, BF16, EVEN> &i
         const char *ahead = row;
         char *out = at.out ? reinterpret_cast<char *>(at.out) + (TALL ? x0 * op : static_cast<int64_t>(x0) * 4) : nullptr;
         int left = rows, ahead_left = rows;
-        Run<PBF16, N> w[2][4][4];
-        auto fetch = [&](int tile) {
+        Run<PBF16, N> w[kTiles][4][4];
+#pragma unroll
+        for (int tile = 0; tile < kTiles; ++tile)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
-                    if (4 * h + b < ahead_left && there > 0) w[tile & 1][q][b].load(ahead + b * pp, param_lane, whole, there);
+                    if (4 * h + b < ahead_left && there > 0) w[tile][q][b].load(ahead + b * pp, param_lane, whole, there);
                 ahead += 8 * pp;
                 ahead_left -= 8;
                 asm volatile("" : "+s"(ahead), "+s"(ahead_left));
             }
-        };
-        fetch(0);
         floatx16 acc[V][T];
         times_poly<TALL>(acc, in, poly, lane, x0 + stride, end);
 #pragma unroll
         for (int tile = 0; tile < kTiles; ++tile) {
-            if (tile + 1 < kTiles) fetch(tile + 1);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
 #pragma unroll
@@ -438,7 +435,7 @@ __device__ __forceinline__ void update_columns(Stream<T, V, TALL, BF16, EVEN> &i
 #pragma unroll
                     for (int e = 0; e < N; ++e) o[e] = (TALL ? acc[0][e][4 * q + b] : acc[e][tile][4 * q + b]) * u.scale;
                     if (4 * h + b < left && there > 0)
-                        w[tile & 1][q][b].update(row + b * pp, param_lane, out ? out + b * op : nullptr, out_lane, whole, there, o,
+                        w[tile][q][b].update(row + b * pp, param_lane, out ? out + b * op : nullptr, out_lane, whole, there, o,
                                                  u.c.decay, u.update);
                 }
                 row += 8 * pp;

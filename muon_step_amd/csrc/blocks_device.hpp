@@ -155,50 +155,6 @@ template <int T> struct Triangle {
     }
 };
 
-// The same from fragments of 16 rows and 32 columns (v_mfma_f32_16x16x32, whose
-// accumulator holds in lane (j, h), j < 16, h < 4, rows 4 h .. 4 h + 3 of column j).
-template <int T> struct FineTriangle {
-    floatx4 tile[tri(2 * T)];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int k = 0; k < tri(2 * T); ++k) tile[k] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    __device__ __forceinline__ void add(const bf16x8 (&hi)[2 * T], const bf16x8 (&lo)[2 * T]) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-#pragma unroll
-            for (int i = 0; i < 2 * T; ++i)
-#pragma unroll
-                for (int j = 0; j <= i; ++j) {
-                    floatx4 &t = tile[tri(i) + j];
-                    t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k == 2 ? lo[i] : hi[i], k == 1 ? lo[j] : hi[j], t, 0, 0, 0);
-                }
-    }
-    __device__ __forceinline__ void reduce(float *dst, float *sh) const {
-        const int j = threadIdx.x & 15, h = threadIdx.x >> 4 & 3;
-#pragma unroll
-        for (int i = 0; i < T; ++i)
-#pragma unroll
-            for (int k = 0; k <= i; ++k)
-                sum_tile(dst + (tri(i) + k) * 1024, sh, tri(i) + k, [&](float *buf) {
-#pragma unroll
-                    for (int a = 0; a < 2; ++a)
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const bool mirror = i == k && b > a;  // of a diagonal tile, the part above the diagonal
-                            const floatx4 &t = mirror ? tile[tri(2 * i + b) + 2 * k + a] : tile[tri(2 * i + a) + 2 * k + b];
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                if (mirror)
-                                    buf[(16 * a + j) * 32 + 16 * b + 4 * h + r] = t[r];
-                                else
-                                    buf[(16 * a + 4 * h + r) * 32 + 16 * b + j] = t[r];
-                            }
-                        }
-                });
-    }
-};
-
 // Calls fn with a kernel's T, TALL, gradient type and EVEN (wide blocks: always) as constants.
 template <class F> hipError_t choose(int s, bool tall, bool bf16, F fn) {
     auto types = [&](auto t) -> hipError_t {

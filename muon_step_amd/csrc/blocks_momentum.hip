@@ -1,12 +1,15 @@
 // The first pass of the block step: momentum, N, and the sums of N N^T (blocks.hpp).
 //
 // Bound by memory (10 bytes an element, and 3 s / 2 products of 16-bit parts for
-// each, a fifth of the matrix cores' rate at s = 128).  What counts is that a
-// wave's accesses cover whole stretches of memory: 64 bytes of M for each row in
-// wide blocks (16 rows by 4 lanes: with 32 rows by 2 lanes, M's stores reached the
-// L2 in pieces of 16 bytes, four times as many, and the pass ran at 3.7 TB/s), and
-// T elements of a row for each of 32 lanes in tall ones; and that the next 32
-// columns are on their way while the present ones are worked on.
+// each, a fifth of the matrix cores' rate at s = 128).  What counts is that
+// neighbouring lanes read and write neighbouring memory, and that the next 32
+// columns are on their way while the present ones are worked on.  The operand
+// layout has neighbouring lanes in different rows; so a wave of a wide block works
+// on M and N as they lie, eight lanes to 128 bytes of a row, and turns N's 16-bit
+// parts through its own piece of shared memory.  (Loads and stores in the operand
+// layout, 16 bytes a lane 32 or 16 rows apart, kept the address units busy: 3.7 and
+// 4.1 TB/s.)  In tall blocks lanes that are neighbours in the operand are so in
+// memory, T elements each.
 #include "blocks_device.hpp"
 
 namespace muon {
@@ -14,11 +17,11 @@ namespace muon {
 namespace {
 
 // M and G of 32 columns of X, and what a lane does with them.
-//   wide  lane (i, h), i < 16, h < 4: of rows 16 b + i, columns 16 e + 4 h + k, e < 2, k < 4
+//   wide  lane 8 i + h, i < 8, h < 8: of rows 8 b + i, columns 4 h .. 4 h + 3
 //   tall  lane (i, h), i < 32, h < 2: of columns 16 q + 8 h + e, e < 8, the T entries from T i on
 template <int T, bool TALL, bool BF16> struct Columns {
-    static constexpr int kSteps = TALL ? 2 : 2 * T;         // parts of the unit, loaded and used in turn
-    static constexpr int kValues = TALL ? 8 * T : 8;
+    static constexpr int kSteps = TALL ? 2 : 4 * T;         // parts of the unit, loaded and used in turn
+    static constexpr int kValues = TALL ? 8 * T : 4;
     static constexpr bool kPacked = BF16 && (!TALL || T % 2 == 0);
     static constexpr int kGrads = kPacked ? kValues / 2 : kValues;
     static constexpr int kGSize = BF16 ? 2 : 4;
@@ -41,11 +44,11 @@ template <int T, bool TALL, bool BF16> struct Columns {
             mom_lane = mom_part = (8 * h * mp + p) * 4;
             grad_lane = grad_part = (8 * h * gp + p) * kGSize;
         } else {
-            i = lane & 15;
-            h = lane >> 4;
-            const uint32_t row = min(i, s - 1), part = (s & 15) ? min(i, (s & 15) - 1) : row;
-            mom_lane = (row * mp + 4 * h) * 4;
-            grad_lane = (row * gp + 4 * h) * kGSize;
+            i = lane >> 3;
+            h = lane & 7;
+            const uint32_t part = (s & 7) ? min(i, (s & 7) - 1) : i;  // the last, partial eight rows
+            mom_lane = (i * mp + 4 * h) * 4;
+            grad_lane = (i * gp + 4 * h) * kGSize;
             mom_part = (part * mp + 4 * h) * 4;
             grad_part = (part * gp + 4 * h) * kGSize;
         }
@@ -83,36 +86,26 @@ template <int T, bool TALL, bool BF16> struct Columns {
             grad_row += 16 * at.grad_pitch * kGSize;
             asm volatile("" : "+s"(mom_row), "+s"(grad_row));
         } else {
-            const bool full = left >= 16;
-            const uint32_t ml = full ? mom_lane : mom_part, gl = full ? grad_lane : grad_part;
+            const bool full = left >= 8;
+            const auto v = load_at<WordsAt<4, 4>::type>(mom_row, full ? mom_lane : mom_part);
+            const auto u = load_at<typename WordsAt<kGrads, kGSize>::type>(grad_row, full ? grad_lane : grad_part);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const auto v = load_at<WordsAt<4, 4>::type>(mom_row + 64 * e, ml);
+            for (int k = 0; k < 4; ++k) m[step][k] = __uint_as_float(v[k]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) m[step][4 * e + k] = __uint_as_float(v[k]);
-                if constexpr (BF16) {
-                    const auto u = load_at<WordsAt<2, 2>::type>(grad_row + 32 * e, gl);
-                    g[step][2 * e] = u[0];
-                    g[step][2 * e + 1] = u[1];
-                } else {
-                    const auto u = load_at<WordsAt<4, 4>::type>(grad_row + 64 * e, gl);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) g[step][4 * e + k] = u[k];
-                }
-            }
-            left -= 16;
+            for (int k = 0; k < kGrads; ++k) g[step][k] = u[k];
+            left -= 8;
             if (left > 0) {  // steps past the last row read that step again
-                mom_row += 16 * at.mom_pitch * 4;
-                grad_row += 16 * at.grad_pitch * kGSize;
+                mom_row += 8 * at.mom_pitch * 4;
+                grad_row += 8 * at.grad_pitch * kGSize;
             } else {
-                left += 16;
+                left += 8;
             }
             asm volatile("" : "+s"(mom_row), "+s"(grad_row), "+s"(left));
         }
     }
     // N of a step's values, zero where there is nothing; M's new ones take the old ones' place.
     __device__ __forceinline__ void input(int step, float factor, float mu, bool nesterov, float (&n)[kValues]) {
-        const bool in = mine(s - 16 * step);
+        const bool in = mine(s - 8 * step);
 #pragma unroll
         for (int k = 0; k < kValues; ++k) {
             float gf;
@@ -137,12 +130,9 @@ template <int T, bool TALL, bool BF16> struct Columns {
             }
             put_row += 16 * at.mom_pitch * 4;
         } else {
-            if (mine(put_left)) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) put_floats<4>(put_row + 64 * e, mom_lane, &m[step][4 * e]);
-            }
-            put_left -= 16;
-            put_row += 16 * at.mom_pitch * 4;
+            if (mine(put_left)) put_floats<4>(put_row, mom_lane, m[step]);
+            put_left -= 8;
+            put_row += 8 * at.mom_pitch * 4;
         }
         asm volatile("" : "+s"(put_row), "+s"(put_left));
     }
@@ -172,9 +162,20 @@ template <int T, bool TALL, bool BF16> struct Columns {
 // One part of one block: M <- mu M + G and the sum of N N^T over the part's
 // columns.  Outside 2^-40 <= max |N| <= 2^40, where squares could leave fp32's
 // range, the part is summed a second time as N 2^-shift.
+// A wave's 32 columns of N as 16-bit parts, row by row; 16 bytes behind each row
+// keep lanes that read rows side by side off one another's banks.
+template <int T> struct Turned {
+    static constexpr int kPitch = 40;
+    __attribute__((aligned(16))) __bf16 hi[32 * T][kPitch], lo[32 * T][kPitch];
+};
+
 template <int T, bool TALL, bool BF16>
 __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTable t, const BlockCall c) {
-    __shared__ __attribute__((aligned(16))) float sh[2 * kWaves * 1024];
+    union Shared {
+        float sums[2 * kWaves * 1024];
+        Turned<TALL ? 1 : T> turned[kWaves];
+    };
+    __shared__ __attribute__((aligned(16))) Shared sh;
     __shared__ uint32_t sh_largest[kWaves];
     const uint32_t block = blockIdx.x / c.parts, part = blockIdx.x % c.parts;  // block: of the launch
     const Place at = locate<BF16 ? 2 : 4, 2>(t, c, c.base + block);
@@ -184,10 +185,39 @@ __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTa
     const float mu = c.mu;
     const bool nesterov = c.nesterov != 0;
     uint32_t largest = 0;
-    typename std::conditional<TALL, Triangle<T>, FineTriangle<T>>::type sum;
+    Triangle<T> sum;
     Columns<T, TALL, BF16> in(at, c.s, lane);
 
     auto note = [&](float n) { largest = max(largest, __float_as_uint(n) & 0x7fffffffu); };
+
+    auto turn = [&](Turned<T> &to, int b, const float (&n)[4]) {
+        bf16x4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = static_cast<__bf16>(n[e]);
+            lo[e] = static_cast<__bf16>(n[e] - static_cast<float>(hi[e]));
+        }
+        *reinterpret_cast<bf16x4 *>(&to.hi[8 * b + in.i][4 * in.h]) = hi;
+        *reinterpret_cast<bf16x4 *>(&to.lo[8 * b + in.i][4 * in.h]) = lo;
+    };
+    // The wave alone writes and reads its piece, and shared memory serves a wave in order.
+    auto add_turned = [&](const Turned<T> &from) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            bf16x8 hi[T], lo[T];
+#pragma unroll
+            for (int k = 0; k < T; ++k) {
+                const int row = 32 * k + (lane & 31), col = 16 * q + 8 * (lane >> 5);
+                hi[k] = *reinterpret_cast<const bf16x8 *>(&from.hi[row][col]);
+                lo[k] = *reinterpret_cast<const bf16x8 *>(&from.lo[row][col]);
+            }
+            sum.add(hi, lo);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
 
     // 32 columns from x0 on, element by element, past-the-end ones as zeros;
     // again: M is up to date, and N is scaled by 2^-shift.
@@ -225,17 +255,16 @@ __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTa
                 sum.add(hi, lo);
             }
         } else {
-            bf16x8 hi[2 * T], lo[2 * T];
+            Turned<T> &turned = sh.turned[wave];
 #pragma unroll
-            for (int b = 0; b < 2 * T; ++b) {
-                float n[8];
+            for (int b = 0; b < 4 * T; ++b) {
+                float n[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    n[e] = one(16 * b + in.i, x0 + 16 * (e >> 2) + 4 * in.h + (e & 3), again, shift);
-                split_bf(n, hi[b], lo[b]);
+                for (int e = 0; e < 4; ++e) n[e] = one(8 * b + in.i, x0 + 4 * in.h + e, again, shift);
+                turn(turned, b, n);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            sum.add(hi, lo);
+            add_turned(turned);
         }
     };
 
@@ -274,19 +303,19 @@ __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTa
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
-            bf16x8 hi[2 * T], lo[2 * T];
+            Turned<T> &turned = sh.turned[wave];
 #pragma unroll
-            for (int b = 0; b < 2 * T; ++b) {
-                float n[8];
+            for (int b = 0; b < in.kSteps; ++b) {
+                float n[4];
                 in.input(b, factor, mu, nesterov, n);
                 in.store(b);
                 if (next < whole) in.load(b);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) note(n[e]);
-                split_bf(n, hi[b], lo[b]);
-                __builtin_amdgcn_sched_barrier(0);
+                for (int e = 0; e < 4; ++e) note(n[e]);
+                turn(turned, b, n);
+                if (b % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
-            sum.add(hi, lo);
+            add_turned(turned);
         }
     }
     // (the wave's next unit, so that every unit has one owner)
@@ -308,7 +337,8 @@ __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTa
         for (x0 = begin + 32 * wave; x0 < end; x0 += kBlockUnit) each(x0, true, shift);
     }
     const int64_t slot = static_cast<int64_t>(block) * c.parts + part;
-    sum.reduce(c.w.gram + slot * tri(T) * 1024, sh);
+    __syncthreads();
+    sum.reduce(c.w.gram + slot * tri(T) * 1024, sh.sums);
     if (threadIdx.x == 0) c.w.parts[slot] = BlockPart{largest, shift};
 }
 
