@@ -44,7 +44,7 @@
 extern "C" {
 #endif
 
-#define MUON_STEP_ABI_VERSION 6
+#define MUON_STEP_ABI_VERSION 5
 
 /* Bytes of the fixed per-GPU device scratch muon_step_noalloc works in. */
 #define MUON_NOALLOC_SCRATCH_BYTES 134217728
@@ -250,6 +250,69 @@ typedef struct muon_block_matrix {
     int32_t grad_dtype;  /* muon_dtype */
 } muon_block_matrix;
 
+/* How a router's logits x become the scores whose mean the balance loss takes.
+ * MUON_SCORE_SOFTMAX: p_i = exp(x_i) / sum_j exp(x_j)
+ * MUON_SCORE_SIGMOID: p_i = sigma(x_i) / sum_j sigma(x_j)
+ * A logit of -infinity is an expert that the token cannot reach: its p is 0, and
+ * a row of nothing else has p 0 everywhere. */
+typedef enum muon_score { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score;
+
+/* One MoE router's batch for muon_router_balance.
+ *   logits   device, dtype, tokens x experts, rows `pitch` elements apart
+ *   dlogits  optional device, dtype, tokens x experts, rows dlogits_pitch apart:
+ *            receives the loss's gradient.  NULL: none is computed.
+ *   chosen   device, tokens x top_k, contiguous: the experts each token was sent
+ *            to, int32 (chosen_bits 32) or int64 (64).  One that is not in [0,
+ *            experts) (-1: a dropped choice) counts for no expert; one that a
+ *            token names twice counts twice.
+ *   offsets  optional device int32, sequences + 1 values in ascending order:
+ *            sequence s holds the tokens offsets[s] .. offsets[s + 1] - 1.  Tokens
+ *            in front of the first and behind the last one belong to none; their
+ *            rows of dlogits stay as they are.  NULL: one sequence of all tokens.
+ *   mask     optional device, one byte a token: 0 for a token that takes no part
+ *            (its choices are not counted, its row of dlogits becomes zero)
+ *   counts   device int64, experts: the choices of each expert in all sequences,
+ *            written, or added to (accumulate)
+ *   loss     device float, written
+ * experts is 1 .. 1024, top_k 1 .. 64, tokens below 2^31 and tokens x top_k
+ * below 2^32; with tokens 0 logits, dlogits, chosen and mask are not looked at.
+ * Addresses are multiples of their element's size; no written element may be an
+ * element of another range of the call (ranges that interleave: as in
+ * muon_block_matrix). */
+typedef struct muon_router {
+    const void *logits;
+    void *dlogits;
+    const void *chosen;
+    const int32_t *offsets;
+    const uint8_t *mask;
+    int64_t *counts;
+    float *loss;
+    int64_t tokens;
+    int64_t pitch, dlogits_pitch;
+    int32_t experts, top_k, sequences;
+    int32_t dtype; /* muon_dtype */
+    int32_t chosen_bits;
+    int32_t reserved;
+} muon_router;
+
+/* coef: the loss's coefficient (finite).  grad_scale: optional device float that
+ * multiplies the gradients, read when the call runs (an incoming gradient of the
+ * loss, a loss scale); it must not lie in memory that the call writes. */
+typedef struct muon_balance_hparams {
+    double coef;
+    const float *grad_scale;
+    int32_t score; /* muon_score */
+    int32_t accumulate;
+} muon_balance_hparams;
+
+/* One router's selection biases for muon_router_bias_step: `experts` (1 .. 2^20)
+ * contiguous values of each. */
+typedef struct muon_router_bias {
+    float *bias;           /* device, in and out */
+    const int64_t *counts; /* device, as muon_router_balance leaves them */
+    int64_t experts;
+} muon_router_bias;
+
 /* One gradient of muon_grad_norm: numel contiguous elements, read only. */
 typedef struct muon_grad {
     const void *grad; /* device */
@@ -264,7 +327,9 @@ typedef struct muon_context muon_context; /* opaque */
  * A caller compares it with its own before the first call: the structures of
  * two versions differ.  Zero a structure before its fields are set (= {0}):
  * fields that a later version adds then hold their "none" (muon_hparams has
- * grad_factor since version 5). */
+ * grad_factor since version 5).  Entry points with structures of their own may be
+ * added within a version (muon_blocks_step, muon_router_balance and
+ * muon_router_bias_step were): a library without one does not export it. */
 int32_t muon_abi_version(void);
 
 /* Static, never-NULL description of a status code. */
@@ -304,6 +369,12 @@ muon_status muon_check_grad_norm_args(const muon_grad *gs, int64_t count, double
 /* Host-only validation of a muon_blocks_step argument list. */
 muon_status muon_check_blocks_args(const muon_block_matrix *mats, int64_t count, const muon_hparams *hp, char *msg,
                                    size_t msg_cap);
+
+/* Host-only validation of the argument lists of muon_router_balance and
+ * muon_router_bias_step (offsets and chosen are device memory: not looked into). */
+muon_status muon_check_router_balance_args(const muon_router *rs, int64_t count, const muon_balance_hparams *hp, char *msg,
+                                           size_t msg_cap);
+muon_status muon_check_router_bias_args(const muon_router_bias *bs, int64_t count, double rate, char *msg, size_t msg_cap);
 
 /* Workspace the library would allocate for this argument list when nothing
  * caps it: the largest per-group chunk of Newton-Schulz buffers (with
@@ -379,6 +450,29 @@ muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
  * the context, and needs it until the last one. */
 muon_status muon_blocks_step(muon_context *ctx, const muon_block_matrix *mats, int64_t count,
                              const muon_hparams *hp, void *hip_stream);
+
+/* The balance loss of `count` MoE routers (host array rs), each by itself: with
+ * n_s the tokens of sequence s that take part, C_si the choices among them that
+ * name expert i, E = experts, K = top_k, S the sequences with n_s > 0,
+ *     loss = coef / S  sum_s sum_i f_si P_si,
+ *     f_si = E C_si / (K n_s),   P_si = (1 / n_s) sum_t p_ti   (0 where S is 0),
+ * the choices C_i summed over sequences, and the gradient
+ *     dlogits_ti = grad_scale coef E / (S K n_s^2)  p_ti (C_si - sum_j C_sj p_tj) q_ti,
+ * q = 1 (softmax) or 1 - sigma(x_ti) (sigmoid), in fp32 from exact counts, sums over
+ * tokens in fp64 in an order that depends on sizes alone, rounded once to dtype.
+ * Non-finite logits other than -infinity make their row of dlogits and the loss
+ * NaN (+infinity: with MUON_SCORE_SIGMOID a sigma of 1).  Works in memory of the
+ * context that grows on first use: under graph capture as muon_blocks_step. */
+muon_status muon_router_balance(muon_context *ctx, const muon_router *rs, int64_t count, const muon_balance_hparams *hp,
+                                void *hip_stream);
+
+/* b_i <- b_i - rate sign(C_i - mean_j C_j) for `count` routers (host array bs): the
+ * biases that are added to scores for the choice of experts move against each
+ * expert's excess.  The comparison is exact in whole numbers (|sum C| and E |C_i|
+ * below 2^63); an expert at the mean stays.  rate (finite) is rounded to fp32.
+ * Nothing is uploaded or allocated; the call may be captured. */
+muon_status muon_router_bias_step(muon_context *ctx, const muon_router_bias *bs, int64_t count, double rate,
+                                  void *hip_stream);
 
 /* Enables (1, the default) or disables (0) the concurrent execution of a
  * muon_step call's groups described above; disabled, every group runs in
@@ -558,7 +652,8 @@ muon_status muon_stream_probe(muon_context *ctx, const void *src, void *dst, int
  * "poly", "apply", "apply_update" (the last product with the fused decay and
  * update), "update", "adamw", "adamw_mixed", "adamw8", "grad_norm",
  * "blocks_momentum", "blocks_chain", "blocks_regram", "blocks_update" (the four
- * launches of muon_blocks_step), "import",
+ * launches of muon_blocks_step), "router_count", "router_balance",
+ * "router_finish" (those of muon_router_balance), "router_bias", "import",
  * "export", "unit_rms" (the per-matrix ||X||^2 reduction and scale of the
  * unit-RMS mode), "stream_probe" (muon_stream_probe), "prenormalize" (the bf16
  * path's normalisation of the matrices whose ||N_t|| lies outside the range

@@ -15,7 +15,7 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmuon_step.so")
 
-MUON_STEP_ABI_VERSION = 6  # of the header that the structures below mirror
+MUON_STEP_ABI_VERSION = 5  # of the header that the structures below mirror
 
 MUON_OK = 0
 MUON_ERR_INVALID_ARGUMENT = 1
@@ -39,6 +39,7 @@ EXPORTS = (
     "muon_stream_probe", "muon_ns_stage", "muon_set_concurrent_groups",
     "muon_adamw_mixed_step", "muon_adamw8_step", "muon_grad_norm", "muon_check_adamw_mixed_args",
     "muon_check_adamw8_args", "muon_check_grad_norm_args", "muon_blocks_step", "muon_check_blocks_args",
+    "muon_router_balance", "muon_check_router_balance_args", "muon_router_bias_step", "muon_check_router_bias_args",
 )
 
 MUON_STAGE_GRAM = 0
@@ -47,6 +48,9 @@ MUON_STAGE_APPLY = 2
 
 MUON_ADAMW8_BLOCK = 32
 MUON_BLOCK_SIDE = 128
+
+MUON_SCORE_SOFTMAX = 0
+MUON_SCORE_SIGMOID = 1
 
 
 class MuonError(RuntimeError):
@@ -110,6 +114,24 @@ class muon_block_matrix(ctypes.Structure):
                 ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
 
 
+class muon_router(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dlogits", ctypes.c_void_p), ("chosen", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("loss", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("pitch", ctypes.c_int64),
+                ("dlogits_pitch", ctypes.c_int64), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("sequences", ctypes.c_int32), ("dtype", ctypes.c_int32), ("chosen_bits", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class muon_balance_hparams(ctypes.Structure):
+    _fields_ = [("coef", ctypes.c_double), ("grad_scale", ctypes.c_void_p), ("score", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
+class muon_router_bias(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("experts", ctypes.c_int64)]
+
+
 class muon_stage_stats(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 32), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double),
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
@@ -162,6 +184,11 @@ def load(path=LIB_PATH):
         "muon_check_grad_norm_args": (i32, [c.POINTER(muon_grad), i64, c.c_double, vp, vp, c.c_char_p, sz]),
         "muon_blocks_step": (i32, [vp, c.POINTER(muon_block_matrix), i64, c.POINTER(muon_hparams), vp]),
         "muon_check_blocks_args": (i32, [c.POINTER(muon_block_matrix), i64, c.POINTER(muon_hparams), c.c_char_p, sz]),
+        "muon_router_balance": (i32, [vp, c.POINTER(muon_router), i64, c.POINTER(muon_balance_hparams), vp]),
+        "muon_check_router_balance_args": (i32, [c.POINTER(muon_router), i64, c.POINTER(muon_balance_hparams),
+                                                 c.c_char_p, sz]),
+        "muon_router_bias_step": (i32, [vp, c.POINTER(muon_router_bias), i64, c.c_double, vp]),
+        "muon_check_router_bias_args": (i32, [c.POINTER(muon_router_bias), i64, c.c_double, c.c_char_p, sz]),
         "muon_ns_only": (i32, [vp, vp, vp, i64, i64, c.POINTER(muon_hparams), vp]),
         "muon_apply_update": (i32, [vp, vp, i32, vp, i64, i64, c.POINTER(muon_hparams), vp]),
         "muon_last_norms": (i32, [vp, c.POINTER(c.c_double), i64, c.POINTER(i64)]),
@@ -172,7 +199,10 @@ def load(path=LIB_PATH):
         "muon_profile_read": (i32, [vp, c.POINTER(muon_stage_stats), i32, c.POINTER(i32)]),
     }
     for name, (res, args) in sig.items():
-        fn = getattr(lib, name)
+        fn = getattr(lib, name, None)
+        if fn is None:
+            raise ImportError(f"{path} does not export {name}: it is older than this package; build it again with "
+                              "`python -m muon_step_amd.build`")
         fn.restype = res
         fn.argtypes = args
     _lib = lib
@@ -427,6 +457,23 @@ class Context:
         st = self.lib.muon_blocks_step(self.handle, arr, len(arr), ctypes.byref(hp), _stream_handle(stream, self.device))
         _check(self.lib, self.handle, st, "muon_blocks_step")
 
+    def muon_router_balance(self, routers, hp, stream=None):
+        """routers: a list of router() or a table() of them; hp: balance_hparams()."""
+        self._check_device(routers, "router")
+        scale = getattr(hp, "_scale", None)
+        if scale is not None and _on_one_gpu([("grad_scale", scale)]) != self.device:
+            raise ValueError(f"grad_scale lives on {scale.device}, the context on cuda:{self.device}")
+        arr = _array(routers, muon_router)
+        st = self.lib.muon_router_balance(self.handle, arr, len(arr), ctypes.byref(hp), _stream_handle(stream, self.device))
+        _check(self.lib, self.handle, st, "muon_router_balance")
+
+    def muon_router_bias_step(self, routers, rate, stream=None):
+        """routers: a list of router_bias() or a table() of them; rate: how far a bias moves in one step."""
+        self._check_device(routers, "router")
+        arr = _array(routers, muon_router_bias)
+        st = self.lib.muon_router_bias_step(self.handle, arr, len(arr), rate, _stream_handle(stream, self.device))
+        _check(self.lib, self.handle, st, "muon_router_bias_step")
+
     def muon_ns_only(self, n_in, x_out, hp, stream=None):
         named = [("n_in", n_in), ("x_out", x_out)]
         for name, t in named:
@@ -666,3 +713,74 @@ def grad(t):
     code = _dtype_code(t)
     dev = _gpu_index(("grad",), (t,))
     return _owning(muon_grad(t.data_ptr(), t.numel(), code, 0), dev, (t,))
+
+
+_ROUTER_NAMES = ("logits", "chosen", "counts", "loss", "dlogits", "offsets", "mask")
+
+
+def router(logits, chosen, counts, loss, dlogits=None, offsets=None, mask=None):
+    """muon_router for torch tensors on one GPU: logits and dlogits tokens x experts, float32 or bfloat16, rows
+    contiguous and any distance apart; chosen tokens x top_k, int32 or int64, contiguous; counts int64, one for each
+    expert; loss one float32 element; offsets int32, sequences + 1; mask bool or uint8, one for each token."""
+    import torch
+    if logits.dim() != 2 or logits.shape[1] == 0:
+        raise ValueError("logits must be tokens x experts")
+    tokens, experts = logits.shape
+    pitches = [experts, experts]
+    for k, (name, t) in enumerate((("logits", logits), ("dlogits", dlogits))):
+        if t is None:
+            continue
+        if t.shape != logits.shape or t.dtype != logits.dtype:
+            raise ValueError("dlogits must have logits' shape and dtype")
+        if tokens and experts > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have contiguous rows, got strides {tuple(t.stride())}")
+        if tokens > 1:
+            pitches[k] = t.stride(0)
+        if pitches[k] < experts:
+            raise ValueError(f"{name}'s rows overlap: strides {tuple(t.stride())}")
+    if chosen.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"chosen must be int32 or int64, got {chosen.dtype}")
+    if chosen.dim() != 2 or chosen.shape[0] != tokens or chosen.shape[1] == 0 or not chosen.is_contiguous():
+        raise ValueError("chosen must be tokens x top_k and contiguous")
+    if counts.dtype != torch.int64 or counts.numel() != experts or not counts.is_contiguous():
+        raise TypeError(f"counts must be {experts} contiguous int64 values")
+    _one_element("loss", loss, torch.float32, "float32")
+    sequences = 1
+    if offsets is not None:
+        if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+            raise TypeError("offsets must be sequences + 1 contiguous int32 values")
+        sequences = offsets.numel() - 1
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (tokens,) or
+                             not mask.is_contiguous()):
+        raise TypeError("mask must be one contiguous bool or uint8 value for each token")
+    named = [(n, t) for n, t in zip(_ROUTER_NAMES, (logits, chosen, counts, loss, dlogits, offsets, mask)) if t is not None]
+    names, tensors = zip(*named)
+    dev = _gpu_index(names, tensors)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    r = muon_router(ptr(logits), ptr(dlogits), ptr(chosen), ptr(offsets), ptr(mask), ptr(counts), ptr(loss), tokens,
+                    pitches[0], pitches[1], experts, chosen.shape[1], sequences, _dtype_code(logits),
+                    8 * chosen.element_size(), 0)
+    return _owning(r, dev, tensors)
+
+
+def balance_hparams(coef, score=MUON_SCORE_SOFTMAX, accumulate=False, grad_scale=None):
+    """muon_balance_hparams; grad_scale is an optional one-element float32 GPU tensor that multiplies the gradients."""
+    import torch
+    if grad_scale is not None:
+        _one_element("grad_scale", grad_scale, torch.float32, "float32")
+        _on_one_gpu([("grad_scale", grad_scale)])
+    hp = muon_balance_hparams(coef, None if grad_scale is None else grad_scale.data_ptr(), score, 1 if accumulate else 0)
+    hp._scale = grad_scale
+    return hp
+
+
+def router_bias(bias, counts):
+    """muon_router_bias for torch tensors: contiguous float32 biases and int64 counts of one router's experts."""
+    import torch
+    _require_f32((("bias", bias),))
+    if counts.dtype != torch.int64:
+        raise TypeError(f"counts must be int64, got {counts.dtype}")
+    if not bias.is_contiguous() or not counts.is_contiguous() or bias.numel() != counts.numel() or bias.numel() == 0:
+        raise ValueError("bias and counts must be contiguous, one value for each expert")
+    dev = _gpu_index(("bias", "counts"), (bias, counts))
+    return _owning(muon_router_bias(bias.data_ptr(), counts.data_ptr(), bias.numel()), dev, (bias, counts))

@@ -1,0 +1,70 @@
+// MoE routers: balance loss, expert counts and gradients, and the step of the
+// selection biases (router.hip): what host and kernels share.
+#pragma once
+
+#include "common.hpp"
+
+namespace muon {
+
+struct RouterDesc {
+    const void *logits;
+    void *dlogits;           // or nullptr
+    const void *chosen;
+    const int32_t *offsets;  // or nullptr: one sequence of all tokens
+    const uint8_t *mask;     // or nullptr
+    int64_t *counts;
+    float *loss;
+    uint32_t *hist;          // [sequence][experts + 1]: choices of each expert, and tokens; zero between calls
+    double *sums;            // of the loss, one for each workgroup
+    uint32_t pitch, dpitch;
+    int32_t tokens, experts, top_k, sequences;
+    int32_t chosen64;
+    int32_t pad_;
+};
+// Routers of one launch, by value: 32 of 104 bytes and their first workgroups.
+constexpr int kRouters = 32;
+struct RouterTable {
+    uint32_t first[64];  // workgroups before each router; 0xffffffff past the last
+    RouterDesc d[kRouters];
+};
+struct RouterCall {
+    double coef;
+    const float *grad_scale;  // or nullptr
+    uint32_t per_block;       // tokens of a workgroup
+    int32_t sigmoid, accumulate;
+};
+
+constexpr int kRouterThreads = 256;
+constexpr int kMaxExperts = 1024;
+
+// Lanes that share a row of `experts` logits, and how many each takes.
+inline int router_lanes(int experts) {
+    int lanes = 1;
+    while (lanes < 64 && lanes * 8 < experts) lanes *= 2;
+    return lanes;
+}
+
+// Counts the choices of each sequence and expert into hist.
+hipError_t launch_router_count(const RouterTable &t, uint32_t blocks, const RouterCall &c, hipStream_t st);
+// Gradients, and the workgroups' sums of the loss.  All routers of the table have
+// the same type and router_lanes().
+hipError_t launch_router_balance(const RouterTable &t, uint32_t blocks, const RouterCall &c, int experts, bool bf16,
+                                 hipStream_t st);
+// Counts and loss from hist and sums (t.first: launch_router_balance's, and its
+// `blocks`); hist is zero behind it.
+hipError_t launch_router_finish(const RouterTable &t, int routers, uint32_t blocks, const RouterCall &c, hipStream_t st);
+// Zeroes memory that hist will lie in.
+hipError_t launch_router_clear(uint32_t *p, int64_t words, hipStream_t st);
+
+struct RouterBiasDesc {
+    float *bias;
+    const int64_t *counts;
+    int64_t experts;
+};
+constexpr int kRouterBiases = 128;
+struct RouterBiasTable {
+    RouterBiasDesc d[kRouterBiases];
+};
+hipError_t launch_router_bias(const RouterBiasTable &t, int routers, float rate, hipStream_t st);
+
+}  // namespace muon

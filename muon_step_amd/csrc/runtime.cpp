@@ -20,6 +20,7 @@
 #include "blocks_plan.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
+#include "router.hpp"
 
 using muon::Geom;
 using muon::MatDesc;
@@ -479,9 +480,29 @@ struct Strided {
 // are told apart where their pitch is the same.
 bool share_memory(const Strided &a, const Strided &b) {
     if ((!a.writable && !b.writable) || a.lo >= b.hi || b.lo >= a.hi) return false;
-    if (a.pitch != b.pitch) return true;
+    if (a.pitch != b.pitch || a.pitch == 0) return true;  // pitch 0: without gaps
     const uintptr_t ahead = (a.lo <= b.lo ? b.lo - a.lo : a.pitch - (a.lo - b.lo) % a.pitch) % a.pitch;  // b's columns after a's
     return ahead < a.width || ahead + b.width > a.pitch;
+}
+
+// INVALID_ARGUMENT where two of the ranges, one of them written, share memory.
+muon_status check_strided(std::vector<Strided> &all, const char *items, char *msg, size_t cap) {
+    std::sort(all.begin(), all.end(), [](const Strided &x, const Strided &y) { return x.lo < y.lo; });
+    std::vector<const Strided *> open;  // those that reach past the current one's begin
+    for (const Strided &cur : all) {
+        size_t kept = 0;
+        for (const Strided *o : open) {
+            if (o->hi <= cur.lo) continue;
+            if (share_memory(*o, cur)) {
+                set_overlap_msg(msg, cap, memory_name(items, o->owner, o->what), memory_name(items, cur.owner, cur.what));
+                return MUON_ERR_INVALID_ARGUMENT;
+            }
+            open[kept++] = o;
+        }
+        open.resize(kept);
+        open.push_back(&cur);
+    }
+    return MUON_OK;
 }
 
 constexpr int64_t kMaxBlockSide = int64_t(1) << 24;   // fp16 holds N 2^shift up to sqrt(128 2^24)
@@ -536,21 +557,8 @@ muon_status check_blocks(const muon_block_matrix *mats, int64_t count, const muo
         const uintptr_t lo = reinterpret_cast<uintptr_t>(hp->grad_factor);
         all.push_back(Strided{lo, lo + 4, 0, 4, false, kNoOwner, "grad_factor"});
     }
-    std::sort(all.begin(), all.end(), [](const Strided &x, const Strided &y) { return x.lo < y.lo; });
-    std::vector<const Strided *> open;  // those that reach past the current one's begin
-    for (const Strided &cur : all) {
-        size_t kept = 0;
-        for (const Strided *o : open) {
-            if (o->hi <= cur.lo) continue;
-            if (share_memory(*o, cur)) {
-                set_overlap_msg(msg, cap, memory_name("matrix", o->owner, o->what), memory_name("matrix", cur.owner, cur.what));
-                return MUON_ERR_INVALID_ARGUMENT;
-            }
-            open[kept++] = o;
-        }
-        open.resize(kept);
-        open.push_back(&cur);
-    }
+    s = check_strided(all, "matrix", msg, cap);
+    if (s != MUON_OK) return s;
     if (hp->ns_precision != MUON_NS_BF16) {
         set_msg(msg, cap, "the block step has no fp32 products: ns_precision must be MUON_NS_BF16");
         return MUON_ERR_UNSUPPORTED;
@@ -558,6 +566,101 @@ muon_status check_blocks(const muon_block_matrix *mats, int64_t count, const muo
     if (!muon::plan_blocks_schedule(hp->schedule, hp->num_ns_steps).fits) {
         set_msg(msg, cap, "the schedule leaves the range of the block step's products");
         return MUON_ERR_UNSUPPORTED;
+    }
+    return MUON_OK;
+}
+
+muon_status check_router_balance(const muon_router *rs, int64_t count, const muon_balance_hparams *hp, char *msg, size_t cap) {
+    if (count < 0) { set_msg(msg, cap, "count < 0"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (count > 0 && !rs) { set_msg(msg, cap, "routers is NULL"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (!hp) { set_msg(msg, cap, "hparams is NULL"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (!finite(hp->coef)) { set_msg(msg, cap, "coef must be finite"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (hp->score != MUON_SCORE_SOFTMAX && hp->score != MUON_SCORE_SIGMOID) {
+        set_msg(msg, cap, "unknown score %d", hp->score);
+        return MUON_ERR_INVALID_ARGUMENT;
+    }
+    if (hp->accumulate != 0 && hp->accumulate != 1) { set_msg(msg, cap, "accumulate must be 0 or 1"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (!aligned_to(hp->grad_scale, 4)) { set_msg(msg, cap, "grad_scale is not 4-byte aligned"); return MUON_ERR_INVALID_ARGUMENT; }
+    std::vector<Strided> all;
+    for (int64_t i = 0; i < count; ++i) {
+        const muon_router &r = rs[i];
+        const long long at = i;
+        if (r.tokens < 0 || r.tokens >= int64_t(1) << 31 || r.experts < 1 || r.experts > muon::kMaxExperts || r.top_k < 1 ||
+            r.top_k > 64 || r.tokens * r.top_k >= int64_t(1) << 32) {
+            set_msg(msg, cap, "router %lld: %lld tokens, %d experts or %d choices out of range", at, (long long)r.tokens, r.experts,
+                    r.top_k);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        if (!known_dtype(r.dtype) || (r.chosen_bits != 32 && r.chosen_bits != 64)) {
+            set_msg(msg, cap, "router %lld: unknown dtype or chosen_bits", at);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        if (r.sequences < 1 || (!r.offsets && r.sequences != 1)) {
+            set_msg(msg, cap, "router %lld: %d sequences %s offsets", at, r.sequences, r.offsets ? "with" : "without");
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        auto add = [&](const void *p, size_t es, int64_t rows, int64_t cols, int64_t pitch, bool wr, const char *what) {
+            if (!p || !aligned_to(p, es)) {
+                set_msg(msg, cap, "router %lld: %s is NULL or not aligned to its elements", at, what);
+                return false;
+            }
+            if (pitch < cols || pitch > kMaxBlockPitch) {
+                set_msg(msg, cap, "router %lld: %s rows of %lld elements cannot lie %lld apart", at, what, (long long)cols,
+                        (long long)pitch);
+                return false;
+            }
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+            all.push_back(Strided{lo, lo + (static_cast<uintptr_t>(rows - 1) * pitch + cols) * es,
+                                  static_cast<uintptr_t>(pitch) * es, static_cast<uintptr_t>(cols) * es, wr, i, what});
+            return true;
+        };
+        // a run of elements is a matrix of one row, whose pitch says nothing
+        auto run = [&](const void *p, size_t es, int64_t n, bool wr, const char *what) {
+            if (!p || !aligned_to(p, es)) return add(p, es, 1, 1, 1, wr, what);
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+            all.push_back(Strided{lo, lo + static_cast<uintptr_t>(n) * es, 0, 0, wr, i, what});
+            return true;
+        };
+        if (!run(r.counts, 8, r.experts, true, "counts") || !run(r.loss, 4, 1, true, "loss") ||
+            (r.offsets && !run(r.offsets, 4, int64_t(r.sequences) + 1, false, "offsets")))
+            return MUON_ERR_INVALID_ARGUMENT;
+        if (r.tokens == 0) continue;
+        if (!add(r.logits, dtype_size(r.dtype), r.tokens, r.experts, r.pitch, false, "logits") ||
+            (r.dlogits && !add(r.dlogits, dtype_size(r.dtype), r.tokens, r.experts, r.dlogits_pitch, true, "dlogits")) ||
+            !run(r.chosen, r.chosen_bits / 8, r.tokens * r.top_k, false, "chosen") ||
+            (r.mask && !run(r.mask, 1, r.tokens, false, "mask")))
+            return MUON_ERR_INVALID_ARGUMENT;
+    }
+    if (hp->grad_scale) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(hp->grad_scale);
+        all.push_back(Strided{lo, lo + 4, 0, 0, false, kNoOwner, "grad_scale"});
+    }
+    return check_strided(all, "router", msg, cap);
+}
+
+muon_status check_router_bias(const muon_router_bias *bs, int64_t count, double rate, char *msg, size_t cap) {
+    if (count < 0) { set_msg(msg, cap, "count < 0"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (count > 0 && !bs) { set_msg(msg, cap, "routers is NULL"); return MUON_ERR_INVALID_ARGUMENT; }
+    if (!finite(rate) || !finite(static_cast<float>(rate))) { set_msg(msg, cap, "rate must be finite"); return MUON_ERR_INVALID_ARGUMENT; }
+    std::vector<Interval> iv;
+    for (int64_t i = 0; i < count; ++i) {
+        const muon_router_bias &b = bs[i];
+        if (b.experts < 1 || b.experts > int64_t(1) << 20) {
+            set_msg(msg, cap, "router %lld: %lld experts out of range", (long long)i, (long long)b.experts);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        if (!b.bias || !b.counts || !aligned_to(b.bias, 4) || !aligned_to(b.counts, 8)) {
+            set_msg(msg, cap, "router %lld: bias or counts is NULL or not aligned to its elements", (long long)i);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        const uintptr_t w = reinterpret_cast<uintptr_t>(b.bias), r = reinterpret_cast<uintptr_t>(b.counts);
+        iv.push_back(Interval{w, w + static_cast<uintptr_t>(b.experts) * 4, true, i, "bias"});
+        iv.push_back(Interval{r, r + static_cast<uintptr_t>(b.experts) * 8, false, i, "counts"});
+    }
+    const Interval *x = nullptr, *y = nullptr;
+    if (find_overlap(iv, &x, &y)) {
+        set_overlap_msg(msg, cap, memory_name("router", x->owner, x->what), memory_name("router", y->owner, y->what));
+        return MUON_ERR_INVALID_ARGUMENT;
     }
     return MUON_OK;
 }
@@ -847,6 +950,8 @@ struct muon_context {
     DevBuf call_nrm2; // per call matrix
     DevBuf mat_desc;  // MatDesc table
     DevBuf adamw_desc;
+    DevBuf routers;   // muon_router_balance's counts, zero between calls, and sums
+    size_t routers_clear = 0;  // words of it that are zero
     DevBuf blocks;    // muon_blocks_step's sums, polynomials and scalars
     std::vector<void *> retired;  // buffers that graphs may hold, and calls no longer
     // muon_grad_norm's sums: of a fixed size and there from creation on, so that
@@ -930,13 +1035,15 @@ muon_status hip_fail(muon_context *ctx, hipError_t e, const char *where) {
 enum Stage {
     ST_MOMENTUM = 0, ST_FINALIZE, ST_NORMALIZE, ST_GRAM, ST_POLY, ST_APPLY, ST_APPLY_UPDATE, ST_UPDATE,
     ST_ADAMW, ST_IMPORT, ST_EXPORT, ST_UNIT_RMS, ST_PRENORM, ST_PROBE, ST_ADAMW_MIXED, ST_ADAMW8, ST_GRAD_NORM,
-    ST_BLOCKS_MOMENTUM, ST_BLOCKS_CHAIN, ST_BLOCKS_REGRAM, ST_BLOCKS_UPDATE, ST_COUNT
+    ST_BLOCKS_MOMENTUM, ST_BLOCKS_CHAIN, ST_BLOCKS_REGRAM, ST_BLOCKS_UPDATE,
+    ST_ROUTER_COUNT, ST_ROUTER_BALANCE, ST_ROUTER_FINISH, ST_ROUTER_BIAS, ST_COUNT
 };
 const char *const kStageNames[ST_COUNT] = {"momentum_nesterov", "norm_finalize", "normalize", "gram", "poly",
                                            "apply", "apply_update", "update", "adamw", "import", "export",
                                            "unit_rms", "prenormalize", "stream_probe", "adamw_mixed", "adamw8",
                                            "grad_norm", "blocks_momentum", "blocks_chain", "blocks_regram",
-                                           "blocks_update"};
+                                           "blocks_update", "router_count", "router_balance", "router_finish",
+                                           "router_bias"};
 
 hipError_t take_event(muon_context *ctx, hipEvent_t *ev) {
     if (ctx->ev_used == ctx->ev_pool.size()) {
@@ -1818,6 +1925,134 @@ muon_status blocks_impl(muon_context *ctx, const muon_block_matrix *mats, int64_
     return MUON_OK;
 }
 
+// ---- muon_router_balance
+
+// Workgroups that the passes over choices and over logits aim at: two and eight
+// for each CU.
+constexpr int64_t kCountWorkgroups = 512, kBalanceWorkgroups = 2048;
+
+size_t router_words(const muon_router &r) { return static_cast<size_t>(r.sequences) * (r.experts + 1); }
+
+// The launches of up to kRouters routers of one type and lane layout.
+muon_status run_router_table(muon_context *ctx, const muon_router *const *rs, int n, const muon_balance_hparams *hp, hipStream_t st) {
+    size_t words = 0;
+    int64_t tokens = 0;
+    for (int i = 0; i < n; ++i) {
+        words += router_words(*rs[i]);
+        tokens += rs[i]->tokens;
+    }
+    const muon_router &like = *rs[0];
+    const int lanes = muon::router_lanes(like.experts);
+    const int64_t turn = muon::kRouterThreads / lanes;  // rows that a workgroup takes at once
+    const int64_t per_balance = round_up(std::max<int64_t>(1, (tokens + kBalanceWorkgroups - 1) / kBalanceWorkgroups), turn);
+    const int64_t per_count = std::max<int64_t>(64, (tokens + kCountWorkgroups - 1) / kCountWorkgroups);
+    const size_t hist_bytes = align_up(words * 4), sums_bytes = (static_cast<size_t>(tokens / per_balance) + n) * 8;
+    const bool graph = capturing(st);
+    const void *before = ctx->routers.p;
+    muon_status s = ensure(ctx, ctx->routers, hist_bytes + sums_bytes, "router workspace", graph);
+    if (ctx->routers.p != before) ctx->routers_clear = 0;
+    if (s != MUON_OK) return s;
+    uint32_t *hist = static_cast<uint32_t *>(ctx->routers.p);
+    double *sums = reinterpret_cast<double *>(static_cast<char *>(ctx->routers.p) + hist_bytes);
+    // sums of an earlier call with fewer counts may lie in what are counts now
+    const size_t clear = std::min(ctx->routers_clear, words);
+    ctx->routers_clear = 0;  // until everything is enqueued
+    if (clear < words) {
+        const hipError_t e = muon::launch_router_clear(hist + clear, static_cast<int64_t>(words - clear), st);
+        if (e != hipSuccess) return hip_fail(ctx, e, "router workspace launch");
+    }
+    muon::RouterTable t{};
+    muon::RouterCall c{};
+    c.coef = hp->coef;
+    c.grad_scale = hp->grad_scale;
+    c.sigmoid = hp->score == MUON_SCORE_SIGMOID;
+    c.accumulate = hp->accumulate;
+    double count_bytes = 0, row_bytes = 0;
+    size_t at = 0;
+    for (int i = 0; i < n; ++i) {
+        const muon_router &r = *rs[i];
+        muon::RouterDesc &d = t.d[i];
+        d.logits = r.logits;
+        d.dlogits = r.dlogits;
+        d.chosen = r.chosen;
+        d.offsets = r.offsets;
+        d.mask = r.mask;
+        d.counts = r.counts;
+        d.loss = r.loss;
+        d.hist = hist + at;
+        d.pitch = static_cast<uint32_t>(r.tokens ? r.pitch : 0);
+        d.dpitch = static_cast<uint32_t>(r.tokens && r.dlogits ? r.dlogits_pitch : 0);
+        d.tokens = static_cast<int32_t>(r.tokens);
+        d.experts = r.experts;
+        d.top_k = r.top_k;
+        d.sequences = r.sequences;
+        d.chosen64 = r.chosen_bits == 64;
+        at += router_words(r);
+        count_bytes += static_cast<double>(r.tokens) * (r.top_k * (r.chosen_bits / 8) + (r.mask ? 1 : 0));
+        row_bytes += static_cast<double>(r.tokens) * r.experts * dtype_size(r.dtype) * (r.dlogits ? 2 : 1);
+    }
+    for (int k = n; k < 64; ++k) t.first[k] = 0xffffffffu;
+    auto spread = [&](int64_t per) {
+        int64_t blocks = 0;
+        for (int i = 0; i < n; ++i) {
+            t.first[i] = static_cast<uint32_t>(blocks);
+            blocks += (rs[i]->tokens + per - 1) / per;
+        }
+        c.per_block = static_cast<uint32_t>(per);
+        return static_cast<uint32_t>(blocks);
+    };
+    hipError_t e = hipSuccess;
+    uint32_t blocks = spread(per_count);
+    if (blocks > 0)
+        e = timed(ctx, ST_ROUTER_COUNT, 0.0, count_bytes, st, [&] { return muon::launch_router_count(t, blocks, c, st); });
+    if (e != hipSuccess) return hip_fail(ctx, e, "router count launch");
+    blocks = spread(per_balance);
+    for (int i = 0; i < n; ++i) t.d[i].sums = sums + t.first[i];
+    if (blocks > 0)
+        e = timed(ctx, ST_ROUTER_BALANCE, 0.0, row_bytes, st,
+                  [&] { return muon::launch_router_balance(t, blocks, c, like.experts, like.dtype == MUON_BF16, st); });
+    if (e != hipSuccess) return hip_fail(ctx, e, "router balance launch");
+    e = timed(ctx, ST_ROUTER_FINISH, 0.0, static_cast<double>(words) * 4, st,
+              [&] { return muon::launch_router_finish(t, n, blocks, c, st); });
+    if (e != hipSuccess) return hip_fail(ctx, e, "router finish launch");
+    // a capture has only recorded that the counts are left at zero
+    ctx->routers_clear = graph ? clear : words;
+    return MUON_OK;
+}
+
+muon_status router_balance_impl(muon_context *ctx, const muon_router *rs, int64_t count, const muon_balance_hparams *hp,
+                                hipStream_t st) {
+    char msg[512];
+    muon_status s = check_router_balance(rs, count, hp, msg, sizeof msg);
+    if (s != MUON_OK) return fail(ctx, s, "%s", msg);
+    DeviceGuard guard(ctx->device);
+    auto key = [&](int64_t i) {
+        return std::make_tuple(muon::router_lanes(rs[i].experts), rs[i].experts > 512, rs[i].dtype);
+    };
+    std::vector<char> done(static_cast<size_t>(count), 0);
+    for (int64_t i = 0; i < count; ++i) {
+        const muon_router *table[muon::kRouters];
+        int n = 0;
+        int64_t tokens = 0;
+        for (int64_t j = i; j < count; ++j) {
+            if (done[j] || key(j) != key(i)) continue;
+            if (n == muon::kRouters || tokens + rs[j].tokens >= int64_t(1) << 31) {
+                s = run_router_table(ctx, table, n, hp, st);
+                if (s != MUON_OK) return s;
+                n = 0;
+                tokens = 0;
+            }
+            table[n++] = rs + j;
+            tokens += rs[j].tokens;
+            done[j] = 1;
+        }
+        if (n > 0) s = run_router_table(ctx, table, n, hp, st);
+        if (s != MUON_OK) return s;
+    }
+    ctx->err.clear();
+    return MUON_OK;
+}
+
 }  // namespace
 
 // ===================================================================== C ABI
@@ -1896,6 +2131,15 @@ muon_status muon_check_grad_norm_args(const muon_grad *gs, int64_t count, double
 muon_status muon_check_blocks_args(const muon_block_matrix *mats, int64_t count, const muon_hparams *hp, char *msg,
                                    size_t msg_cap) {
     return guarded(msg, msg_cap, [&] { return check_blocks(mats, count, hp, msg, msg_cap); });
+}
+
+muon_status muon_check_router_balance_args(const muon_router *rs, int64_t count, const muon_balance_hparams *hp, char *msg,
+                                           size_t msg_cap) {
+    return guarded(msg, msg_cap, [&] { return check_router_balance(rs, count, hp, msg, msg_cap); });
+}
+
+muon_status muon_check_router_bias_args(const muon_router_bias *bs, int64_t count, double rate, char *msg, size_t msg_cap) {
+    return guarded(msg, msg_cap, [&] { return check_router_bias(bs, count, rate, msg, msg_cap); });
 }
 
 muon_status muon_workspace_bytes(const muon_matrix *mats, int64_t count, const muon_hparams *hp,
@@ -1979,7 +2223,7 @@ muon_status muon_destroy(muon_context *ctx) {
     if (!ctx) return MUON_OK;
     DeviceGuard guard(ctx->device);
     (void)hipDeviceSynchronize();
-    for (DevBuf *b : {&ctx->ws, &ctx->tabs, &ctx->call_nrm2, &ctx->mat_desc, &ctx->adamw_desc, &ctx->blocks})
+    for (DevBuf *b : {&ctx->ws, &ctx->tabs, &ctx->call_nrm2, &ctx->mat_desc, &ctx->adamw_desc, &ctx->blocks, &ctx->routers})
         if (b->p) (void)hipFree(b->p);
     for (void *p : ctx->retired) (void)hipFree(p);
     if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
@@ -2013,6 +2257,37 @@ muon_status muon_blocks_step(muon_context *ctx, const muon_block_matrix *mats, i
                              void *hip_stream) {
     if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
     return guarded(ctx, [&] { return blocks_impl(ctx, mats, count, hp, static_cast<hipStream_t>(hip_stream)); });
+}
+
+muon_status muon_router_balance(muon_context *ctx, const muon_router *rs, int64_t count, const muon_balance_hparams *hp,
+                                void *hip_stream) {
+    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+    return guarded(ctx, [&] { return router_balance_impl(ctx, rs, count, hp, static_cast<hipStream_t>(hip_stream)); });
+}
+
+muon_status muon_router_bias_step(muon_context *ctx, const muon_router_bias *bs, int64_t count, double rate, void *hip_stream) {
+    if (!ctx) return MUON_ERR_INVALID_ARGUMENT;
+    return guarded(ctx, [&]() -> muon_status {
+        char msg[512];
+        const muon_status s = check_router_bias(bs, count, rate, msg, sizeof msg);
+        if (s != MUON_OK) return fail(ctx, s, "%s", msg);
+        DeviceGuard guard(ctx->device);
+        hipStream_t st = static_cast<hipStream_t>(hip_stream);
+        for (int64_t i = 0; i < count;) {
+            muon::RouterBiasTable t;
+            int n = 0;
+            double bytes = 0;
+            for (; i < count && n < muon::kRouterBiases; ++i, ++n) {
+                t.d[n] = muon::RouterBiasDesc{bs[i].bias, bs[i].counts, bs[i].experts};
+                bytes += 16.0 * static_cast<double>(bs[i].experts);
+            }
+            const hipError_t e = timed(ctx, ST_ROUTER_BIAS, 0.0, bytes, st,
+                                       [&] { return muon::launch_router_bias(t, n, static_cast<float>(rate), st); });
+            if (e != hipSuccess) return hip_fail(ctx, e, "router bias launch");
+        }
+        ctx->err.clear();
+        return MUON_OK;
+    });
 }
 
 muon_status muon_ns_only(muon_context *ctx, const float *n_in, float *x_out, int64_t rows, int64_t cols,
