@@ -22,7 +22,6 @@ namespace muon {
 namespace {
 
 constexpr int kWaves = kRouterThreads / 64;
-constexpr int kCountWords = 8192;  // of a workgroup's own counts
 
 // A sequence's tokens; what offsets leave out of the tokens is left out here.
 struct Span {
@@ -35,7 +34,6 @@ __device__ __forceinline__ Span span_of(const RouterDesc &d, int s) {
 }
 // The last sequence of [lo, hi] that begins at or before the token.
 __device__ __forceinline__ int sequence_of(const RouterDesc &d, int token, int lo, int hi) {
-    if (!d.offsets) return 0;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (as_global(d.offsets)[mid] <= token)
@@ -45,13 +43,59 @@ __device__ __forceinline__ int sequence_of(const RouterDesc &d, int token, int l
     }
     return lo;
 }
+// The same for a token that the wave has in common: 64 places are looked at in turn.
+__device__ __forceinline__ int wave_sequence_of(const RouterDesc &d, int token) {
+    int lo = 0, n = d.offsets ? d.sequences : 1;
+    while (n > 1) {
+        const int width = (n + 63) / 64, at = lo + static_cast<int>(threadIdx.x & 63) * width;
+        const bool begun = at < lo + n && as_global(d.offsets)[at] <= token;
+        const int k = max(__popcll(__ballot(begun)) - 1, 0);
+        n = min(width, n - k * width);
+        lo += k * width;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
 __device__ __forceinline__ bool takes_part(const RouterDesc &d, int token, int s) {
     const Span p = span_of(d, s);
     return token >= p.begin && token < p.end && (!d.mask || as_global(d.mask)[token] != 0);
 }
 
-// One choice a thread and turn.  Counts of the sequences that the workgroup's
-// tokens begin with are gathered in shared memory, as many as fit there.
+// Adds the choices of tokens [begin, end), a token for each thread at a time, to
+// `own`, which holds the counts of the sequences from s0 on (`window` of them),
+// and to hist past those.
+__device__ __forceinline__ void count_tokens(const RouterDesc &d, int begin, int end, int s0, int s1, uint32_t *own, int window) {
+    const int stride = d.experts + 1, top = d.top_k;
+    for (int token = begin + threadIdx.x; token < end; token += blockDim.x) {
+        const int s = sequence_of(d, token, s0, s1);
+        const bool in = takes_part(d, token, s);
+        const int64_t at = static_cast<int64_t>(token) * top;
+        const bool near = s - s0 < window;
+        uint32_t *to = near ? own + (s - s0) * stride : d.hist + static_cast<int64_t>(s) * stride;
+        auto add = [&](int i) {
+            if (near)
+                __hip_atomic_fetch_add((uint32_t __attribute__((address_space(3))) *)(own + (s - s0) * stride + i), 1u,
+                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            else
+                atomicAdd(to + i, 1u);
+        };
+        if (in) add(d.experts);
+        for (int j0 = 0; j0 < top; j0 += 4) {
+            int64_t x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t k = at + min(j0 + j, top - 1);
+                x[j] = d.chosen64 ? as_global(static_cast<const int64_t *>(d.chosen))[k]
+                                  : as_global(static_cast<const int32_t *>(d.chosen))[k];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in && j0 + j < top && x[j] >= 0 && x[j] < d.experts) add(static_cast<int>(x[j]));
+        }
+    }
+}
+
+// Counts of the sequences that the workgroup's tokens begin with are gathered in
+// shared memory, as many as fit there.
 __global__ __launch_bounds__(kRouterThreads) void router_count_kernel(const RouterTable t, const RouterCall c) {
     __shared__ uint32_t own[kCountWords];
     const Owners<64> owners(t.first);
@@ -60,85 +104,75 @@ __global__ __launch_bounds__(kRouterThreads) void router_count_kernel(const Rout
     const int begin = (blockIdx.x - t.first[e]) * c.per_block, end = min(begin + static_cast<int>(c.per_block), d.tokens);
     if (begin >= end) return;
     const int stride = d.experts + 1;
-    const int s0 = sequence_of(d, begin, 0, d.sequences - 1), s1 = sequence_of(d, end - 1, s0, d.sequences - 1);
+    const int s0 = wave_sequence_of(d, begin), s1 = wave_sequence_of(d, end - 1);
     const int window = min(kCountWords / stride, s1 - s0 + 1);
     for (int k = threadIdx.x; k < window * stride; k += kRouterThreads) own[k] = 0;
     __syncthreads();
-    const uint32_t top = d.top_k;
-    const int64_t first = static_cast<int64_t>(begin) * top;
-    const uint32_t choices = (end - begin) * top;
-    for (uint32_t k = threadIdx.x; k < choices; k += kRouterThreads) {
-        const uint32_t row = k / top;
-        const int token = begin + row;
-        const int s = sequence_of(d, token, s0, s1);
-        if (!takes_part(d, token, s)) continue;
-        uint32_t *to = s - s0 < window ? own + (s - s0) * stride : nullptr;
-        uint32_t *far = d.hist + static_cast<int64_t>(s) * stride;
-        const int64_t x = d.chosen64 ? as_global(static_cast<const int64_t *>(d.chosen))[first + k]
-                                     : as_global(static_cast<const int32_t *>(d.chosen))[first + k];
-        auto add = [&](int i) {
-            if (to)
-                atomicAdd(to + i, 1u);
-            else
-                atomicAdd(far + i, 1u);
-        };
-        if (x >= 0 && x < d.experts) add(static_cast<int>(x));
-        if (k == row * top) add(d.experts);
-    }
+    count_tokens(d, begin, end, s0, s1, own, window);
     __syncthreads();
     for (int k = threadIdx.x; k < window * stride; k += kRouterThreads)
         if (own[k] != 0) atomicAdd(d.hist + static_cast<int64_t>(s0) * stride + k, own[k]);
 }
 
-// Sum and maximum over the LANES lanes of a row.
-template <int LANES> __device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-    for (int off = 1; off < LANES; off *= 2) x += __shfl_xor(x, off, 64);
+// The value of lane ^ OFF, for values that are the same in each OFF neighbours
+// already: within 16 lanes by a lane permutation in the instruction itself
+// (mirrors serve for 4 and 8), beyond by swaps of halves.
+template <int OFF> __device__ __forceinline__ float across(float x) {
+    const int v = __float_as_int(x);
+    if constexpr (OFF == 1) return __int_as_float(__builtin_amdgcn_mov_dpp(v, 0xb1, 0xf, 0xf, true));   // quad 1 0 3 2
+    if constexpr (OFF == 2) return __int_as_float(__builtin_amdgcn_mov_dpp(v, 0x4e, 0xf, 0xf, true));   // quad 2 3 0 1
+    if constexpr (OFF == 4) return __int_as_float(__builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true));  // mirror of 8
+    if constexpr (OFF == 8) return __int_as_float(__builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true));  // mirror of 16
+    return __shfl_xor(x, OFF, 64);
+}
+// Sum and maximum over the LANES lanes of a row, in all of them.
+template <int LANES, int OFF = 1> __device__ __forceinline__ float row_sum(float x) {
+    if constexpr (OFF < LANES) return row_sum<LANES, 2 * OFF>(x + across<OFF>(x));
     return x;
 }
-template <int LANES> __device__ __forceinline__ float row_max(float x) {
-#pragma unroll
-    for (int off = 1; off < LANES; off *= 2) x = fmaxf(x, __shfl_xor(x, off, 64));
+template <int LANES, int OFF = 1> __device__ __forceinline__ float row_max(float x) {
+    if constexpr (OFF < LANES) return row_max<LANES, 2 * OFF>(fmaxf(x, across<OFF>(x)));
     return x;
 }
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
-// The lane's logits of a row, those past the row's end as -inf (their score is zero).
-template <int PER, bool BF16> __device__ __forceinline__ void load_row(const void *p, int64_t at, int there, float (&x)[PER]) {
-    if (there >= PER) {
-        if constexpr (BF16) {
+// The lane's logits of a row as they lie in memory, and as numbers; those past the
+// row's end are -inf (their score is zero).
+template <int PER, bool BF16> struct Row {
+    static constexpr int kWords = BF16 ? PER / 2 : PER;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void load(const void *p, int64_t at, int there) {
+        const char *from = static_cast<const char *>(p) + at * (BF16 ? 2 : 4);
+        if (there >= PER) {
 #pragma unroll
-            for (int k = 0; k < PER; k += 8) {
-                uint32_t w[4];
-                load_words<4, 2>(static_cast<const uint16_t *>(p) + at + k, w);
+            for (int k = 0; k < kWords; k += 4) {
+                uint32_t v[4];
+                load_words<4, BF16 ? 2 : 4>(from + 4 * k, v);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    x[k + 2 * q] = __uint_as_float(w[q] << 16);
-                    x[k + 2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
-                }
+                for (int q = 0; q < 4; ++q) w[k + q] = v[q];
             }
         } else {
+            constexpr uint32_t kNone = BF16 ? 0xff80ff80u : 0xff800000u;
 #pragma unroll
-            for (int k = 0; k < PER; k += 4) {
-                uint32_t w[4];
-                load_words<4, 4>(static_cast<const float *>(p) + at + k, w);
+            for (int k = 0; k < kWords; ++k) w[k] = kNone;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) x[k + q] = __uint_as_float(w[q]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-            x[k] = -INFINITY;
-            if (k < there) {
-                if constexpr (BF16)
-                    x[k] = bf16_bits_to_float(as_global(static_cast<const uint16_t *>(p))[at + k]);
-                else
-                    x[k] = as_global(static_cast<const float *>(p))[at + k];
-            }
+            for (int k = 0; k < PER; ++k)
+                if (k < there) {
+                    if constexpr (BF16) {
+                        const uint32_t v = as_global(reinterpret_cast<const uint16_t *>(from))[k];
+                        w[k / 2] = k % 2 ? (w[k / 2] & 0xffffu) | v << 16 : (w[k / 2] & 0xffff0000u) | v;
+                    } else {
+                        w[k] = as_global(reinterpret_cast<const uint32_t *>(from))[k];
+                    }
+                }
         }
     }
-}
+    __device__ __forceinline__ float operator[](int k) const {
+        if constexpr (BF16) return __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+        return __uint_as_float(w[k]);
+    }
+};
 template <int PER, bool BF16> __device__ __forceinline__ void store_row(void *p, int64_t at, int there, const float (&x)[PER]) {
     if (there >= PER) {
         if constexpr (BF16) {
@@ -168,66 +202,70 @@ template <int PER, bool BF16> __device__ __forceinline__ void store_row(void *p,
     }
 }
 
-// LANES lanes take a row of up to LANES x PER logits, 64 / LANES rows a wave.
-template <int LANES, int PER, bool BF16, bool SIGMOID>
-__global__ __launch_bounds__(kRouterThreads) void router_balance_kernel(const RouterTable t, const RouterCall c) {
-    __shared__ double sh_sum[kWaves];
-    __shared__ int sh_sequences;
-    constexpr int kRows = 64 / LANES;
-    const Owners<64> owners(t.first);
-    const int e = owners.of(blockIdx.x);
-    const RouterDesc &d = t.d[e];
-    const uint32_t mine = blockIdx.x - t.first[e];
-    const int begin = mine * c.per_block, end = min(begin + static_cast<int>(c.per_block), d.tokens);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int row0 = lane / LANES, i0 = lane % LANES * PER;  // the lane's row of a wave's rows, and its first expert
-    const int stride = d.experts + 1, there = d.experts - i0;
-    const float grad_scale = c.grad_scale ? *as_global(c.grad_scale) : 1.0f;
-
-    // the sequences that have tokens
-    if (threadIdx.x == 0) sh_sequences = 0;
-    __syncthreads();
-    int found = 0;
-    for (int s = threadIdx.x; s < d.sequences; s += kRouterThreads)
-        found += as_global(d.hist)[static_cast<int64_t>(s) * stride + d.experts] != 0;
-    if (found) atomicAdd(&sh_sequences, found);
-    __syncthreads();
-    const int sequences = sh_sequences;
-
-    double loss = 0.0;
+// What a lane needs of its row's sequence: its span, and how far the factors of the
+// lane's experts lie from their mean.
+template <int PER> struct Factors {
     int s = -1;
     Span span{0, 0};
     float away[PER], mean = 0.0f;
+};
+
+// Gradients of tokens [begin, end), LANES lanes to a row of up to LANES x PER
+// logits, 64 / LANES rows a wave, and the lane's part of the loss.  hist: counts of
+// the sequences from s0 on; `live`: how many sequences have tokens.
+template <int LANES, int PER, bool BF16, bool SIGMOID>
+__device__ __forceinline__ double balance_rows(const RouterDesc &d, const RouterCall &c, const uint32_t *hist, int begin, int end,
+                                               int s0, int s1, int live) {
+    constexpr int kRows = 64 / LANES;
+    const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int row0 = lane / LANES, i0 = lane % LANES * PER;  // the lane's row of a wave's rows, and its first expert
+    const int stride = d.experts + 1, there = d.experts - i0;
+    const float grad_scale = c.grad_scale ? *as_global(c.grad_scale) : 1.0f;
+    double loss = 0.0;
+    Factors<PER> f;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) away[k] = 0.0f;
-    for (int base = begin + wave * kRows; base < end; base += kWaves * kRows) {
-        const int token = base + row0;
-        if (token < end && (s < 0 || token >= span.end)) {
-            // the row's sequence, and how far its experts' factors lie from their mean
-            s = sequence_of(d, token, max(s, 0), d.sequences - 1);
-            span = span_of(d, s);
-            const uint32_t *hist = d.hist + static_cast<int64_t>(s) * stride;
-            const double n = as_global(hist)[d.experts];
-            double total = 0.0;
-            uint32_t got[PER];
+    for (int k = 0; k < PER; ++k) f.away[k] = 0.0f;
+
+    auto find = [&](int token) {
+        f.s = sequence_of(d, token, max(f.s, s0), s1);
+        f.span = span_of(d, f.s);
+        const uint32_t *h = hist + static_cast<int64_t>(f.s - s0) * stride;
+        const double n = h[d.experts];
+        double total = 0.0;
+        uint32_t got[PER];
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                got[k] = k < there ? as_global(hist)[i0 + k] : 0;
-                total += got[k];
-            }
-#pragma unroll
-            for (int off = 1; off < LANES; off *= 2) total += __shfl_xor(total, off, 64);
-            const double unit = n > 0 ? c.coef / (static_cast<double>(sequences) * d.top_k * n * n) : 0.0;
-            mean = static_cast<float>(unit * total);
-#pragma unroll
-            for (int k = 0; k < PER; ++k) away[k] = k < there ? static_cast<float>(unit * (static_cast<double>(d.experts) * got[k] - total)) : 0.0f;
+        for (int k = 0; k < PER; ++k) {
+            got[k] = k < there ? h[i0 + k] : 0;
+            total += got[k];
         }
-        const bool inside = token < end && token >= span.begin && token < span.end;
-        const bool taking = inside && (!d.mask || as_global(d.mask)[token] != 0);
-        float x[PER];
-        load_row<PER, BF16>(d.logits, static_cast<int64_t>(taking ? token : begin) * d.pitch + i0, taking ? there : 0, x);
+#pragma unroll
+        for (int off = 1; off < LANES; off *= 2) total += __shfl_xor(total, off, 64);
+        const double unit = n > 0 ? c.coef / (static_cast<double>(live) * d.top_k * n * n) : 0.0;
+        f.mean = static_cast<float>(unit * total);
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            f.away[k] = k < there ? static_cast<float>(unit * (static_cast<double>(d.experts) * got[k] - total)) : 0.0f;
+    };
+    // a wave's next rows are on their way while it works on these
+    Row<PER, BF16> next;
+    uint8_t next_mask = 1;
+    auto fetch = [&](int base) {
+        const int token = min(base + row0, end - 1);
+        next.load(d.logits, static_cast<int64_t>(token) * d.pitch + i0, there);
+        next_mask = d.mask ? as_global(d.mask)[token] : 1;
+    };
+    int base = begin + wave * kRows;
+    if (base < end) fetch(base);
+    for (; base < end; base += waves * kRows) {
+        const int token = base + row0;
+        Row<PER, BF16> x = next;
+        const bool unmasked = next_mask != 0;
+        if (base + waves * kRows < end) fetch(base + waves * kRows);
+        if (token < end && (f.s < 0 || token >= f.span.end)) find(token);
+        const bool inside = token < end && token >= f.span.begin && token < f.span.end;
+        const bool taking = inside && unmasked;
         // w: a score, not yet normalised; q: its derivative's factor
-        float w[PER], q[PER], sum = 0.0f, dot = 0.0f;
+        float w[PER], q[PER], sum, dot;
         auto shifted = [&]() {  // exp(x - max)
             float most = -3.402823466e38f;
 #pragma unroll
@@ -242,7 +280,7 @@ __global__ __launch_bounds__(kRouterThreads) void router_balance_kernel(const Ro
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
                 sum += w[k];
-                dot = __builtin_fmaf(away[k], w[k], dot);
+                dot = __builtin_fmaf(f.away[k], w[k], dot);
             }
             sum = row_sum<LANES>(sum);
             dot = row_sum<LANES>(dot);
@@ -250,9 +288,14 @@ __global__ __launch_bounds__(kRouterThreads) void router_balance_kernel(const Ro
         if constexpr (SIGMOID) {
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
-                const float z = exp_of(-fabsf(x[k])), r = __builtin_amdgcn_rcpf(1.0f + z), zr = z * r;
-                w[k] = x[k] >= 0.0f ? r : zr;
-                q[k] = x[k] >= 0.0f ? zr : r;
+                // sigma and 1 - sigma, each without cancellation; past x = -87.5 sigma is held at 1e-38
+                const float z = fminf(exp_of(-x[k]), 1e38f);
+                w[k] = __builtin_amdgcn_rcpf(1.0f + z);
+                q[k] = z * w[k];
+            }
+            if (there < PER) {
+#pragma unroll
+                for (int k = 0; k < PER; ++k) w[k] = k < there ? w[k] : 0.0f;
             }
             add();
             // rows whose sigmoids all vanish in fp32: there sigma(x) is exp(x)
@@ -275,29 +318,86 @@ __global__ __launch_bounds__(kRouterThreads) void router_balance_kernel(const Ro
             add();
         }
         // a row without any score: no probability, no gradient
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
         dot *= inv;
-        if (taking && lane % LANES == 0) loss += static_cast<double>(dot) + (sum == 0.0f ? 0.0f : mean);
+        if (taking && lane % LANES == 0) loss += static_cast<double>(dot) + (sum == 0.0f ? 0.0f : f.mean);
         if (inside && d.dlogits) {
             float g[PER];
-            const float scale = taking ? inv * grad_scale : 0.0f;
+            const float scale = inv * grad_scale;
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
-                g[k] = w[k] * (away[k] - dot) * scale;
+                g[k] = w[k] * ((f.away[k] - dot) * scale);
                 if constexpr (SIGMOID) g[k] *= q[k];
-                if (!taking) g[k] = 0.0f;
+            }
+            if (!taking) {
+#pragma unroll
+                for (int k = 0; k < PER; ++k) g[k] = 0.0f;
             }
             store_row<PER, BF16>(d.dlogits, static_cast<int64_t>(token) * d.dpitch + i0, there, g);
         }
     }
+    return loss;
+}
+
+// Sum over the workgroup, in thread 0.
+__device__ __forceinline__ double block_sum(double x, double *sh) {
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) loss += __shfl_down(loss, off, 64);
-    if (lane == 0) sh_sum[wave] = loss;
+    for (int off = 32; off > 0; off >>= 1) x += __shfl_down(x, off, 64);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        double sum = 0.0;
-        for (int k = 0; k < kWaves; ++k) sum += sh_sum[k];
-        d.sums[mine] = sum;
+    double sum = 0.0;
+    if (threadIdx.x == 0)
+        for (uint32_t k = 0; k < blockDim.x >> 6; ++k) sum += sh[k];
+    return sum;
+}
+// How many of the sequences have tokens.
+__device__ __forceinline__ int live_sequences(const RouterDesc &d, const uint32_t *hist, int *sh) {
+    if (threadIdx.x == 0) *sh = 0;
+    __syncthreads();
+    int found = 0;
+    for (int s = threadIdx.x; s < d.sequences; s += blockDim.x) found += hist[static_cast<int64_t>(s) * (d.experts + 1) + d.experts] != 0;
+    if (found) atomicAdd(sh, found);
+    __syncthreads();
+    return *sh;
+}
+
+template <int LANES, int PER, bool BF16, bool SIGMOID>
+__global__ __launch_bounds__(kRouterThreads) void router_balance_kernel(const RouterTable t, const RouterCall c) {
+    __shared__ double sh_sum[kWaves];
+    __shared__ int sh_live;
+    const Owners<64> owners(t.first);
+    const int e = owners.of(blockIdx.x);
+    const RouterDesc &d = t.d[e];
+    const uint32_t mine = blockIdx.x - t.first[e];
+    const int begin = mine * c.per_block, end = min(begin + static_cast<int>(c.per_block), d.tokens);
+    const int s0 = wave_sequence_of(d, begin), s1 = wave_sequence_of(d, end - 1);
+    const int live = live_sequences(d, d.hist, &sh_live);
+    const double loss = balance_rows<LANES, PER, BF16, SIGMOID>(d, c, d.hist + static_cast<int64_t>(s0) * (d.experts + 1), begin,
+                                                                end, s0, s1, live);
+    const double sum = block_sum(loss, sh_sum);
+    if (threadIdx.x == 0) d.sums[mine] = sum;
+}
+
+// Small batches: one workgroup for each router does all of it, counts in shared memory.
+template <int LANES, int PER, bool BF16, bool SIGMOID>
+__global__ __launch_bounds__(kSmallThreads) void router_small_kernel(const RouterTable t, const RouterCall c) {
+    __shared__ uint32_t hist[kCountWords];
+    __shared__ double sh_sum[kSmallThreads / 64];
+    __shared__ int sh_live;
+    const RouterDesc &d = t.d[blockIdx.x];
+    const int stride = d.experts + 1;
+    for (int k = threadIdx.x; k < d.sequences * stride; k += kSmallThreads) hist[k] = 0;
+    __syncthreads();
+    count_tokens(d, 0, d.tokens, 0, d.offsets ? d.sequences - 1 : 0, hist, d.sequences);
+    __syncthreads();
+    const int live = live_sequences(d, hist, &sh_live);
+    const double loss = balance_rows<LANES, PER, BF16, SIGMOID>(d, c, hist, 0, d.tokens, 0, d.offsets ? d.sequences - 1 : 0, live);
+    const double sum = block_sum(loss, sh_sum);
+    if (threadIdx.x == 0) *d.loss = static_cast<float>(sum);
+    for (int i = threadIdx.x; i < d.experts; i += kSmallThreads) {
+        int64_t n = 0;
+        for (int s = 0; s < d.sequences; ++s) n += hist[s * stride + i];
+        as_global(d.counts)[i] = c.accumulate ? as_global(d.counts)[i] + n : n;
     }
 }
 
@@ -365,21 +465,35 @@ __global__ __launch_bounds__(kRouterThreads) void router_bias_kernel(const Route
     }
 }
 
-template <int LANES, int PER>
-hipError_t launch_rows(const RouterTable &t, uint32_t blocks, const RouterCall &c, bool bf16, hipStream_t st) {
-    const dim3 grid(blocks), block(kRouterThreads);
-    if (c.sigmoid) {
-        if (bf16)
-            hipLaunchKernelGGL((router_balance_kernel<LANES, PER, true, true>), grid, block, 0, st, t, c);
-        else
-            hipLaunchKernelGGL((router_balance_kernel<LANES, PER, false, true>), grid, block, 0, st, t, c);
-    } else {
-        if (bf16)
-            hipLaunchKernelGGL((router_balance_kernel<LANES, PER, true, false>), grid, block, 0, st, t, c);
-        else
-            hipLaunchKernelGGL((router_balance_kernel<LANES, PER, false, false>), grid, block, 0, st, t, c);
-    }
+template <int LANES, int PER, bool BF16, bool SIGMOID>
+hipError_t launch_as(const RouterTable &t, uint32_t blocks, const RouterCall &c, bool small, hipStream_t st) {
+    if (small)
+        hipLaunchKernelGGL((router_small_kernel<LANES, PER, BF16, SIGMOID>), dim3(blocks), dim3(kSmallThreads), 0, st, t, c);
+    else
+        hipLaunchKernelGGL((router_balance_kernel<LANES, PER, BF16, SIGMOID>), dim3(blocks), dim3(kRouterThreads), 0, st, t, c);
     return hipGetLastError();
+}
+template <int LANES, int PER>
+hipError_t launch_rows(const RouterTable &t, uint32_t blocks, const RouterCall &c, bool bf16, bool small, hipStream_t st) {
+    if (c.sigmoid)
+        return bf16 ? launch_as<LANES, PER, true, true>(t, blocks, c, small, st)
+                    : launch_as<LANES, PER, false, true>(t, blocks, c, small, st);
+    return bf16 ? launch_as<LANES, PER, true, false>(t, blocks, c, small, st)
+                : launch_as<LANES, PER, false, false>(t, blocks, c, small, st);
+}
+hipError_t launch_any(const RouterTable &t, uint32_t blocks, const RouterCall &c, int experts, bool bf16, bool small,
+                      hipStream_t st) {
+    switch (router_lanes(experts)) {
+        case 1: return launch_rows<1, 8>(t, blocks, c, bf16, small, st);
+        case 2: return launch_rows<2, 8>(t, blocks, c, bf16, small, st);
+        case 4: return launch_rows<4, 8>(t, blocks, c, bf16, small, st);
+        case 8: return launch_rows<8, 8>(t, blocks, c, bf16, small, st);
+        case 16: return launch_rows<16, 8>(t, blocks, c, bf16, small, st);
+        case 32: return launch_rows<32, 8>(t, blocks, c, bf16, small, st);
+        default:
+            return experts <= 512 ? launch_rows<64, 8>(t, blocks, c, bf16, small, st)
+                                  : launch_rows<64, 16>(t, blocks, c, bf16, small, st);
+    }
 }
 
 }  // namespace
@@ -391,15 +505,11 @@ hipError_t launch_router_count(const RouterTable &t, uint32_t blocks, const Rout
 
 hipError_t launch_router_balance(const RouterTable &t, uint32_t blocks, const RouterCall &c, int experts, bool bf16,
                                  hipStream_t st) {
-    switch (router_lanes(experts)) {
-        case 1: return launch_rows<1, 8>(t, blocks, c, bf16, st);
-        case 2: return launch_rows<2, 8>(t, blocks, c, bf16, st);
-        case 4: return launch_rows<4, 8>(t, blocks, c, bf16, st);
-        case 8: return launch_rows<8, 8>(t, blocks, c, bf16, st);
-        case 16: return launch_rows<16, 8>(t, blocks, c, bf16, st);
-        case 32: return launch_rows<32, 8>(t, blocks, c, bf16, st);
-        default: return experts <= 512 ? launch_rows<64, 8>(t, blocks, c, bf16, st) : launch_rows<64, 16>(t, blocks, c, bf16, st);
-    }
+    return launch_any(t, blocks, c, experts, bf16, false, st);
+}
+
+hipError_t launch_router_small(const RouterTable &t, int routers, const RouterCall &c, int experts, bool bf16, hipStream_t st) {
+    return launch_any(t, routers, c, experts, bf16, true, st);
 }
 
 hipError_t launch_router_finish(const RouterTable &t, int routers, uint32_t blocks, const RouterCall &c, hipStream_t st) {

@@ -36,6 +36,11 @@ struct RouterCall {
 
 constexpr int kRouterThreads = 256;
 constexpr int kMaxExperts = 1024;
+constexpr int kCountWords = 8192;    // counts that a workgroup has room for
+constexpr int kSmallThreads = 1024;
+// Routers with at most this many logits, and counts that fit a workgroup, are one
+// workgroup's work each.
+constexpr int64_t kSmallLogits = 65536;
 
 // Lanes that share a row of `experts` logits, and how many each takes.
 inline int router_lanes(int experts) {
@@ -50,6 +55,8 @@ hipError_t launch_router_count(const RouterTable &t, uint32_t blocks, const Rout
 // the same type and router_lanes().
 hipError_t launch_router_balance(const RouterTable &t, uint32_t blocks, const RouterCall &c, int experts, bool bf16,
                                  hipStream_t st);
+// All of it for routers that are one workgroup's work each: hist and sums are not used.
+hipError_t launch_router_small(const RouterTable &t, int routers, const RouterCall &c, int experts, bool bf16, hipStream_t st);
 // Counts and loss from hist and sums (t.first: launch_router_balance's, and its
 // `blocks`); hist is zero behind it.
 hipError_t launch_router_finish(const RouterTable &t, int routers, uint32_t blocks, const RouterCall &c, hipStream_t st);

@@ -1927,9 +1927,9 @@ muon_status blocks_impl(muon_context *ctx, const muon_block_matrix *mats, int64_
 
 // ---- muon_router_balance
 
-// Workgroups that the passes over choices and over logits aim at: two and eight
-// for each CU.
-constexpr int64_t kCountWorkgroups = 512, kBalanceWorkgroups = 2048;
+// Workgroups that the passes over choices and over logits aim at: two and six
+// for each CU (all of them resident at once).
+constexpr int64_t kCountWorkgroups = 512, kBalanceWorkgroups = 1536;
 
 size_t router_words(const muon_router &r) { return static_cast<size_t>(r.sequences) * (r.experts + 1); }
 
@@ -1942,6 +1942,41 @@ muon_status run_router_table(muon_context *ctx, const muon_router *const *rs, in
         tokens += rs[i]->tokens;
     }
     const muon_router &like = *rs[0];
+    const bool bf16 = like.dtype == MUON_BF16;
+    muon::RouterTable t{};
+    muon::RouterCall c{};
+    c.coef = hp->coef;
+    c.grad_scale = hp->grad_scale;
+    c.sigmoid = hp->score == MUON_SCORE_SIGMOID;
+    c.accumulate = hp->accumulate;
+    double count_bytes = 0, row_bytes = 0;
+    bool small = true;
+    for (int i = 0; i < n; ++i) {
+        const muon_router &r = *rs[i];
+        muon::RouterDesc &d = t.d[i];
+        d.logits = r.logits;
+        d.dlogits = r.dlogits;
+        d.chosen = r.chosen;
+        d.offsets = r.offsets;
+        d.mask = r.mask;
+        d.counts = r.counts;
+        d.loss = r.loss;
+        d.pitch = static_cast<uint32_t>(r.tokens ? r.pitch : 0);
+        d.dpitch = static_cast<uint32_t>(r.tokens && r.dlogits ? r.dlogits_pitch : 0);
+        d.tokens = static_cast<int32_t>(r.tokens);
+        d.experts = r.experts;
+        d.top_k = r.top_k;
+        d.sequences = r.sequences;
+        d.chosen64 = r.chosen_bits == 64;
+        small &= r.tokens * r.experts <= muon::kSmallLogits && router_words(r) <= static_cast<size_t>(muon::kCountWords);
+        count_bytes += static_cast<double>(r.tokens) * (r.top_k * (r.chosen_bits / 8) + (r.mask ? 1 : 0));
+        row_bytes += static_cast<double>(r.tokens) * r.experts * dtype_size(r.dtype) * (r.dlogits ? 2 : 1);
+    }
+    if (small) {
+        const hipError_t e = timed(ctx, ST_ROUTER_BALANCE, 0.0, count_bytes + row_bytes, st,
+                                   [&] { return muon::launch_router_small(t, n, c, like.experts, bf16, st); });
+        return e == hipSuccess ? MUON_OK : hip_fail(ctx, e, "router launch");
+    }
     const int lanes = muon::router_lanes(like.experts);
     const int64_t turn = muon::kRouterThreads / lanes;  // rows that a workgroup takes at once
     const int64_t per_balance = round_up(std::max<int64_t>(1, (tokens + kBalanceWorkgroups - 1) / kBalanceWorkgroups), turn);
@@ -1961,35 +1996,10 @@ muon_status run_router_table(muon_context *ctx, const muon_router *const *rs, in
         const hipError_t e = muon::launch_router_clear(hist + clear, static_cast<int64_t>(words - clear), st);
         if (e != hipSuccess) return hip_fail(ctx, e, "router workspace launch");
     }
-    muon::RouterTable t{};
-    muon::RouterCall c{};
-    c.coef = hp->coef;
-    c.grad_scale = hp->grad_scale;
-    c.sigmoid = hp->score == MUON_SCORE_SIGMOID;
-    c.accumulate = hp->accumulate;
-    double count_bytes = 0, row_bytes = 0;
     size_t at = 0;
     for (int i = 0; i < n; ++i) {
-        const muon_router &r = *rs[i];
-        muon::RouterDesc &d = t.d[i];
-        d.logits = r.logits;
-        d.dlogits = r.dlogits;
-        d.chosen = r.chosen;
-        d.offsets = r.offsets;
-        d.mask = r.mask;
-        d.counts = r.counts;
-        d.loss = r.loss;
-        d.hist = hist + at;
-        d.pitch = static_cast<uint32_t>(r.tokens ? r.pitch : 0);
-        d.dpitch = static_cast<uint32_t>(r.tokens && r.dlogits ? r.dlogits_pitch : 0);
-        d.tokens = static_cast<int32_t>(r.tokens);
-        d.experts = r.experts;
-        d.top_k = r.top_k;
-        d.sequences = r.sequences;
-        d.chosen64 = r.chosen_bits == 64;
-        at += router_words(r);
-        count_bytes += static_cast<double>(r.tokens) * (r.top_k * (r.chosen_bits / 8) + (r.mask ? 1 : 0));
-        row_bytes += static_cast<double>(r.tokens) * r.experts * dtype_size(r.dtype) * (r.dlogits ? 2 : 1);
+        t.d[i].hist = hist + at;
+        at += router_words(*rs[i]);
     }
     for (int k = n; k < 64; ++k) t.first[k] = 0xffffffffu;
     auto spread = [&](int64_t per) {
@@ -2010,7 +2020,7 @@ muon_status run_router_table(muon_context *ctx, const muon_router *const *rs, in
     for (int i = 0; i < n; ++i) t.d[i].sums = sums + t.first[i];
     if (blocks > 0)
         e = timed(ctx, ST_ROUTER_BALANCE, 0.0, row_bytes, st,
-                  [&] { return muon::launch_router_balance(t, blocks, c, like.experts, like.dtype == MUON_BF16, st); });
+                  [&] { return muon::launch_router_balance(t, blocks, c, like.experts, bf16, st); });
     if (e != hipSuccess) return hip_fail(ctx, e, "router balance launch");
     e = timed(ctx, ST_ROUTER_FINISH, 0.0, static_cast<double>(words) * 4, st,
               [&] { return muon::launch_router_finish(t, n, blocks, c, st); });
