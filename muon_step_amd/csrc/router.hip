@@ -136,36 +136,47 @@ template <int LANES, int OFF = 1> __device__ __forceinline__ float row_max(float
 }
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
-// The lane's logits of a row as they lie in memory, and as numbers; those past the
-// row's end are -inf (their score is zero).
-template <int PER, bool BF16> struct Row {
-    static constexpr int kWords = BF16 ? PER / 2 : PER;
-    uint32_t w[kWords];
+// A lane of LANES to a row takes PER of its elements, eight side by side and the
+// next eight 8 LANES further on: element k is expert 8 lane + at(k).
+template <int LANES> __device__ __forceinline__ constexpr int at(int k) { return k / 8 * 8 * LANES + k % 8; }
 
-    __device__ __forceinline__ void load(const void *p, int64_t at, int there) {
-        const char *from = static_cast<const char *>(p) + at * (BF16 ? 2 : 4);
-        if (there >= PER) {
+// The lane's logits of a row as they lie in memory, and as numbers; those past the
+// row's end (`there` of them and more, from the lane's first one on) are -inf: their
+// score is zero.
+template <int LANES, int PER, bool BF16> struct Row {
+    static constexpr int kEight = BF16 ? 4 : 8;  // words of eight
+    uint32_t w[PER / 8 * kEight];
+
+    __device__ __forceinline__ void load(const void *p, int64_t first, int there) {
+        const char *from = static_cast<const char *>(p) + first * (BF16 ? 2 : 4);
 #pragma unroll
-            for (int k = 0; k < kWords; k += 4) {
-                uint32_t v[4];
-                load_words<4, BF16 ? 2 : 4>(from + 4 * k, v);
+        for (int s = 0; s < PER / 8; ++s) {
+            const char *place = from + at<LANES>(8 * s) * (BF16 ? 2 : 4);
+            const int left = there - at<LANES>(8 * s);
+            if (left >= 8) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) w[k + q] = v[q];
-            }
-        } else {
-            constexpr uint32_t kNone = BF16 ? 0xff80ff80u : 0xff800000u;
+                for (int k = 0; k < kEight; k += 4) {
+                    uint32_t v[4];
+                    load_words<4, BF16 ? 2 : 4>(place + 4 * k, v);
 #pragma unroll
-            for (int k = 0; k < kWords; ++k) w[k] = kNone;
-#pragma unroll
-            for (int k = 0; k < PER; ++k)
-                if (k < there) {
-                    if constexpr (BF16) {
-                        const uint32_t v = as_global(reinterpret_cast<const uint16_t *>(from))[k];
-                        w[k / 2] = k % 2 ? (w[k / 2] & 0xffffu) | v << 16 : (w[k / 2] & 0xffff0000u) | v;
-                    } else {
-                        w[k] = as_global(reinterpret_cast<const uint32_t *>(from))[k];
-                    }
+                    for (int q = 0; q < 4; ++q) w[s * kEight + k + q] = v[q];
                 }
+            } else {
+                constexpr uint32_t kNone = BF16 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+                for (int k = 0; k < kEight; ++k) w[s * kEight + k] = kNone;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < left) {
+                        if constexpr (BF16) {
+                            uint32_t &to = w[s * kEight + k / 2];
+                            const uint32_t v = as_global(reinterpret_cast<const uint16_t *>(place))[k];
+                            to = k % 2 ? (to & 0xffffu) | v << 16 : (to & 0xffff0000u) | v;
+                        } else {
+                            w[s * kEight + k] = as_global(reinterpret_cast<const uint32_t *>(place))[k];
+                        }
+                    }
+            }
         }
     }
     __device__ __forceinline__ float operator[](int k) const {
@@ -173,32 +184,37 @@ template <int PER, bool BF16> struct Row {
         return __uint_as_float(w[k]);
     }
 };
-template <int PER, bool BF16> __device__ __forceinline__ void store_row(void *p, int64_t at, int there, const float (&x)[PER]) {
-    if (there >= PER) {
-        if constexpr (BF16) {
+template <int LANES, int PER, bool BF16>
+__device__ __forceinline__ void store_row(void *p, int64_t first, int there, const float (&x)[PER]) {
+    char *to = static_cast<char *>(p) + first * (BF16 ? 2 : 4);
 #pragma unroll
-            for (int k = 0; k < PER; k += 8) {
-                const uint32_t w[4] = {pack_bf16x2(x[k], x[k + 1]), pack_bf16x2(x[k + 2], x[k + 3]),
-                                       pack_bf16x2(x[k + 4], x[k + 5]), pack_bf16x2(x[k + 6], x[k + 7])};
-                store_words<4, 2>(static_cast<uint16_t *>(p) + at + k, w);
+    for (int s = 0; s < PER / 8; ++s) {
+        char *place = to + at<LANES>(8 * s) * (BF16 ? 2 : 4);
+        const int left = there - at<LANES>(8 * s);
+        const float *y = x + 8 * s;
+        if (left >= 8) {
+            if constexpr (BF16) {
+                const uint32_t w[4] = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                       pack_bf16x2(y[6], y[7])};
+                store_words<4, 2>(place, w);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; k += 4) {
+                    const uint32_t w[4] = {__float_as_uint(y[k]), __float_as_uint(y[k + 1]), __float_as_uint(y[k + 2]),
+                                           __float_as_uint(y[k + 3])};
+                    store_words<4, 4>(place + 4 * k, w);
+                }
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < PER; k += 4) {
-                const uint32_t w[4] = {__float_as_uint(x[k]), __float_as_uint(x[k + 1]), __float_as_uint(x[k + 2]),
-                                       __float_as_uint(x[k + 3])};
-                store_words<4, 4>(static_cast<float *>(p) + at + k, w);
-            }
+            for (int k = 0; k < 8; ++k)
+                if (k < left) {
+                    if constexpr (BF16)
+                        as_global(reinterpret_cast<uint16_t *>(place))[k] = float_to_bf16_bits(y[k]);
+                    else
+                        as_global(reinterpret_cast<float *>(place))[k] = y[k];
+                }
         }
-    } else {
-#pragma unroll
-        for (int k = 0; k < PER; ++k)
-            if (k < there) {
-                if constexpr (BF16)
-                    as_global(static_cast<uint16_t *>(p))[at + k] = float_to_bf16_bits(x[k]);
-                else
-                    as_global(static_cast<float *>(p))[at + k] = x[k];
-            }
     }
 }
 
@@ -218,7 +234,7 @@ __device__ __forceinline__ double balance_rows(const RouterDesc &d, const Router
                                                int s0, int s1, int live) {
     constexpr int kRows = 64 / LANES;
     const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int row0 = lane / LANES, i0 = lane % LANES * PER;  // the lane's row of a wave's rows, and its first expert
+    const int row0 = lane / LANES, i0 = lane % LANES * 8;  // the lane's row of a wave's rows, and its first expert
     const int stride = d.experts + 1, there = d.experts - i0;
     const float grad_scale = c.grad_scale ? *as_global(c.grad_scale) : 1.0f;
     double loss = 0.0;
@@ -235,7 +251,7 @@ __device__ __forceinline__ double balance_rows(const RouterDesc &d, const Router
         uint32_t got[PER];
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            got[k] = k < there ? h[i0 + k] : 0;
+            got[k] = at<LANES>(k) < there ? h[i0 + at<LANES>(k)] : 0;
             total += got[k];
         }
 #pragma unroll
@@ -244,10 +260,10 @@ __device__ __forceinline__ double balance_rows(const RouterDesc &d, const Router
         f.mean = static_cast<float>(unit * total);
 #pragma unroll
         for (int k = 0; k < PER; ++k)
-            f.away[k] = k < there ? static_cast<float>(unit * (static_cast<double>(d.experts) * got[k] - total)) : 0.0f;
+            f.away[k] = at<LANES>(k) < there ? static_cast<float>(unit * (static_cast<double>(d.experts) * got[k] - total)) : 0.0f;
     };
     // a wave's next rows are on their way while it works on these
-    Row<PER, BF16> next;
+    Row<LANES, PER, BF16> next;
     uint8_t next_mask = 1;
     auto fetch = [&](int base) {
         const int token = min(base + row0, end - 1);
@@ -258,7 +274,7 @@ __device__ __forceinline__ double balance_rows(const RouterDesc &d, const Router
     if (base < end) fetch(base);
     for (; base < end; base += waves * kRows) {
         const int token = base + row0;
-        Row<PER, BF16> x = next;
+        Row<LANES, PER, BF16> x = next;
         const bool unmasked = next_mask != 0;
         if (base + waves * kRows < end) fetch(base + waves * kRows);
         if (token < end && (f.s < 0 || token >= f.span.end)) find(token);
@@ -266,13 +282,13 @@ __device__ __forceinline__ double balance_rows(const RouterDesc &d, const Router
         const bool taking = inside && unmasked;
         // w: a score, not yet normalised; q: its derivative's factor
         float w[PER], q[PER], sum, dot;
-        auto shifted = [&]() {  // exp(x - max)
+        auto shifted = [&](float (&to)[PER]) {  // exp(x - max)
             float most = -3.402823466e38f;
 #pragma unroll
             for (int k = 0; k < PER; ++k) most = fmaxf(most, x[k]);
             most = row_max<LANES>(most);
 #pragma unroll
-            for (int k = 0; k < PER; ++k) w[k] = exp_of(x[k] - most);
+            for (int k = 0; k < PER; ++k) to[k] = exp_of(x[k] - most);
         };
         auto add = [&]() {
             sum = 0.0f;
@@ -293,28 +309,22 @@ __device__ __forceinline__ double balance_rows(const RouterDesc &d, const Router
                 w[k] = __builtin_amdgcn_rcpf(1.0f + z);
                 q[k] = z * w[k];
             }
-            if (there < PER) {
+            if (there < at<LANES>(PER - 1) + 1) {
 #pragma unroll
-                for (int k = 0; k < PER; ++k) w[k] = k < there ? w[k] : 0.0f;
+                for (int k = 0; k < PER; ++k) w[k] = at<LANES>(k) < there ? w[k] : 0.0f;
             }
             add();
             // rows whose sigmoids all vanish in fp32: there sigma(x) is exp(x)
             const bool vanish = taking && sum < 1e-30f;
             if (__any(vanish)) {
-                float kept[PER], kept_sum = sum, kept_dot = dot;
+                float other[PER];
+                shifted(other);
 #pragma unroll
-                for (int k = 0; k < PER; ++k) kept[k] = w[k];
-                shifted();
+                for (int k = 0; k < PER; ++k) w[k] = vanish ? other[k] : w[k];
                 add();
-                if (!vanish) {
-                    sum = kept_sum;
-                    dot = kept_dot;
-#pragma unroll
-                    for (int k = 0; k < PER; ++k) w[k] = kept[k];
-                }
             }
         } else {
-            shifted();
+            shifted(w);
             add();
         }
         // a row without any score: no probability, no gradient
@@ -323,17 +333,17 @@ __device__ __forceinline__ double balance_rows(const RouterDesc &d, const Router
         if (taking && lane % LANES == 0) loss += static_cast<double>(dot) + (sum == 0.0f ? 0.0f : f.mean);
         if (inside && d.dlogits) {
             float g[PER];
-            const float scale = inv * grad_scale;
+            const float scale = inv * grad_scale, off = -dot * scale;
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
-                g[k] = w[k] * ((f.away[k] - dot) * scale);
+                g[k] = w[k] * __builtin_fmaf(f.away[k], scale, off);
                 if constexpr (SIGMOID) g[k] *= q[k];
             }
             if (!taking) {
 #pragma unroll
                 for (int k = 0; k < PER; ++k) g[k] = 0.0f;
             }
-            store_row<PER, BF16>(d.dlogits, static_cast<int64_t>(token) * d.dpitch + i0, there, g);
+            store_row<LANES, PER, BF16>(d.dlogits, static_cast<int64_t>(token) * d.dpitch + i0, there, g);
         }
     }
     return loss;
@@ -483,16 +493,19 @@ hipError_t launch_rows(const RouterTable &t, uint32_t blocks, const RouterCall &
 }
 hipError_t launch_any(const RouterTable &t, uint32_t blocks, const RouterCall &c, int experts, bool bf16, bool small,
                       hipStream_t st) {
+    if (experts <= 32) {
+        switch (router_lanes(experts)) {
+            case 1: return launch_rows<1, 8>(t, blocks, c, bf16, small, st);
+            case 2: return launch_rows<2, 8>(t, blocks, c, bf16, small, st);
+            default: return launch_rows<4, 8>(t, blocks, c, bf16, small, st);
+        }
+    }
     switch (router_lanes(experts)) {
-        case 1: return launch_rows<1, 8>(t, blocks, c, bf16, small, st);
-        case 2: return launch_rows<2, 8>(t, blocks, c, bf16, small, st);
-        case 4: return launch_rows<4, 8>(t, blocks, c, bf16, small, st);
-        case 8: return launch_rows<8, 8>(t, blocks, c, bf16, small, st);
-        case 16: return launch_rows<16, 8>(t, blocks, c, bf16, small, st);
-        case 32: return launch_rows<32, 8>(t, blocks, c, bf16, small, st);
-        default:
-            return experts <= 512 ? launch_rows<64, 8>(t, blocks, c, bf16, small, st)
-                                  : launch_rows<64, 16>(t, blocks, c, bf16, small, st);
+        case 4: return launch_rows<4, 16>(t, blocks, c, bf16, small, st);
+        case 8: return launch_rows<8, 16>(t, blocks, c, bf16, small, st);
+        case 16: return launch_rows<16, 16>(t, blocks, c, bf16, small, st);
+        case 32: return launch_rows<32, 16>(t, blocks, c, bf16, small, st);
+        default: return launch_rows<64, 16>(t, blocks, c, bf16, small, st);
     }
 }
 

@@ -42,10 +42,12 @@ constexpr int kSmallThreads = 1024;
 // workgroup's work each.
 constexpr int64_t kSmallLogits = 65536;
 
-// Lanes that share a row of `experts` logits, and how many each takes.
+// Lanes that share a row of `experts` logits: 8 of them each up to 32 experts, 16
+// above (which halves what a row costs beside its elements).
 inline int router_lanes(int experts) {
+    const int each = experts <= 32 ? 8 : 16;
     int lanes = 1;
-    while (lanes < 64 && lanes * 8 < experts) lanes *= 2;
+    while (lanes * each < experts) lanes *= 2;
     return lanes;
 }
 

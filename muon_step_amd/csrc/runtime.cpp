@@ -1929,7 +1929,7 @@ muon_status blocks_impl(muon_context *ctx, const muon_block_matrix *mats, int64_
 
 // Workgroups that the passes over choices and over logits aim at: two and six
 // for each CU (all of them resident at once).
-constexpr int64_t kCountWorkgroups = 512, kBalanceWorkgroups = 1536;
+constexpr int64_t kCountWorkgroups = 512, kBalanceWorkgroups = 1024;
 
 size_t router_words(const muon_router &r) { return static_cast<size_t>(r.sequences) * (r.experts + 1); }
 
@@ -2037,7 +2037,7 @@ muon_status router_balance_impl(muon_context *ctx, const muon_router *rs, int64_
     if (s != MUON_OK) return fail(ctx, s, "%s", msg);
     DeviceGuard guard(ctx->device);
     auto key = [&](int64_t i) {
-        return std::make_tuple(muon::router_lanes(rs[i].experts), rs[i].experts > 512, rs[i].dtype);
+        return std::make_tuple(muon::router_lanes(rs[i].experts), rs[i].experts > 32, rs[i].dtype);
     };
     std::vector<char> done(static_cast<size_t>(count), 0);
     for (int64_t i = 0; i < count; ++i) {
