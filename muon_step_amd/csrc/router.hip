@@ -156,8 +156,7 @@ template <int LANES, int PER, bool BF16> struct Row {
             if (left >= 8) {
 #pragma unroll
                 for (int k = 0; k < kEight; k += 4) {
-                    uint32_t v[4];
-                    load_words<4, BF16 ? 2 : 4>(place + 4 * k, v);
+                    const auto v = *(const typename Words<4, BF16 ? 2 : 4>::type __attribute__((address_space(1))) *)(place + 4 * k);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) w[s * kEight + k + q] = v[q];
                 }
