@@ -71,7 +71,7 @@ struct BlockScalars {
 };
 // The sum of squares' range of one part of a block.
 struct BlockPart {
-    uint32_t largest;  // bits of max |N|
+    uint32_t largest;  // bits of max |N|; of a NaN where N holds one
     int32_t shift;     // its Gram is that of N 2^-shift
 };
 struct BlockWork {
@@ -103,6 +103,8 @@ struct BlockChain {
     int32_t first, last;       // segment
     int32_t unit_rms, tall;
     float update;              // lr gamma sqrt(max(n, m)); unit RMS: lr gamma sqrt(n m)
+    float poly_scale;          // what P's fragments of the segment before are to be multiplied by
+    float out_scale;           // what this segment's are multiplied by, from what P leaves the last step as
     struct Step {
         float a, b, c;
         int32_t exp_in, exp_out;  // P 2^-exp is what enters and leaves the step as fp16 pairs

@@ -24,7 +24,7 @@ namespace {
 template <int T, int V, bool TALL, bool BF16, bool EVEN> struct Stream {
     static_assert(!TALL || V == 1, "a tall block's lane holds one column");
     static constexpr int kPhases = TALL ? 2 : 2 * T, kChunks = TALL ? T : 1;
-    static constexpr int kSlots = V == 4 ? 2 : V == 2 && T == 4 ? 4 : kPhases;
+    static constexpr int kSlots = V > 1 ? 2 : kPhases;
     static constexpr int kValues = 8 * kChunks * V;              // of a phase
     static constexpr int kGrads = BF16 && (TALL || V > 1) ? kValues / 2 : kValues;  // words of G
     static constexpr int kGSize = BF16 ? 2 : 4;
@@ -34,18 +34,26 @@ template <int T, int V, bool TALL, bool BF16, bool EVEN> struct Stream {
     uint32_t g[kSlots][kGrads];
     const Place &at;
     const BlockCall &c;
-    float factor;
-    int j, h, shift;
-    // wide: where the next phase's rows begin, and a lane's bytes behind a row's
-    // begin: in a whole group of eight rows, and for each b in the last, partial one
-    Bytes mom_row = nullptr, grad_row = nullptr, mom_first = nullptr, grad_first = nullptr;
-    int left = 0;  // rows from there to the block's end
-    uint32_t mom_lane = 0, grad_lane = 0, mom_part[4] = {}, grad_part[4] = {};
+    int j, h;
+    float from_mom, from_grad;  // N 2^shift = from_mom M + from_grad G
+    int left_shift = 0;         // what they could not hold of the shift
+    // wide: where the next group of eight rows begins, how many rows lie from there
+    // to the block's end, and the bytes from there to the lane's row 4 h + b and column
+    Bytes mom_row = nullptr, grad_row = nullptr;
+    int left = 0;
+    uint32_t mom_lane[4] = {}, grad_lane[4] = {};
     int64_t mom_at = 0, grad_at = 0;  // tall: the lane's row of memory
 
-    __device__ __forceinline__ Stream(const Place &place, const BlockCall &call, float f, int lane, int sh)
-        : at(place), c(call), factor(f), j(lane & 31), h(lane >> 5), shift(sh) {
-        if constexpr (!TALL && V > 1) lanes(V * j);
+    __device__ __forceinline__ Stream(const Place &place, const BlockCall &call, float factor, int lane, int shift)
+        : at(place), c(call), j(lane & 31), h(lane >> 5) {
+        // O and X need no more of N than 2^-24: scale and momentum go into one
+        // factor each.  Beyond 2^100 (an N near fp32's ends) the rest is applied behind.
+        const int held = min(max(shift, -100), 100);
+        left_shift = shift - held;
+        const float scale = __builtin_amdgcn_ldexpf(1.0f, held);
+        from_mom = (c.nesterov ? c.mu : 1.0f) * scale;
+        from_grad = c.nesterov ? factor * scale : 0.0f;
+        if constexpr (!TALL && V > 1) lanes(V * j, 8);
     }
     // Before the phases of columns x0 ..; `end`: the first column that is not there.
     __device__ __forceinline__ void begin(int x0, int end) {
@@ -54,11 +62,9 @@ template <int T, int V, bool TALL, bool BF16, bool EVEN> struct Stream {
             mom_at = row * at.mom_pitch;
             grad_at = row * at.grad_pitch;
         } else {
-            if constexpr (V == 1) lanes(min(j, end - 1 - x0));
-            mom_first = reinterpret_cast<Bytes>(at.mom + x0);
-            grad_first = at.grad + static_cast<int64_t>(x0) * kGSize;
-            mom_row = mom_first;
-            grad_row = grad_first;
+            if (V == 1 || c.s % 8 != 0) lanes(V > 1 ? V * j : min(j, end - 1 - x0), min(c.s, 8));
+            mom_row = reinterpret_cast<Bytes>(at.mom + x0);
+            grad_row = at.grad + static_cast<int64_t>(x0) * kGSize;
             left = c.s;
         }
     }
@@ -83,23 +89,24 @@ template <int T, int V, bool TALL, bool BF16, bool EVEN> struct Stream {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int i = TALL ? ((e >> 2) * 4 + (e & 3)) * T + sub : e * V + v;
-            float n = m[ph % kSlots][i];
-            if (c.nesterov) n = c.mu * n + grad_value(ph % kSlots, i) * factor;
-            x[e] = __builtin_amdgcn_ldexpf(n, shift);
+            x[e] = __builtin_fmaf(from_mom, m[ph % kSlots][i], from_grad * grad_value(ph % kSlots, i));
+        }
+        if (left_shift != 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_ldexpf(x[e], left_shift);
         }
         split_half(x, hi, lo);
     }
 
   private:
-    __device__ __forceinline__ void lanes(uint32_t col) {
+    // The lane's places in a group of which `rows` rows are there, others read as the last of these.
+    __device__ __forceinline__ void lanes(uint32_t col, int rows) {
         const uint32_t mp = static_cast<uint32_t>(at.mom_pitch), gp = static_cast<uint32_t>(at.grad_pitch);
-        mom_lane = (4 * h * mp + col) * 4;
-        grad_lane = (4 * h * gp + col) * kGSize;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const uint32_t row = min(4 * h + b, max((c.s & 7) - 1, 0));  // unused where s % 8 == 0
-            mom_part[b] = (row * mp + col) * 4;
-            grad_part[b] = (row * gp + col) * kGSize;
+            const uint32_t row = min(4 * h + b, rows - 1);
+            mom_lane[b] = (row * mp + col) * 4;
+            grad_lane[b] = (row * gp + col) * kGSize;
         }
     }
     // The next phase of the columns begun, into the slot of `ph`.
@@ -120,28 +127,28 @@ template <int T, int V, bool TALL, bool BF16, bool EVEN> struct Stream {
         } else {
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
-                const bool there = left > 0, full = (there ? left : c.s) >= 8;
-                const Bytes mr = there ? mom_row : mom_first, gr = there ? grad_row : grad_first;
+                const Bytes mp = mom_row, gp = grad_row;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     const int e = 4 * a + b;
-                    const Bytes mp = mr + (full ? b * at.mom_pitch * 4 : 0), gp = gr + (full ? b * at.grad_pitch * kGSize : 0);
-                    const uint32_t ml = full ? mom_lane : mom_part[b], gl = full ? grad_lane : grad_part[b];
                     if constexpr (V == 1) {
-                        m[k][e] = load_at<float>(mp, ml);
-                        g[k][e] = BF16 ? static_cast<uint32_t>(load_at<uint16_t>(gp, gl)) : load_at<uint32_t>(gp, gl);
+                        m[k][e] = load_at<float>(mp, mom_lane[b]);
+                        g[k][e] = BF16 ? static_cast<uint32_t>(load_at<uint16_t>(gp, grad_lane[b])) : load_at<uint32_t>(gp, grad_lane[b]);
                     } else {
-                        const auto v = load_at<typename WordsAt<V, 4>::type>(mp, ml);
-                        const auto u = load_at<typename WordsAt<BF16 ? V / 2 : V, kGSize>::type>(gp, gl);
+                        const auto v = load_at<typename WordsAt<V, 4>::type>(mp, mom_lane[b]);
+                        const auto u = load_at<typename WordsAt<BF16 ? V / 2 : V, kGSize>::type>(gp, grad_lane[b]);
 #pragma unroll
                         for (int i = 0; i < V; ++i) m[k][V * e + i] = __uint_as_float(v[i]);
 #pragma unroll
                         for (int i = 0; i < (BF16 ? V / 2 : V); ++i) g[k][(BF16 ? V / 2 : V) * e + i] = u[i];
                     }
                 }
-                mom_row += 8 * at.mom_pitch * 4;
-                grad_row += 8 * at.grad_pitch * kGSize;
-                left -= 8;
+                if (left > 8) {  // groups past the last one read that one again
+                    mom_row += 8 * at.mom_pitch * 4;
+                    grad_row += 8 * at.grad_pitch * kGSize;
+                    left -= 8;
+                    if (left < 8) lanes(mom_lane[0] / 4 - 4 * h * static_cast<uint32_t>(at.mom_pitch), left);
+                }
                 // the compiler would form every row's address ahead of the loop, and spill them
                 asm volatile("" : "+s"(mom_row), "+s"(grad_row), "+s"(left));
             }
@@ -228,10 +235,11 @@ __device__ __forceinline__ void times_poly(floatx16 (&acc)[V][T], Stream<T, V, T
     }
 }
 
-// Columns x0, x0 + stride, ... below `end` of a wave: the sum of X X^T, X = P N 2^shift scale.
+// Columns x0, x0 + stride, ... below `end` of a wave: the sum of X X^T, X = P N 2^shift
+// (the host scales P so that its entries suit fp16).
 template <int T, int V, bool TALL, bool BF16, bool EVEN>
 __device__ __forceinline__ void regram_columns(Triangle<T> &sum, Stream<T, V, TALL, BF16, EVEN> &in, const Poly<T> &poly, int lane,
-                                               float scale, int x0, int stride, int end) {
+                                               int x0, int stride, int end) {
     for (; x0 < end; x0 += stride) {
         floatx16 acc[V][T];
         times_poly<true>(acc, in, poly, lane, x0 + stride, end);
@@ -250,7 +258,7 @@ __device__ __forceinline__ void regram_columns(Triangle<T> &sum, Stream<T, V, TA
                 for (int i = 0; i < T; ++i) {
                     float x[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = acc[v][i][8 * q + e] * scale;
+                    for (int e = 0; e < 8; ++e) x[e] = acc[v][i][8 * q + e];
                     split_half(x, hi[i], lo[i]);
                 }
                 sum.add(hi, lo);
@@ -273,7 +281,7 @@ __global__ __launch_bounds__(kThreads) void blocks_regram_kernel(const BlockTabl
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int begin = part * c.part_len, end = min(begin + c.part_len, c.l);
     const BlockScalars k = c.w.scalars[block];
-    const float scale = c.poly_scale * k.inv_norm * kScaleX, factor = c.factor ? *c.factor : 1.0f;
+    const float factor = c.factor ? *c.factor : 1.0f;
     // whole units for all waves, V columns a lane; then what is left, one a lane
     const int whole = V == 1 ? begin : begin + (end - begin) / (V * kBlockUnit) * (V * kBlockUnit);
     Stream<T, V, TALL, BF16, EVEN> in(at, c, factor, lane, k.shift);
@@ -285,14 +293,14 @@ __global__ __launch_bounds__(kThreads) void blocks_regram_kernel(const BlockTabl
     sh.poly.load(c.w.poly + static_cast<int64_t>(block) * (T * T * 2048));
     __syncthreads();
     if constexpr (V > 1) {
-        regram_columns(sum, in, sh.poly, lane, scale, x0, V * kBlockUnit, whole);
+        regram_columns(sum, in, sh.poly, lane, x0, V * kBlockUnit, whole);
         if (x1 < end) {
             Stream<T, 1, TALL, BF16, EVEN> rest(at, c, factor, lane, k.shift);
             rest.start(x1, end);
-            regram_columns(sum, rest, sh.poly, lane, scale, x1, kBlockUnit, end);
+            regram_columns(sum, rest, sh.poly, lane, x1, kBlockUnit, end);
         }
     } else {
-        regram_columns(sum, in, sh.poly, lane, scale, x1, kBlockUnit, end);
+        regram_columns(sum, in, sh.poly, lane, x1, kBlockUnit, end);
     }
     __syncthreads();
     sum.reduce(c.w.gram + (static_cast<int64_t>(block) * c.parts + part) * tri(T) * 1024, sh.sums);
@@ -401,8 +409,12 @@ __device__ __forceinline__ void update_columns(Stream<T, V, TALL, BF16, EVEN> &i
     // the lane's place behind the begin of the first of eight rows
     const int64_t pp = at.param_pitch * kPSize, op = at.out_pitch * 4;
     const uint32_t across = N * j;
-    const uint32_t param_lane = 4 * h * static_cast<uint32_t>(pp) + across * kPSize;
-    const uint32_t out_lane = 4 * h * static_cast<uint32_t>(op) + across * 4;
+    uint32_t param_lane[4], out_lane[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        param_lane[b] = (4 * h + b) * static_cast<uint32_t>(pp) + across * kPSize;
+        out_lane[b] = (4 * h + b) * static_cast<uint32_t>(op) + across * 4;
+    }
     for (; x0 < end; x0 += stride) {
         // rows of memory from the first one to the end, and elements of a row from the lane's on
         const int rows = TALL ? end - x0 : u.c.s, there = (TALL ? u.c.s : end - x0) - static_cast<int>(across);
@@ -418,7 +430,7 @@ __device__ __forceinline__ void update_columns(Stream<T, V, TALL, BF16, EVEN> &i
             for (int q = 0; q < 4; ++q) {
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
-                    if (4 * h + b < ahead_left && there > 0) w[tile][q][b].load(ahead + b * pp, param_lane, whole, there);
+                    if (4 * h + b < ahead_left && there > 0) w[tile][q][b].load(ahead, param_lane[b], whole, there);
                 ahead += 8 * pp;
                 ahead_left -= 8;
                 asm volatile("" : "+s"(ahead), "+s"(ahead_left));
@@ -435,7 +447,7 @@ __device__ __forceinline__ void update_columns(Stream<T, V, TALL, BF16, EVEN> &i
 #pragma unroll
                     for (int e = 0; e < N; ++e) o[e] = (TALL ? acc[0][e][4 * q + b] : acc[e][tile][4 * q + b]) * u.scale;
                     if (4 * h + b < left && there > 0)
-                        w[tile][q][b].update(row + b * pp, param_lane, out ? out + b * op : nullptr, out_lane, whole, there, o,
+                        w[tile][q][b].update(row, param_lane[b], out, out_lane[b], whole, there, o,
                                                  u.c.decay, u.update);
                 }
                 row += 8 * pp;

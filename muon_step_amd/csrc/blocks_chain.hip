@@ -179,11 +179,12 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
             c.w.scalars[block] = out;
         }
     } else {
-        constexpr float unscale = 1.0f / (kScaleX * kScaleX);
+        // the sums are of P's fragments times N 2^shift
+        const float scale = c.poly_scale * c.w.scalars[block].inv_norm;
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) a.v[t][r] *= unscale;
+            for (int r = 0; r < 16; ++r) a.v[t][r] = a.v[t][r] * scale * scale;
     }
 
     // P: the identity, or what the segments before made it.  Its rows and columns
@@ -302,8 +303,8 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const float x = zero ? 0.0f : bad ? nan : p.v[t][r];
-            if (!c.last) own[(t * 16 + r) * 64 + lane] = x * whole;
-            sh.rows[32 * t + acc_row(r, h)][col] = x;
+            if (!c.last) as_global(own)[(t * 16 + r) * 64 + lane] = x * whole;
+            sh.rows[32 * t + acc_row(r, h)][col] = x * c.out_scale;
         }
     __syncthreads();
     half8 *frag = reinterpret_cast<half8 *>(c.w.poly) + block * (T * T * 256);

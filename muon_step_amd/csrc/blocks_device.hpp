@@ -57,8 +57,6 @@ __device__ __forceinline__ void split_bf(const float (&x)[8], bf16x8 &hi, bf16x8
 // Scales of the fp16 pairs: |A| <= 16, |Q| <= 60 and |A Q| <= 60 in the schedules
 // that the host admits, so A Q's product of scales, 1024, keeps it below 65504 too.
 constexpr float kScaleA = 64.0f, kScaleQ = 16.0f;
-// X of the second and later segments' Gram, |X| <= 4.
-constexpr float kScaleX = 8192.0f;
 
 // ---------------------------------------------------------------- places in memory
 

@@ -105,7 +105,6 @@ template <int T, bool TALL, bool BF16> struct Columns {
     }
     // N of a step's values, zero where there is nothing; M's new ones take the old ones' place.
     __device__ __forceinline__ void input(int step, float factor, float mu, bool nesterov, float (&n)[kValues]) {
-        const bool in = mine(s - 8 * step);
 #pragma unroll
         for (int k = 0; k < kValues; ++k) {
             float gf;
@@ -118,8 +117,12 @@ template <int T, bool TALL, bool BF16> struct Columns {
             gf *= factor;
             float &v = m[step][k];
             v = mu * v + gf;
-            const float x = nesterov ? mu * v + gf : v;
-            n[k] = in ? x : 0.0f;
+            n[k] = nesterov ? __builtin_fmaf(mu, v, gf) : v;  // for the sums alone: one rounding
+        }
+        if (TALL ? s < 32 * T : s < 8 * (step + 1)) {
+            const bool in = mine(s - 8 * step);
+#pragma unroll
+            for (int k = 0; k < kValues; ++k) n[k] = in ? n[k] : 0.0f;
         }
     }
     __device__ __forceinline__ void store(int step) {
@@ -184,11 +187,11 @@ __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTa
     const float factor = c.factor ? *c.factor : 1.0f;
     const float mu = c.mu;
     const bool nesterov = c.nesterov != 0;
-    uint32_t largest = 0;
+    float most = 0.0f;
     Triangle<T> sum;
     Columns<T, TALL, BF16> in(at, c.s, lane);
 
-    auto note = [&](float n) { largest = max(largest, __float_as_uint(n) & 0x7fffffffu); };
+    auto note = [&](float n) { most = fmaxf(most, fabsf(n)); };  // leaves NaNs out
 
     auto turn = [&](Turned<T> &to, int b, const float (&n)[4]) {
         bf16x4 hi, lo;
@@ -320,6 +323,7 @@ __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTa
     }
     // (the wave's next unit, so that every unit has one owner)
     for (; x0 < end; x0 += kBlockUnit) each(x0, false, 0);
+    uint32_t largest = __float_as_uint(most);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
         largest = max(largest, static_cast<uint32_t>(__shfl_xor(static_cast<int>(largest), off, 64)));
@@ -336,8 +340,15 @@ __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTa
         sum.clear();
         for (x0 = begin + 32 * wave; x0 < end; x0 += kBlockUnit) each(x0, true, shift);
     }
+    // sums in range: a NaN on their diagonal was one in N
+    bool spoilt = false;
+#pragma unroll
+    for (int k = 0; k < T; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) spoilt |= __builtin_isnan(sum.tile[tri(k) + k][r]);
+    spoilt = __syncthreads_or(spoilt) != 0;
+    if (spoilt) largest = 0x7fc00000u;
     const int64_t slot = static_cast<int64_t>(block) * c.parts + part;
-    __syncthreads();
     sum.reduce(c.w.gram + slot * tri(T) * 1024, sh.sums);
     if (threadIdx.x == 0) c.w.parts[slot] = BlockPart{largest, shift};
 }

@@ -1861,11 +1861,16 @@ muon_status run_block_table(muon_context *ctx, const muon::BlockTable &t, int64_
                 chain.step[i] = muon::BlockChain::Step{static_cast<float>(co.a), static_cast<float>(co.b),
                                                        static_cast<float>(co.c), plan.exp_in[seg.first + i], out};
             }
+            // P's fragments as P 2^-at: N 2^shift has a 2-norm of sqrt(s l) / 2 to sqrt(s l),
+            // and P N, with |X| <= 4, shall stay below fp16's largest value
+            const int at = std::max(out, static_cast<int>(std::ceil(0.5 * std::log2(static_cast<double>(g.s) * g.l))) - 13);
+            chain.poly_scale = c.poly_scale;
+            chain.out_scale = std::ldexp(1.0f, (seg.steps > 0 ? out : 0) - at);
             e = timed(ctx, ST_BLOCKS_CHAIN, static_cast<double>(now) * seg.steps * 3 * side * side * (side + 1), 0.0, st, [&] {
                 return muon::launch_blocks_chain(chain, static_cast<uint32_t>(now), st);
             });
             if (e != hipSuccess) return hip_fail(ctx, e, "block polynomial launch");
-            c.poly_scale = std::ldexp(1.0f, out);
+            c.poly_scale = std::ldexp(1.0f, at);
         }
         e = timed(ctx, ST_BLOCKS_UPDATE, elems * 2 * side, elems * (4.0 + gs + 2 * ps), st, [&] {
             return muon::launch_blocks_update(t, c, static_cast<uint32_t>(now), g.tall, gb, pb, st);
