@@ -45,6 +45,26 @@ inline double polynomial_bound(double c0, double c1, double c2, int power, doubl
     return best;
 }
 
+// Largest |x (a + b x^2 + c x^4)| on [0, top].
+inline double map_bound(double a, double b, double c, double top) {
+    auto value = [&](double l) { return std::fabs(std::sqrt(l) * (a + (b + c * l) * l)); };
+    const double end = top * top;
+    double best = value(end);
+    auto at = [&](double l) {
+        if (l > 0.0 && l < end) best = std::max(best, value(l));
+    };
+    if (c == 0.0) {  // roots of a + 3 b l + 5 c l^2
+        if (b != 0.0) at(-a / (3.0 * b));
+    } else {
+        const double d = 9.0 * b * b - 20.0 * a * c;
+        if (d >= 0.0) {
+            at((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+            at((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+        }
+    }
+    return best;
+}
+
 // The exponent e that brings magnitudes up to `bound` to 2^11 at most as x 2^-e.
 inline int pair_exponent(double bound) {
     return static_cast<int>(std::ceil(std::log2(std::max(bound, 0x1p-20)))) - 11;
@@ -59,14 +79,7 @@ inline BlockSchedule plan_blocks_schedule(const muon_ns_coeff *c, int n) {
         const double q = polynomial_bound(c[k].a, c[k].b, c[k].c, 0, top);
         const double r = polynomial_bound(c[k].a, c[k].b, c[k].c, 1, top);
         out.exp_in.push_back(pair_exponent(p));
-        // |X'|^2 = |lambda Q^2|: the bound of Q lambda times that of Q, and the map's own at its grid's points
-        double next = 0.0;
-        constexpr int kGrid = 4096;
-        for (int i = 0; i <= kGrid; ++i) {
-            const double s = x * i / kGrid, l = s * s;
-            next = std::max(next, std::fabs(s * (c[k].a + (c[k].b + c[k].c * l) * l)));
-        }
-        next *= 1.01;  // between the points
+        const double next = map_bound(c[k].a, c[k].b, c[k].c, x);
         p *= q;
         if (!(q <= 60.0 && r <= 60.0 && next <= 3.9 && p <= 0x1p60)) return out;
         x = std::max(next, 0x1p-20);
