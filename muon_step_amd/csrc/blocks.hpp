@@ -75,7 +75,7 @@ struct BlockPart {
     int32_t shift;     // its Gram is that of N 2^-shift
 };
 struct BlockWork {
-    float *gram;           // [block][part][tile][32 x 32], the lower triangle's tiles
+    float *gram;           // [block][part][tile], the lower triangle's tiles as lanes hold them
     BlockPart *parts;      // [block][part]
     _Float16 *poly;        // [block]: P's rows as operand fragments, hi then lo
     float *poly_own;       // [block]: P's columns as the chain holds them

@@ -120,25 +120,18 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
         for (int r = 0; r < 16; ++r) a.v[t][r] = 0.0f;
     auto add_parts = [&](int first, auto count) {
         constexpr int N = count.value;
-        float v[N][T][16], weight[N];
+        floatx4 v[N][T][4];
+        float weight[N];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const float *g = c.w.gram + (block * c.parts + first + n) * tri(T) * 1024;
+            const float *g = c.w.gram + (block * c.parts + first + n) * tri(T) * 1024 + 4 * lane;
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
+            for (int t = 0; t < T; ++t)
                 if (t >= wave) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) v[n][t][r] = as_global(g)[(tri(t) + wave) * 1024 + acc_row(r, h) * 32 + j];
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const floatx4 u = *(const floatx4 __attribute__((address_space(1))) *)(
-                            g + (tri(wave) + t) * 1024 + j * 32 + 8 * q + 4 * h);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[n][t][4 * q + e] = u[e];
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        v[n][t][q] = *(const floatx4 __attribute__((address_space(1))) *)(g + (tri(t) + wave) * 1024 + 256 * q);
                 }
-            }
             weight[n] = 1.0f;
             if (c.first) weight[n] = parts[first + n].largest == 0 ? 0.0f : ldexpf(1.0f, 2 * (parts[first + n].shift - common));
         }
@@ -146,13 +139,30 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int t = 0; t < T; ++t)
+                if (t >= wave) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) a.v[t][r] = __builtin_fmaf(weight[n], v[n][t][r], a.v[t][r]);
+                    for (int r = 0; r < 16; ++r) a.v[t][r] = __builtin_fmaf(weight[n], v[n][t][r >> 2][r & 3], a.v[t][r]);
+                }
     };
     // some parts' loads at once
     int k = 0;
     for (; k + 4 <= c.parts; k += 4) add_parts(k, std::integral_constant<int, 4>{});
     for (; k < c.parts; ++k) add_parts(k, std::integral_constant<int, 1>{});
+    // the tiles above the diagonal, from the waves that hold their mirror images
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        if (t > wave) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sh.rows[32 * t + acc_row(r, h)][col] = a.v[t][r];
+        }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        if (t < wave) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) a.v[t][r] = sh.rows[col][32 * t + acc_row(r, h)];
+        }
+    __syncthreads();
     if (c.first) {
         float trace = 0.0f;
 #pragma unroll

@@ -12,7 +12,7 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef __fp16 fp16x2_t __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4;  // of a streaming workgroup
+constexpr int kWaves = 4;  // of a streaming workgroup (sum_tile adds up as many)
 constexpr int kThreads = kWaves * 64;
 
 constexpr int tri(int t) { return t * (t + 1) / 2; }
@@ -105,18 +105,23 @@ template <int N, int A> struct WordsAt {
     typedef uint32_t type __attribute__((ext_vector_type(N), aligned(A)));
 };
 
-// Sum of a value over the waves of a workgroup, 1024 values of each, to dst: `put`
-// writes a wave's own to the buffer it is given.  k alternates between two buffers
-// of sh (4 KB for each wave each), so that one barrier a tile suffices.
-template <class F> __device__ __forceinline__ void sum_tile(float *dst, float *sh, int k, F put) {
-    const int wave = threadIdx.x >> 6;
+// Sum of a tile over the waves of a workgroup to dst, as its lanes hold it (four
+// rows of a column a lane: register 4 q + e of lane i at 256 q + 4 i + e).  k
+// alternates between two buffers of sh (4 KB for each wave each), so that one
+// barrier a tile suffices.
+__device__ __forceinline__ void sum_tile(float *dst, float *sh, int k, const floatx16 &tile) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     float *buf = sh + (k & 1) * kWaves * 1024;
-    put(buf + wave * 1024);
-    __syncthreads();
-    floatx4 v = *reinterpret_cast<const floatx4 *>(buf + threadIdx.x * 4);
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const floatx4 *>(buf + w * 1024 + threadIdx.x * 4);
-    *(floatx4 __attribute__((address_space(1))) *)(dst + threadIdx.x * 4) = v;
+    for (int r = 0; r < 16; ++r) buf[wave * 1024 + r * 64 + lane] = tile[r];
+    __syncthreads();
+    floatx4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float *x = buf + (4 * wave + e) * 64 + lane;
+        v[e] = ((x[0] + x[1024]) + x[2048]) + x[3072];
+    }
+    *(floatx4 __attribute__((address_space(1))) *)(dst + 256 * wave + 4 * lane) = v;
 }
 
 // The lower triangle's 32 x 32 tiles of a sum of X X^T over columns of X, from
@@ -141,15 +146,10 @@ template <int T> struct Triangle {
                     t = mfma(k == 2 ? lo[i] : hi[i], k == 1 ? lo[j] : hi[j], t);
                 }
     }
-    // The workgroup's sum, row-major tile by tile, to dst; entered behind a barrier.
+    // The workgroup's sum to dst, tile by tile; entered behind a barrier.
     __device__ __forceinline__ void reduce(float *dst, float *sh) const {
-        const int lane = threadIdx.x & 63;
 #pragma unroll
-        for (int k = 0; k < tri(T); ++k)
-            sum_tile(dst + k * 1024, sh, k, [&](float *buf) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) buf[acc_row(r, lane >> 5) * 32 + (lane & 31)] = tile[k][r];
-            });
+        for (int k = 0; k < tri(T); ++k) sum_tile(dst + k * 1024, sh, k, tile[k]);
     }
 };
 

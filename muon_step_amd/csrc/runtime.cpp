@@ -1756,8 +1756,8 @@ muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage,
 // ---- muon_blocks_step
 
 // Blocks with this many parts of their long side in all fill the card: 512
-// workgroups, two for each CU.
-constexpr int64_t kBlockWorkgroups = 512;
+// workgroups, one for each CU.
+constexpr int64_t kBlockWorkgroups = 256;
 constexpr int64_t kMaxBlockParts = 32;
 // What the blocks of one launch may hold in the context.
 constexpr size_t kBlockMemory = size_t(256) << 20;
