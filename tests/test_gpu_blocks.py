@@ -173,3 +173,196 @@ def test_spread_spectra(ctx, s, l):
     weights = [Weight(rng, (2, 1), (s, l), "bf16", "bf16", "spread"), Weight(rng, (1, 2), (l, s), "f32", "bf16", "spread")]
     step(ctx, weights)
     say(s, l, ["%.2e" % w.check(SPREAD) for w in weights])
+
+
+@pytest.mark.parametrize("columns", [False, True])
+def test_schedules_and_modes(ctx, columns):
+    """Schedules of none, one and more steps than a segment; plain momentum; updates scaled by their own RMS; a factor."""
+    import torch
+    rng = np.random.default_rng(7)
+    block, grid = ((700, 72), (1, 2)) if columns else ((72, 700), (2, 1))
+    for coeffs in ([], [(1.5, -0.5, 0.0)], [(2.0, -1.5, 0.5)] * 20, QUINTIC, [(3.4445, -4.7750, 2.0315)] * 12):
+        for unit_rms in (False, True):
+            w = Weight(rng, grid, block, "f32", "f32")
+            step(ctx, [w], coeffs=coeffs, scale_mode=ms.MUON_SCALE_UNIT_RMS if unit_rms else ms.MUON_SCALE_SQRT_MAX)
+            w.check(WELL, coeffs=coeffs, unit_rms=unit_rms)
+    w = Weight(rng, grid, block, "bf16", "bf16")
+    step(ctx, [w], nesterov=False)
+    w.check(WELL, nesterov=False)
+    factor = torch.full((1,), 0.37, device="cuda")
+    w = Weight(rng, grid, block, "bf16", "bf16")
+    step(ctx, [w], grad_factor=factor)
+    w.check(WELL, factor=float(factor))
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-14, 1e12, 1e20, 1e30])
+def test_scale_does_not_matter(ctx, scale):
+    """From gradients whose squares vanish in fp32 to ones whose squares overflow it, whole and ragged blocks."""
+    rng = np.random.default_rng(9)
+    weights = [Weight(rng, (2, 1), (64, 384), "f32", "f32", scale=scale),
+               Weight(rng, (1, 2), (333, 50), "f32", "f32", scale=scale)]
+    step(ctx, weights)
+    for w in weights:
+        w.check(WELL if scale > 1e-37 else 5e-3)  # at 1e-38 N itself has as few as 18 bits left: 2^-18 x what a step grows
+
+
+def test_parts_of_different_scale(ctx):
+    """A block most of whose columns are so small that their squares vanish, and some zero: they add nothing that counts."""
+    rng = np.random.default_rng(10)
+    w = Weight(rng, (1, 1), (64, 4096), "f32", "f32")
+    for name in ("grad", "momentum"):
+        w.dev[name][:, 256:2048] *= 1e-30
+        w.dev[name][:, 2048:] = 0
+        w.before[name] = w.dev[name].cpu().numpy()
+    step(ctx, [w])
+    w.check(WELL)
+
+
+@pytest.mark.parametrize("columns", [False, True])
+def test_empty_and_spoilt_blocks(ctx, columns):
+    """A block of zeros decays; one with an infinity or a NaN becomes NaN as a whole; their neighbours are as ever."""
+    rng = np.random.default_rng(11)
+    s, l = 48, 300
+    block, grid = ((l, s), (1, 5)) if columns else ((s, l), (5, 1))
+    w = Weight(rng, grid, block, "f32", "bf16")
+
+    def at(k):
+        return (slice(None), slice(k * s, (k + 1) * s)) if columns else (slice(k * s, (k + 1) * s), slice(None))
+
+    for name in ("grad", "momentum"):
+        w.dev[name][at(1)] = 0
+    spot = lambda k: (7, k * s + 3) if columns else (k * s + 3, 7)  # noqa: E731
+    w.dev["grad"][spot(2)] = float("inf")
+    w.dev["momentum"][spot(3)] = float("nan")
+    w.before = {k: t.float().cpu().numpy() for k, t in w.dev.items()}
+    step(ctx, [w])
+    skip = {(0, k) if columns else (k, 0) for k in (1, 2, 3)}
+    with np.errstate(all="ignore"):
+        w.check(WELL, skip=skip)
+    import oracle
+    got = w.got("param")
+    assert np.isnan(got[at(2)]).all() and np.isnan(got[at(3)]).all()
+    assert np.isnan(w.got("ns_out")[at(2)]).all() and np.isnan(w.got("ns_out")[at(3)]).all()
+    zero = np.zeros_like(w.before["param"][at(1)])
+    assert_bitexact(got[at(1)], oracle.apply_update_f32(w.before["param"][at(1)], zero, LR, WD, GAMMA, False), "decay")
+    # all of N a NaN, and unit RMS of zeros
+    for value, mode in ((float("nan"), ms.MUON_SCALE_SQRT_MAX), (0.0, ms.MUON_SCALE_UNIT_RMS)):
+        w = Weight(rng, (1, 1), (16, 100), "f32", "f32")
+        for name in ("grad", "momentum"):
+            w.dev[name][:] = value
+        step(ctx, [w], scale_mode=mode)
+        got = w.got("param")
+        assert np.isnan(got).all() if value != 0 else np.array_equal(got, np.float32(1 - LR * WD) * w.before["param"])
+
+
+def test_block_does_not_depend_on_the_others(ctx):
+    """70 weights in one call (more than one launch holds) of three shapes, each weight alone, in other orders, in a
+    context with little memory, and again: the same bits."""
+    import torch
+    rng = np.random.default_rng(12)
+    shapes = [((2, 2), (24, 160)), ((1, 3), (200, 40)), ((3, 1), (128, 130))]
+    weights = [Weight(rng, *shapes[k % 3], "bf16", "bf16") for k in range(70 * 3)]
+    start = [{k: t.clone() for k, t in w.dev.items()} for w in weights]
+
+    def again(how):
+        for w, s in zip(weights, start):
+            for k, t in w.dev.items():
+                t.copy_(s[k])
+        how()
+        torch.cuda.synchronize()
+        return [{k: t.clone() for k, t in w.dev.items()} for w in weights]
+
+    ref = again(lambda: step(ctx, weights))
+    small = ms.Context(0, workspace_cap_bytes=3 << 20)
+    for how in (lambda: step(ctx, weights), lambda: step(ctx, weights[::-1]), lambda: [step(ctx, [w]) for w in weights],
+                lambda: step(small, weights)):
+        out = again(how)
+        # how long columns are split goes by the number of blocks: sums in another order, O by less than WELL
+        for a, b in zip(ref, out):
+            assert torch.equal(a["momentum"], b["momentum"])
+            assert float((a["ns_out"] - b["ns_out"]).norm()) <= WELL * float(a["ns_out"].norm())
+    same = again(lambda: step(ctx, weights))
+    for a, b in zip(ref, same):
+        assert all(torch.equal(a[k], b[k]) for k in a), "two calls alike"
+    small.close()
+
+
+def test_other_stream_and_graph(ctx):
+    """On a stream of its own, and captured: replays step as eager calls do, other work in between."""
+    import torch
+    rng = np.random.default_rng(13)
+    mine = ms.Context(0)
+    a, b = (Weight(np.random.default_rng(13), (2, 2), (40, 200), "bf16", "bf16") for _ in range(2))
+    hp = ms.make_hparams(lr=LR, momentum=MU, weight_decay=WD, gamma=GAMMA)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(ms.MuonError) as e, torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+        mine.muon_blocks_step([b.item()], hp, stream=torch.cuda.current_stream())
+    assert e.value.status == 2
+    with torch.cuda.stream(side):
+        mine.muon_blocks_step([a.item()], hp)
+        mine.muon_blocks_step([b.item()], hp)
+    side.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        mine.muon_blocks_step([b.item()], hp, stream=torch.cuda.current_stream())
+    other = Weight(rng, (9, 1), (128, 3000), "f32", "f32")  # grows the context's memory: the graph keeps its own
+    for turn in range(4):
+        mine.muon_blocks_step([a.item()], hp)
+        torch.cuda.synchronize()
+        if turn == 1:
+            step(mine, [other])
+            other.check(WELL)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in a.dev:
+            assert torch.equal(a.dev[name], b.dev[name]), (turn, name)
+    mine.close()
+
+
+def test_interleaved_and_fused_views(ctx):
+    """Slices of the columns of one buffer as weights of their own, and a fused weight whose slices have other blocks."""
+    import torch
+    rng = np.random.default_rng(14)
+    base = {k: torch.from_numpy(rng.standard_normal((192, 320)).astype(np.float32)).cuda() for k in ("param", "grad", "momentum")}
+    whole = {k: t.clone() for k, t in base.items()}
+    hp = ms.make_hparams(lr=LR, momentum=MU, weight_decay=WD, gamma=GAMMA)
+
+    def items(d):
+        left = [d[k][:, :128] for k in ("param", "grad", "momentum")]
+        right = [d[k][:, 128:] for k in ("param", "grad", "momentum")]
+        return [ms.block_matrix(*left, 192, 64), ms.block_matrix(*right, 64, 192)]
+
+    ctx.muon_blocks_step(items(base), hp)
+    for it in items(whole):
+        ctx.muon_blocks_step([it], hp)
+    torch.cuda.synchronize()
+    assert torch.equal(base["momentum"], whole["momentum"])
+    n = (np.float32(MU) * base["momentum"].cpu().numpy() + base["grad"].cpu().numpy()).astype(np.float64)
+    scale = LR * GAMMA
+    for rows, cols in [(slice(None), slice(0, 64)), (slice(None), slice(64, 128))] + [(slice(64 * k, 64 * k + 64), slice(128, 320)) for k in range(3)]:
+        o = exact_o(n[rows, cols])
+        moved = (1 - LR * WD) * 0 + (whole["param"][rows, cols] - base["param"][rows, cols]).cpu().numpy()
+        assert np.abs(moved).max() <= 2 * WELL * scale * math.sqrt(192) * np.abs(o).max() * 8
+
+
+def test_matches_muon_step(ctx):
+    """A contiguous weight that is one block: muon_step's momentum bit for bit, its update within that step's 2e-2."""
+    import torch
+    rng = np.random.default_rng(15)
+    w = Weight(rng, (1, 1), (96, 640), "bf16", "bf16")
+    p, g, m, o = (w.view(k).clone() for k in ("param", "grad", "momentum", "ns_out"))
+    step(ctx, [w])
+    ctx.muon_step([ms.matrix(p, g, m, o)], ms.make_hparams(lr=LR, momentum=MU, weight_decay=WD, gamma=GAMMA))
+    torch.cuda.synchronize()
+    assert torch.equal(m, w.view("momentum"))
+    assert float((o - w.view("ns_out")).norm()) <= 2e-2 * float(o.norm())
+
+
+def test_long_side_past_a_launch(ctx):
+    """One block of 65537 columns, and one of as many rows: 32 parts and a last column of its own."""
+    rng = np.random.default_rng(16)
+    weights = [Weight(rng, (1, 1), (20, 65537), "bf16", "bf16", gap=1), Weight(rng, (1, 1), (65537, 20), "bf16", "f32", gap=3)]
+    step(ctx, weights)
+    for w in weights:
+        w.check(WELL)
