@@ -49,7 +49,8 @@ __device__ __forceinline__ int wave_sequence_of(const RouterDesc &d, int token) 
     while (n > 1) {
         const int width = (n + 63) / 64, at = lo + static_cast<int>(threadIdx.x & 63) * width;
         const bool begun = at < lo + n && as_global(d.offsets)[at] <= token;
-        const int k = max(__popcll(__ballot(begun)) - 1, 0);
+        // the count is unsigned: where no place has begun, one less would be the largest of all
+        const int k = max(static_cast<int>(__popcll(__ballot(begun))) - 1, 0);
         n = min(width, n - k * width);
         lo += k * width;
     }
@@ -303,8 +304,9 @@ __device__ __forceinline__ double balance_rows(const RouterDesc &d, const Router
         if constexpr (SIGMOID) {
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
-                // sigma and 1 - sigma, each without cancellation; past x = -87.5 sigma is held at 1e-38
-                const float z = fminf(exp_of(-x[k]), 1e38f);
+                // sigma and 1 - sigma, each without cancellation; past x = -87.2 sigma is held at 1.25e-38:
+                // v_rcp_f32 gives zero for what lies below the smallest normal number, 1.18e-38
+                const float e = exp_of(-x[k]), z = e > 8e37f ? 8e37f : e;  // a NaN stays one
                 w[k] = __builtin_amdgcn_rcpf(1.0f + z);
                 q[k] = z * w[k];
             }

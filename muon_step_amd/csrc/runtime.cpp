@@ -950,8 +950,9 @@ struct muon_context {
     DevBuf call_nrm2; // per call matrix
     DevBuf mat_desc;  // MatDesc table
     DevBuf adamw_desc;
-    DevBuf routers;   // muon_router_balance's counts, zero between calls, and sums
+    DevBuf routers;   // muon_router_balance's counts, zero between calls: captured calls rely on that
     size_t routers_clear = 0;  // words of it that are zero
+    DevBuf router_sums;
     DevBuf blocks;    // muon_blocks_step's sums, polynomials and scalars
     std::vector<void *> retired;  // buffers that graphs may hold, and calls no longer
     // muon_grad_norm's sums: of a fixed size and there from creation on, so that
@@ -1986,16 +1987,16 @@ muon_status run_router_table(muon_context *ctx, const muon_router *const *rs, in
     const int64_t turn = muon::kRouterThreads / lanes;  // rows that a workgroup takes at once
     const int64_t per_balance = round_up(std::max<int64_t>(1, (tokens + kBalanceWorkgroups - 1) / kBalanceWorkgroups), turn);
     const int64_t per_count = std::max<int64_t>(64, (tokens + kCountWorkgroups - 1) / kCountWorkgroups);
-    const size_t hist_bytes = align_up(words * 4), sums_bytes = (static_cast<size_t>(tokens / per_balance) + n) * 8;
     const bool graph = capturing(st);
     const void *before = ctx->routers.p;
-    muon_status s = ensure(ctx, ctx->routers, hist_bytes + sums_bytes, "router workspace", graph);
+    muon_status s = ensure(ctx, ctx->routers, words * 4, "router counts", graph);
     if (ctx->routers.p != before) ctx->routers_clear = 0;
     if (s != MUON_OK) return s;
+    s = ensure(ctx, ctx->router_sums, (static_cast<size_t>(tokens / per_balance) + n) * 8, "router workspace", graph);
+    if (s != MUON_OK) return s;
     uint32_t *hist = static_cast<uint32_t *>(ctx->routers.p);
-    double *sums = reinterpret_cast<double *>(static_cast<char *>(ctx->routers.p) + hist_bytes);
-    // sums of an earlier call with fewer counts may lie in what are counts now
-    const size_t clear = std::min(ctx->routers_clear, words);
+    double *sums = static_cast<double *>(ctx->router_sums.p);
+    const size_t clear = ctx->routers_clear;
     ctx->routers_clear = 0;  // until everything is enqueued
     if (clear < words) {
         const hipError_t e = muon::launch_router_clear(hist + clear, static_cast<int64_t>(words - clear), st);
@@ -2031,7 +2032,7 @@ muon_status run_router_table(muon_context *ctx, const muon_router *const *rs, in
               [&] { return muon::launch_router_finish(t, n, blocks, c, st); });
     if (e != hipSuccess) return hip_fail(ctx, e, "router finish launch");
     // a capture has only recorded that the counts are left at zero
-    ctx->routers_clear = graph ? clear : words;
+    ctx->routers_clear = graph ? clear : std::max(clear, words);
     return MUON_OK;
 }
 
@@ -2238,7 +2239,8 @@ muon_status muon_destroy(muon_context *ctx) {
     if (!ctx) return MUON_OK;
     DeviceGuard guard(ctx->device);
     (void)hipDeviceSynchronize();
-    for (DevBuf *b : {&ctx->ws, &ctx->tabs, &ctx->call_nrm2, &ctx->mat_desc, &ctx->adamw_desc, &ctx->blocks, &ctx->routers})
+    for (DevBuf *b : {&ctx->ws, &ctx->tabs, &ctx->call_nrm2, &ctx->mat_desc, &ctx->adamw_desc, &ctx->blocks, &ctx->routers,
+                      &ctx->router_sums})
         if (b->p) (void)hipFree(b->p);
     for (void *p : ctx->retired) (void)hipFree(p);
     if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);

@@ -151,3 +151,181 @@ def test_many_short_sequences(ctx):
     b = Batch(rng, offsets[-1], 300, 3, offsets=offsets, dtype="f32")
     run(ctx, [b])
     b.check()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("experts", [8, 64, 100, 256])
+def test_long_batches(ctx, experts, dtype, score):
+    """Past what one workgroup takes: counted, balanced and finished by many; uneven sequences, mask, rows with gaps."""
+    rng = np.random.default_rng(experts + 1)
+    tokens = 20011
+    offsets = [3, 9, 9, 5000, 5001, 12345, 20000]
+    b = Batch(rng, tokens, experts, 6, offsets=offsets, score=score, dtype=dtype, mask=True, gap=5, drop=0.05)
+    run(ctx, [b], score)
+    say(experts, dtype, score, "%.2f of the bound" % b.check())
+
+
+def test_accumulate_scale_and_no_gradient(ctx):
+    import torch
+    rng = np.random.default_rng(21)
+    for tokens in (200, 9000):
+        b = Batch(rng, tokens, 48, 4)
+        scale = torch.full((1,), -3.5, device="cuda")
+        run(ctx, [b], accumulate=True, grad_scale=scale)
+        loss, counts, grad, bound, _ = oracle(b.x, b.chosen, b.offsets, b.mask, "softmax", -3.5)
+        assert np.array_equal(b.counts.cpu().numpy(), counts + 7)
+        assert (np.abs(b.dfull.cpu().numpy() - grad) <= 2.0 ** -16 * np.abs(bound) + 2.0 ** -24 * np.abs(grad)).all()
+        run(ctx, [b], accumulate=True, grad_scale=scale)
+        assert np.array_equal(b.counts.cpu().numpy(), 2 * counts + 7)
+        kept = b.dfull.clone()
+        b.loss.zero_()
+        run(ctx, [b], grads=False)
+        assert torch.equal(kept, b.dfull) and abs(float(b.loss) - loss) <= 2.0 ** -17 * loss
+        assert np.array_equal(b.counts.cpu().numpy(), counts)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("tokens", [64, 9000])
+def test_infinities_and_vanishing_rows(ctx, tokens, score):
+    """Experts that cannot be reached (-infinity, the type's lowest value), rows of nothing else, rows whose sigmoids vanish,
+    large logits; masked rows hold NaN and infinities."""
+    import torch
+    rng = np.random.default_rng(22)
+    experts = 40
+    x = rng.standard_normal((tokens, experts)) * 3
+    x[::7, 3:20] = -np.inf
+    x[1::7] = -np.inf
+    x[2::7] -= 95.0
+    x[3::7, 5] = 60.0
+    x[4::7, :30] = np.finfo(np.float32).min
+    b = Batch(rng, tokens, experts, 4, score=score, mask=True, logits=x)
+    b.mask[:] = True
+    b.mask[5::7] = False
+    b.dev_mask.copy_(torch.from_numpy(b.mask))
+    b.full[5::7] = float("nan")
+    b.full[12::14] = float("inf")
+    run(ctx, [b], score)
+    b.x[5::7] = 0.0
+    b.check()
+    assert bool((b.dfull[5::7] == 0).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("tokens", [64, 9000])
+def test_nan_rows(ctx, tokens, score):
+    """A NaN logit makes its row of the gradient and the loss NaN, no other row and no count."""
+    rng = np.random.default_rng(23)
+    b, ref = (Batch(np.random.default_rng(23), tokens, 32, 3, score=score) for _ in range(2))
+    del rng
+    b.full[11, 4] = float("nan")
+    run(ctx, [b, ref], score)
+    assert np.isnan(float(b.loss)) and not np.isnan(float(ref.loss))
+    got, want = b.dfull.cpu().numpy(), ref.dfull.cpu().numpy()
+    assert np.isnan(got[11]).all()
+    got[11] = want[11]
+    assert np.array_equal(got, want) and np.array_equal(b.counts.cpu().numpy(), ref.counts.cpu().numpy())
+
+
+def test_gradient_against_differences(ctx):
+    """Central differences of the loss itself: exact loss in 64 bits at x +- h, h^2 / 6 of its third derivative below
+    2^-14 of the gradient's terms for h = 2^-7."""
+    rng = np.random.default_rng(24)
+    for score in ("softmax", "sigmoid"):
+        b = Batch(rng, 12, 10, 3, offsets=[0, 5, 12], score=score)
+        run(ctx, [b], score)
+        grad, h = b.dfull.cpu().numpy(), 2.0 ** -7
+        bound = oracle(b.x, b.chosen, b.offsets, b.mask, score)[3]
+        for t, i in [(0, 0), (3, 7), (5, 2), (11, 9)]:
+            loss = []
+            for sign in (1, -1):
+                x = b.x.astype(np.float64)
+                x[t, i] += sign * h
+                loss.append(oracle(x, b.chosen, b.offsets, b.mask, score)[0])
+            assert abs((loss[0] - loss[1]) / (2 * h) - grad[t, i]) <= 2.0 ** -13 * bound[t, i] + 2.0 ** -16 * bound[t, i]
+
+
+def test_many_routers_and_no_tokens(ctx):
+    """More routers than a launch holds, of several widths, types and lengths, some without tokens; as alone."""
+    import torch
+    rng = np.random.default_rng(25)
+    batches = []
+    for k in range(75):
+        tokens = [0, 40, 3000, 5000][k % 4]
+        batches.append(Batch(rng, tokens, [16, 64, 33][k % 3], 4, dtype=["f32", "bf16"][k % 2]))
+    run(ctx, batches)
+    for b in batches:
+        b.check()
+        assert b.x.shape[0] or (float(b.loss) == 0 and int(b.counts.sum()) == 0)
+    before = [(b.dfull.clone(), b.loss.clone()) for b in batches]
+    for b in batches:
+        run(ctx, [b])
+    for b, (g, loss) in zip(batches, before):
+        # how tokens are spread over workgroups goes by their number: the loss's sums in another order
+        assert torch.equal(b.dfull, g) and abs(float(b.loss) - float(loss)) <= 2.0 ** -23 * abs(float(loss))
+
+
+def test_other_stream_and_graph(ctx):
+    """Captured and replayed with eager calls of other sizes in between, small and long batches."""
+    import torch
+    mine = ms.Context(0)
+    for tokens in (100, 9000):
+        rng = np.random.default_rng(26)
+        b = Batch(rng, tokens, 64, 4, offsets=[0, tokens // 3, tokens], mask=True)
+        long = Batch(rng, 30000, 80, 4)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        hp = ms.balance_hparams(COEF)
+        with torch.cuda.stream(side):
+            mine.muon_router_balance([b.item()], hp)
+        side.synchronize()
+        b.check()
+        want = b.dfull.clone(), b.loss.clone(), b.counts.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            mine.muon_router_balance([b.item()], hp, stream=torch.cuda.current_stream())
+        for turn in range(4):
+            for t in (b.dfull[:, :64], b.loss, b.counts):
+                t.zero_()
+            if turn % 2:
+                run(mine, [long])
+                long.check()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip((b.dfull, b.loss, b.counts), want)), turn
+    mine.close()
+
+
+def test_offsets_that_are_no_offsets(ctx):
+    """Past the tokens, in front of them, descending: nothing outside the buffers is touched, whatever the result."""
+    import torch
+    rng = np.random.default_rng(27)
+    for tokens in (100, 9000):
+        for offsets in ([-50, 2 ** 31 - 1], [tokens, 0], [5, 3, -7, tokens + 9], [2 ** 31 - 1, -2 ** 31]):
+            b = Batch(rng, tokens, 16, 2, offsets=offsets)
+            run(ctx, [b])
+            assert torch.equal(b.full.cpu(), torch.from_numpy(b.x))
+    b = Batch(rng, 500, 16, 2)
+    run(ctx, [b])
+    b.check()
+
+
+@pytest.mark.parametrize("experts", [1, 3, 64, 300, 5000])
+def test_bias_step(ctx, experts):
+    import torch
+    rng = np.random.default_rng(experts)
+    items, want, biases = [], [], []
+    for k in range(130 if experts == 64 else 3):
+        counts = rng.integers(0, 5, experts) * 10 ** rng.integers(0, 12)
+        if k % 3 == 1:
+            counts[:] = 7
+        bias = rng.standard_normal(experts).astype(np.float32)
+        t = torch.from_numpy(bias).cuda()
+        biases.append(t)
+        items.append(ms.router_bias(t, torch.from_numpy(counts.astype(np.int64)).cuda()))
+        sign = [(experts * int(c) > int(counts.sum())) - (experts * int(c) < int(counts.sum())) for c in counts]
+        want.append(bias - np.float32(1e-3) * np.array(sign, np.float32))
+    ctx.muon_router_bias_step(items, 1e-3)
+    torch.cuda.synchronize()
+    for t, w in zip(biases, want):
+        assert np.array_equal(t.cpu().numpy(), w)
