@@ -274,8 +274,8 @@ typedef enum muon_score { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_
  *   counts   device int64, experts: the choices of each expert in all sequences,
  *            written, or added to (accumulate)
  *   loss     device float, written
- * experts is 1 .. 1024, top_k 1 .. 64, tokens below 2^31 and tokens x top_k
- * below 2^32; with tokens 0 logits, dlogits, chosen and mask are not looked at.
+ * experts is 1 .. 1024, top_k 1 .. 64, tokens and sequences at most 2^30 and
+ * tokens x top_k below 2^32; with tokens 0 logits, dlogits, chosen and mask are not looked at.
  * Addresses are multiples of their element's size; no written element may be an
  * element of another range of the call (ranges that interleave: as in
  * muon_block_matrix). */

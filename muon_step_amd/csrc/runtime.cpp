@@ -570,6 +570,8 @@ muon_status check_blocks(const muon_block_matrix *mats, int64_t count, const muo
     return MUON_OK;
 }
 
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // kernels count past the last one in 32 bits
+
 muon_status check_router_balance(const muon_router *rs, int64_t count, const muon_balance_hparams *hp, char *msg, size_t cap) {
     if (count < 0) { set_msg(msg, cap, "count < 0"); return MUON_ERR_INVALID_ARGUMENT; }
     if (count > 0 && !rs) { set_msg(msg, cap, "routers is NULL"); return MUON_ERR_INVALID_ARGUMENT; }
@@ -585,7 +587,7 @@ muon_status check_router_balance(const muon_router *rs, int64_t count, const muo
     for (int64_t i = 0; i < count; ++i) {
         const muon_router &r = rs[i];
         const long long at = i;
-        if (r.tokens < 0 || r.tokens >= int64_t(1) << 31 || r.experts < 1 || r.experts > muon::kMaxExperts || r.top_k < 1 ||
+        if (r.tokens < 0 || r.tokens > kMaxTokens || r.experts < 1 || r.experts > muon::kMaxExperts || r.top_k < 1 ||
             r.top_k > 64 || r.tokens * r.top_k >= int64_t(1) << 32) {
             set_msg(msg, cap, "router %lld: %lld tokens, %d experts or %d choices out of range", at, (long long)r.tokens, r.experts,
                     r.top_k);
@@ -595,7 +597,7 @@ muon_status check_router_balance(const muon_router *rs, int64_t count, const muo
             set_msg(msg, cap, "router %lld: unknown dtype or chosen_bits", at);
             return MUON_ERR_INVALID_ARGUMENT;
         }
-        if (r.sequences < 1 || (!r.offsets && r.sequences != 1)) {
+        if (r.sequences < 1 || r.sequences > kMaxTokens || (!r.offsets && r.sequences != 1)) {
             set_msg(msg, cap, "router %lld: %d sequences %s offsets", at, r.sequences, r.offsets ? "with" : "without");
             return MUON_ERR_INVALID_ARGUMENT;
         }
@@ -2146,15 +2148,18 @@ muon_status muon_check_grad_norm_args(const muon_grad *gs, int64_t count, double
 
 muon_status muon_check_blocks_args(const muon_block_matrix *mats, int64_t count, const muon_hparams *hp, char *msg,
                                    size_t msg_cap) {
+    set_msg(msg, msg_cap, "%s", "");
     return guarded(msg, msg_cap, [&] { return check_blocks(mats, count, hp, msg, msg_cap); });
 }
 
 muon_status muon_check_router_balance_args(const muon_router *rs, int64_t count, const muon_balance_hparams *hp, char *msg,
                                            size_t msg_cap) {
+    set_msg(msg, msg_cap, "%s", "");
     return guarded(msg, msg_cap, [&] { return check_router_balance(rs, count, hp, msg, msg_cap); });
 }
 
 muon_status muon_check_router_bias_args(const muon_router_bias *bs, int64_t count, double rate, char *msg, size_t msg_cap) {
+    set_msg(msg, msg_cap, "%s", "");
     return guarded(msg, msg_cap, [&] { return check_router_bias(bs, count, rate, msg, msg_cap); });
 }
 
