@@ -156,7 +156,10 @@ def moe16b_step(args):
     Muon on all 5292 matrices in one call, then AdamW on the 102400x2048
     embedding and head) and prints one JSON line of its own.  --clip-norm
     measures the norm of all gradients first and clips every step with it;
-    --adamw8 holds the embedding's and the head's moments in 8 bits."""
+    --adamw8 holds the embedding's and the head's moments in 8 bits;
+    --head-blocks orthogonalises the attention matrices head by head (16 of 128
+    rows, or columns of the fourth); --balance adds the 27 routers' balance loss
+    over 8192 tokens each, with its gradient, and the step of their biases."""
     import torch
 
     import muon_step_amd as ms
@@ -178,7 +181,19 @@ def moe16b_step(args):
     params = [(torch.randn(sp.rows, sp.cols, generator=gen, device="cuda") * synth.gen.PARAM_STD).to(torch.bfloat16)
               for sp in specs]
     moms = [torch.zeros(sp.rows, sp.cols, device="cuda") for sp in specs]
-    mats = [ms.matrix(params[i], grads[i], moms[i]) for i in range(len(specs))]
+    heads = [i for i, sp in enumerate(specs) if args.head_blocks and (sp.rows, sp.cols) == (2048, 2048)]
+    by_head = ms.table(ms.block_matrix(params[i], grads[i], moms[i], *((2048, 128) if k % 4 == 3 else (128, 2048)))
+                       for k, i in enumerate(heads)) if heads else None
+    mats = [ms.matrix(params[i], grads[i], moms[i]) for i in sorted(set(range(len(specs))) - set(heads))]
+    routers, biases, router_bufs = None, None, []
+    if args.balance:
+        for _ in range(27):
+            logits = torch.randn(8192, 64, generator=gen, device="cuda")
+            router_bufs.append((logits, torch.topk(logits, 6, dim=1).indices, torch.zeros(64, dtype=torch.int64, device="cuda"),
+                                torch.zeros(1, device="cuda"), torch.empty_like(logits), torch.zeros(64, device="cuda")))
+        routers = ms.table(ms.router(x, chosen, counts, loss, dlogits=dx) for x, chosen, counts, loss, dx, _ in router_bufs)
+        biases = ms.table(ms.router_bias(b[5], b[2]) for b in router_bufs)
+        bhp = ms.balance_hparams(1e-3)
     adamw_bufs = []  # the descriptors hold raw pointers: keep every tensor alive
     for _, n in wl.adamw:
         p = torch.randn(n, generator=gen, device="cuda") * synth.gen.PARAM_STD
@@ -202,9 +217,13 @@ def moe16b_step(args):
     stream = torch.cuda.current_stream()
 
     def step(i):
+        if routers is not None:
+            ctx.muon_router_balance(routers, bhp, stream)
         if args.clip_norm is not None:
             ctx.muon_grad_norm(all_grads, args.clip_norm, norm, factor, stream)
         ctx.muon_step(mats, hp, stream)
+        if by_head is not None:
+            ctx.muon_blocks_step(by_head, hp, stream)
         ahp = ms.adamw_hparams(step=i + 1)
         if args.adamw8:
             ctx.muon_adamw8_step(tensors, ahp, seed=5, grad_factor=factor, stream=stream)
@@ -212,6 +231,8 @@ def moe16b_step(args):
             ctx.muon_adamw_mixed_step(tensors, ahp, grad_factor=factor, stream=stream)
         else:
             ctx.muon_adamw_step(tensors, ahp, stream)
+        if biases is not None:
+            ctx.muon_router_bias_step(biases, 1e-3, stream)
 
     for i in range(args.warmup):
         step(i)
@@ -238,7 +259,8 @@ def moe16b_step(args):
         "steps": args.steps, "warmup": args.warmup, "n_gpus": 1, "dtype": "bf16", "data": "synthetic",
         "config": {"workload": "moe16b_full_step", "muon_matrices": len(specs),
                    "workspace_cap_gib": args.workspace_gib, "scale_mode": args.scale_mode,
-                   "clip_norm": args.clip_norm, "adamw_moments": "8 bits" if args.adamw8 else "fp32"},
+                   "clip_norm": args.clip_norm, "adamw_moments": "8 bits" if args.adamw8 else "fp32",
+                   "attention_blocks": 16 * len(heads), "balanced_routers": len(router_bufs)},
         "ns_tflops": round(ns_flops / ns_ms / 1e9, 2) if ns_ms else None,
         "ns_frac_bf16_peak": round(ns_flops / ns_ms / 1e9 / PEAK_BF16_TFLOPS, 4) if ns_ms else None,
         "stage_ms_per_step": breakdown}), flush=True)
@@ -379,6 +401,8 @@ def main():
     ap.add_argument("--clip-norm", type=float, default=None,
                     help="moe16b: measure the norm of all gradients and clip them to this one in every step")
     ap.add_argument("--adamw8", action="store_true", help="moe16b: AdamW moments of embedding and head in 8 bits")
+    ap.add_argument("--head-blocks", action="store_true", help="moe16b: Muon on each head of the attention matrices")
+    ap.add_argument("--balance", action="store_true", help="moe16b: the routers' balance loss, gradients and bias step too")
     ap.add_argument("--library-baseline", action="store_true",
                     help="only time torch bf16 batched products of the same shapes (64 matrices)")
     ap.add_argument("--hbm-probe", action="store_true",
@@ -386,6 +410,8 @@ def main():
     args = ap.parse_args()
     if args.workload != "moe16b" and (args.clip_norm is not None or args.adamw8):
         ap.error("--clip-norm and --adamw8 go with --workload moe16b")
+    if args.workload != "moe16b" and (args.head_blocks or args.balance):
+        ap.error("--head-blocks and --balance go with --workload moe16b")
     if args.clip_norm is not None and not args.clip_norm > 0:
         ap.error("--clip-norm must be positive")
     if args.copy_calibration:

@@ -1,4 +1,12 @@
 // The passes of the block step that multiply N by P (blocks.hpp).
+//
+// A wave holds P's rows as fragments in turn from shared memory, and N's columns
+// from M and G, formed and split in registers: nothing between is stored.  Bound by
+// memory (6 bytes an element read for X X^T, 8 or 10 more for W), and close behind
+// by the vector units' splitting of N and by the matrix cores: 3 x 2 s 16-bit
+// operations an element for P N, 3 s for X X^T.  1728 heads of 128 x 2048, bf16:
+// X X^T 0.75 ms, 3.6 TB/s; update 1.05 ms, 4.3 TB/s.  V = 2 columns a lane halves
+// the accesses; V = 4 spills.
 #include "blocks_device.hpp"
 
 namespace muon {

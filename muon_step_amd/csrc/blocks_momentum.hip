@@ -1,7 +1,7 @@
 // The first pass of the block step: momentum, N, and the sums of N N^T (blocks.hpp).
 //
-// Bound by memory (10 bytes an element, and 3 s / 2 products of 16-bit parts for
-// each, a fifth of the matrix cores' rate at s = 128).  What counts is that
+// Bound by memory (10 bytes an element, and 4 s / 2 products of 16-bit parts for
+// each, a quarter of the matrix cores' rate at s = 128).  What counts is that
 // neighbouring lanes read and write neighbouring memory, and that the next 32
 // columns are on their way while the present ones are worked on.  The operand
 // layout has neighbouring lanes in different rows; so a wave of a wide block works
@@ -9,7 +9,8 @@
 // parts through its own piece of shared memory.  (Loads and stores in the operand
 // layout, 16 bytes a lane 32 or 16 rows apart, kept the address units busy: 3.7 and
 // 4.1 TB/s.)  In tall blocks lanes that are neighbours in the operand are so in
-// memory, T elements each.
+// memory, T elements each.  1728 heads of 128 x 2048, bf16 gradients (4.5 GB): 1.02
+// ms, 4.4 TB/s, where a copy moves 4.9; 16 heads 16 us.
 #include "blocks_device.hpp"
 
 namespace muon {

@@ -38,9 +38,12 @@ constexpr int kRouterThreads = 256;
 constexpr int kMaxExperts = 1024;
 constexpr int kCountWords = 8192;    // counts that a workgroup has room for
 constexpr int kSmallThreads = 1024;
-// Routers with at most this many logits, and counts that fit a workgroup, are one
-// workgroup's work each.
-constexpr int64_t kSmallLogits = 65536;
+// Routers whose logits, and 24 for each token's choices, are at most this many, and
+// whose counts fit a workgroup, are one workgroup's work each.  In us, as one launch
+// and as three: 2048 tokens of 8 experts 10.2 and 11.4, 4096 16.2 and 11.8; 512 of 64
+// 9.1 and 12.9, 1024 12.8 and 12.8; 128 of 256 9.1 and 13.5, 512 19.2 and 13.8.
+constexpr int64_t kSmallWork = 81920;
+inline bool small_router(int64_t tokens, int64_t experts) { return tokens * (experts + 24) <= kSmallWork; }
 
 // Lanes that share a row of `experts` logits: 8 of them each up to 32 experts, 16
 // above (which halves what a row costs beside its elements).

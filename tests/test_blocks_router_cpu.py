@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 
@@ -233,3 +234,10 @@ def test_checks_under_asan_and_ubsan(tmp_path):
     res = _run([exe], env=env, timeout=300)
     assert "sanitized block and router checks: ok" in res.stdout
     assert "runtime error" not in res.stderr
+
+
+@pytest.mark.parametrize("args", [["--head-blocks"], ["--balance"], ["--workload", "dense_block_bf16", "--balance"]])
+def test_bench_refuses_options_of_another_workload(args):
+    res = subprocess.run([sys.executable, os.path.join(ROOT, "bench.py"), *args], capture_output=True, text=True, timeout=100)
+    assert res.returncode == 2 and res.stdout == ""
+    assert "--head-blocks and --balance go with" in res.stderr.splitlines()[-1]
