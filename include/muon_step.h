@@ -432,8 +432,8 @@ muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
  *     W <- (1 - lr wd) W - lr O,  O as hp's scale_mode says, RMS block by block.
  * M has muon_step's bits (and hp's grad_factor its meaning).  Operands of the
  * products are fp32 values as pairs of 16-bit parts, so X is far closer to the
- * exact iteration than MUON_NS_BF16's (relative Frobenius error 1e-6 to 1e-4,
- * more only in directions whose singular value is below 1e-4 of ||N||); hp's
+ * exact iteration than MUON_NS_BF16's (relative Frobenius error 1e-6 to 3e-5, to
+ * 3e-4 for squares, whose smallest singular values are small indeed); hp's
  * ns_precision must be MUON_NS_BF16 (MUON_NS_F32: UNSUPPORTED).  The schedule
  * must keep every singular value of [0, 1] within 3.9 at each step, with
  * |a + b x + c x^2| and its product with x at most 60 on the x it meets
@@ -441,7 +441,8 @@ muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
  * whose N is all zero gets the decay-only update, one with an infinity or a NaN
  * in N becomes NaN in all its elements, and no other block does; the scale of N
  * does not matter, from the smallest fp32 values to the largest.  A block's
- * result does not depend on the other blocks of the call.
+ * result does not depend on the other blocks of the call, but for the order of its
+ * sums, which goes by their number.
  * Descriptors travel as kernel arguments; the step works in memory of the
  * context, at most its workspace cap, which grows on first use: under graph
  * capture the call works once a call with the same list has run, and is refused

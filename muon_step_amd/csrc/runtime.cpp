@@ -505,6 +505,7 @@ muon_status check_strided(std::vector<Strided> &all, const char *items, char *ms
     return MUON_OK;
 }
 
+constexpr int64_t kMaxBlocks = int64_t(1) << 31;
 constexpr int64_t kMaxBlockSide = int64_t(1) << 24;   // fp16 holds N 2^shift up to sqrt(128 2^24)
 constexpr int64_t kMaxBlockPitch = int64_t(1) << 26;   // lanes address 8 rows in 32 bits
 
@@ -525,6 +526,10 @@ muon_status check_blocks(const muon_block_matrix *mats, int64_t count, const muo
         if (m.block_rows < 1 || m.block_cols < 1 || m.rows % m.block_rows != 0 || m.cols % m.block_cols != 0) {
             set_msg(msg, cap, "matrix %lld: blocks of %lld x %lld do not divide %lld x %lld", (long long)i,
                     (long long)m.block_rows, (long long)m.block_cols, (long long)m.rows, (long long)m.cols);
+            return MUON_ERR_INVALID_ARGUMENT;
+        }
+        if (m.rows / m.block_rows >= kMaxBlocks / (m.cols / m.block_cols)) {
+            set_msg(msg, cap, "matrix %lld: too many blocks", (long long)i);
             return MUON_ERR_INVALID_ARGUMENT;
         }
         if (std::min(m.block_rows, m.block_cols) > MUON_BLOCK_SIDE || std::max(m.block_rows, m.block_cols) > kMaxBlockSide) {
@@ -1786,24 +1791,39 @@ BlockShape block_shape(const muon_block_matrix &m, int64_t blocks) {
     return g;
 }
 
-// The launches of up to kBlockTensors weights with blocks of one shape and type.
-muon_status run_block_table(muon_context *ctx, const muon::BlockTable &t, int64_t total, const muon_block_matrix &like,
-                            const muon_hparams *hp, const muon::BlockSchedule &plan, hipStream_t st) {
+// Up to kBlockTensors weights with blocks of one shape and type: `total` blocks, n of
+// them at a time.
+struct BlockRun {
+    muon::BlockTable t;
+    int64_t total, n;
+    const muon_block_matrix *like;
+    BlockShape g;
+};
+// Sets g and n of a run, and `need` to what it takes of the context.
+muon_status size_block_run(muon_context *ctx, BlockRun &r, size_t *need) {
     size_t room = kBlockMemory;
     if (ctx->cap > 0) room = std::min(room, ctx->cap);
     const size_t slack = 8 * 256;
-    BlockShape g = block_shape(like, total);
-    int64_t most = room > slack ? static_cast<int64_t>((room - slack) / g.per_block) : 0;
-    if (most < total) {  // several launches after one another, of blocks enough for all CUs
-        g = block_shape(like, std::max<int64_t>(1, most));
-        most = room > slack ? static_cast<int64_t>((room - slack) / g.per_block) : 0;
+    r.g = block_shape(*r.like, r.total);
+    int64_t most = room > slack ? static_cast<int64_t>((room - slack) / r.g.per_block) : 0;
+    if (most < r.total) {  // several launches after one another, of blocks enough for all CUs
+        r.g = block_shape(*r.like, std::max<int64_t>(1, most));
+        most = room > slack ? static_cast<int64_t>((room - slack) / r.g.per_block) : 0;
         if (most < 1)
             return fail(ctx, MUON_ERR_OUT_OF_MEMORY, "workspace cap of %zu bytes: one block of %lld x %lld needs %zu", ctx->cap,
-                        (long long)like.block_rows, (long long)like.block_cols, g.per_block + slack);
+                        (long long)r.like->block_rows, (long long)r.like->block_cols, r.g.per_block + slack);
     }
-    const int64_t n = std::min(most, total);
-    muon_status s = ensure(ctx, ctx->blocks, g.per_block * n + slack, "block workspace", capturing(st));
-    if (s != MUON_OK) return s;
+    r.n = std::min(most, r.total);
+    *need = r.g.per_block * r.n + slack;
+    return MUON_OK;
+}
+
+muon_status run_blocks(muon_context *ctx, const BlockRun &r, const muon_hparams *hp, const muon::BlockSchedule &plan,
+                       hipStream_t st) {
+    const muon::BlockTable &t = r.t;
+    const muon_block_matrix &like = *r.like;
+    const BlockShape &g = r.g;
+    const int64_t n = r.n, total = r.total;
     const size_t tiles = muon::block_tiles(g.s);
     muon::BlockCall c{};
     char *at = static_cast<char *>(ctx->blocks.p);
@@ -1898,37 +1918,44 @@ muon_status blocks_impl(muon_context *ctx, const muon_block_matrix *mats, int64_
         return std::make_tuple(m.block_rows, m.block_cols, m.param_dtype, m.grad_dtype);
     };
     std::vector<char> done(static_cast<size_t>(count), 0);
+    std::vector<BlockRun> runs;
     for (int64_t i = 0; i < count; ++i) {
         if (done[i]) continue;
-        muon::BlockTable t;
-        int n = 0;
-        int64_t blocks = 0;
-        auto flush = [&]() -> muon_status {
-            for (int k = n; k < muon::kBlockTensors; ++k) t.first[k] = 0xffffffffu;
-            const muon_status r = run_block_table(ctx, t, blocks, mats[i], hp, plan, st);
-            n = 0;
-            blocks = 0;
-            return r;
-        };
+        int n = muon::kBlockTensors;
         for (int64_t j = i; j < count; ++j) {
             if (done[j] || key(j) != key(i)) continue;
             const muon_block_matrix &m = mats[j];
-            const int64_t across = m.cols / m.block_cols, nb = m.rows / m.block_rows * across;
-            if (nb >= int64_t(1) << 31) return fail(ctx, MUON_ERR_INVALID_ARGUMENT, "matrix %lld: too many blocks", (long long)j);
-            if (n == muon::kBlockTensors || blocks + nb >= int64_t(1) << 31) {
-                s = flush();
-                if (s != MUON_OK) return s;
+            const int64_t across = m.cols / m.block_cols, blocks = m.rows / m.block_rows * across;
+            if (n == muon::kBlockTensors || runs.back().total + blocks >= kMaxBlocks) {
+                runs.emplace_back();
+                runs.back().like = mats + i;
+                runs.back().total = 0;
+                for (uint32_t &first : runs.back().t.first) first = 0xffffffffu;
+                n = 0;
             }
-            t.first[n] = static_cast<uint32_t>(blocks);
-            t.d[n] = muon::BlockDesc{m.param, m.grad, m.momentum, m.ns_out,
-                                     static_cast<uint32_t>(m.param_pitch), static_cast<uint32_t>(m.grad_pitch),
-                                     static_cast<uint32_t>(m.momentum_pitch), static_cast<uint32_t>(m.ns_out ? m.ns_out_pitch : 0),
-                                     static_cast<uint32_t>(across), 0};
+            BlockRun &r = runs.back();
+            r.t.first[n] = static_cast<uint32_t>(r.total);
+            r.t.d[n] = muon::BlockDesc{m.param, m.grad, m.momentum, m.ns_out,
+                                       static_cast<uint32_t>(m.param_pitch), static_cast<uint32_t>(m.grad_pitch),
+                                       static_cast<uint32_t>(m.momentum_pitch), static_cast<uint32_t>(m.ns_out ? m.ns_out_pitch : 0),
+                                       static_cast<uint32_t>(across), 0};
             ++n;
-            blocks += nb;
+            r.total += blocks;
             done[j] = 1;
         }
-        s = flush();
+    }
+    // memory for all runs before the first of them is enqueued
+    size_t most = 0;
+    for (BlockRun &r : runs) {
+        size_t need = 0;
+        s = size_block_run(ctx, r, &need);
+        if (s != MUON_OK) return s;
+        most = std::max(most, need);
+    }
+    if (most > 0) s = ensure(ctx, ctx->blocks, most, "block workspace", capturing(st));
+    if (s != MUON_OK) return s;
+    for (const BlockRun &r : runs) {
+        s = run_blocks(ctx, r, hp, plan, st);
         if (s != MUON_OK) return s;
     }
     ctx->err.clear();
@@ -1944,14 +1971,32 @@ constexpr int64_t kCountWorkgroups = 512, kBalanceWorkgroups = 1024;
 
 size_t router_words(const muon_router &r) { return static_cast<size_t>(r.sequences) * (r.experts + 1); }
 
-// The launches of up to kRouters routers of one type and lane layout.
-muon_status run_router_table(muon_context *ctx, const muon_router *const *rs, int n, const muon_balance_hparams *hp, hipStream_t st) {
-    size_t words = 0;
-    int64_t tokens = 0;
-    for (int i = 0; i < n; ++i) {
-        words += router_words(*rs[i]);
-        tokens += rs[i]->tokens;
+// Up to kRouters routers of one type and lane layout, which launch together.
+struct RouterRun {
+    const muon_router *rs[muon::kRouters];
+    int n = 0;
+    int64_t tokens = 0, per_balance = 0;
+    size_t words = 0;  // of counts, 0 where each router is one workgroup's work
+    size_t sums = 0;
+};
+void size_router_run(RouterRun &r) {
+    bool small = true;
+    for (int i = 0; i < r.n; ++i) {
+        const size_t words = router_words(*r.rs[i]);
+        r.words += words;
+        small &= muon::small_router(r.rs[i]->tokens, r.rs[i]->experts) && words <= static_cast<size_t>(muon::kCountWords);
     }
+    const int64_t turn = muon::kRouterThreads / muon::router_lanes(r.rs[0]->experts);  // rows that a workgroup takes at once
+    r.per_balance = round_up(std::max<int64_t>(1, (r.tokens + kBalanceWorkgroups - 1) / kBalanceWorkgroups), turn);
+    r.sums = static_cast<size_t>(r.tokens / r.per_balance) + r.n;
+    if (small) r.words = r.sums = 0;
+}
+
+muon_status run_routers(muon_context *ctx, const RouterRun &r, const muon_balance_hparams *hp, hipStream_t st) {
+    const muon_router *const *rs = r.rs;
+    const int n = r.n;
+    const int64_t tokens = r.tokens, per_balance = r.per_balance;
+    const size_t words = r.words;
     const muon_router &like = *rs[0];
     const bool bf16 = like.dtype == MUON_BF16;
     muon::RouterTable t{};
@@ -1961,7 +2006,6 @@ muon_status run_router_table(muon_context *ctx, const muon_router *const *rs, in
     c.sigmoid = hp->score == MUON_SCORE_SIGMOID;
     c.accumulate = hp->accumulate;
     double count_bytes = 0, row_bytes = 0;
-    bool small = true;
     for (int i = 0; i < n; ++i) {
         const muon_router &r = *rs[i];
         muon::RouterDesc &d = t.d[i];
@@ -1979,26 +2023,16 @@ muon_status run_router_table(muon_context *ctx, const muon_router *const *rs, in
         d.top_k = r.top_k;
         d.sequences = r.sequences;
         d.chosen64 = r.chosen_bits == 64;
-        small &= muon::small_router(r.tokens, r.experts) && router_words(r) <= static_cast<size_t>(muon::kCountWords);
         count_bytes += static_cast<double>(r.tokens) * (r.top_k * (r.chosen_bits / 8) + (r.mask ? 1 : 0));
         row_bytes += static_cast<double>(r.tokens) * r.experts * dtype_size(r.dtype) * (r.dlogits ? 2 : 1);
     }
-    if (small) {
+    if (words == 0) {
         const hipError_t e = timed(ctx, ST_ROUTER_BALANCE, 0.0, count_bytes + row_bytes, st,
                                    [&] { return muon::launch_router_small(t, n, c, like.experts, bf16, st); });
         return e == hipSuccess ? MUON_OK : hip_fail(ctx, e, "router launch");
     }
-    const int lanes = muon::router_lanes(like.experts);
-    const int64_t turn = muon::kRouterThreads / lanes;  // rows that a workgroup takes at once
-    const int64_t per_balance = round_up(std::max<int64_t>(1, (tokens + kBalanceWorkgroups - 1) / kBalanceWorkgroups), turn);
     const int64_t per_count = std::max<int64_t>(64, (tokens + kCountWorkgroups - 1) / kCountWorkgroups);
     const bool graph = capturing(st);
-    const void *before = ctx->routers.p;
-    muon_status s = ensure(ctx, ctx->routers, words * 4, "router counts", graph);
-    if (ctx->routers.p != before) ctx->routers_clear = 0;
-    if (s != MUON_OK) return s;
-    s = ensure(ctx, ctx->router_sums, (static_cast<size_t>(tokens / per_balance) + n) * 8, "router workspace", graph);
-    if (s != MUON_OK) return s;
     uint32_t *hist = static_cast<uint32_t *>(ctx->routers.p);
     double *sums = static_cast<double *>(ctx->router_sums.p);
     const size_t clear = ctx->routers_clear;
@@ -2051,23 +2085,37 @@ muon_status router_balance_impl(muon_context *ctx, const muon_router *rs, int64_
         return std::make_tuple(muon::router_lanes(rs[i].experts), rs[i].experts > 32, rs[i].dtype);
     };
     std::vector<char> done(static_cast<size_t>(count), 0);
+    std::vector<RouterRun> runs;
     for (int64_t i = 0; i < count; ++i) {
-        const muon_router *table[muon::kRouters];
-        int n = 0;
-        int64_t tokens = 0;
+        if (done[i]) continue;
+        runs.emplace_back();
         for (int64_t j = i; j < count; ++j) {
             if (done[j] || key(j) != key(i)) continue;
-            if (n == muon::kRouters || tokens + rs[j].tokens >= int64_t(1) << 31) {
-                s = run_router_table(ctx, table, n, hp, st);
-                if (s != MUON_OK) return s;
-                n = 0;
-                tokens = 0;
-            }
-            table[n++] = rs + j;
-            tokens += rs[j].tokens;
+            if (runs.back().n == muon::kRouters || runs.back().tokens + rs[j].tokens >= int64_t(1) << 31) runs.emplace_back();
+            RouterRun &r = runs.back();
+            r.rs[r.n++] = rs + j;
+            r.tokens += rs[j].tokens;
             done[j] = 1;
         }
-        if (n > 0) s = run_router_table(ctx, table, n, hp, st);
+    }
+    // memory for all runs before the first of them is enqueued
+    size_t words = 0, sums = 0;
+    for (RouterRun &r : runs) {
+        size_router_run(r);
+        words = std::max(words, r.words);
+        sums = std::max(sums, r.sums);
+    }
+    if (words > 0) {
+        const bool graph = capturing(st);
+        const void *before = ctx->routers.p;
+        s = ensure(ctx, ctx->routers, words * 4, "router counts", graph);
+        if (ctx->routers.p != before) ctx->routers_clear = 0;
+        if (s != MUON_OK) return s;
+        s = ensure(ctx, ctx->router_sums, sums * 8, "router workspace", graph);
+        if (s != MUON_OK) return s;
+    }
+    for (const RouterRun &r : runs) {
+        s = run_routers(ctx, r, hp, st);
         if (s != MUON_OK) return s;
     }
     ctx->err.clear();

@@ -241,3 +241,10 @@ def test_bench_refuses_options_of_another_workload(args):
     res = subprocess.run([sys.executable, os.path.join(ROOT, "bench.py"), *args], capture_output=True, text=True, timeout=100)
     assert res.returncode == 2 and res.stdout == ""
     assert "--head-blocks and --balance go with" in res.stderr.splitlines()[-1]
+
+
+def test_more_blocks_than_a_launch_numbers():
+    big = dict(rows=1 << 16, cols=1 << 16, block_rows=1, block_cols=1, param_pitch=1 << 16, grad_pitch=1 << 16,
+               momentum_pitch=1 << 16)
+    st, msg = check_blocks([block(**big)])
+    assert st == ms.MUON_ERR_INVALID_ARGUMENT and "too many blocks" in msg

@@ -366,3 +366,28 @@ def test_long_side_past_a_launch(ctx):
     step(ctx, weights)
     for w in weights:
         w.check(WELL)
+
+
+def test_memory_for_all_blocks_or_none():
+    """A list of which one shape does not fit the cap, or would have to grow the memory under capture, steps nothing."""
+    import torch
+    rng = np.random.default_rng(41)
+    fits, large = Weight(rng, (1, 1), (16, 64), "f32", "f32"), Weight(rng, (2, 1), (128, 2048), "f32", "f32")
+    state = lambda: [w.dev[k].clone() for w in (fits, large) for k in ("param", "momentum")]  # noqa: E731
+    before = state()
+    hp = ms.make_hparams(lr=LR, momentum=MU, weight_decay=WD, gamma=GAMMA)
+    capped = ms.Context(0, workspace_cap_bytes=64 << 10)
+    with pytest.raises(ms.MuonError, match="workspace cap"):
+        capped.muon_blocks_step([fits.item(), large.item()], hp)
+    capped.close()
+    fresh = ms.Context(0)
+    idle = Weight(rng, (1, 1), (16, 64), "f32", "f32")
+    fresh.muon_blocks_step([idle.item()], hp)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ms.MuonError, match="block workspace"):
+            fresh.muon_blocks_step([fits.item(), large.item()], hp, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(state(), before))
+    fresh.close()

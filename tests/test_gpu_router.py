@@ -329,3 +329,26 @@ def test_bias_step(ctx, experts):
     torch.cuda.synchronize()
     for t, w in zip(biases, want):
         assert np.array_equal(t.cpu().numpy(), w)
+
+
+def test_capture_needs_memory_of_an_earlier_call():
+    """A long batch under capture is refused before any of the list is enqueued; a short one needs no memory."""
+    import torch
+    rng = np.random.default_rng(43)
+    mine = ms.Context(0)
+    short, long = Batch(rng, 50, 8, 2), Batch(rng, 9000, 64, 4)
+    hp = ms.balance_hparams(COEF)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ms.MuonError, match="router counts"):
+            mine.muon_router_balance([short.item(), long.item()], hp, stream=torch.cuda.current_stream())
+        mine.muon_router_balance([short.item()], hp, stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert int(short.counts.sum()) == 7 * 8 and int(long.counts.sum()) == 7 * 64
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        short.check()
+        run(mine, [long])
+        long.check()
+    mine.close()
