@@ -119,7 +119,9 @@ __device__ __forceinline__ void sum_tile(float *dst, float *sh, int k, const flo
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float *x = buf + (4 * wave + e) * 64 + lane;
-        v[e] = ((x[0] + x[1024]) + x[2048]) + x[3072];
+        v[e] = x[0];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) v[e] += x[1024 * w];
     }
     *(floatx4 __attribute__((address_space(1))) *)(dst + 256 * wave + 4 * lane) = v;
 }

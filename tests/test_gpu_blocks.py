@@ -391,3 +391,28 @@ def test_memory_for_all_blocks_or_none():
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(state(), before))
     fresh.close()
+
+
+@pytest.mark.parametrize("block", [(16, 64), (64, 16)])
+def test_offsets_past_32_bits(ctx, block):
+    """Rows as far apart as they may be: the last of them lie past 2^32 bytes; as the same blocks packed."""
+    import torch
+    rng = np.random.default_rng(44)
+    pitch, shape = 1 << 26, (2 * block[0] if block[0] == 16 else block[0], block[1])
+    rows = shape[0]
+    host = {k: rng.standard_normal(shape).astype(np.float32) for k in ("param", "grad", "momentum")}
+    outs = []
+    for wide in (False, True):
+        t = {}
+        for k, x in host.items():
+            kind = torch.float32 if k == "momentum" else torch.bfloat16
+            full = torch.empty(((rows - 1) * pitch + shape[1]) if wide else x.size, dtype=kind, device="cuda")
+            t[k] = full.as_strided(shape, (pitch if wide else shape[1], 1))
+            t[k].copy_(torch.from_numpy(x))
+        ctx.muon_blocks_step([ms.block_matrix(t["param"], t["grad"], t["momentum"], *block)],
+                             ms.make_hparams(lr=LR, momentum=MU, weight_decay=WD, gamma=GAMMA))
+        torch.cuda.synchronize()
+        outs.append((t["param"].clone(), t["momentum"].clone()))
+        del t, full
+        torch.cuda.empty_cache()
+    assert all(torch.equal(x, y) for x, y in zip(*outs))

@@ -352,3 +352,24 @@ def test_capture_needs_memory_of_an_earlier_call():
         run(mine, [long])
         long.check()
     mine.close()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_offsets_past_32_bits(ctx, score):
+    """Rows 2^18 elements apart: the last of them lie past 2^32 bytes; as the same rows packed, bit for bit."""
+    import torch
+    rng = np.random.default_rng(45)
+    b = Batch(rng, 5000, 40, 3, offsets=[0, 1200, 4990], score=score, mask=True)
+    run(ctx, [b], score)
+    b.check()
+    far = [torch.empty(4999 * (1 << 18) + 40, device="cuda").as_strided((5000, 40), (1 << 18, 1)) for _ in range(2)]
+    far[0].copy_(b.full)
+    far[1].copy_(torch.from_numpy(b.before))
+    loss, counts = torch.zeros_like(b.loss), torch.zeros_like(b.counts)
+    code = ms.MUON_SCORE_SIGMOID if score == "sigmoid" else ms.MUON_SCORE_SOFTMAX
+    ctx.muon_router_balance([ms.router(far[0], b.dev_chosen, counts, loss, dlogits=far[1], offsets=b.dev_offsets,
+                                       mask=b.dev_mask)], ms.balance_hparams(COEF, score=code))
+    torch.cuda.synchronize()
+    assert torch.equal(far[1], b.dfull) and torch.equal(loss, b.loss) and torch.equal(counts, b.counts)
+    del far
+    torch.cuda.empty_cache()
