@@ -248,3 +248,31 @@ def test_more_blocks_than_a_launch_numbers():
                momentum_pitch=1 << 16)
     st, msg = check_blocks([block(**big)])
     assert st == ms.MUON_ERR_INVALID_ARGUMENT and "too many blocks" in msg
+
+
+def test_overlap_against_brute_force():
+    """Random layouts in one buffer: what is taken shares no written byte; ranges of one pitch are refused only for one."""
+    import random
+    rng = random.Random(5)
+    taken = refused = 0
+    for _ in range(4000):
+        items, spans = [], []
+        pitches = [rng.choice((8, 8, 8, 12)) for _ in range(2)]
+        for i in range(2):
+            rows, cols = rng.randint(1, 3), rng.randint(1, 6)
+            at = {k: rng.randint(0, 60) for k in ("param", "grad", "momentum")}
+            if i or rng.random() < 0.7:  # mostly apart from each other, close to the other weight's
+                at = {k: v + 100 * n for n, (k, v) in enumerate(at.items())}
+            items.append(block(rows=rows, cols=cols, block_rows=rows, block_cols=cols, param_dtype=ms.MUON_F32,
+                               grad_dtype=ms.MUON_F32, **{k: BASE + 4 * v for k, v in at.items()},
+                               **{k + "_pitch": pitches[i] for k in at}))
+            for k, v in at.items():
+                spans.append((k != "grad", pitches[i], {v + r * pitches[i] + c for r in range(rows) for c in range(cols)}))
+        pairs = [(a, b) for n, a in enumerate(spans) for b in spans[:n] if a[0] or b[0]]
+        shared = any(a[2] & b[2] for a, b in pairs)
+        hulls = any(a[1] != b[1] and min(a[2]) <= max(b[2]) and min(b[2]) <= max(a[2]) for a, b in pairs)
+        st = check_blocks(items)[0]
+        assert st == (ms.MUON_ERR_INVALID_ARGUMENT if shared or hulls else ms.MUON_OK), (items, shared, hulls)
+        taken += st == ms.MUON_OK
+        refused += st != ms.MUON_OK
+    assert taken > 500 and refused > 500, (taken, refused)
