@@ -46,7 +46,9 @@ constexpr int64_t kSmallWork = 81920;
 inline bool small_router(int64_t tokens, int64_t experts) { return tokens * (experts + 24) <= kSmallWork; }
 
 // Lanes that share a row of `experts` logits: 8 of them each up to 32 experts, 16
-// above (which halves what a row costs beside its elements).
+// above (which halves what a row costs beside its elements: 27 x 8192 x 64 41.5 to
+// 36.7 us).  24 where that leaves fewer places empty are slower, with fewer bytes on
+// their way: 72 experts 31 to 34 us, 384 47 to 56.
 inline int router_lanes(int experts) {
     const int each = experts <= 32 ? 8 : 16;
     int lanes = 1;
