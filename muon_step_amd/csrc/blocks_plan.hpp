@@ -90,9 +90,10 @@ inline BlockSchedule plan_blocks_schedule(const muon_ns_coeff *c, int n) {
     // values by a^2, relative to what Q makes of them.  A segment goes on while
     // that stays below 2^11 times fp32's rounding (1e-4 of a small direction's
     // gain); the last one, whose noise no later step can grow, up to 2^17.
-    // Measured on spectra over three decades, error against 64 bits: the hybrid
-    // schedule as 4 + 6 steps 2.9e-5, as 5 + 5 6.0e-5, as 4 + 4 + 2 2.5e-5 (which
-    // is another pass over M and G), every step's A from X in fp32 4.8e-6.
+    // Error against 64 bits on spectra over three decades, s of 16 to 128 in long
+    // blocks and (in squares), emulated: the hybrid schedule as 4 + 6 steps 6e-6 to
+    // 1.1e-5 (1.9e-4), as 3 + 7 5e-6 to 9e-6 (2e-3), as 5 + 5 3e-5 to 1.1e-4 (1e-4), as
+    // 2 + 3 + 5, which is another pass over M and G, 5e-6 (7e-5).
     auto gain = [&](int k) { return std::max(1.0, c[k].a * c[k].a); };
     int at = 0;
     while (at < n) {
