@@ -436,8 +436,12 @@ muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
  * 3e-4 for squares, whose smallest singular values are small indeed); hp's
  * ns_precision must be MUON_NS_BF16 (MUON_NS_F32: UNSUPPORTED).  The schedule
  * must keep every singular value of [0, 1] within 3.9 at each step, with
- * |a + b x + c x^2| and its product with x at most 60 on the x it meets
- * (UNSUPPORTED otherwise; the named schedules stay within 1.3 and 4).  A block
+ * |a + b x + c x^2| and its product with x at most 60 on the x it meets, the
+ * largest singular value above 0.044 wherever in [128^-1/2, 1] it begins, and the
+ * product over the steps of the largest |a + b x + c x^2|, its gain, at most 2^22
+ * (UNSUPPORTED otherwise).  The named schedules stay within 1.3 and 4, above 0.3
+ * and within 2^17; 12 steps of the quintic or 22 of (2, -1.5, 0.5) are the
+ * longest.  A block
  * whose N is all zero gets the decay-only update, one with an infinity or a NaN
  * in N becomes NaN in all its elements, and no other block does; the scale of N
  * does not matter, from the smallest fp32 values to the largest.  A block's

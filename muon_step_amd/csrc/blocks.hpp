@@ -67,7 +67,7 @@ struct BlockScalars {
     float inv_norm;   // 1 / ||N 2^shift||
     int32_t shift;    // N 2^shift has an rms of 1/2 to 1
     float update;     // lr x scale of the block's update
-    int32_t pad_;
+    int32_t poly;     // P's fragments are those of P 2^-poly
 };
 // The sum of squares' range of one part of a block.
 struct BlockPart {
@@ -91,7 +91,6 @@ struct BlockCall {
     int32_t parts, part_len;        // a block's l columns in `parts` ranges of part_len
     float mu;
     int32_t nesterov;
-    float poly_scale;               // what P's fragments are to be multiplied by
     float decay;
 };
 
@@ -103,11 +102,9 @@ struct BlockChain {
     int32_t first, last;       // segment
     int32_t unit_rms, tall;
     float update;              // lr gamma sqrt(max(n, m)); unit RMS: lr gamma sqrt(n m)
-    float poly_scale;          // what P's fragments of the segment before are to be multiplied by
-    float out_scale;           // what this segment's are multiplied by, from what P leaves the last step as
+    int32_t poly_least;        // P's fragments are those of P 2^-e, e at least this
     struct Step {
         float a, b, c;
-        int32_t exp_in, exp_out;  // P 2^-exp is what enters and leaves the step as fp16 pairs
     } step[kMaxChainSteps];
 };
 

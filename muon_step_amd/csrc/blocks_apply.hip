@@ -244,7 +244,7 @@ __device__ __forceinline__ void times_poly(floatx16 (&acc)[V][T], Stream<T, V, T
 }
 
 // Columns x0, x0 + stride, ... below `end` of a wave: the sum of X X^T, X = P N 2^shift
-// (the host scales P so that its entries suit fp16).
+// (the chain scales P so that its entries suit fp16).
 template <int T, int V, bool TALL, bool BF16, bool EVEN>
 __device__ __forceinline__ void regram_columns(Triangle<T> &sum, Stream<T, V, TALL, BF16, EVEN> &in, const Poly<T> &poly, int lane,
                                                int x0, int stride, int end) {
@@ -481,7 +481,7 @@ __global__ __launch_bounds__(kThreads) void blocks_update_kernel(const BlockTabl
     const int begin = part * c.part_len, end = min(begin + c.part_len, c.l);
     const BlockScalars k = c.w.scalars[block];
     const float factor = c.factor ? *c.factor : 1.0f;
-    const Update u{at, c, c.poly_scale * k.inv_norm, k.update};
+    const Update u{at, c, __builtin_amdgcn_ldexpf(k.inv_norm, k.poly), k.update};
     const int whole = V == 1 ? begin : begin + (end - begin) / (V * kBlockUnit) * (V * kBlockUnit);
     Stream<T, V, TALL, BF16, EVEN> in(at, c, factor, lane, k.shift);
     const int x0 = begin + 32 * V * wave, x1 = whole + 32 * wave;

@@ -88,6 +88,7 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
     };
     __shared__ __attribute__((aligned(16))) Shared sh;
     __shared__ float sh_sum[T];
+    __shared__ int sh_exp[T];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, j = lane & 31, h = lane >> 5;
     const int64_t block = blockIdx.x;
     const int col = 32 * wave + j;
@@ -192,12 +193,12 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
             out.shift = zero || bad ? 0 : e - common;
             out.inv_norm = zero || bad ? 1.0f : 1.0f / ldexpf(n, e);
             out.update = c.update;
-            out.pad_ = 0;
+            out.poly = 0;
             c.w.scalars[block] = out;
         }
     } else {
         // the sums are of P's fragments times N 2^shift
-        const float scale = c.poly_scale * c.w.scalars[block].inv_norm;
+        const float scale = __builtin_amdgcn_ldexpf(c.w.scalars[block].inv_norm, c.w.scalars[block].poly);
 #pragma unroll
         for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -215,14 +216,35 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
         for (int r = 0; r < 16; ++r)
             p.v[t][r] = c.first ? (on_diagonal(t, r) && there ? 1.0f : 0.0f) : as_global(own)[(t * 16 + r) * 64 + lane];
 
-    // A, Q and P as they enter the products: A 64, Q 16, P 2^-exp_in, A Q 1024.
+    // P as it enters the products: each column p 2^p_exp, its largest entry p below 2^12
+    // and at least half of that.  How large P's entries become goes by the spectrum (by
+    // its smallest singular value, up to the schedule's gain, where N has one): a scale
+    // for the worst of them would leave an even one's P below fp16's smallest values.
+    // A column stays in its lanes as a right operand, so its scale needs no other wave.
+    int p_exp = 0;
+    auto normalize = [&]() {
+        float most = 0.0f;
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) most = fmaxf(most, fabsf(p.v[t][r]));
+        most = fmaxf(most, __shfl_xor(most, 32, 64));
+        const int up = 12 - __builtin_amdgcn_frexp_expf(most);
+        p_exp -= up;
+        return __builtin_amdgcn_ldexpf(1.0f, up);
+    };
+    auto scale_p = [&](float by) {
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) p.v[t][r] *= by;
+    };
+    scale_p(normalize());
+    // A and Q as they enter the products: A 64, Q 16, A Q 1024.
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            a.v[t][r] *= kScaleA;
-            p.v[t][r] *= c.steps > 0 ? ldexpf(1.0f, -c.step[0].exp_in) : 1.0f;
-        }
+        for (int r = 0; r < 16; ++r) a.v[t][r] *= kScaleA;
     float square = 1.0f;  // ||O||^2
     for (int k = 0; k < c.steps; ++k) {
         const BlockChain::Step step = c.step[k];
@@ -284,7 +306,6 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
             sh.left.lo[wave][i][lane] = pairs.lo[i];
         }
         __syncthreads();
-        const float rescale = ldexpf(1.0f / kScaleQ, step.exp_in - step.exp_out);
         if (more) {
             floatx16 acc[2][T];
             product<T, 2>(acc, sh.left, lane, [&](int b, int i, half8 &hi, half8 &lo) { split_chunk(b ? ar : p, i, hi, lo); });
@@ -292,7 +313,7 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
             for (int t = 0; t < T; ++t)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    p.v[t][r] = acc[0][t][r] * rescale;
+                    p.v[t][r] = acc[0][t][r];
                     a.v[t][r] = acc[1][t][r] * (1.0f / (kScaleQ * kScaleQ));
                 }
         } else {
@@ -301,8 +322,10 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
 #pragma unroll
             for (int t = 0; t < T; ++t)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) p.v[t][r] = acc[0][t][r] * rescale;
+                for (int r = 0; r < 16; ++r) p.v[t][r] = acc[0][t][r];
         }
+        p_exp -= kLogScaleQ;
+        scale_p(normalize());
         __syncthreads();
     }
 
@@ -311,17 +334,26 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
         c.w.scalars[block].update = zero || !(o > 0) ? 0.0f : static_cast<float>(c.update / o);
     }
 
-    // P's columns for the next segment, and its rows as fragments for the products with N.
-    const float whole = c.steps > 0 ? ldexpf(1.0f, c.step[c.steps - 1].exp_out) : 1.0f;  // what P is held short of
-    const float nan = __builtin_nanf("");
+    // P's columns for the next segment, and its rows as fragments for the products with
+    // N, of P 2^-poly: its largest entry below 2^15, and P N below 2^15.
+    int largest_exp = there ? p_exp : -1000;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) largest_exp = max(largest_exp, __shfl_xor(largest_exp, off, 64));
+    if (lane == 0) sh_exp[wave] = largest_exp;
     __syncthreads();
+#pragma unroll
+    for (int w = 0; w < T; ++w) largest_exp = max(largest_exp, sh_exp[w]);
+    const int poly = max(largest_exp + 12 - 15, c.poly_least);
+    if (threadIdx.x == 0) c.w.scalars[block].poly = poly;
+    const float nan = __builtin_nanf("");
+    const float whole = __builtin_amdgcn_ldexpf(1.0f, p_exp), part = __builtin_amdgcn_ldexpf(1.0f, p_exp - poly);
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const float x = zero ? 0.0f : bad ? nan : p.v[t][r];
             if (!c.last) as_global(own)[(t * 16 + r) * 64 + lane] = x * whole;
-            sh.rows[32 * t + acc_row(r, h)][col] = x * c.out_scale;
+            sh.rows[32 * t + acc_row(r, h)][col] = x * part;
         }
     __syncthreads();
     half8 *frag = reinterpret_cast<half8 *>(c.w.poly) + block * (T * T * 256);

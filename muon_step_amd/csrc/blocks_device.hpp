@@ -54,9 +54,11 @@ __device__ __forceinline__ void split_bf(const float (&x)[8], bf16x8 &hi, bf16x8
     }
 }
 
-// Scales of the fp16 pairs: |A| <= 16, |Q| <= 60 and |A Q| <= 60 in the schedules
-// that the host admits, so A Q's product of scales, 1024, keeps it below 65504 too.
-constexpr float kScaleA = 64.0f, kScaleQ = 16.0f;
+// Scales of the fp16 pairs of A and Q: |A| <= 16, |Q| <= 60 and |A Q| <= 60 in the
+// schedules that the host admits, so A Q's product of scales, 1024, keeps it below
+// 65504 too, and |A| >= 2^-9 (blocks_plan.hpp).  P has no such bounds.
+constexpr int kLogScaleQ = 4;
+constexpr float kScaleA = 64.0f, kScaleQ = 1 << kLogScaleQ;
 
 // ---------------------------------------------------------------- places in memory
 

@@ -1,8 +1,9 @@
 // Which schedules the block step can run, and where it cuts them (host only).
 //
-// The chain (blocks.hip) holds A, Q = a + b A + c A^2, A Q and P as scaled fp16
-// pairs, so a schedule has to keep them within bounds on every spectrum that a
-// normalised X can have, singular values in [0, 1].
+// The chain (blocks_chain.hip) holds A, Q = a + b A + c A^2 and A Q as fp16 pairs
+// of fixed scales, so a schedule has to keep them within bounds, from above and from
+// below, on every spectrum that a normalised X can have: singular values in [0, 1],
+// the largest of them at least 128^-1/2.
 #pragma once
 
 #include <algorithm>
@@ -20,9 +21,14 @@ struct BlockSegment {
 struct BlockSchedule {
     bool fits = false;
     std::vector<BlockSegment> segments;  // at least one
-    std::vector<int> exp_in;             // of each step; exp_out is the next one's, last_exp after the last
-    int last_exp = 0;
 };
+// The largest gain that a schedule may give a vanishing singular value.  P holds that
+// gain, rounded to 24 bits, wherever N has such a direction (a rank below the smaller
+// side), and what the rounding adds to O is 2^-24 of it.
+constexpr double kMaxGain = 0x1p22;
+// What the largest singular value may fall to.  A, which is at least its square on
+// the diagonal of an even spectrum, then keeps 22 bits as fp16 pairs of 64 A.
+constexpr double kLeastSigma = 0.044;
 
 // Largest |c0 + c1 x + c2 x^2| x^power on [0, top], power 0 or 1.
 inline double polynomial_bound(double c0, double c1, double c2, int power, double top) {
@@ -65,26 +71,44 @@ inline double map_bound(double a, double b, double c, double top) {
     return best;
 }
 
-// The exponent e that brings magnitudes up to `bound` to 2^11 at most as x 2^-e.
-inline int pair_exponent(double bound) {
-    return static_cast<int>(std::ceil(std::log2(std::max(bound, 0x1p-20)))) - 11;
+// Smallest |x (a + b x^2 + c x^4)| on [least, top], least > 0.
+inline double map_least(double a, double b, double c, double least, double top) {
+    auto value = [&](double l) { return std::sqrt(l) * (a + (b + c * l) * l); };
+    const double begin = least * least, end = top * top, first = value(begin);
+    double best = std::fabs(first);
+    auto at = [&](double l) {
+        const double v = l >= begin && l <= end ? value(l) : first;
+        best = first * v > 0.0 ? std::min(best, std::fabs(v)) : 0.0;  // a change of sign passes zero
+    };
+    at(end);
+    if (c == 0.0) {  // roots of a + 3 b l + 5 c l^2
+        if (b != 0.0) at(-a / (3.0 * b));
+    } else {
+        const double d = 9.0 * b * b - 20.0 * a * c;
+        if (d >= 0.0) {
+            at((-3.0 * b + std::sqrt(d)) / (10.0 * c));
+            at((-3.0 * b - std::sqrt(d)) / (10.0 * c));
+        }
+    }
+    return best;
 }
 
 inline BlockSchedule plan_blocks_schedule(const muon_ns_coeff *c, int n) {
     BlockSchedule out;
     if (n > kMaxChainSteps) return out;
-    double x = 1.0, p = 1.0;  // bounds of |X| and |P|
+    double x = 1.0, p = 1.0;                                            // bounds of |X| and |P|
+    double least = 1.0 / std::sqrt(static_cast<double>(kBlockSide));  // of X's largest singular value
     for (int k = 0; k < n; ++k) {
         const double top = x * x;
         const double q = polynomial_bound(c[k].a, c[k].b, c[k].c, 0, top);
         const double r = polynomial_bound(c[k].a, c[k].b, c[k].c, 1, top);
-        out.exp_in.push_back(pair_exponent(p));
         const double next = map_bound(c[k].a, c[k].b, c[k].c, x);
         p *= q;
-        if (!(q <= 60.0 && r <= 60.0 && next <= 3.9 && p <= 0x1p60)) return out;
-        x = std::max(next, 0x1p-20);
+        if (!(q <= 60.0 && r <= 60.0 && next <= 3.9 && p <= kMaxGain)) return out;
+        least = map_least(c[k].a, c[k].b, c[k].c, least, x);
+        if (!(least >= kLeastSigma)) return out;
+        x = next;
     }
-    out.last_exp = pair_exponent(p);
     out.fits = true;
     // A step multiplies what noise has put in the directions of vanishing singular
     // values by a^2, relative to what Q makes of them.  A segment goes on while

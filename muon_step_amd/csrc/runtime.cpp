@@ -1857,6 +1857,9 @@ muon_status run_blocks(muon_context *ctx, const BlockRun &r, const muon_hparams 
     chain.s = g.s;
     chain.l = g.l;
     chain.parts = g.parts;
+    // N 2^shift has a 2-norm of sqrt(s l) / 2 to sqrt(s l), and P 2^-e N 2^shift, with |X| <= 4, shall stay
+    // below fp16's largest value
+    chain.poly_least = static_cast<int32_t>(std::ceil(0.5 * std::log2(static_cast<double>(g.s) * g.l))) - 13;
     const bool gb = like.grad_dtype == MUON_BF16, pb = like.param_dtype == MUON_BF16;
     const double gs = dtype_size(like.grad_dtype), ps = dtype_size(like.param_dtype);
     for (int64_t base = 0; base < total; base += n) {
@@ -1878,24 +1881,15 @@ muon_status run_blocks(muon_context *ctx, const BlockRun &r, const muon_hparams 
             chain.first = k == 0;
             chain.last = k + 1 == plan.segments.size();
             chain.steps = seg.steps;
-            int out = 0;
             for (int i = 0; i < seg.steps; ++i) {
                 const muon_ns_coeff &co = hp->schedule[seg.first + i];
-                const size_t next = static_cast<size_t>(seg.first + i + 1);
-                out = next < plan.exp_in.size() ? plan.exp_in[next] : plan.last_exp;
                 chain.step[i] = muon::BlockChain::Step{static_cast<float>(co.a), static_cast<float>(co.b),
-                                                       static_cast<float>(co.c), plan.exp_in[seg.first + i], out};
+                                                       static_cast<float>(co.c)};
             }
-            // P's fragments as P 2^-at: N 2^shift has a 2-norm of sqrt(s l) / 2 to sqrt(s l),
-            // and P N, with |X| <= 4, shall stay below fp16's largest value
-            const int at = std::max(out, static_cast<int>(std::ceil(0.5 * std::log2(static_cast<double>(g.s) * g.l))) - 13);
-            chain.poly_scale = c.poly_scale;
-            chain.out_scale = std::ldexp(1.0f, (seg.steps > 0 ? out : 0) - at);
             e = timed(ctx, ST_BLOCKS_CHAIN, static_cast<double>(now) * seg.steps * 3 * side * side * (side + 1), 0.0, st, [&] {
                 return muon::launch_blocks_chain(chain, static_cast<uint32_t>(now), st);
             });
             if (e != hipSuccess) return hip_fail(ctx, e, "block polynomial launch");
-            c.poly_scale = std::ldexp(1.0f, at);
         }
         e = timed(ctx, ST_BLOCKS_UPDATE, elems * 2 * side, elems * (4.0 + gs + 2 * ps), st, [&] {
             return muon::launch_blocks_update(t, c, static_cast<uint32_t>(now), g.tall, gb, pb, st);
