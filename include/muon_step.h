@@ -431,9 +431,11 @@ muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
  *     X <- a X + b (X X^T) X + c (X X^T)^2 X  for each step of the schedule,
  *     W <- (1 - lr wd) W - lr O,  O as hp's scale_mode says, RMS block by block.
  * M has muon_step's bits (and hp's grad_factor its meaning).  Operands of the
- * products are fp32 values as pairs of 16-bit parts, so X is far closer to the
- * exact iteration than MUON_NS_BF16's (relative Frobenius error 1e-6 to 3e-5, to
- * 3e-4 for squares, whose smallest singular values are small indeed); hp's
+ * products are fp32 values as pairs of 16-bit parts, sums are fp32, so X is far
+ * closer to the exact iteration than MUON_NS_BF16's.  Relative Frobenius error of
+ * the default schedule: 1e-6 on blocks whose singular values lie within a factor
+ * of ten, 1e-5 to 3e-5 where they spread over three decades, 1e-4 to 3e-4 for squares,
+ * whose smallest ones are small indeed; hp's
  * ns_precision must be MUON_NS_BF16 (MUON_NS_F32: UNSUPPORTED).  The schedule
  * must keep every singular value of [0, 1] within 3.9 at each step, with
  * |a + b x + c x^2| and its product with x at most 60 on the x it meets, the

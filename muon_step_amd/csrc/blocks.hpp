@@ -20,7 +20,7 @@
 // Products run on the matrix cores with each fp32 operand as a sum of two
 // 16-bit parts, hi and lo, and three products hi hi + hi lo + lo hi in fp32
 // accumulators: bf16 parts (16 bits of significand), and lo lo too, for the first
-// N N^T, whose scale is not known before it, fp16 parts (21 bits) of suitably
+// N N^T, whose scale is not known before it, fp16 parts (23 bits) of suitably
 // scaled matrices everywhere else.
 //
 // Index basis of the smaller side.  A wave reads 32 lanes x T tiles of it; where

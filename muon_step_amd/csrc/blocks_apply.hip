@@ -103,7 +103,7 @@ template <int T, int V, bool TALL, bool BF16, bool EVEN> struct Stream {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_ldexpf(x[e], left_shift);
         }
-        split_half(x, hi, lo);
+        split_half<false>(x, hi, lo);
     }
 
   private:
@@ -267,7 +267,7 @@ __device__ __forceinline__ void regram_columns(Triangle<T> &sum, Stream<T, V, TA
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = acc[v][i][8 * q + e];
-                    split_half(x, hi[i], lo[i]);
+                    split_half<false>(x, hi[i], lo[i]);
                 }
                 sum.add(hi, lo);
                 __builtin_amdgcn_sched_barrier(0);

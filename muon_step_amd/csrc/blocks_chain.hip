@@ -35,7 +35,7 @@ template <int T> __device__ __forceinline__ void split_chunk(const Slab<T> &m, i
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = m.v[c >> 1][8 * (c & 1) + e];
-    split_half(x, hi, lo);
+    split_half<true>(x, hi, lo);
 }
 // left^T times the columns whose fragments `right(b, c, hi, lo)` gives, for B
 // right operands at once; every chunk's fragments are fetched and split during
@@ -363,7 +363,7 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = sh.rows[col][16 * k + 8 * (e >> 2) + 4 * h + (e & 3)];
         half8 hi, lo;
-        split_half(x, hi, lo);
+        split_half<true>(x, hi, lo);
         frag[(wave * 2 * T + k) * 64 + lane] = hi;
         frag[T * T * 128 + (wave * 2 * T + k) * 64 + lane] = lo;
     }

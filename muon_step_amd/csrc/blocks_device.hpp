@@ -10,7 +10,6 @@ namespace muon {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-typedef __fp16 fp16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;  // of a streaming workgroup (sum_tile adds up as many)
 constexpr int kThreads = kWaves * 64;
@@ -27,18 +26,25 @@ __device__ __forceinline__ floatx16 mfma(bf16x8 a, bf16x8 b, floatx16 c) {
 // The row of an accumulator's register r in lane half h.
 __device__ __forceinline__ int acc_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
-// x = hi + lo to 2^-21 of x (both parts truncated, two values an instruction),
-// |x| below 65504; parts below 2^-24 are lost.
-__device__ __forceinline__ void split_half(const float (&x)[8], half8 &hi, half8 &lo) {
+// x = hi + lo to 2^-24 of x, each part rounded to nearest (two values an instruction),
+// |x| below 65504; parts below 2^-25 are lost.  Truncated parts (2% faster in the
+// chain) err to one side, and what lo lo leaves out adds up: O is 3e-6 off on even
+// spectra instead of 1e-6.
+// HI: which parts the compiler has to hold as two to a register from the conversion
+// on.  Left to itself, or told of the others, it spills 53 to 74 registers in the chain
+// (HI) and up to 29 in X X^T (low parts; 128 blocks of 128 x 4096 568 us instead of 558).
+template <bool HI> __device__ __forceinline__ void split_half(const float (&x)[8], half8 &hi, half8 &lo) {
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
-        const uint32_t h = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(x[k], x[k + 1]));
+        uint32_t h = __builtin_bit_cast(uint32_t, half2_t{static_cast<_Float16>(x[k]), static_cast<_Float16>(x[k + 1])});
+        if constexpr (HI) asm("" : "+v"(h));
         // x - hi, with the conversion of hi in the same instruction
         float d0, d1;
         asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel_hi:[1,0,0]" : "=v"(d0) : "v"(h), "v"(x[k]));
         asm("v_fma_mix_f32 %0, -%1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(d1) : "v"(h), "v"(x[k + 1]));
-        const half2_t l = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_pkrtz(d0, d1));
-        const half2_t hh = __builtin_bit_cast(half2_t, h);
+        uint32_t lw = __builtin_bit_cast(uint32_t, half2_t{static_cast<_Float16>(d0), static_cast<_Float16>(d1)});
+        if constexpr (!HI) asm("" : "+v"(lw));
+        const half2_t hh = __builtin_bit_cast(half2_t, h), l = __builtin_bit_cast(half2_t, lw);
         hi[k] = hh[0];
         hi[k + 1] = hh[1];
         lo[k] = l[0];

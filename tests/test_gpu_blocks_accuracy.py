@@ -1,21 +1,28 @@
-"""How far muon_blocks_step's O is from the iteration in 64 bits: schedules of every length that is taken.
+"""How far muon_blocks_step's O is from the iteration in 64 bits: schedules of every length that is taken, and spectra.
 
 SHORT: blocks whose singular values lie within a factor of ten.  Every product's operands are pairs of 16-bit parts, 2^-20
 of an operand at most with the part that falls out.  Where nothing grows them, errors of steps add up like independent
 ones, and 3e-5 is what the header gives for any of them.  A schedule that does not settle (the quintic's singular values
 keep moving between 0.68 and 1.21) passes a relative error of a singular value on by sigma f'(sigma) / f(sigma) a step;
-`sensitivity` is the root mean square of what a whole schedule makes of it, and any arithmetic's error has that factor."""
+`sensitivity` is the root mean square of what a whole schedule makes of it, and any arithmetic's error has that factor.
+
+EVEN: the same blocks in 1e-6, which the header gives, times a margin of 4.  Both parts of a pair are rounded to nearest, 2^-24
+of the operand together, and lo lo is left out, 2^-24 again: a product of two is off by 3 x 2^-24, its fp32 sums over up to 24
+accumulations by about as much, and the three products of a step by 10 (the coefficients' magnitudes) x 2^-22 = 2.4e-6 at most;
+they are independent, and the schedule settles what it does not move.  WIDE, SQUARE: the header's figures for spectra over three
+decades, where the noise of A grows by a^2 a step in small directions; a margin of two for squares, whose smallest singular
+values are a matter of luck."""
 
 import numpy as np
 import pytest
 
 import muon_step_amd as ms
 from gpu_util import rel_fro, say
-from test_gpu_blocks import HYBRID, LR, MU, WD, GAMMA, Weight, exact_o, step
+from test_gpu_blocks import HYBRID, MU, Weight, exact_o, step
 
 pytestmark = pytest.mark.gpu
 
-SHORT = 3e-5
+SHORT, EVEN, WIDE, SQUARE = 3e-5, 4e-6, 3e-5, 6e-4
 QUINTIC, CUBIC, SLOW = (3.4445, -4.7750, 2.0315), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0)
 
 
@@ -64,3 +71,25 @@ def test_schedules_of_every_length(ctx, shape):
             for err, k in errors(w, coeffs):
                 assert err <= SHORT * k, f"{len(coeffs)} steps from {coeffs[0]}: {err:.2e}, sensitivity {k:.1f}"
         say(shape, len(coeffs), coeffs[0][0], "%.1e of %.1f" % max(errors(wide, coeffs)))
+
+
+@pytest.mark.parametrize("shape", [(1, 64), (7, 300), (16, 2048), (32, 500), (33, 400), (64, 1000), (72, 700), (96, 1536), (128, 2048)])
+def test_even_spectra(ctx, shape):
+    for coeffs in (HYBRID, [QUINTIC] * 5, [QUINTIC] * 12, [CUBIC] * 20, [SLOW] * 10, [SLOW] * 37, []):
+        rng = np.random.default_rng(len(coeffs) + 1)
+        weights = [Weight(rng, (2, 1), shape, "f32", "f32"), Weight(rng, (1, 2), shape[::-1], "f32", "f32")]
+        step(ctx, weights, coeffs=coeffs)
+        found = [e for w in weights for e in errors(w, coeffs)]
+        say(shape, len(coeffs), coeffs[:1], ["%.1e of %.1f" % f for f in found])
+        assert all(err <= EVEN * k for err, k in found)
+
+
+@pytest.mark.parametrize("s, l, tol", [(16, 2048, WIDE), (48, 700, WIDE), (64, 1000, WIDE), (80, 1407, WIDE), (96, 1536, WIDE),
+                                       (128, 2048, WIDE), (128, 128, SQUARE), (64, 64, SQUARE)])
+def test_spread_spectra(ctx, s, l, tol):
+    rng = np.random.default_rng(6)
+    weights = [Weight(rng, (2, 1), (s, l), "f32", "f32", "spread"), Weight(rng, (1, 2), (l, s), "bf16", "f32", "spread")]
+    step(ctx, weights)
+    found = [err for w in weights for err, _ in errors(w, HYBRID)]
+    say(s, l, ["%.1e" % f for f in found])
+    assert max(found) <= tol
