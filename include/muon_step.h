@@ -433,9 +433,12 @@ muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
  * M has muon_step's bits (and hp's grad_factor its meaning).  Operands of the
  * products are fp32 values as pairs of 16-bit parts, sums are fp32, so X is far
  * closer to the exact iteration than MUON_NS_BF16's.  Relative Frobenius error of
- * the default schedule: 1e-6 on blocks whose singular values lie within a factor
+ * the named schedules: 1e-6 on blocks whose singular values lie within a factor
  * of ten, 1e-5 to 3e-5 where they spread over three decades, 1e-4 to 3e-4 for squares,
- * whose smallest ones are small indeed; hp's
+ * whose smallest ones are small indeed; below full rank a few times 2^-24 of the
+ * schedule's gain (below; 4e-3 to 1e-2 for "deepseekv4").  A schedule that does not settle
+ * multiplies this by its own sensitivity to its input (the quintic's singular values
+ * keep moving: 1 to 2 after 5 steps, up to 20 after 12); hp's
  * ns_precision must be MUON_NS_BF16 (MUON_NS_F32: UNSUPPORTED).  The schedule
  * must keep every singular value of [0, 1] within 3.9 at each step, with
  * |a + b x + c x^2| and its product with x at most 60 on the x it meets, the

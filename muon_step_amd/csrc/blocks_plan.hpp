@@ -111,22 +111,30 @@ inline BlockSchedule plan_blocks_schedule(const muon_ns_coeff *c, int n) {
     }
     out.fits = true;
     // A step multiplies what noise has put in the directions of vanishing singular
-    // values by a^2, relative to what Q makes of them.  A segment goes on while
-    // that stays below 2^11 times fp32's rounding (1e-4 of a small direction's
-    // gain); the last one, whose noise no later step can grow, up to 2^17.
+    // values by a^2, relative to what Q makes of them.  A segment goes on while that
+    // stays below 2^11 times fp32's rounding (1e-4 of a small direction's gain); the last
+    // one, whose noise no later step can grow, up to 2^17.  Both hold where the
+    // schedule's last two steps settle what noise does to singular values near 1;
+    // otherwise O shows it as it is, and no segment may pass 2^8.
     // Error against 64 bits on spectra over three decades, s of 16 to 128 in long
-    // blocks and (in squares), emulated: the hybrid schedule as 4 + 6 steps 6e-6 to
-    // 1.1e-5 (1.9e-4), as 3 + 7 5e-6 to 9e-6 (2e-3), as 5 + 5 3e-5 to 1.1e-4 (1e-4), as
-    // 2 + 3 + 5, which is another pass over M and G, 5e-6 (7e-5).
+    // blocks and (in squares), emulated: the hybrid schedule as 4 + 6 steps 1.3e-5
+    // (1.9e-4), as 3 + 7 4e-6 to 1.1e-5 (1.2e-3), as 5 + 5 7e-5 (1.7e-4), as 2 + 3 + 5, which
+    // is another pass over M and G, 4e-6 to 1e-5 (1.4e-4).  Five quintic steps as one
+    // segment 8e-5 to 1.5e-4, as 3 + 2 6e-6; twelve as 4 + 4 + 4 1e-4 to 2e-4, as four times
+    // three 1e-5 to 3e-5.  Each segment is another pass: five quintic steps over 1728 heads
+    // of 128 x 2048 take 3.28 ms as 3 + 2, 2.52 as one.
     auto gain = [&](int k) { return std::max(1.0, c[k].a * c[k].a); };
+    auto settles = [&](int k) { return k >= 0 && std::fabs(c[k].a + 3.0 * c[k].b + 5.0 * c[k].c) < 0.25; };  // |f'(1)|
+    const bool settled = settles(n - 1) && settles(n - 2);
+    const double most = settled ? 0x1p11 : 0x1p8, most_last = settled ? 0x1p17 : 0x1p8;
     int at = 0;
     while (at < n) {
         double rest = 1.0;
         for (int k = at; k + 1 < n; ++k) rest *= gain(k);
         int steps = n - at;
-        if (rest > 0x1p17) {
+        if (rest > most_last) {
             double g = 1.0;
-            for (steps = 1; at + steps < n && (g *= gain(at + steps - 1)) <= 0x1p11; ++steps) {
+            for (steps = 1; at + steps < n && (g *= gain(at + steps - 1)) <= most; ++steps) {
             }
         }
         out.segments.push_back(BlockSegment{at, steps});

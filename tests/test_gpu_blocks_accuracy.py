@@ -11,7 +11,8 @@ of the operand together, and lo lo is left out, 2^-24 again: a product of two is
 accumulations by about as much, and the three products of a step by 10 (the coefficients' magnitudes) x 2^-22 = 2.4e-6 at most;
 they are independent, and the schedule settles what it does not move.  WIDE, SQUARE: the header's figures for spectra over three
 decades, where the noise of A grows by a^2 a step in small directions; a margin of two for squares, whose smallest singular
-values are a matter of luck."""
+values are a matter of luck.  DEFICIENT: P's rounding, 2^-24 of its largest entries, which are the schedule's gain where N has
+no direction, meets all of N; a product has two roundings of P's and N's each: four times that."""
 
 import numpy as np
 import pytest
@@ -22,7 +23,7 @@ from test_gpu_blocks import HYBRID, MU, Weight, exact_o, step
 
 pytestmark = pytest.mark.gpu
 
-SHORT, EVEN, WIDE, SQUARE = 3e-5, 4e-6, 3e-5, 6e-4
+SHORT, EVEN, WIDE, SQUARE, DEFICIENT = 3e-5, 4e-6, 3e-5, 6e-4, 4 * 2.0 ** -24 * 3.4445 ** 8 * 4
 QUINTIC, CUBIC, SLOW = (3.4445, -4.7750, 2.0315), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0)
 
 
@@ -93,3 +94,34 @@ def test_spread_spectra(ctx, s, l, tol):
     found = [err for w in weights for err, _ in errors(w, HYBRID)]
     say(s, l, ["%.1e" % f for f in found])
     assert max(found) <= tol
+
+
+@pytest.mark.parametrize("shape", [(16, 2048), (33, 400), (72, 700), (128, 2048)])
+def test_spread_spectra_of_other_schedules(ctx, shape):
+    """Ones that settle and ones that do not, of every length."""
+    polar = [(8.2872, -23.5959, 17.3004), (4.1071, -2.9479, 0.5448), (3.9487, -2.9089, 0.5518)]
+    for coeffs in LENGTHS + [polar]:
+        rng = np.random.default_rng(len(coeffs))
+        weights = [Weight(rng, (2, 1), shape, "f32", "f32", "spread"), Weight(rng, (1, 2), shape[::-1], "f32", "f32", "spread")]
+        step(ctx, weights, coeffs=coeffs)
+        found = [e for w in weights for e in errors(w, coeffs)]
+        say(shape, len(coeffs), coeffs[0][0], "%.1e of %.1f" % max(found))
+        assert all(err <= WIDE * k for err, k in found)
+
+
+@pytest.mark.parametrize("s, l", [(8, 300), (16, 2048), (64, 1000), (128, 2048)])
+def test_ranks_below_the_smaller_side(ctx, s, l):
+    """A quarter of the directions, and nothing but the values' own rounding in the others."""
+    import torch
+    rng = np.random.default_rng(8)
+    weights = [Weight(rng, (2, 1), (s, l), "f32", "f32"), Weight(rng, (1, 2), (l, s), "f32", "f32")]
+    for w in weights:
+        left = rng.standard_normal((w.shape[0] // w.grid[0], s // 4)), rng.standard_normal((s // 4, w.shape[1] // w.grid[1]))
+        full = np.tile(left[0] @ left[1], w.grid).astype(np.float32)
+        for name in ("grad", "momentum"):
+            w.dev[name].copy_(torch.from_numpy(full))
+            w.before[name] = full
+    step(ctx, weights)
+    found = [err for w in weights for err, _ in errors(w, HYBRID)]
+    say(s, l, ["%.1e" % f for f in found])
+    assert max(found) <= DEFICIENT
