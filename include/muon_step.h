@@ -435,7 +435,8 @@ muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
  * closer to the exact iteration than MUON_NS_BF16's.  Relative Frobenius error of
  * the named schedules: 1e-6 on blocks whose singular values lie within a factor
  * of ten, 1e-5 to 3e-5 where they spread over three decades, 1e-4 to 3e-4 for squares,
- * whose smallest ones are small indeed; below full rank a few times 2^-24 of the
+ * whose smallest ones are small indeed; of sides up to 16, which work in fp64, 2e-7, 2e-6
+ * and 1e-5; below full rank a few times 2^-24 of the
  * schedule's gain (below; 4e-3 to 1e-2 for "deepseekv4").  A schedule that does not settle
  * multiplies this by its own sensitivity to its input (the quintic's singular values
  * keep moving: 1 to 2 after 5 steps, up to 20 after 12); hp's

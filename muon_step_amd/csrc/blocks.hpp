@@ -14,6 +14,8 @@
 //     regram:    X = P N, the partial sums of X X^T               (reads G, M)
 //     chain:     the second segment's P
 //     update:    O = P N, W                                       (reads G, M, W; writes W)
+// Blocks with a smaller side of at most 16 take their sums and polynomials in fp64, in
+// which the schedule is one segment (blocks_narrow.hip): momentum, chain, update.
 // N is formed from M and G wherever it is needed: 6 bytes read an element, where
 // a stored X would be 4 written and 4 read.
 //
@@ -61,6 +63,11 @@ struct BlockTable {
 constexpr int kBlockSide = 128;      // largest smaller side of a block: four tiles of 32
 constexpr int kBlockUnit = 128;      // columns of X that a workgroup takes at once: 32 for each wave
 constexpr int kMaxChainSteps = 64;
+// Largest smaller side of blocks that are worked on in fp64: one tile of its matrix
+// instructions, whose products cost less there than their latency.  Sides of 17 to 32
+// would take eight times as many: 8.5 us of a CU for ten steps, or 340 us for 10000 blocks of
+// 32 x 256, which the other passes move in 300.
+constexpr int kNarrowSide = 16;
 
 // What one block needs between the launches (index: block of the launch).
 struct BlockScalars {
@@ -76,6 +83,7 @@ struct BlockPart {
 };
 struct BlockWork {
     float *gram;           // [block][part][tile], the lower triangle's tiles as lanes hold them
+    double *narrow;        // [block][part]: the same of a side of kNarrowSide
     BlockPart *parts;      // [block][part]
     _Float16 *poly;        // [block]: P's rows as operand fragments, hi then lo
     float *poly_own;       // [block]: P's columns as the chain holds them
@@ -108,11 +116,26 @@ struct BlockChain {
     } step[kMaxChainSteps];
 };
 
+// All steps of the schedule, for sides up to kNarrowSide.
+struct NarrowChain {
+    BlockWork w;
+    int32_t s, l, parts, steps;
+    int32_t unit_rms, poly_least;  // as in BlockChain
+    float update;
+    int32_t pad_;
+    struct Step {
+        double a, b, c;
+    } step[kMaxChainSteps];
+};
+
 inline int block_tiles(int64_t s) { return static_cast<int>((s + 31) / 32); }
 
 hipError_t launch_blocks_momentum(const BlockTable &t, const BlockCall &c, uint32_t blocks, bool tall, bool grad_bf16,
                                   hipStream_t st);
 hipError_t launch_blocks_chain(const BlockChain &c, uint32_t blocks, hipStream_t st);
+hipError_t launch_narrow_momentum(const BlockTable &t, const BlockCall &c, uint32_t blocks, bool tall, bool grad_bf16,
+                                  hipStream_t st);
+hipError_t launch_narrow_chain(const NarrowChain &c, uint32_t blocks, hipStream_t st);
 hipError_t launch_blocks_regram(const BlockTable &t, const BlockCall &c, uint32_t blocks, bool tall, bool grad_bf16,
                                 hipStream_t st);
 hipError_t launch_blocks_update(const BlockTable &t, const BlockCall &c, uint32_t blocks, bool tall, bool grad_bf16,

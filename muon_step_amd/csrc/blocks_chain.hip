@@ -356,17 +356,7 @@ template <int T> __global__ __launch_bounds__(64 * T, 1) void blocks_chain_kerne
             sh.rows[32 * t + acc_row(r, h)][col] = x * part;
         }
     __syncthreads();
-    half8 *frag = reinterpret_cast<half8 *>(c.w.poly) + block * (T * T * 256);
-#pragma unroll
-    for (int k = 0; k < 2 * T; ++k) {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = sh.rows[col][16 * k + 8 * (e >> 2) + 4 * h + (e & 3)];
-        half8 hi, lo;
-        split_half<true>(x, hi, lo);
-        frag[(wave * 2 * T + k) * 64 + lane] = hi;
-        frag[T * T * 128 + (wave * 2 * T + k) * 64 + lane] = lo;
-    }
+    store_poly<T>(c.w.poly, block, sh.rows, wave, lane);
 }
 
 }  // namespace

@@ -66,6 +66,24 @@ __device__ __forceinline__ void split_bf(const float (&x)[8], bf16x8 &hi, bf16x8
 constexpr int kLogScaleQ = 4;
 constexpr float kScaleA = 64.0f, kScaleQ = 1 << kLogScaleQ;
 
+// The rows 32 wave .. 32 wave + 31 of a block's P as operand fragments, hi and lo.
+template <int T>
+__device__ __forceinline__ void store_poly(_Float16 *poly, int64_t block, const float (&rows)[32 * T][32 * T + 4], int wave,
+                                           int lane) {
+    half8 *frag = reinterpret_cast<half8 *>(poly) + block * (T * T * 256);
+    const int h = lane >> 5;
+#pragma unroll
+    for (int k = 0; k < 2 * T; ++k) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = rows[32 * wave + (lane & 31)][16 * k + 8 * (e >> 2) + 4 * h + (e & 3)];
+        half8 hi, lo;
+        split_half<true>(x, hi, lo);
+        frag[(wave * 2 * T + k) * 64 + lane] = hi;
+        frag[T * T * 128 + (wave * 2 * T + k) * 64 + lane] = lo;
+    }
+}
+
 // ---------------------------------------------------------------- places in memory
 
 // A block: its addresses, whatever its weight.

@@ -1774,8 +1774,12 @@ constexpr size_t kBlockMemory = size_t(256) << 20;
 
 struct BlockShape {
     int32_t s, l, parts, part_len;
-    bool tall;
+    bool tall, narrow;
     size_t per_block;
+    size_t sums() const {  // bytes of a part's sums
+        const size_t t = muon::block_tiles(s);
+        return narrow ? 2048 : t * (t + 1) / 2 * 4096;
+    }
 };
 BlockShape block_shape(const muon_block_matrix &m, int64_t blocks) {
     BlockShape g{};
@@ -1786,8 +1790,9 @@ BlockShape block_shape(const muon_block_matrix &m, int64_t blocks) {
     const int64_t parts = std::max<int64_t>(1, std::min(most, (kBlockWorkgroups + blocks - 1) / blocks));
     g.part_len = static_cast<int32_t>(round_up((g.l + parts - 1) / parts, muon::kBlockUnit));
     g.parts = (g.l + g.part_len - 1) / g.part_len;
+    g.narrow = g.s <= muon::kNarrowSide;
     const size_t t = muon::block_tiles(g.s);
-    g.per_block = g.parts * (t * (t + 1) / 2 * 4096 + sizeof(muon::BlockPart)) + t * t * 8192 + sizeof(muon::BlockScalars);
+    g.per_block = g.parts * (g.sums() + sizeof(muon::BlockPart)) + t * t * 8192 + sizeof(muon::BlockScalars);
     return g;
 }
 
@@ -1832,7 +1837,9 @@ muon_status run_blocks(muon_context *ctx, const BlockRun &r, const muon_hparams 
         at += align_up(bytes);
         return p;
     };
-    c.w.gram = reinterpret_cast<float *>(take(n * g.parts * tiles * (tiles + 1) / 2 * 4096));
+    char *sums = take(n * g.parts * g.sums());
+    c.w.gram = reinterpret_cast<float *>(sums);
+    c.w.narrow = reinterpret_cast<double *>(sums);
     c.w.poly = reinterpret_cast<_Float16 *>(take(n * tiles * tiles * 4096));
     c.w.poly_own = reinterpret_cast<float *>(take(n * tiles * tiles * 4096));
     c.w.parts = reinterpret_cast<muon::BlockPart *>(take(n * g.parts * sizeof(muon::BlockPart)));
@@ -1860,6 +1867,19 @@ muon_status run_blocks(muon_context *ctx, const BlockRun &r, const muon_hparams 
     // N 2^shift has a 2-norm of sqrt(s l) / 2 to sqrt(s l), and P 2^-e N 2^shift, with |X| <= 4, shall stay
     // below fp16's largest value
     chain.poly_least = static_cast<int32_t>(std::ceil(0.5 * std::log2(static_cast<double>(g.s) * g.l))) - 13;
+    muon::NarrowChain narrow{};
+    if (g.narrow) {
+        narrow.w = c.w;
+        narrow.s = g.s;
+        narrow.l = g.l;
+        narrow.parts = g.parts;
+        narrow.steps = hp->num_ns_steps;
+        narrow.unit_rms = chain.unit_rms;
+        narrow.poly_least = chain.poly_least;
+        narrow.update = chain.update;
+        for (int i = 0; i < hp->num_ns_steps; ++i)
+            narrow.step[i] = muon::NarrowChain::Step{hp->schedule[i].a, hp->schedule[i].b, hp->schedule[i].c};
+    }
     const bool gb = like.grad_dtype == MUON_BF16, pb = like.param_dtype == MUON_BF16;
     const double gs = dtype_size(like.grad_dtype), ps = dtype_size(like.param_dtype);
     for (int64_t base = 0; base < total; base += n) {
@@ -1867,10 +1887,16 @@ muon_status run_blocks(muon_context *ctx, const BlockRun &r, const muon_hparams 
         const double elems = static_cast<double>(now) * g.s * g.l, side = g.s;
         c.base = static_cast<uint32_t>(base);
         hipError_t e = timed(ctx, ST_BLOCKS_MOMENTUM, elems * (side + 1), elems * (8.0 + gs), st, [&] {
-            return muon::launch_blocks_momentum(t, c, static_cast<uint32_t>(now), g.tall, gb, st);
+            return g.narrow ? muon::launch_narrow_momentum(t, c, static_cast<uint32_t>(now), g.tall, gb, st)
+                            : muon::launch_blocks_momentum(t, c, static_cast<uint32_t>(now), g.tall, gb, st);
         });
         if (e != hipSuccess) return hip_fail(ctx, e, "block momentum launch");
-        for (size_t k = 0; k < plan.segments.size(); ++k) {
+        if (g.narrow) {
+            e = timed(ctx, ST_BLOCKS_CHAIN, static_cast<double>(now) * narrow.steps * 3 * side * side * (side + 1), 0.0, st,
+                      [&] { return muon::launch_narrow_chain(narrow, static_cast<uint32_t>(now), st); });
+            if (e != hipSuccess) return hip_fail(ctx, e, "block polynomial launch");
+        }
+        for (size_t k = 0; k < plan.segments.size() && !g.narrow; ++k) {
             const muon::BlockSegment &seg = plan.segments[k];
             if (k > 0) {
                 e = timed(ctx, ST_BLOCKS_REGRAM, elems * (3 * side + 1), elems * (4.0 + gs), st, [&] {
