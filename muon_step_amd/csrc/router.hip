@@ -304,24 +304,28 @@ __device__ __forceinline__ double balance_rows(const RouterDesc &d, const Router
         if constexpr (SIGMOID) {
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
-                // sigma and 1 - sigma, each without cancellation; past x = -87.2 sigma is held at 1.25e-38:
-                // v_rcp_f32 gives zero for what lies below the smallest normal number, 1.18e-38
-                const float e = exp_of(-x[k]), z = e > 8e37f ? 8e37f : e;  // a NaN stays one
-                w[k] = __builtin_amdgcn_rcpf(1.0f + z);
-                q[k] = z * w[k];
+                // sigma and 1 - sigma, each without cancellation.  v_rcp_f32 gives zero for what lies below the
+                // smallest normal number: a sigma below 1.18e-38 is zero, as one of a logit of -infinity is
+                const float e = exp_of(-x[k]);
+                w[k] = __builtin_amdgcn_rcpf(1.0f + e);
+                q[k] = fminf(e, 3e38f) * w[k];  // a NaN is one in w
             }
             if (there < at<LANES>(PER - 1) + 1) {
 #pragma unroll
                 for (int k = 0; k < PER; ++k) w[k] = at<LANES>(k) < there ? w[k] : 0.0f;
             }
             add();
-            // rows whose sigmoids all vanish in fp32: there sigma(x) is exp(x)
-            const bool vanish = taking && sum < 1e-30f;
+            // rows whose sigmoids are all small: there sigma(x) is exp(x) and 1 - sigma(x) is 1, to fp32's last bit,
+            // and no score need be below the smallest normal number
+            const bool vanish = taking && sum < 0x1p-26f;
             if (__any(vanish)) {
                 float other[PER];
                 shifted(other);
 #pragma unroll
-                for (int k = 0; k < PER; ++k) w[k] = vanish ? other[k] : w[k];
+                for (int k = 0; k < PER; ++k) {
+                    w[k] = vanish ? other[k] : w[k];
+                    q[k] = vanish ? 1.0f : q[k];
+                }
                 add();
             }
         } else {
