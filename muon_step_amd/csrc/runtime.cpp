@@ -2127,9 +2127,9 @@ muon_status router_balance_impl(muon_context *ctx, const muon_router *rs, int64_
     }
     if (words > 0) {
         const bool graph = capturing(st);
-        const void *before = ctx->routers.p;
+        const size_t before = ctx->routers.n;
         s = ensure(ctx, ctx->routers, words * 4, "router counts", graph);
-        if (ctx->routers.p != before) ctx->routers_clear = 0;
+        if (ctx->routers.n != before) ctx->routers_clear = 0;  // other memory, at whatever address
         if (s != MUON_OK) return s;
         s = ensure(ctx, ctx->router_sums, sums * 8, "router workspace", graph);
         if (s != MUON_OK) return s;
