@@ -63,9 +63,11 @@ __device__ __forceinline__ bool takes_part(const RouterDesc &d, int token, int s
 
 // Adds the choices of tokens [begin, end), a token for each thread at a time, to
 // `own`, which holds the counts of the sequences from s0 on (`window` of them),
-// and to hist past those.
-__device__ __forceinline__ void count_tokens(const RouterDesc &d, int begin, int end, int s0, int s1, uint32_t *own, int window) {
+// and to hist past those.  Returns how many sequences the thread has given their first
+// token in hist.
+__device__ __forceinline__ int count_tokens(const RouterDesc &d, int begin, int end, int s0, int s1, uint32_t *own, int window) {
     const int stride = d.experts + 1, top = d.top_k;
+    int found = 0;
     for (int token = begin + threadIdx.x; token < end; token += blockDim.x) {
         const int s = sequence_of(d, token, s0, s1);
         const bool in = takes_part(d, token, s);
@@ -79,7 +81,12 @@ __device__ __forceinline__ void count_tokens(const RouterDesc &d, int begin, int
             else
                 atomicAdd(to + i, 1u);
         };
-        if (in) add(d.experts);
+        if (in) {
+            if (near)
+                add(d.experts);
+            else
+                found += atomicAdd(to + d.experts, 1u) == 0;
+        }
         for (int j0 = 0; j0 < top; j0 += 4) {
             int64_t x[4];
 #pragma unroll
@@ -93,10 +100,15 @@ __device__ __forceinline__ void count_tokens(const RouterDesc &d, int begin, int
                 if (in && j0 + j < top && x[j] >= 0 && x[j] < d.experts) add(static_cast<int>(x[j]));
         }
     }
+    return found;
 }
 
 // Counts of the sequences that the workgroup's tokens begin with are gathered in
-// shared memory, as many as fit there.
+// shared memory, as many as fit there.  Whoever gives a sequence its first token counts
+// it as one that has any: the pass over the logits needs their number.  Looking through
+// all sequences there, in every workgroup, is no faster where they are few (one layer in 5
+// sequences 17.4 us, 17.2 so) and was, with one workgroup to a router in the last launch,
+// most of 427 us at 4096 sequences of 256 experts, which take 80 now.
 __global__ __launch_bounds__(kRouterThreads) void router_count_kernel(const RouterTable t, const RouterCall c) {
     __shared__ uint32_t own[kCountWords];
     const Owners<64> owners(t.first);
@@ -109,10 +121,20 @@ __global__ __launch_bounds__(kRouterThreads) void router_count_kernel(const Rout
     const int window = min(kCountWords / stride, s1 - s0 + 1);
     for (int k = threadIdx.x; k < window * stride; k += kRouterThreads) own[k] = 0;
     __syncthreads();
-    count_tokens(d, begin, end, s0, s1, own, window);
+    int found = count_tokens(d, begin, end, s0, s1, own, window);
+    __syncthreads();
+    uint32_t *hist = d.hist + static_cast<int64_t>(s0) * stride;
+    for (int k = threadIdx.x * stride + d.experts; k < window * stride; k += kRouterThreads * stride)
+        if (own[k] != 0) {
+            found += atomicAdd(hist + k, own[k]) == 0;
+            own[k] = 0;
+        }
     __syncthreads();
     for (int k = threadIdx.x; k < window * stride; k += kRouterThreads)
-        if (own[k] != 0) atomicAdd(d.hist + static_cast<int64_t>(s0) * stride + k, own[k]);
+        if (own[k] != 0) atomicAdd(hist + k, own[k]);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) found += __shfl_xor(found, off, 64);
+    if ((threadIdx.x & 63) == 0 && found != 0) atomicAdd(c.live + e, static_cast<uint32_t>(found));
 }
 
 // The value of lane ^ OFF, for values that are the same in each OFF neighbours
@@ -365,32 +387,33 @@ __device__ __forceinline__ double block_sum(double x, double *sh) {
         for (uint32_t k = 0; k < blockDim.x >> 6; ++k) sum += sh[k];
     return sum;
 }
-// How many of the sequences have tokens.
-__device__ __forceinline__ int live_sequences(const RouterDesc &d, const uint32_t *hist, int *sh) {
-    if (threadIdx.x == 0) *sh = 0;
-    __syncthreads();
-    int found = 0;
-    for (int s = threadIdx.x; s < d.sequences; s += blockDim.x) found += hist[static_cast<int64_t>(s) * (d.experts + 1) + d.experts] != 0;
-    if (found) atomicAdd(sh, found);
-    __syncthreads();
-    return *sh;
-}
-
 template <int LANES, int PER, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(kRouterThreads) void router_balance_kernel(const RouterTable t, const RouterCall c) {
     __shared__ double sh_sum[kWaves];
-    __shared__ int sh_live;
     const Owners<64> owners(t.first);
     const int e = owners.of(blockIdx.x);
     const RouterDesc &d = t.d[e];
     const uint32_t mine = blockIdx.x - t.first[e];
+    if (mine == 0 && !c.accumulate)  // what the next launch adds to
+        for (int i = threadIdx.x; i < d.experts; i += kRouterThreads) as_global(d.counts)[i] = 0;
     const int begin = mine * c.per_block, end = min(begin + static_cast<int>(c.per_block), d.tokens);
     const int s0 = wave_sequence_of(d, begin), s1 = wave_sequence_of(d, end - 1);
-    const int live = live_sequences(d, d.hist, &sh_live);
+    const int live = static_cast<int>(as_global(c.live)[e]);
     const double loss = balance_rows<LANES, PER, BF16, SIGMOID>(d, c, d.hist + static_cast<int64_t>(s0) * (d.experts + 1), begin,
                                                                 end, s0, s1, live);
     const double sum = block_sum(loss, sh_sum);
     if (threadIdx.x == 0) d.sums[mine] = sum;
+}
+
+// How many of the sequences have tokens, by their counts in shared memory.
+__device__ __forceinline__ int live_sequences(const RouterDesc &d, const uint32_t *hist, int *sh) {
+    if (threadIdx.x == 0) *sh = 0;
+    __syncthreads();
+    int found = 0;
+    for (int s = threadIdx.x; s < d.sequences; s += blockDim.x) found += hist[s * (d.experts + 1) + d.experts] != 0;
+    if (found) atomicAdd(sh, found);
+    __syncthreads();
+    return *sh;
 }
 
 // Small batches: one workgroup for each router does all of it, counts in shared memory.
@@ -416,20 +439,25 @@ __global__ __launch_bounds__(kSmallThreads) void router_small_kernel(const Route
     }
 }
 
-constexpr int kFinishThreads = 1024;
-__global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(const RouterTable t, uint32_t blocks, const RouterCall c) {
+// One workgroup for each router and `slices` times kFinishWords of its counts, in
+// whole sequences: adds them up by experts and leaves them at zero; the first one
+// adds up the loss.
+__global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(const RouterTable t, uint32_t blocks, uint32_t slices,
+                                                                       const RouterCall c) {
     __shared__ double sh_sum[kFinishThreads / 64];
     __shared__ unsigned long long counts[kMaxExperts + 1];
     const int e = blockIdx.x;
     const RouterDesc &d = t.d[e];
     const uint32_t next = e + 1 < kRouters ? min(t.first[e + 1], blocks) : blocks, count = next - t.first[e];
     const uint32_t stride = d.experts + 1;
+    const int64_t slice = static_cast<int64_t>(finish_sequences(d.experts)) * slices * stride;
+    const int64_t begin = blockIdx.y * slice, end = min(begin + slice, static_cast<int64_t>(d.sequences) * stride);
+    if (blockIdx.y > 0 && begin >= end) return;
     for (uint32_t i = threadIdx.x; i < stride; i += kFinishThreads) counts[i] = 0;
     __syncthreads();
-    const int64_t words = static_cast<int64_t>(d.sequences) * stride;
     uint32_t i = threadIdx.x % stride;
     const uint32_t turn = kFinishThreads % stride;
-    for (int64_t k = threadIdx.x; k < words; k += kFinishThreads) {
+    for (int64_t k = begin + threadIdx.x; k < end; k += kFinishThreads) {
         const uint32_t n = as_global(d.hist)[k];
         if (n != 0) {
             atomicAdd(&counts[i], static_cast<unsigned long long>(n));
@@ -439,23 +467,25 @@ __global__ __launch_bounds__(kFinishThreads) void router_finish_kernel(const Rou
         if (i >= stride) i -= stride;
     }
     double sum = 0.0;
-    for (uint32_t k = threadIdx.x; k < count; k += kFinishThreads) sum += as_global(d.sums)[k];
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) sum += __shfl_down(sum, off, 64);
-    if ((threadIdx.x & 63) == 0) sh_sum[threadIdx.x >> 6] = sum;
-    __syncthreads();
+    if (blockIdx.y == 0)
+        for (uint32_t k = threadIdx.x; k < count; k += kFinishThreads) sum += as_global(d.sums)[k];
+    sum = block_sum(sum, sh_sum);  // (a barrier for the counts, too)
+    // of several workgroups each adds to the zeros that the pass over the logits has left (if it had any tokens)
+    const bool write = (gridDim.y == 1 || count == 0) && !c.accumulate;
     for (uint32_t k = threadIdx.x; k < stride - 1; k += kFinishThreads) {
-        const int64_t n = static_cast<int64_t>(counts[k]);
-        as_global(d.counts)[k] = c.accumulate ? as_global(d.counts)[k] + n : n;
+        if (write)
+            as_global(d.counts)[k] = static_cast<int64_t>(counts[k]);
+        else if (counts[k] != 0)
+            atomicAdd(reinterpret_cast<unsigned long long *>(d.counts) + k, counts[k]);
     }
-    if (threadIdx.x == 0) {
-        double all = 0.0;
-        for (int k = 0; k < kFinishThreads / 64; ++k) all += sh_sum[k];
-        *d.loss = static_cast<float>(all);
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        *d.loss = static_cast<float>(sum);
+        as_global(c.live)[e] = 0;
     }
 }
 
-__global__ __launch_bounds__(kRouterThreads) void router_clear_kernel(uint32_t *p, int64_t words) {
+__global__ __launch_bounds__(kRouterThreads) void router_clear_kernel(uint32_t *p, int64_t words, uint32_t *live) {
+    if (blockIdx.x == 0 && threadIdx.x < kRouters) live[threadIdx.x] = 0;
     for (int64_t k = static_cast<int64_t>(blockIdx.x) * kRouterThreads + threadIdx.x; k < words;
          k += static_cast<int64_t>(gridDim.x) * kRouterThreads)
         p[k] = 0;
@@ -531,14 +561,21 @@ hipError_t launch_router_small(const RouterTable &t, int routers, const RouterCa
 }
 
 hipError_t launch_router_finish(const RouterTable &t, int routers, uint32_t blocks, const RouterCall &c, hipStream_t st) {
-    hipLaunchKernelGGL(router_finish_kernel, dim3(routers), dim3(kFinishThreads), 0, st, t, blocks, c);
+    uint32_t most = 1;
+    for (int i = 0; i < routers; ++i) {
+        const uint32_t each = finish_sequences(t.d[i].experts), of = (t.d[i].sequences + each - 1) / each;
+        most = of > most ? of : most;
+    }
+    const uint32_t slices = (most + kFinishSlices - 1) / kFinishSlices;
+    hipLaunchKernelGGL(router_finish_kernel, dim3(routers, (most + slices - 1) / slices), dim3(kFinishThreads), 0, st, t, blocks,
+                       slices, c);
     return hipGetLastError();
 }
 
-hipError_t launch_router_clear(uint32_t *p, int64_t words, hipStream_t st) {
+hipError_t launch_router_clear(uint32_t *p, int64_t words, uint32_t *live, hipStream_t st) {
     const int64_t blocks = (words + kRouterThreads - 1) / kRouterThreads;
     hipLaunchKernelGGL(router_clear_kernel, dim3(static_cast<uint32_t>(blocks < 1024 ? blocks : 1024)), dim3(kRouterThreads), 0,
-                       st, p, words);
+                       st, p, words, live);
     return hipGetLastError();
 }
 

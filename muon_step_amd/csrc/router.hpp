@@ -30,6 +30,7 @@ struct RouterTable {
 struct RouterCall {
     double coef;
     const float *grad_scale;  // or nullptr
+    uint32_t *live;           // [router of the launch]: sequences that have tokens; zero between calls
     uint32_t per_block;       // tokens of a workgroup
     int32_t sigmoid, accumulate;
 };
@@ -38,6 +39,12 @@ constexpr int kRouterThreads = 256;
 constexpr int kMaxExperts = 1024;
 constexpr int kCountWords = 8192;    // counts that a workgroup has room for
 constexpr int kSmallThreads = 1024;
+constexpr int kFinishThreads = 1024;
+// Counts that one of the last launch's workgroups adds up, unless there would be more
+// of these than kFinishSlices.  131072 tokens of 256 experts take 50 us in 37 sequences,
+// 80 in 4096, of 64 experts 100 in 131072.
+constexpr int kFinishWords = 16384, kFinishSlices = 1024;
+__host__ __device__ inline uint32_t finish_sequences(int experts) { return kFinishWords / (experts + 1); }  // 15 at least
 // Routers whose logits, and 24 for each token's choices, are at most this many, and
 // whose counts fit a workgroup, are one workgroup's work each.  In us, as one launch
 // and as three: 2048 tokens of 8 experts 10.2 and 11.4, 4096 16.2 and 11.8; 512 of 64
@@ -67,8 +74,8 @@ hipError_t launch_router_small(const RouterTable &t, int routers, const RouterCa
 // Counts and loss from hist and sums (t.first: launch_router_balance's, and its
 // `blocks`); hist is zero behind it.
 hipError_t launch_router_finish(const RouterTable &t, int routers, uint32_t blocks, const RouterCall &c, hipStream_t st);
-// Zeroes memory that hist will lie in.
-hipError_t launch_router_clear(uint32_t *p, int64_t words, hipStream_t st);
+// Zeroes memory that hist will lie in, and `live`.
+hipError_t launch_router_clear(uint32_t *p, int64_t words, uint32_t *live, hipStream_t st);
 
 struct RouterBiasDesc {
     float *bias;

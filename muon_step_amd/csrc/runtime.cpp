@@ -960,6 +960,7 @@ struct muon_context {
     DevBuf routers;   // muon_router_balance's counts, zero between calls: captured calls rely on that
     size_t routers_clear = 0;  // words of it that are zero
     DevBuf router_sums;
+    uint32_t *router_live = nullptr;  // of fixed size, there from creation on, and zero between calls
     DevBuf blocks;    // muon_blocks_step's sums, polynomials and scalars
     std::vector<void *> retired;  // buffers that graphs may hold, and calls no longer
     // muon_grad_norm's sums: of a fixed size and there from creation on, so that
@@ -2025,6 +2026,7 @@ muon_status run_routers(muon_context *ctx, const RouterRun &r, const muon_balanc
     c.grad_scale = hp->grad_scale;
     c.sigmoid = hp->score == MUON_SCORE_SIGMOID;
     c.accumulate = hp->accumulate;
+    c.live = ctx->router_live;
     double count_bytes = 0, row_bytes = 0;
     for (int i = 0; i < n; ++i) {
         const muon_router &r = *rs[i];
@@ -2058,7 +2060,7 @@ muon_status run_routers(muon_context *ctx, const RouterRun &r, const muon_balanc
     const size_t clear = ctx->routers_clear;
     ctx->routers_clear = 0;  // until everything is enqueued
     if (clear < words) {
-        const hipError_t e = muon::launch_router_clear(hist + clear, static_cast<int64_t>(words - clear), st);
+        const hipError_t e = muon::launch_router_clear(hist + clear, static_cast<int64_t>(words - clear), ctx->router_live, st);
         if (e != hipSuccess) return hip_fail(ctx, e, "router workspace launch");
     }
     size_t at = 0;
@@ -2276,12 +2278,16 @@ muon_status muon_create(muon_context **out, int32_t hip_device, size_t workspace
             delete ctx;
             return MUON_ERR_DEVICE;
         }
-        void *zeros = std::calloc(1, sizeof(muon::NormWorkspace));
+        const size_t live = muon::kRouters * sizeof(uint32_t);
+        void *zeros = std::calloc(1, std::max(sizeof(muon::NormWorkspace), live));
         if (!zeros || hipMalloc(reinterpret_cast<void **>(&ctx->norm_ws), sizeof(muon::NormWorkspace)) != hipSuccess ||
-            hipMemcpy(ctx->norm_ws, zeros, sizeof(muon::NormWorkspace), hipMemcpyHostToDevice) != hipSuccess) {
+            hipMemcpy(ctx->norm_ws, zeros, sizeof(muon::NormWorkspace), hipMemcpyHostToDevice) != hipSuccess ||
+            hipMalloc(reinterpret_cast<void **>(&ctx->router_live), live) != hipSuccess ||
+            hipMemcpy(ctx->router_live, zeros, live, hipMemcpyHostToDevice) != hipSuccess) {
             (void)hipGetLastError();
             std::free(zeros);
             if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
+            if (ctx->router_live) (void)hipFree(ctx->router_live);
             (void)hipEventDestroy(ctx->upload_done);
             (void)hipEventDestroy(ctx->noalloc_upload_done);
             delete ctx;
@@ -2320,6 +2326,7 @@ muon_status muon_destroy(muon_context *ctx) {
         if (b->p) (void)hipFree(b->p);
     for (void *p : ctx->retired) (void)hipFree(p);
     if (ctx->norm_ws) (void)hipFree(ctx->norm_ws);
+    if (ctx->router_live) (void)hipFree(ctx->router_live);
     if (ctx->pinned) (void)hipHostFree(ctx->pinned);
     if (ctx->noalloc_pinned) (void)hipHostFree(ctx->noalloc_pinned);
     if (ctx->upload_done) (void)hipEventDestroy(ctx->upload_done);

@@ -84,7 +84,7 @@ status hipLaunchKernel(const void *fn, dim3 g, dim3 b, void **args, size_t s, vo
     calls[n_calls].name = "";
     for (int i = 0; i < n_kernels; ++i)
         if (kernels[i].fn == fn) calls[n_calls].name = kernels[i].name;
-    calls[n_calls].blocks = g.x;
+    calls[n_calls].blocks = g.x * g.y * g.z;
     calls[n_calls].threads = b.x;
     calls[n_calls].a = calls[n_calls].b = 0;
     if (strstr(calls[n_calls].name, "router_clear")) {  /* (uint32_t *, int64_t) */

@@ -52,3 +52,40 @@ def test_rows_of_small_sigmoids(ctx, tokens, experts):
     off = np.abs(b.dfull.cpu().numpy() - grad)
     assert (off <= 2.0 ** -16 * bound + 2.0 ** -24 * np.abs(grad) + 2.0 ** -100 * away + 1e-38).all()
     assert abs(float(b.loss) - loss) <= 2.0 ** -17 * loss and np.array_equal(b.counts.cpu().numpy(), counts)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts, sequences", [(64, 20000), (256, 4096), (1000, 300), (5, 30000)])
+def test_thousands_of_sequences(ctx, experts, sequences, score):
+    """Sequences of no token, one and some, and masked ones; another router of few in the same launch; again, and added up."""
+    import torch
+    rng = np.random.default_rng(53)
+    cuts = np.sort(rng.integers(0, 30001, sequences - 1)).tolist()
+    mine = ms.Context(0)
+    many = Batch(rng, 30000, experts, 3, offsets=[0, *cuts, 30000], mask=True, bits=32, score=score)
+    few = Batch(rng, 9000, experts, 3, offsets=[0, 4000, 4000, 9000], score=score)
+    none = Batch(rng, 0, experts, 3, offsets=[0] * 40, score=score)
+    for turn in range(3):
+        run(mine, [few, many, none], score)
+        for b in (many, few, none):
+            b.check()
+    first = [(b.counts.clone(), b.loss.clone(), b.dfull.clone()) for b in (many, few)]
+    for b in (many, few, none):
+        b.counts.fill_(7)
+    run(mine, [few, many, none], score, accumulate=True)
+    for b, (counts, loss, grad) in zip((many, few), first):
+        assert torch.equal(b.counts, counts + 7) and torch.equal(b.loss, loss) and torch.equal(b.dfull, grad)
+    assert bool((none.counts == 7).all())
+    graph, hp = torch.cuda.CUDAGraph(), ms.balance_hparams(1e-2, score=ms.MUON_SCORE_SIGMOID if score == "sigmoid" else ms.MUON_SCORE_SOFTMAX)
+    with torch.cuda.graph(graph):
+        mine.muon_router_balance([few.item(), many.item(), none.item()], hp, stream=torch.cuda.current_stream())
+    for turn in range(3):
+        run(mine, [few], score)
+        for b in (many, few):
+            b.counts.zero_()
+            b.loss.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for b, kept in zip((many, few), first):
+            assert all(torch.equal(x, y) for x, y in zip((b.counts, b.loss, b.dfull), kept)), turn
+    mine.close()

@@ -105,6 +105,17 @@ def test_counts_in_memory_of_a_refused_call(ctx):
     assert st == ms.MUON_OK and kinds(calls) == ["router_count", "router_balance", "router_finish"]
 
 
+def test_many_sequences_are_spread(ctx):
+    """The last launch adds up all counts of all sequences: one workgroup for each router and 16384 of them, in whole
+    sequences (252 of 65, 63 of 257, 16 of 1024), or more where that would be above 1024 workgroups."""
+    for sequences, experts, workgroups in ((1, 64, 1), (252, 64, 1), (253, 64, 2), (4096, 256, 66), (1 << 20, 1023, 1024)):
+        one = router(tokens=1 << 20, offsets=BASE + (8 << 32), sequences=sequences, experts=experts, pitch=1024, dlogits_pitch=1024)
+        st, calls = ctx.balance(one)
+        assert st == ms.MUON_OK and kinds(calls)[-1] == "router_finish" and calls[-1][1] == workgroups, sequences
+        few = router(1, tokens=9000, experts=experts, pitch=1024, dlogits_pitch=1024)
+        assert ctx.balance(one, few)[1][-1][1] == 2 * workgroups
+
+
 QUINTIC, CUBIC = (3.4445, -4.7750, 2.0315), (2.0, -1.5, 0.5)
 
 
