@@ -619,7 +619,7 @@ def block_matrix(param, grad, momentum, block_rows, block_cols, ns_out=None):
             raise ValueError("param, grad, momentum and ns_out must be 2-D, not empty and of one shape")
         if cols > 1 and t.stride(1) != 1:
             raise ValueError(f"{name} must have contiguous rows, got strides {tuple(t.stride())}")
-        pitches.append(max(t.stride(0), cols) if rows == 1 else t.stride(0))
+        pitches.append(cols if rows == 1 else t.stride(0))
         if pitches[-1] < cols:
             raise ValueError(f"{name}'s rows overlap: strides {tuple(t.stride())}")
     _require_f32(list(zip(_MATRIX_NAMES, tensors))[2:])
