@@ -32,7 +32,8 @@
  *   - A context is not thread-safe; calls on one context must be ordered by
  *     the caller (one stream at a time, or explicit synchronisation).
  *   - Results are deterministic: identical inputs give bit-identical outputs
- *     (no atomic adds up values; muon_grad_norm's one counts workgroups).
+ *     (atomics add up whole numbers only: muon_grad_norm's counts workgroups,
+ *     muon_router_balance's choices and sequences).
  */
 #ifndef MUON_STEP_H
 #define MUON_STEP_H
@@ -430,29 +431,31 @@ muon_status muon_step(muon_context *ctx, const muon_matrix *mats, int64_t count,
  *     M <- mu M + G,  N = mu M + G (or M),  X = N / ||N||_F,
  *     X <- a X + b (X X^T) X + c (X X^T)^2 X  for each step of the schedule,
  *     W <- (1 - lr wd) W - lr O,  O as hp's scale_mode says, RMS block by block.
- * M has muon_step's bits (and hp's grad_factor its meaning).  Operands of the
- * products are fp32 values as pairs of 16-bit parts, sums are fp32, so X is far
- * closer to the exact iteration than MUON_NS_BF16's.  Relative Frobenius error of
- * the named schedules: 1e-6 on blocks whose singular values lie within a factor
- * of ten, 1e-5 to 3e-5 where they spread over three decades, 1e-4 to 3e-4 for squares,
- * whose smallest ones are small indeed; of sides up to 16, which work in fp64, 2e-7, 2e-6
- * and 1e-5; below full rank a few times 2^-24 of the
- * schedule's gain (below; 4e-3 to 1e-2 for "deepseekv4").  A schedule that does not settle
- * multiplies this by its own sensitivity to its input (the quintic's singular values
- * keep moving: 1 to 2 after 5 steps, up to 20 after 12); hp's
- * ns_precision must be MUON_NS_BF16 (MUON_NS_F32: UNSUPPORTED).  The schedule
- * must keep every singular value of [0, 1] within 3.9 at each step, with
- * |a + b x + c x^2| and its product with x at most 60 on the x it meets, the
+ * M has muon_step's bits (and hp's grad_factor its meaning).  hp's ns_precision
+ * must be MUON_NS_BF16 (MUON_NS_F32: UNSUPPORTED), but X is far closer to the exact
+ * iteration than that of muon_step: operands of the products are fp32 values as
+ * pairs of 16-bit parts with fp32 sums, and blocks with a side of at most 16 are
+ * worked on in fp64 but for the last product.  Relative Frobenius error of O with
+ * the named schedules (in brackets: sides up to 16)
+ *     singular values within a factor of ten      1e-6            (2e-7)
+ *     spread over three decades                   1e-5 to 3e-5    (2e-6)
+ *     squares of such spectra                     3e-5 to 3e-4    (1e-6 to 2e-4)
+ *     rank below the smaller side                 4e-3 to 1e-2    (the same),
+ * where an iteration in fp32 has 1e-6, 2e-6, 2e-6 to 1e-5 and 2e-3.  The last is a few times
+ * 2^-24 of the schedule's gain (below).  A schedule that does not settle multiplies
+ * all of it, in any arithmetic, by its sensitivity to its input (the quintic's
+ * singular values keep moving: 1 to 2 after 5 steps, up to 20 after 12).
+ * The schedule must keep every singular value of [0, 1] within 3.9 at each step,
+ * with |a + b x + c x^2| and its product with x at most 60 on the x it meets, the
  * largest singular value above 0.044 wherever in [128^-1/2, 1] it begins, and the
  * product over the steps of the largest |a + b x + c x^2|, its gain, at most 2^22
  * (UNSUPPORTED otherwise).  The named schedules stay within 1.3 and 4, above 0.3
- * and within 2^17; 12 steps of the quintic or 22 of (2, -1.5, 0.5) are the
- * longest.  A block
- * whose N is all zero gets the decay-only update, one with an infinity or a NaN
- * in N becomes NaN in all its elements, and no other block does; the scale of N
- * does not matter, from the smallest fp32 values to the largest.  A block's
- * result does not depend on the other blocks of the call, but for the order of its
- * sums, which goes by their number.
+ * and within 2^17; 12 steps of the quintic or 22 of (2, -1.5, 0.5) are the longest.
+ * A block whose N is all zero gets the decay-only update, one with an infinity or a
+ * NaN in N becomes NaN in all its elements, and no other block does; the scale of N
+ * does not matter, from the smallest fp32 values to the largest.  A block's result
+ * does not depend on the other blocks of the call, but for the order of its sums,
+ * which goes by their number.
  * Descriptors travel as kernel arguments; the step works in memory of the
  * context, at most its workspace cap, which grows on first use: under graph
  * capture the call works once a call with the same list has run, and is refused

@@ -610,7 +610,8 @@ _MATRIX_NAMES = ("param", "grad", "momentum", "ns_out")
 
 def block_matrix(param, grad, momentum, block_rows, block_cols, ns_out=None):
     """muon_block_matrix for torch tensors: 2-D, of one shape, rows contiguous and any distance apart (views of a
-    larger tensor, too), one GPU; momentum and ns_out float32, param and grad float32 or bfloat16."""
+    larger tensor, too; a single row's stride does not matter), one GPU; momentum and ns_out float32, param and grad
+    float32 or bfloat16."""
     tensors = (param, grad, momentum) if ns_out is None else (param, grad, momentum, ns_out)
     rows, cols = param.shape if param.dim() == 2 else (0, 0)
     pitches = []
@@ -775,7 +776,8 @@ def balance_hparams(coef, score=MUON_SCORE_SOFTMAX, accumulate=False, grad_scale
 
 
 def router_bias(bias, counts):
-    """muon_router_bias for torch tensors: contiguous float32 biases and int64 counts of one router's experts."""
+    """muon_router_bias for torch tensors: contiguous float32 biases and int64 counts of one router's experts.  It holds
+    addresses and sizes only: a program whose tensors stay where they are makes a table() of them once."""
     import torch
     _require_f32((("bias", bias),))
     if counts.dtype != torch.int64:

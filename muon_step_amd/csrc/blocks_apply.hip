@@ -1,12 +1,13 @@
 // The passes of the block step that multiply N by P (blocks.hpp).
 //
 // A wave holds P's rows as fragments in turn from shared memory, and N's columns
-// from M and G, formed and split in registers: nothing between is stored.  Bound by
-// memory (6 bytes an element read for X X^T, 8 or 10 more for W), and close behind
-// by the vector units' splitting of N and by the matrix cores: 3 x 2 s 16-bit
-// operations an element for P N, 3 s for X X^T.  1728 heads of 128 x 2048, bf16:
-// X X^T 0.75 ms, 3.6 TB/s; update 1.05 ms, 4.3 TB/s.  V = 2 columns a lane halves
-// the accesses; V = 4 spills.
+// from M and G, formed and split in registers: nothing between is stored.  1728 heads
+// of 128 x 2048, bf16: X X^T 0.74 ms, 3.7 TB/s of 6 bytes read an element; update 1.06 ms,
+// 4.3 TB/s of 10 (a copy: 4.9).  The update is bound by memory (matrix cores 14%, vector
+// units 21% busy).  X X^T is not: its sums and P N leave room for one wave a SIMD, in
+// which loads, splits (23%) and products (31%: 3 x 2 s 16-bit operations an element for
+// P N, 3 s for X X^T) follow one another.  V = 2 columns a lane halves the accesses; V = 4
+// spills.
 #include "blocks_device.hpp"
 
 namespace muon {
@@ -471,7 +472,7 @@ __device__ __forceinline__ void update_columns(Stream<T, V, TALL, BF16, EVEN> &i
 // The last pass: O = P N / ||N|| and W of one part of one block.
 template <int T, bool TALL, bool BF16, bool PBF16, bool EVEN>
 __global__ __launch_bounds__(kThreads) void blocks_update_kernel(const BlockTable t, const BlockCall c) {
-    // four columns a lane, 16 and 8 bytes of fp32 and bf16 data, where the part is
+    // two columns a lane, 8 and 4 bytes of fp32 and bf16 data, where the part is
     // long enough for whole units of all waves
     constexpr int V = TALL ? 1 : 2;
     __shared__ __attribute__((aligned(16))) Poly<T> poly;

@@ -1,7 +1,8 @@
-// The first pass of the block step: momentum, N, and the sums of N N^T (blocks.hpp).
+// The first pass of the block step: momentum, N, and the sums of N N^T (blocks.hpp), for
+// sides above 16.
 //
 // Bound by memory (10 bytes an element, and 4 s / 2 products of 16-bit parts for
-// each, a quarter of the matrix cores' rate at s = 128).  What counts is that
+// each: matrix cores 11%, vector units 15% busy at s = 128).  What counts is that
 // neighbouring lanes read and write neighbouring memory, and that the next 32
 // columns are on their way while the present ones are worked on.  The operand
 // layout has neighbouring lanes in different rows; so a wave of a wide block works
@@ -9,8 +10,8 @@
 // parts through its own piece of shared memory.  (Loads and stores in the operand
 // layout, 16 bytes a lane 32 or 16 rows apart, kept the address units busy: 3.7 and
 // 4.1 TB/s.)  In tall blocks lanes that are neighbours in the operand are so in
-// memory, T elements each.  1728 heads of 128 x 2048, bf16 gradients (4.5 GB): 1.02
-// ms, 4.4 TB/s, where a copy moves 4.9; 16 heads 16 us.
+// memory, T elements each.  1728 heads of 128 x 2048, bf16 gradients (4.5 GB): 1.03
+// ms, 4.4 TB/s, where a copy moves 4.9; 16 heads 14 us.
 #include "blocks_device.hpp"
 
 namespace muon {
@@ -163,9 +164,6 @@ template <int T, bool TALL, bool BF16> struct Columns {
     }
 };
 
-// One part of one block: M <- mu M + G and the sum of N N^T over the part's
-// columns.  Outside 2^-40 <= max |N| <= 2^40, where squares could leave fp32's
-// range, the part is summed a second time as N 2^-shift.
 // A wave's 32 columns of N as 16-bit parts, row by row; 16 bytes behind each row
 // keep lanes that read rows side by side off one another's banks.
 template <int T> struct Turned {
@@ -173,6 +171,9 @@ template <int T> struct Turned {
     __attribute__((aligned(16))) __bf16 hi[32 * T][kPitch], lo[32 * T][kPitch];
 };
 
+// One part of one block: M <- mu M + G and the sum of N N^T over the part's
+// columns.  Outside 2^-40 <= max |N| <= 2^40, where squares could leave fp32's
+// range, the part is summed a second time as N 2^-shift.
 template <int T, bool TALL, bool BF16>
 __global__ __launch_bounds__(kThreads) void blocks_momentum_kernel(const BlockTable t, const BlockCall c) {
     union Shared {

@@ -1765,9 +1765,11 @@ muon_status run_tables(muon_context *ctx, const T *ts, int64_t count, int stage,
 // ---- muon_blocks_step
 
 // Blocks with this many parts of their long side in all fill the card, one for each
-// CU: fewer, larger parts leave sums to join and bandwidth idle, more of them repeat
-// what a part costs beside its columns.  27 adapters, 16 heads, 21 ragged blocks in us
-// with 512: 46, 190, 161; 256: 40.5, 189, 161; 128: 43.7, 174, 199; 64: 49, 187, 240.
+// CU: fewer, larger parts leave bandwidth idle, more of them repeat what a part costs
+// beside its columns, and their sums have to be joined.  27 adapters of 16 x 2048, 16
+// heads by rows and by columns, 21 blocks of 80 x 1407, 128 of 128 x 4096, 1728 of 128 x
+// 2048 in us with 128: 27, 175, 177, 204, 702, 3708; 256: 23, 182, 174, 166, 573, 3680;
+// 512: 24, 183, 175, 165, 590, 3680; 1024: 24, 183, 174, 166, 602, 3804.
 constexpr int64_t kBlockWorkgroups = 256;
 constexpr int64_t kMaxBlockParts = 32;
 // What the blocks of one launch may hold in the context.
