@@ -65,8 +65,8 @@ constexpr int kBlockUnit = 128;      // columns of X that a workgroup takes at o
 constexpr int kMaxChainSteps = 64;
 // Largest smaller side of blocks that are worked on in fp64: one tile of its matrix
 // instructions, whose products cost less there than their latency.  Sides of 17 to 32
-// would take eight times as many: 8.5 us of a CU for ten steps, or 340 us for 10000 blocks of
-// 32 x 256, which the other passes move in 300.
+// would take eight times as many: by their rate 8.5 us of a CU for ten steps, or 340 us for
+// 10000 blocks of 32 x 256, whose bytes a copy moves in 320.
 constexpr int kNarrowSide = 16;
 
 // What one block needs between the launches (index: block of the launch).
